@@ -69,6 +69,12 @@
  *                                   outside [-1, node)
  *                             1024  (top-k / top-p verification) top_k
  *                                   outside [1, 4096] or top_p outside (0, 1]
+ *                             2048  (KV cache) a sequence length or row count
+ *                                   that does not fit (see specv_kv_cache)
+ *                             4096  (KV cache) a block table entry in use
+ *                                   outside the pool
+ *                             8192  (KV cache compaction) a path that is not
+ *                                   strictly increasing inside [0, M)
  *                              The walk checks position 0, 1, ... in order and
  *                              stops at the first position with an error; a
  *                              row with any of the bits 1, 2, 4, 8, 32, 64, 512, 1024 set
@@ -246,6 +252,119 @@ specv_status specv_rollback(specv_handle h, const int32_t *num_accepted, int bat
                             int32_t *block_tables, int max_blocks, int32_t *num_blocks, int block_size,
                             int32_t *free_list, int64_t free_capacity, int32_t *free_count, int32_t *row_status,
                             void *stream);
+
+/* A paged KV cache of one layer, as specv_rollback keeps it ("LLM Inference &
+ * Speculative Decoding: From Roofline Physics to Lossless Acceleration", s.1,
+ * PagedKVCacheManager: a pool of blocks [blocks, heads, block_size, head_dim]
+ * for the keys, one for the values, and a block table per sequence).  Every
+ * pointer is device memory:
+ *   k, v          the two pools, element type dtype.  Inside a block
+ *                 [kv_heads, block_size, head_dim] without gaps; block_stride
+ *                 elements from one block to the next (the same in both), so
+ *                 that a pool may be a slice of a larger tensor
+ *   block_tables  [B, max_blocks] int32: block of each logical block
+ *   seq_lens      [B] int32: positions held, the rows of the current pass the
+ *                 last of them (position t is in block t / block_size of the
+ *                 table, at t % block_size).  0: an idle sequence (padding of
+ *                 a batch): nothing of it is read, its status is 0
+ * head_dim is a multiple of 16 from 16 to 256, block_size 1..65536, blocks at
+ * most 2^31 - 1; k, v and the tensors of the calls below are 16-byte aligned,
+ * and so is block_stride in bytes.  Sizes outside these, or a block_stride
+ * below kv_heads * block_size * head_dim: SPECV_ERR_INVALID_ARGUMENT.
+ * A sequence is refused, with its row_status saying why, if its length is
+ * negative, below the rows of the pass (0 aside) or above max_blocks *
+ * block_size (bit 2048), or if an entry of its table that the call needs is
+ * outside [0, blocks) (bit 4096). */
+typedef struct {
+    specv_dtype dtype;
+    int kv_heads, head_dim, block_size, max_blocks;
+    void *k, *v;
+    int64_t blocks;
+    int64_t block_stride;
+    const int32_t *block_tables;
+    const int32_t *seq_lens;
+} specv_kv_cache;
+
+/* Append the keys and values of a pass to the cache, with rotary positions
+ * applied on the way (the page's PagedKVCacheManager.append, and the depth
+ * positions of "Multi-Draft Tree Speculation", s.3).  rows tokens a sequence:
+ * row 0 follows the verified prefix, row 1 + i is draft node i.
+ *   k, v        [B, rows, kv_heads, head_dim], element type cache->dtype;
+ *               k_stride, v_stride elements from one row to the next (rows of
+ *               a sequence and sequences alike), a multiple of 16 bytes
+ *   q           as k, with q_heads heads (nullable: q_heads, q_stride and
+ *               q_out are then not looked at)
+ *   q_out       [B, rows, q_heads, head_dim] out, without gaps: q rotated; it
+ *               may be q itself (q_stride = q_heads * head_dim).  Zero for
+ *               padding rows, idle and refused sequences
+ *   inv_freq    [rot_dim / 2] fp32: the first rot_dim (even, <= head_dim)
+ *               values of each head of q and k turn in pairs by the angle
+ *               position * inv_freq[j]; pair j is (j, j + rot_dim / 2), or
+ *               (2j, 2j + 1) if interleaved.  rot_dim 0: no rotation
+ *               (inv_freq may be NULL).  The angle is formed in float64, the
+ *               products in fp32, rounded once
+ *   parents     [B, rows - 1] int32 as for specv_verify_tree_greedy; NULL:
+ *               every sequence is a chain (then rows is not bounded by max_k,
+ *               so that prompts can be appended)
+ *   row_counts  [B] int32, 0..rows: the rows of each sequence that are tokens,
+ *               the others being padding that is not read; NULL: all rows
+ *               (none of an idle sequence).  Outside: bit 2048
+ *   row_status  [B] out (nullable): 0, or bits 512 (a parent outside
+ *               [-1, i)), 2048, 4096.  Of a refused sequence nothing is written
+ *               to the cache
+ * Row r goes to cache position base + r, base = seq_lens - row count, and has
+ * the rotary position base + depth(r): depth(0) = 0, a child one more than
+ * its parent, so that a kept path keeps its rotation when specv_cache_compact
+ * moves it.  Sequences of a batch must not share the blocks they write to. */
+specv_status specv_cache_append(specv_handle h, const specv_kv_cache *cache, const void *q, int64_t q_stride,
+                                int q_heads, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                const float *inv_freq, int rot_dim, int interleaved, const int32_t *parents,
+                                const int32_t *row_counts, int batch, int rows, void *q_out, int32_t *row_status,
+                                void *stream);
+
+/* Attention of a pass's rows over the cache they were appended to ("LLM
+ * Inference & Speculative Decoding: From Roofline Physics to Lossless
+ * Acceleration", s.3, the ancestor mask): row r of a sequence sees every
+ * position before the pass's rows, and of these itself and its ancestors
+ * (row 0 is an ancestor of all).
+ *   q           [B, rows, q_heads, head_dim], q_stride elements between rows;
+ *               q_heads a multiple of kv_heads, query head h reads kv head
+ *               h / (q_heads / kv_heads)
+ *   parents     [B, rows - 1] int32; NULL: chains.  1 <= rows <= max_k + 1;
+ *               rows = 1 is plain decoding
+ *   scale       factor of the scores before the softmax, finite
+ *   out         [B, rows, q_heads, head_dim] out, without gaps
+ *   lse         [B, rows, q_heads] fp32 out (nullable): log of the sum of
+ *               the exponentials of the scaled scores
+ *   row_status  [B] out (nullable): 0, or bits 512, 2048, 4096.  out of an
+ *               idle or refused sequence is 0, lse -infinity
+ *   workspace   device memory of specv_tree_attention_workspace(...) bytes,
+ *               256-byte aligned, the call's own until it has run
+ * Positions that a row does not see take no part, whatever they hold (NaN and
+ * infinities among them). */
+specv_status specv_tree_attention(specv_handle h, const specv_kv_cache *cache, const void *q, int64_t q_stride,
+                                  int q_heads, const int32_t *parents, int batch, int rows, float scale, void *out,
+                                  float *lse, int32_t *row_status, void *workspace, int64_t workspace_bytes,
+                                  void *stream);
+
+/* Bytes of workspace that specv_tree_attention needs for these sizes (it does
+ * not depend on lengths); 0 if none or if the sizes are invalid. */
+int64_t specv_tree_attention_workspace(specv_handle h, specv_dtype dtype, int kv_heads, int head_dim, int q_heads,
+                                       int batch, int rows);
+
+/* Move the kept path of a verified tree together in the cache, before
+ * specv_rollback cuts the sequence off behind it: node path[i] (at position
+ * seq_len - M + path[i]) is copied to position seq_len - M + i, for i <
+ * num_accepted, in keys and values of `layers` layers at once (layer l of a
+ * pool at l * layer_stride elements; 1 for a cache that is a tensor a layer).
+ *   path, num_accepted  [B, M], [B] as specv_verify_tree_greedy gives them
+ *   row_status          [B] out (nullable): 0, or bits 128 (num_accepted
+ *                       outside [0, M]), 2048 (a length below M, 0 aside),
+ *                       4096, 8192.  A refused sequence is left as it is
+ * Positions behind the path keep what they held.  1 <= M <= max_k. */
+specv_status specv_cache_compact(specv_handle h, const specv_kv_cache *cache, int layers, int64_t layer_stride,
+                                 const int32_t *path, const int32_t *num_accepted, int batch, int M,
+                                 int32_t *row_status, void *stream);
 
 /* Number of CTAs per sequence (thread-block cluster size, 1..16) that the
  * next call with these sizes would use; 0 if the sizes are invalid. */

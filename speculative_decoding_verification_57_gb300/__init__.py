@@ -11,8 +11,8 @@ from __future__ import annotations
 import ctypes
 
 from . import _lib
-from ._lib import (ST_ERROR_MASK, ST_NONFINITE, ST_Q_INVALID, ST_TEMPERATURE, ST_TIMEOUT, ST_TOKEN_RANGE,
-                   ST_UNIFORM_RANGE, ST_ZERO_RESIDUAL, SPECV_BF16, SPECV_F32)
+from ._lib import (ST_BLOCK, ST_ERROR_MASK, ST_LENGTH, ST_NONFINITE, ST_PARENT, ST_PATH, ST_Q_INVALID, ST_TEMPERATURE,
+                   ST_TIMEOUT, ST_TOKEN_RANGE, ST_UNIFORM_RANGE, ST_ZERO_RESIDUAL, SPECV_BF16, SPECV_F32)
 
 __all__ = [
     "SpecvError",
@@ -22,6 +22,9 @@ __all__ = [
     "specv_verify_sample",
     "specv_verify_greedy",
     "specv_verify_sample_host",
+    "specv_cache_append",
+    "specv_tree_attention",
+    "specv_cache_compact",
     "specv_plan_cluster",
     "specv_test_withhold_stage",
     "specv_launch_count",
@@ -33,6 +36,10 @@ __all__ = [
     "ST_ZERO_RESIDUAL",
     "ST_Q_INVALID",
     "ST_TIMEOUT",
+    "ST_PARENT",
+    "ST_LENGTH",
+    "ST_BLOCK",
+    "ST_PATH",
 ]
 
 
@@ -296,6 +303,220 @@ def specv_rollback(h: Handle, num_accepted, k, seq_lens, block_tables, num_block
         ctypes.c_void_p(ptrs[3]), int(block_size), ctypes.c_void_p(ptrs[4]), free_list.numel(),
         ctypes.c_void_p(ptrs[5]), ctypes.c_void_p(prs), _stream_ptr(stream))
     _check(st, "specv_rollback")
+
+
+# ------------------------------------------------------------------ paged KV cache
+def _on(h, t, dtype, name, shape=None):
+    """A contiguous CUDA tensor on the handle's device."""
+    p = _dev(t, dtype, name, shape)
+    if t.device.index != h.device:
+        raise ValueError(f"{name} is on {t.device}, the handle on cuda:{h.device}")
+    return p
+
+
+def _inner(t, n):
+    """Whether the last n dimensions of ``t`` lie behind one another without
+    gaps (dimensions of size one may have any stride); their size."""
+    want = 1
+    for size, stride in zip(reversed(t.shape[-n:]), reversed(t.stride()[-n:])):
+        if size != 1 and stride != want:
+            return None
+        want *= size
+    return want
+
+
+def _kv_cache(h, k_cache, v_cache, block_tables, seq_lens, layered=False):
+    """The descriptor of a cache; with ``layered`` the pools may have a
+    leading dimension of layers.  Returns (descriptor, layers, layer_stride)."""
+    torch = _torch()
+    dt = _cache_dtype(k_cache)
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not t.is_cuda or t.device.index != h.device:
+            raise ValueError(f"{name} must be on the handle's device, cuda:{h.device}")
+    if v_cache.dtype != k_cache.dtype:
+        raise TypeError(f"v_cache must be {k_cache.dtype}, got {v_cache.dtype}")
+    if k_cache.dim() != 4 and not (layered and k_cache.dim() == 5):
+        raise ValueError("the cache pools have the shape "
+                         + ("[layers, blocks, heads, block_size, head_dim] or " if layered else "")
+                         + "[blocks, heads, block_size, head_dim]")
+    if v_cache.shape != k_cache.shape:
+        raise ValueError(f"v_cache has shape {tuple(v_cache.shape)}, expected {tuple(k_cache.shape)}")
+    blocks, heads, block_size, head_dim = k_cache.shape[-4:]
+    inner = _inner(k_cache, 3)
+    if inner is None or _inner(v_cache, 3) is None:
+        raise ValueError("the cache pools must be contiguous inside a block")
+    layers = k_cache.shape[0] if k_cache.dim() == 5 else 1
+    for i in range(k_cache.dim() - 3):
+        if k_cache.shape[i] > 1 and k_cache.stride(i) != v_cache.stride(i):
+            raise ValueError("k_cache and v_cache must have the same strides")
+    block_stride = k_cache.stride(-4) if blocks > 1 else inner
+    layer_stride = k_cache.stride(0) if layers > 1 else 0
+    tables = _on(h, block_tables, torch.int32, "block_tables")
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must have the shape [B, max_blocks]")
+    lens = _on(h, seq_lens, torch.int32, "seq_lens", (block_tables.shape[0],))
+    c = _lib.SpecvKvCache(dt, heads, head_dim, block_size, block_tables.shape[1], k_cache.data_ptr(),
+                          v_cache.data_ptr(), blocks, block_stride, tables, lens)
+    return c, layers, layer_stride
+
+
+def _cache_dtype(t):
+    torch = _torch()
+    if isinstance(t, torch.Tensor):
+        if t.dtype == torch.bfloat16:
+            return SPECV_BF16
+        if t.dtype == torch.float32:
+            return SPECV_F32
+    raise TypeError("the cache pools must be bfloat16 or float32 tensors")
+
+
+def _token_rows(h, t, name, like, shape):
+    """Pointer and row stride of a [B, rows, heads, head_dim] tensor whose
+    rows are evenly spaced (a slice of a fused projection will do)."""
+    if not t.is_cuda or t.device.index != h.device:
+        raise ValueError(f"{name} must be on the handle's device, cuda:{h.device}")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if t.dim() != 4 or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    B, rows = shape[:2]
+    inner = _inner(t, 2)
+    stride = t.stride(1) if rows > 1 else t.stride(0) if B > 1 else inner
+    if inner is None or (B > 1 and rows > 1 and t.stride(0) != rows * stride):
+        raise ValueError(f"{name} must have contiguous heads and evenly spaced rows")
+    return t.data_ptr(), stride
+
+
+def _device_stream(h, stream):
+    return stream if stream is not None else _torch().cuda.current_stream(h.device)
+
+
+def _empty(h, shape, dtype, stream):
+    """A tensor for a call on ``stream``: allocated there, so that its memory
+    is not handed on before the call has run."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", h.device))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", h.device))
+
+
+def specv_cache_append(h: Handle, k_cache, v_cache, block_tables, seq_lens, k, v, *, q=None, inv_freq=None,
+                       interleaved=False, parents=None, row_counts=None, out=None, stream=None):
+    """Append the keys and values of a pass to a paged cache, in place, and
+    rotate queries and keys by their positions on the way.  k_cache, v_cache
+    [blocks, kv_heads, block_size, head_dim] bf16 or fp32; block_tables
+    [B, max_blocks], seq_lens [B] int32, the lengths with the pass's rows;
+    k, v [B, rows, kv_heads, head_dim] and q [B, rows, q_heads, head_dim]
+    (optional) of the caches' type, rows evenly spaced; inv_freq
+    [rot_dim / 2] fp32 (None: no rotation); parents [B, rows - 1] int32
+    (None: chains, or prompts); row_counts [B] int32 (None: all rows are
+    tokens).  Returns a dict: q_out (with q) and row_status [B]; ``out`` may
+    supply them."""
+    torch = _torch()
+    c, _, _ = _kv_cache(h, k_cache, v_cache, block_tables, seq_lens)
+    if k.dim() != 4:
+        raise ValueError("k must have the shape [B, rows, kv_heads, head_dim]")
+    B, rows = k.shape[:2]
+    if B != block_tables.shape[0]:
+        raise ValueError(f"k holds {B} sequences, block_tables {block_tables.shape[0]}")
+    pk, k_stride = _token_rows(h, k, "k", k_cache, (B, rows, c.kv_heads, c.head_dim))
+    pv, v_stride = _token_rows(h, v, "v", k_cache, (B, rows, c.kv_heads, c.head_dim))
+    pf, rot = None, 0
+    if inv_freq is not None:
+        pf = _on(h, inv_freq, torch.float32, "inv_freq")
+        rot = 2 * inv_freq.numel()
+    pp = None if parents is None else _on(h, parents, torch.int32, "parents", (B, rows - 1))
+    pc = None if row_counts is None else _on(h, row_counts, torch.int32, "row_counts", (B,))
+    out = {} if out is None else out
+    pq, q_stride, q_heads, po = None, 0, 0, None
+    if q is not None:
+        if q.dim() != 4:
+            raise ValueError("q must have the shape [B, rows, q_heads, head_dim]")
+        q_heads = q.shape[2]
+        pq, q_stride = _token_rows(h, q, "q", k_cache, (B, rows, q_heads, c.head_dim))
+        if "q_out" not in out:
+            out["q_out"] = _empty(h, (B, rows, q_heads, c.head_dim), k_cache.dtype, stream)
+        po = _on(h, out["q_out"], k_cache.dtype, "q_out", (B, rows, q_heads, c.head_dim))
+    if "row_status" not in out:
+        out["row_status"] = _empty(h, (B,), torch.int32, stream)
+    ps = _on(h, out["row_status"], torch.int32, "row_status", (B,))
+    st = _lib.load().specv_cache_append(
+        h.ptr, c, pq, q_stride, q_heads, pk, k_stride, pv, v_stride, pf, rot, 1 if interleaved else 0, pp, pc, B, rows,
+        po, ps, _device_stream(h, stream).cuda_stream)
+    _check(st, "specv_cache_append")
+    return out
+
+
+def specv_tree_attention(h: Handle, q, k_cache, v_cache, block_tables, seq_lens, *, parents=None, scale=None,
+                         lse=False, out=None, workspace=None, stream=None):
+    """Attention of a pass's rows over the paged cache they were appended to:
+    q [B, rows, q_heads, head_dim], rows evenly spaced, rows <= max_k + 1;
+    the caches, block_tables and seq_lens as for specv_cache_append; parents
+    [B, rows - 1] int32 (None: chains); scale defaults to head_dim ** -0.5.
+    Returns a dict: out [B, rows, q_heads, head_dim], row_status [B] and,
+    with ``lse``, lse [B, rows, q_heads] fp32; ``out`` may supply them.
+    ``workspace`` may supply a CUDA uint8 tensor of at least
+    specv_tree_attention_workspace bytes that no other call uses meanwhile."""
+    torch = _torch()
+    c, _, _ = _kv_cache(h, k_cache, v_cache, block_tables, seq_lens)
+    if q.dim() != 4:
+        raise ValueError("q must have the shape [B, rows, q_heads, head_dim]")
+    B, rows, q_heads = q.shape[:3]
+    if B != block_tables.shape[0]:
+        raise ValueError(f"q holds {B} sequences, block_tables {block_tables.shape[0]}")
+    pq, q_stride = _token_rows(h, q, "q", k_cache, (B, rows, q_heads, c.head_dim))
+    pp = None if parents is None else _on(h, parents, torch.int32, "parents", (B, rows - 1))
+    out = {} if out is None else out
+    if "out" not in out:
+        out["out"] = _empty(h, (B, rows, q_heads, c.head_dim), k_cache.dtype, stream)
+    po = _on(h, out["out"], k_cache.dtype, "out", (B, rows, q_heads, c.head_dim))
+    if "row_status" not in out:
+        out["row_status"] = _empty(h, (B,), torch.int32, stream)
+    ps = _on(h, out["row_status"], torch.int32, "row_status", (B,))
+    pl = None
+    if lse:
+        if "lse" not in out:
+            out["lse"] = _empty(h, (B, rows, q_heads), torch.float32, stream)
+        pl = _on(h, out["lse"], torch.float32, "lse", (B, rows, q_heads))
+    lib = _lib.load()
+    if workspace is None:
+        need = lib.specv_tree_attention_workspace(h.ptr, c.dtype, c.kv_heads, c.head_dim, q_heads, B, rows)
+        workspace = _empty(h, (need,), torch.uint8, stream) if need else None
+    pw = None if workspace is None else _on(h, workspace, torch.uint8, "workspace")
+    st = lib.specv_tree_attention(
+        h.ptr, c, pq, q_stride, q_heads, pp, B, rows, c.head_dim ** -0.5 if scale is None else scale, po, pl, ps, pw,
+        0 if workspace is None else workspace.numel(), _device_stream(h, stream).cuda_stream)
+    _check(st, "specv_tree_attention")
+    return out
+
+
+def specv_tree_attention_workspace(h: Handle, dtype, kv_heads, head_dim, q_heads, batch, rows) -> int:
+    """Bytes of workspace a specv_tree_attention call of these sizes needs
+    (dtype SPECV_BF16 or SPECV_F32)."""
+    return int(_lib.load().specv_tree_attention_workspace(h.ptr, dtype, kv_heads, head_dim, q_heads, batch, rows))
+
+
+def specv_cache_compact(h: Handle, k_cache, v_cache, block_tables, seq_lens, path, num_accepted, *, row_status=None,
+                        stream=None):
+    """Move the kept path of a verified tree together in the caches, in place,
+    before specv_rollback: path [B, M] and num_accepted [B] int32 as
+    specv_verify_tree_greedy returns them, the caches [blocks, kv_heads,
+    block_size, head_dim] or [layers, blocks, ...] for all layers at once,
+    seq_lens [B] with the tree's nodes the last M.  row_status [B] (optional)
+    receives 0 or the bits of a refused sequence."""
+    torch = _torch()
+    c, layers, layer_stride = _kv_cache(h, k_cache, v_cache, block_tables, seq_lens, layered=True)
+    B = block_tables.shape[0]
+    if path.dim() != 2:
+        raise ValueError("path must have the shape [B, M]")
+    M = path.shape[1]
+    pp = _on(h, path, torch.int32, "path", (B, M))
+    pn = _on(h, num_accepted, torch.int32, "num_accepted", (B,))
+    ps = None if row_status is None else _on(h, row_status, torch.int32, "row_status", (B,))
+    st = _lib.load().specv_cache_compact(h.ptr, c, layers, layer_stride, pp, pn, B, M, ps,
+                                         _device_stream(h, stream).cuda_stream)
+    _check(st, "specv_cache_compact")
 
 
 def specv_plan_cluster(h: Handle, logits_dtype, B, k, V) -> int:

@@ -23,6 +23,9 @@ ST_Q_INVALID = 32
 ST_TIMEOUT = 64
 ST_PARENT = 512
 ST_FILTER = 1024
+ST_LENGTH = 2048
+ST_BLOCK = 4096
+ST_PATH = 8192
 ST_ERROR_MASK = (ST_NONFINITE | ST_TOKEN_RANGE | ST_UNIFORM_RANGE | ST_TEMPERATURE | ST_Q_INVALID | ST_TIMEOUT
                  | ST_PARENT | ST_FILTER)
 
@@ -34,6 +37,22 @@ class SpecvDebug(ctypes.Structure):
         ("row_max", ctypes.c_void_p),
         ("row_sumexp", ctypes.c_void_p),
         ("residual_mass", ctypes.c_void_p),
+    ]
+
+
+class SpecvKvCache(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int),
+        ("kv_heads", ctypes.c_int),
+        ("head_dim", ctypes.c_int),
+        ("block_size", ctypes.c_int),
+        ("max_blocks", ctypes.c_int),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("blocks", ctypes.c_int64),
+        ("block_stride", ctypes.c_int64),
+        ("block_tables", ctypes.c_void_p),
+        ("seq_lens", ctypes.c_void_p),
     ]
 
 
@@ -69,6 +88,17 @@ def load(build_if_missing=True):
     lib.specv_verify_tree_greedy.argtypes = [vp, i32, vp, vp, vp, i32, i32, i64, vp, vp, vp, vp, vp]
     lib.specv_rollback.restype = i32
     lib.specv_rollback.argtypes = [vp, vp, i32, i32, vp, vp, i32, vp, i32, vp, i64, vp, vp, vp]
+    cache = ctypes.POINTER(SpecvKvCache)
+    lib.specv_cache_append.restype = i32
+    lib.specv_cache_append.argtypes = [vp, cache, vp, i64, i32, vp, i64, vp, i64, vp, i32, i32, vp, vp, i32, i32, vp,
+                                       vp, vp]
+    lib.specv_tree_attention.restype = i32
+    lib.specv_tree_attention.argtypes = [vp, cache, vp, i64, i32, vp, i32, i32, ctypes.c_float, vp, vp, vp, vp, i64,
+                                         vp]
+    lib.specv_tree_attention_workspace.restype = i64
+    lib.specv_tree_attention_workspace.argtypes = [vp, i32, i32, i32, i32, i32, i32]
+    lib.specv_cache_compact.restype = i32
+    lib.specv_cache_compact.argtypes = [vp, cache, i32, i64, vp, vp, i32, i32, vp, vp]
     lib.specv_plan_cluster.restype = i32
     lib.specv_plan_cluster.argtypes = [vp, i32, i32, i32, i64]
     lib.specv_test_withhold_stage.restype = i32

@@ -1,6 +1,6 @@
 """In-tree build of the CUDA library (``libspecv.so``) for sm_103a.
 
-One translation unit (``csrc/specv.cu``) compiled by nvcc with the CUDA
+One translation unit (``csrc/library.cu``) compiled by nvcc with the CUDA
 runtime linked statically; the result sits next to this file, where the
 binding loads it.  Rebuilt when any source or the public header is newer.
 """
@@ -41,7 +41,7 @@ def build(force=False, verbose=False):
     tmp = LIB + ".tmp"
     cmd = [
         nvcc_path(), ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
-        "-o", tmp, os.path.join(PKG, "csrc", "specv.cu"),
+        "-o", tmp, os.path.join(PKG, "csrc", "library.cu"),
     ]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:

@@ -1,0 +1,180 @@
+// cache_api.cuh -- C ABI of the paged KV cache: argument checks and launches
+// of append, tree attention and compaction.  Included behind specv.cu, whose
+// handle and error handling it uses.
+#pragma once
+#include "cache_append.cuh"
+#include "cache_compact.cuh"
+#include "tree_attention.cuh"
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// The cache of a call as the kernels see it; false if a size, pointer or
+// alignment is outside what specv_kv_cache allows.
+bool make_view(const specv_ctx* h, const specv_kv_cache* c, int batch, KvView& view) {
+    if (!h || !c || batch < 0 || batch > h->max_batch) return false;
+    if (c->dtype != SPECV_F32 && c->dtype != SPECV_BF16) return false;
+    if (c->kv_heads < 1 || c->kv_heads > 65536 || c->head_dim < 16 || c->head_dim > 256 || c->head_dim % 16)
+        return false;
+    if (c->block_size < 1 || c->block_size > 65536 || c->max_blocks < 0 || c->blocks < 0 || c->blocks > INT32_MAX)
+        return false;
+    const int64_t inner = static_cast<int64_t>(c->kv_heads) * c->block_size * c->head_dim;
+    const int64_t vec = c->dtype == SPECV_BF16 ? 8 : 4;
+    if (c->block_stride < inner || c->block_stride % vec) return false;
+    if (c->block_stride > INT64_MAX / 8 / (c->blocks > 0 ? c->blocks : 1)) return false;
+    if (batch > 0 && (!c->seq_lens || (c->max_blocks > 0 && !c->block_tables) || (c->blocks > 0 && (!c->k || !c->v))))
+        return false;
+    if (!aligned16(c->k) || !aligned16(c->v)) return false;
+    view.k = c->k;
+    view.v = c->v;
+    view.tables = c->block_tables;
+    view.lens = c->seq_lens;
+    view.block_stride = c->block_stride;
+    view.blocks = static_cast<int>(c->blocks);
+    view.max_blocks = c->max_blocks;
+    view.heads = c->kv_heads;
+    view.dim = c->head_dim;
+    view.block = FastDiv(static_cast<uint32_t>(c->block_size));
+    return true;
+}
+
+// A tensor of rows [.., heads, head_dim]: its pointer and row stride.
+bool rows_ok(const specv_kv_cache* c, const void* p, int64_t stride) {
+    const int64_t vec = c->dtype == SPECV_BF16 ? 8 : 4;
+    return p && aligned16(p) && stride >= 0 && stride % vec == 0;
+}
+
+// Launch errors of the calls below.
+specv_status launched(specv_ctx* h, const char* what) {
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, what);
+    h->launches.fetch_add(1, std::memory_order_relaxed);
+    return SPECV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+specv_status specv_cache_append(specv_handle h, const specv_kv_cache* cache, const void* q, int64_t q_stride,
+                                int q_heads, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                const float* inv_freq, int rot_dim, int interleaved, const int32_t* parents,
+                                const int32_t* row_counts, int batch, int rows, void* q_out, int32_t* row_status,
+                                void* stream) {
+    AppendArgs a = {};
+    if (!make_view(h, cache, batch, a.kv)) return SPECV_ERR_INVALID_ARGUMENT;
+    if (rows < 1 || (parents && rows - 1 > h->max_k)) return SPECV_ERR_INVALID_ARGUMENT;
+    if (static_cast<int64_t>(batch) * rows > INT32_MAX) return SPECV_ERR_INVALID_ARGUMENT;
+    if (rot_dim < 0 || rot_dim > cache->head_dim || rot_dim % 2 || (rot_dim > 0 && !inv_freq))
+        return SPECV_ERR_INVALID_ARGUMENT;
+    if (batch == 0) return SPECV_OK;
+    if (!rows_ok(cache, k, k_stride) || !rows_ok(cache, v, v_stride)) return SPECV_ERR_INVALID_ARGUMENT;
+    if (q && (!rows_ok(cache, q, q_stride) || !q_out || !aligned16(q_out) || q_heads < 1 || q_heads > 65536 ||
+              (q_out == q && q_stride != static_cast<int64_t>(q_heads) * cache->head_dim)))
+        return SPECV_ERR_INVALID_ARGUMENT;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_out = q_out;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.inv_freq = inv_freq;
+    a.parents = rows > 1 ? parents : nullptr;
+    a.row_counts = row_counts;
+    a.row_status = row_status;
+    a.q_heads = q ? q_heads : 0;
+    a.rot = rot_dim;
+    a.interleaved = interleaved != 0;
+    a.rows = rows;
+    DeviceGuard g(h->device);
+    if (!g.ok) return cuda_fail(cudaErrorInvalidDevice, "cudaSetDevice");
+    const unsigned grid = static_cast<unsigned>(batch) * static_cast<unsigned>(rows);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (cache->dtype == SPECV_BF16)
+        cache_append_kernel<__nv_bfloat16><<<grid, kAppendThreads, 0, s>>>(a);
+    else
+        cache_append_kernel<float><<<grid, kAppendThreads, 0, s>>>(a);
+    return launched(h, "cache_append launch");
+}
+
+int64_t specv_tree_attention_workspace(specv_handle h, specv_dtype dtype, int kv_heads, int head_dim, int q_heads,
+                                       int batch, int rows) {
+    return 0;
+}
+
+specv_status specv_tree_attention(specv_handle h, const specv_kv_cache* cache, const void* q, int64_t q_stride,
+                                  int q_heads, const int32_t* parents, int batch, int rows, float scale, void* out,
+                                  float* lse, int32_t* row_status, void* workspace, int64_t workspace_bytes,
+                                  void* stream) {
+    AttnArgs a = {};
+    if (!make_view(h, cache, batch, a.kv)) return SPECV_ERR_INVALID_ARGUMENT;
+    if (rows < 1 || rows - 1 > h->max_k || q_heads < 1 || q_heads > 65536 || q_heads % cache->kv_heads ||
+        !std::isfinite(scale))
+        return SPECV_ERR_INVALID_ARGUMENT;
+    if (batch == 0) return SPECV_OK;
+    if (!rows_ok(cache, q, q_stride) || !out || !aligned16(out)) return SPECV_ERR_INVALID_ARGUMENT;
+    const int64_t need = specv_tree_attention_workspace(h, cache->dtype, cache->kv_heads, cache->head_dim, q_heads,
+                                                        batch, rows);
+    if (need > 0 && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)))
+        return SPECV_ERR_INVALID_ARGUMENT;
+    a.q = q;
+    a.q_stride = q_stride;
+    a.parents = rows > 1 ? parents : nullptr;
+    a.out = out;
+    a.lse = lse;
+    a.row_status = row_status;
+    a.q_heads = q_heads;
+    a.group = q_heads / cache->kv_heads;
+    a.rows = rows;
+    a.scale = scale;
+    DeviceGuard g(h->device);
+    if (!g.ok) return cuda_fail(cudaErrorInvalidDevice, "cudaSetDevice");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const dim3 grid(static_cast<unsigned>(q_heads), static_cast<unsigned>(rows), static_cast<unsigned>(batch));
+    if (batch > 65535) return SPECV_ERR_INVALID_ARGUMENT;
+    if (cache->dtype == SPECV_BF16)
+        tree_attention_kernel<__nv_bfloat16><<<grid, kAttnThreads, 0, s>>>(a);
+    else
+        tree_attention_kernel<float><<<grid, kAttnThreads, 0, s>>>(a);
+    return launched(h, "tree_attention launch");
+}
+
+specv_status specv_cache_compact(specv_handle h, const specv_kv_cache* cache, int layers, int64_t layer_stride,
+                                 const int32_t* path, const int32_t* num_accepted, int batch, int M,
+                                 int32_t* row_status, void* stream) {
+    CompactArgs c = {};
+    if (!make_view(h, cache, batch, c.kv)) return SPECV_ERR_INVALID_ARGUMENT;
+    const int vec = cache->dtype == SPECV_BF16 ? 8 : 4;
+    if (M < 1 || M > h->max_k || layers < 0 || layers > 65536 || layer_stride < 0 || layer_stride % vec)
+        return SPECV_ERR_INVALID_ARGUMENT;
+    // (layers overlap unless the pools or the blocks of one lie apart; either order of the two strides is fine)
+    if (layers > 1 && layer_stride < static_cast<int64_t>(cache->kv_heads) * cache->block_size * cache->head_dim)
+        return SPECV_ERR_INVALID_ARGUMENT;
+    if (layers > 0 && layer_stride > INT64_MAX / 16 / layers) return SPECV_ERR_INVALID_ARGUMENT;
+    if (batch == 0) return SPECV_OK;
+    if (!path || !num_accepted) return SPECV_ERR_INVALID_ARGUMENT;
+    c.path = path;
+    c.num_accepted = num_accepted;
+    c.row_status = row_status;
+    c.layer_stride = layer_stride;
+    c.M = M;
+    c.layers = layers;
+    c.vec_elems = vec;
+    c.vecs = cache->head_dim / vec;
+    DeviceGuard g(h->device);
+    if (!g.ok) return cuda_fail(cudaErrorInvalidDevice, "cudaSetDevice");
+    const int64_t pieces = static_cast<int64_t>(layers) * 2 * cache->kv_heads * c.vecs;
+    if (pieces > INT32_MAX / 2) return SPECV_ERR_INVALID_ARGUMENT;
+    const int64_t want = (pieces + kCompactThreads - 1) / kCompactThreads;
+    const dim3 grid(static_cast<unsigned>(batch), static_cast<unsigned>(want < 1 ? 1 : want > 64 ? 64 : want), 1);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (cache->dtype == SPECV_BF16)
+        cache_compact_kernel<__nv_bfloat16><<<grid, kCompactThreads, 0, s>>>(c);
+    else
+        cache_compact_kernel<float><<<grid, kCompactThreads, 0, s>>>(c);
+    return launched(h, "cache_compact launch");
+}
+
+}  // extern "C"

@@ -53,6 +53,57 @@ specv_status launched(specv_ctx* h, const char* what) {
     return SPECV_OK;
 }
 
+// Tree attention of one shape: its kernel and, behind it, the join.  The
+// join's CTAs may be placed while the kernel before still runs (they wait for
+// its end), so that they do not add a launch to the call.
+template <typename S>
+cudaError_t launch_attention(const AttnArgs& a, int ctas, cudaStream_t stream) {
+    cudaError_t e = cudaFuncSetAttribute(tree_attention_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         S::kSmem);
+    if (e != cudaSuccess) return e;
+    tree_attention_kernel<S><<<ctas, S::kThreads, S::kSmem, stream>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), S::TM / 4, 1);
+    cfg.blockDim = dim3(kJoinThreads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_attention_join<S>, a, ctas);
+}
+
+struct AttnPlan {
+    int dp, tm, ctas;  // padded head_dim, rows of a tile, CTAs an SM
+    cudaError_t (*launch)(const AttnArgs&, int, cudaStream_t);
+};
+
+template <typename S>
+constexpr AttnPlan plan_of() {
+    return AttnPlan{S::DP, S::TM, S::kCtas, launch_attention<S>};
+}
+
+// The narrowest row tile that holds the rows * group rows of a kv head, or
+// the widest: a tile's keys and values are read once for all of its rows.
+const AttnPlan& attn_plan(specv_dtype dt, int dim, int m) {
+    using B = __nv_bfloat16;
+    static constexpr AttnPlan plans[2][3][3] = {
+        {{plan_of<AttnShape<float, 64, 1, 1>>(), plan_of<AttnShape<float, 64, 1, 2>>(),
+          plan_of<AttnShape<float, 64, 2, 2>>()},
+         {plan_of<AttnShape<float, 128, 1, 1>>(), plan_of<AttnShape<float, 128, 1, 2>>(),
+          plan_of<AttnShape<float, 128, 2, 2>>()},
+         {plan_of<AttnShape<float, 256, 1, 1>>(), plan_of<AttnShape<float, 256, 1, 2>>(),
+          plan_of<AttnShape<float, 256, 1, 2>>()}},
+        {{plan_of<AttnShape<B, 64, 1, 1>>(), plan_of<AttnShape<B, 64, 1, 2>>(), plan_of<AttnShape<B, 64, 2, 2>>()},
+         {plan_of<AttnShape<B, 128, 1, 1>>(), plan_of<AttnShape<B, 128, 1, 2>>(), plan_of<AttnShape<B, 128, 2, 2>>()},
+         {plan_of<AttnShape<B, 256, 1, 1>>(), plan_of<AttnShape<B, 256, 1, 2>>(),
+          plan_of<AttnShape<B, 256, 1, 2>>()}}};
+    return plans[dt == SPECV_BF16 ? 1 : 0][dim <= 64 ? 0 : dim <= 128 ? 1 : 2][m <= 16 ? 0 : m <= 32 ? 1 : 2];
+}
+
 }  // namespace
 
 extern "C" {
@@ -101,7 +152,12 @@ specv_status specv_cache_append(specv_handle h, const specv_kv_cache* cache, con
 
 int64_t specv_tree_attention_workspace(specv_handle h, specv_dtype dtype, int kv_heads, int head_dim, int q_heads,
                                        int batch, int rows) {
-    return 0;
+    if (!h || (dtype != SPECV_F32 && dtype != SPECV_BF16) || kv_heads < 1 || head_dim < 16 || head_dim > 256 ||
+        head_dim % 16 || q_heads < 1 || q_heads % kv_heads || batch < 1 || batch > h->max_batch || rows < 1 ||
+        rows - 1 > h->max_k)
+        return 0;
+    const AttnPlan& p = attn_plan(dtype, head_dim, rows * (q_heads / kv_heads));
+    return attn_work_bytes(h->sm_count * p.ctas, p.tm, p.dp);
 }
 
 specv_status specv_tree_attention(specv_handle h, const specv_kv_cache* cache, const void* q, int64_t q_stride,
@@ -115,9 +171,11 @@ specv_status specv_tree_attention(specv_handle h, const specv_kv_cache* cache, c
         return SPECV_ERR_INVALID_ARGUMENT;
     if (batch == 0) return SPECV_OK;
     if (!rows_ok(cache, q, q_stride) || !out || !aligned16(out)) return SPECV_ERR_INVALID_ARGUMENT;
-    const int64_t need = specv_tree_attention_workspace(h, cache->dtype, cache->kv_heads, cache->head_dim, q_heads,
-                                                        batch, rows);
-    if (need > 0 && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)))
+    const int group = q_heads / cache->kv_heads;
+    const AttnPlan& p = attn_plan(cache->dtype, cache->head_dim, rows * group);
+    const int ctas = h->sm_count * p.ctas;
+    if (!workspace || workspace_bytes < attn_work_bytes(ctas, p.tm, p.dp) ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255))
         return SPECV_ERR_INVALID_ARGUMENT;
     a.q = q;
     a.q_stride = q_stride;
@@ -125,20 +183,19 @@ specv_status specv_tree_attention(specv_handle h, const specv_kv_cache* cache, c
     a.out = out;
     a.lse = lse;
     a.row_status = row_status;
+    a.workspace = static_cast<unsigned char*>(workspace);
+    a.group = FastDiv(static_cast<uint32_t>(group));
     a.q_heads = q_heads;
-    a.group = q_heads / cache->kv_heads;
     a.rows = rows;
+    a.batch = batch;
+    a.row_tiles = (rows * group + p.tm - 1) / p.tm;
     a.scale = scale;
     DeviceGuard g(h->device);
     if (!g.ok) return cuda_fail(cudaErrorInvalidDevice, "cudaSetDevice");
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const dim3 grid(static_cast<unsigned>(q_heads), static_cast<unsigned>(rows), static_cast<unsigned>(batch));
-    if (batch > 65535) return SPECV_ERR_INVALID_ARGUMENT;
-    if (cache->dtype == SPECV_BF16)
-        tree_attention_kernel<__nv_bfloat16><<<grid, kAttnThreads, 0, s>>>(a);
-    else
-        tree_attention_kernel<float><<<grid, kAttnThreads, 0, s>>>(a);
-    return launched(h, "tree_attention launch");
+    const cudaError_t e = p.launch(a, ctas, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "tree_attention launch");
+    h->launches.fetch_add(2, std::memory_order_relaxed);
+    return SPECV_OK;
 }
 
 specv_status specv_cache_compact(specv_handle h, const specv_kv_cache* cache, int layers, int64_t layer_stride,

@@ -3,13 +3,31 @@
 //
 // Row r of sequence b sees the positions before the pass's rows and, of
 // these, itself and its ancestors.  o = sum_j p_j v_j / sum_j p_j with
-// p_j = exp(scale q.k_j - m), m the running maximum of the scores seen so far.
+// p_j = 2^(c q.k_j - m), c = scale log2(e), m a running maximum.  Parts over
+// different positions (m, l = sum p, a = sum p v) join by
+// m = max m_i, l = sum l_i 2^(m_i - m), a = sum a_i 2^(m_i - m).
+//
+// Work.  The query heads of a kv head and the pass's rows are one matrix of
+// rows * group rows, in row tiles of TM; its product with the keys is cut
+// into tiles of positions.  A segment is (sequence, kv head, row tile); all
+// segments' tiles form one line, which is cut into equal runs, one a CTA, so
+// that ragged lengths load every SM alike and a single long sequence is
+// spread over all of them.  The cut is computed from seq_lens on the device
+// by every CTA alike: no plan, no host copy, and a captured graph follows the
+// lengths.  A segment inside one CTA's run is written at once; one that is
+// cut leaves partial results in the workspace, which tree_attention_join
+// adds up in position order.
+//
+// A tile comes by 16-byte cp.async into swizzled shared memory, two tiles
+// ahead of the products, the block numbers of a tile one tile before that.
+// Warps own positions (KW of each tile) and rows: every key and value is
+// read from shared memory by the warps of its positions only, and the
+// softmax state of a warp is its own until its segment ends.
 #pragma once
 #include "kv_cache.cuh"
+#include "ptx.cuh"
 
 namespace specv {
-
-constexpr int kAttnThreads = 128;
 
 struct AttnArgs {
     KvView kv;
@@ -19,89 +37,743 @@ struct AttnArgs {
     void* out;
     float* lse;
     int32_t* row_status;
-    int q_heads, group, rows;
+    unsigned char* workspace;
+    FastDiv group;  // query heads of a kv head
+    int q_heads, rows, batch;
+    int row_tiles;
     float scale;
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kAttnThreads) tree_attention_kernel(const AttnArgs a) {
-    __shared__ float s_q[256], s_p[kAttnThreads], s_red[4];
-    __shared__ int s_blk[kAttnThreads], s_status;
-    __shared__ uint32_t s_anc;
-    const int h = blockIdx.x, r = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-    const KvView& kv = a.kv;
-    const int dim = kv.dim, kvh = h / a.group;
-    const int len = kv.lens[b];
-    if (tid < 32) {
-        uint32_t anc;
-        int depth;
-        const bool ok = warp_tree(a.parents ? a.parents + static_cast<int64_t>(b) * (a.rows - 1) : nullptr, a.rows,
-                                  tid, anc, depth);
-        if (tid == r) s_anc = anc;
-        if (tid == 0) {
-            s_status = ok || len == 0 ? 0 : KV_PARENT;
-            if (len < 0 || (len > 0 && (len < a.rows || !kv.fits(len)))) s_status |= KV_LENGTH;
+// ------------------------------------------------------------------ the cut
+// Positions of sequence b that are attended to; -1 if it is refused by its length.
+__device__ __forceinline__ int attn_len(const AttnArgs& a, int b) {
+    const int len = a.kv.lens[b];
+    return len == 0 || (len >= a.rows && a.kv.fits(len)) ? len : -1;
+}
+
+// An idle or refused sequence counts as a tile, whose CTA writes its zeros.
+__device__ __forceinline__ int attn_tiles(int len, int tile) { return len <= 0 ? 1 : (len + tile - 1) / tile; }
+
+// Run of CTA c of n over `units` tiles, and the CTA that has unit x.
+__device__ __forceinline__ int64_t attn_run(int64_t units, int c, int n) { return units * c / n; }
+__device__ __forceinline__ int attn_owner(int64_t units, int64_t x, int n) {
+    return static_cast<int>(((x + 1) * n - 1) / units);
+}
+
+// A CTA takes at least this many tiles (while there are fewer than CTAs *
+// this, fewer CTAs run): a run's start costs about as much as two tiles.
+constexpr int kAttnLeast = 2;
+
+// Where a run stands on the line of tiles.
+struct AttnCursor {
+    int b, s, tile;  // sequence, segment of it (kv head * row_tiles + row tile), tile
+    int tiles, len;  // of the sequence
+
+    __device__ __forceinline__ void next(const AttnArgs& a, int tile_keys) {
+        if (++tile < tiles) return;
+        tile = 0;
+        if (++s < a.kv.heads * a.row_tiles) return;
+        s = 0;
+        if (++b < a.batch) {
+            len = attn_len(a, b);
+            tiles = attn_tiles(len, tile_keys);
         }
     }
-    const int64_t token = static_cast<int64_t>(b) * a.rows + r;
-    const T* q = static_cast<const T*>(a.q) + token * a.q_stride + h * dim;
-    T* out = static_cast<T*>(a.out) + (token * a.q_heads + h) * dim;
-    for (int d = tid; d < dim; d += kAttnThreads) s_q[d] = KvType<T>::load(q[d]);
+};
+
+// The line's length, the number of CTAs that share it and the start of this
+// CTA's run, by the whole CTA (THREADS threads, a multiple of 32).
+template <int THREADS>
+__device__ void attn_cut(const AttnArgs& a, int tile_keys, int cta, int ctas, int64_t& units, int& used, int64_t& lo,
+                         int64_t& hi, AttnCursor& cur) {
+    __shared__ int64_t s_sum[THREADS / 32];
+    __shared__ int64_t s_at;
+    __shared__ int s_b;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int segs = a.kv.heads * a.row_tiles;
+    // the total, then the sequence that holds `lo`: a pass over the lengths
+    // for each (one load a thread serves both for up to THREADS sequences)
+    int64_t sum = 0, mine = 0;
+    for (int b = tid; b < a.batch; b += THREADS) {
+        mine = attn_tiles(attn_len(a, b), tile_keys);
+        sum += mine;
+    }
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (lane == 0) s_sum[warp] = sum;
     __syncthreads();
-    const uint32_t anc = s_anc;
-    const int base = len - a.rows;
-    float m = -INFINITY, sum = 0.0f, acc[2] = {0.0f, 0.0f};
-    const bool go = s_status == 0 && len > 0;
+    int64_t total = 0;
+    for (int w = 0; w < THREADS / 32; ++w) total += s_sum[w];
+    units = total * segs;
+    const int64_t most = (units + kAttnLeast - 1) / kAttnLeast;
+    used = static_cast<int>(most < ctas ? most : ctas);
+    if (cta >= used) {
+        lo = hi = 0;
+        return;
+    }
+    lo = attn_run(units, cta, used);
+    hi = attn_run(units, cta + 1, used);
+    int64_t before = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += THREADS) {
+        const int b = b0 + tid;
+        if (a.batch > THREADS) mine = b < a.batch ? attn_tiles(attn_len(a, b), tile_keys) : 0;
+        if (b >= a.batch) mine = 0;
+        int64_t incl = mine;
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t o = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += o;
+        }
+        __syncthreads();
+        if (lane == 31) s_sum[warp] = incl;
+        __syncthreads();
+        int64_t ahead = before;
+        for (int w = 0; w < warp; ++w) ahead += s_sum[w];
+        const int64_t start = (ahead + incl - mine) * segs, end = (ahead + incl) * segs;
+        if (mine > 0 && start <= lo && lo < end) {
+            s_b = b;
+            s_at = start;
+        }
+        for (int w = warp; w < THREADS / 32; ++w) ahead += s_sum[w];
+        before = ahead;
+        if (before * segs > lo) break;
+    }
     __syncthreads();
-    for (int t0 = 0; go && t0 < len; t0 += kAttnThreads) {
-        const int t = t0 + tid;
-        float s = -INFINITY;
-        int blk = -1;
-        if (t < len) {
-            const int lb = kv.block.div(t);
-            blk = kv.tables[static_cast<int64_t>(b) * kv.max_blocks + lb];
-            if (!kv.valid(blk)) {
-                s_status = KV_BLOCK;
-                blk = -1;
-            } else if (t < base || (anc >> (t - base) & 1)) {
-                const T* k = static_cast<const T*>(kv.k) + kv.at(blk, kvh, t - lb * kv.block_size());
-                s = 0.0f;
-                for (int d = 0; d < dim; ++d) s = fmaf(s_q[d], KvType<T>::load(k[d]), s);
-                s *= a.scale;
-            } else {
-                blk = -1;
+    cur.b = s_b;
+    cur.len = attn_len(a, cur.b);
+    cur.tiles = attn_tiles(cur.len, tile_keys);
+    const int64_t off = lo - s_at;
+    cur.s = static_cast<int>(off / cur.tiles);
+    cur.tile = static_cast<int>(off - static_cast<int64_t>(cur.s) * cur.tiles);
+}
+
+// ------------------------------------------------------------------ workspace
+// For every CTA a note on the segment that starts in its run and goes on
+// past it, and two partial results: [0] of the segment its run starts in the
+// middle of, [1] of the segment it starts and does not finish.
+struct AttnNote {
+    int b, s;      // b < 0: none
+    int last;      // the CTA with the segment's last tile
+    int pad;
+};
+
+struct AttnWork {
+    AttnNote* notes;   // [ctas]
+    int* status;       // [ctas * 2]
+    float2* ml;        // [ctas * 2][TM]: maximum and sum of the weights
+    float* acc;        // [ctas * 2][TM][DP]
+};
+
+__host__ __device__ inline int64_t attn_work_bytes(int ctas, int tm, int dp) {
+    return static_cast<int64_t>(ctas) * (sizeof(AttnNote) + 2 * sizeof(int) + 2 * tm * (sizeof(float2) + dp * 4ll));
+}
+
+__host__ __device__ inline AttnWork attn_work(unsigned char* p, int ctas, int tm, int dp) {
+    // each part before the last is a multiple of 16 bytes (so are tm and dp)
+    AttnWork w;
+    w.notes = reinterpret_cast<AttnNote*>(p);
+    w.ml = reinterpret_cast<float2*>(w.notes + ctas);
+    w.acc = reinterpret_cast<float*>(w.ml + static_cast<int64_t>(ctas) * 2 * tm);
+    w.status = reinterpret_cast<int*>(w.acc + static_cast<int64_t>(ctas) * 2 * tm * dp);
+    return w;
+}
+
+// ------------------------------------------------------------------ matrix instructions
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// x = hi + lo with both in tf32 (11 significant bits each): a product of two
+// such pairs without lo * lo is off by 3 * 2^-22 of its size.
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+    const float rest = x - __uint_as_float(hi);
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(rest));
+}
+
+// 16 bytes global -> shared; zeros if !take (src is then not read)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
+    const int n = take ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ void attn_store4(float* p, float a, float b, float c, float d) {
+    *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
+}
+__device__ __forceinline__ void attn_store4(__nv_bfloat16* p, float a, float b, float c, float d) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(a, b), pack_bf16(c, d));
+}
+
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
+
+// ------------------------------------------------------------------ shapes
+// DP: head_dim rounded up to 64, 128 or 256 (the columns past head_dim are
+// zeros in shared memory); RG row groups of 16 a warp, WR warps over rows, 4
+// over positions: a row tile of TM = 16 RG WR rows.
+template <typename T, int DP_, int RG_, int WR_>
+struct AttnShape {
+    using Type = T;
+    static constexpr bool kBf16 = sizeof(T) == 2;
+    static constexpr int DP = DP_, RG = RG_, WR = WR_, WK = 4;
+    static constexpr int TM = 16 * RG * WR;
+    static constexpr int KW = kBf16 ? 16 : 8;  // positions of a warp in a tile: the k of its matrix instruction
+    static constexpr int KT = KW * WK;         // positions of a tile
+    static constexpr int kThreads = 32 * WR * WK;
+    static constexpr int kRow = DP * static_cast<int>(sizeof(T));  // bytes of a position
+    static constexpr int kHalf = KT * kRow;                        // keys, or values, of a tile
+    static constexpr int kStages = DP == 256 ? 2 : 3;
+    static constexpr int kAhead = kStages - 1;
+    static constexpr int kQ = TM * kRow;  // bytes of a row tile of queries
+    static constexpr int kSmem = kStages * (2 * kHalf + kQ);
+    // queries in registers for as long as a segment, unless the outputs need these
+    static constexpr bool kQRegs = kBf16 && RG * DP <= 128;
+    // resident CTAs: by shared memory (227 KB, 1 KB a CTA taken, about 3 KB
+    // static) and by registers (outputs, queries, and about 100 others)
+    static constexpr int kFit = 227 * 1024 / (kSmem + 4096);
+    static constexpr int kRegs = RG * DP / 2 + (kQRegs ? RG * DP / 4 : 0) + 100;
+    static constexpr int kMost = 65536 / (kRegs * kThreads) > 1 ? 65536 / (kRegs * kThreads) : 1;
+    static constexpr int kCtas = kFit > kMost ? kMost : kFit;
+    // a segment's end reduces the warps' results in the tile last consumed
+    static_assert(TM * DP * 4 <= 2 * kHalf, "the reduction fits a stage");
+};
+
+// Byte offset of 16-byte piece c of row r: pieces change places within a row
+// by the row, so that eight rows of the same piece lie in different banks.
+template <typename S>
+__device__ __forceinline__ uint32_t attn_at(int r, int c) {
+    return static_cast<uint32_t>(r * S::kRow + ((c ^ (r & 7)) << 4));
+}
+
+// ------------------------------------------------------------------ the kernel
+template <typename S>
+__global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(const AttnArgs a) {
+    using T = typename S::Type;
+    constexpr int DP = S::DP, RG = S::RG, KT = S::KT, KW = S::KW, TM = S::TM, kStages = S::kStages, kAhead = S::kAhead;
+    constexpr int kVec = KvType<T>::kVec;
+    constexpr int kPieces = DP / kVec;  // 16-byte pieces of a position
+    constexpr int NT = DP / 8;          // 8-wide column tiles of the output
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ int64_t s_row[2][KT];                 // where the positions of a tile lie (< 0: nowhere)
+    __shared__ int s_hole[4][KT / 32 > 0 ? KT / 32 : 1];  // whether a position's block is outside the pool
+    __shared__ int s_parents[kStages][32];
+    __shared__ float2 s_ml[4][TM];
+    __shared__ uint32_t s_wild[2];  // nodes with values that are not finite, of a segment and the next
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int wk = warp & 3, wr = warp >> 2;
+    const int quad = lane >> 2, two = (lane & 3) * 2;
+    const KvView& kv = a.kv;
+    const int cta = blockIdx.x, ctas = gridDim.x;
+    const AttnWork work = attn_work(a.workspace, ctas, TM, DP);
+    const uint32_t base_s = smem_u32(smem);
+    const int m_rows = a.rows * static_cast<int>(a.group.d);  // rows of a kv head
+    const float c_scale = a.scale * 1.44269504f;
+
+    int64_t units, lo, hi;
+    int used;
+    AttnCursor cur, ahead, ids;
+    attn_cut<S::kThreads>(a, KT, cta, ctas, units, used, lo, hi, cur);
+    if (tid == 0) {
+        s_wild[0] = s_wild[1] = 0;
+        work.notes[cta].b = -1;
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this grid's end
+    if (cta >= used) return;
+    const int n = static_cast<int>(hi - lo);
+    ids = ahead = cur;
+
+    // block numbers of tile `i` of the run, whose cursor `ids` is: into a register ...
+    int64_t my_row = -1;
+    bool my_hole = false;
+    int ids_i = 0;
+    auto fetch_row = [&]() {
+        my_row = -1;
+        my_hole = false;
+        if (ids_i < n) {
+            const int t = ids.tile * KT + tid;
+            if (tid < KT && t < ids.len) {
+                const int lb = kv.block.div(t);
+                const int blk = __ldg(kv.tables + static_cast<int64_t>(ids.b) * kv.max_blocks + lb);
+                my_hole = !kv.valid(blk);
+                const int h = ids.s / a.row_tiles;
+                if (!my_hole) my_row = kv.at(blk, h, t - lb * kv.block_size());
+            }
+            ids.next(a, KT);
+        }
+        ++ids_i;
+    };
+    // ... and from there to shared memory, for the copies of tile i
+    auto post_row = [&](int i) {
+        if (tid < KT) {
+            s_row[i & 1][tid] = my_row;
+            const bool any = __any_sync(0xffffffffu, my_hole);
+            if (lane == 0) s_hole[i & 3][warp] = any;
+        }
+    };
+    // copies of tile i of the run (its cursor is `ahead`); the first tile of a segment brings its queries and parents
+    int ahead_seg = 0;
+    auto copy_tile = [&](int i) {
+        if (i < n) {
+            const uint32_t st = base_s + (i % kStages) * 2 * S::kHalf;
+            const T* k = static_cast<const T*>(kv.k);
+            const T* v = static_cast<const T*>(kv.v);
+            const int row0 = tid / kPieces, c = tid % kPieces;
+            constexpr int kStep = S::kThreads / kPieces;
+#pragma unroll
+            for (int r = row0; r < KT; r += kStep) {
+                const int64_t at = s_row[i & 1][r];
+                const bool take = at >= 0 && c * kVec < kv.dim;
+                const int64_t off = take ? at + c * kVec : 0;
+                const uint32_t dst = st + attn_at<S>(r, c);
+                cp_async16(dst, k + off, take);
+                cp_async16(dst + S::kHalf, v + off, take);
+            }
+            if (ahead.tile == 0 || i == 0) {
+                const int slot = ahead_seg % kStages;
+                const uint32_t sq = base_s + kStages * 2 * S::kHalf + slot * S::kQ;
+                const int h = ahead.s / a.row_tiles, rt = ahead.s - h * a.row_tiles;
+                const T* q = static_cast<const T*>(a.q);
+                for (int m = row0; m < TM; m += kStep) {
+                    const int row = rt * TM + m;
+                    const bool take = row < m_rows && c * kVec < kv.dim;
+                    const int r = a.group.div(row), g = row - r * static_cast<int>(a.group.d);
+                    const int64_t off = (static_cast<int64_t>(ahead.b) * a.rows + r) * a.q_stride +
+                                        (static_cast<int64_t>(h) * a.group.d + g) * kv.dim + c * kVec;
+                    cp_async16(sq + attn_at<S>(m, c), q + (take ? off : 0), take);
+                }
+                if (a.parents && tid < a.rows - 1)
+                    cp_async4(smem_u32(&s_parents[slot][tid]),
+                              a.parents + static_cast<int64_t>(ahead.b) * (a.rows - 1) + tid);
+                ++ahead_seg;
+            }
+            ahead.next(a, KT);
+        }
+        cp_commit();
+    };
+
+    // fill the pipeline
+    for (int i = 0; i < kAhead; ++i) {
+        fetch_row();
+        post_row(i);
+        __syncthreads();
+        copy_tile(i);
+    }
+    fetch_row();
+
+    float o[RG][NT][4];
+    float m_run[RG][2], l_run[RG][2];
+    uint32_t anc[RG][2];
+    uint32_t qf[S::kQRegs ? RG : 1][S::kQRegs ? DP / 16 : 1][4];
+    int seg = 0, status = 0, first_tile = 0;
+
+    for (int i = 0; i < n; ++i) {
+        post_row(i + kAhead);
+        fetch_row();
+        cp_wait<kAhead - 1>();
+        __syncthreads();
+        copy_tile(i + kAhead);
+        const uint32_t sk = base_s + (i % kStages) * 2 * S::kHalf, sv = sk + S::kHalf;
+        const int slot = seg % kStages;
+        const uint32_t sq = base_s + kStages * 2 * S::kHalf + slot * S::kQ;
+        const int h = cur.s / a.row_tiles, rt = cur.s - h * a.row_tiles;
+        if (cur.tile == 0 || i == 0) {  // a segment starts
+            first_tile = cur.tile;
+            if (tid == 0) s_wild[(seg + 1) & 1] = 0;
+            status = cur.len < 0 ? KV_LENGTH : 0;
+            uint32_t line;
+            int depth;
+            if (!warp_tree(a.parents ? s_parents[slot] : nullptr, a.rows, lane, line, depth) && cur.len > 0)
+                status |= KV_PARENT;
+#pragma unroll
+            for (int g = 0; g < RG; ++g) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int row = rt * TM + (wr * RG + g) * 16 + quad + 8 * e;
+                    anc[g][e] = __shfl_sync(0xffffffffu, line, a.group.div(row < m_rows ? row : 0));
+                    m_run[g][e] = -INFINITY;
+                    l_run[g][e] = 0.0f;
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[g][t][e] = 0.0f;
+                if constexpr (S::kQRegs) {
+#pragma unroll
+                    for (int kk = 0; kk < DP / 16; ++kk)
+                        ldsm4(sq + attn_at<S>((wr * RG + g) * 16 + (lane & 15), kk * 2 + (lane >> 4)), qf[g][kk]);
+                }
             }
         }
-        float top = s;
-        for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        if ((tid & 31) == 0) s_red[tid >> 5] = top;
-        __syncthreads();
-        const float m_new = fmaxf(m, fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3])));
-        const float m_use = m_new == -INFINITY ? 0.0f : m_new;
-        s_p[tid] = blk >= 0 ? expf(s - m_use) : 0.0f;
-        s_blk[tid] = blk;
-        __syncthreads();
-        const float keep = expf(m - m_use);
-        m = m_new;
-        sum *= keep;
-        acc[0] *= keep;
-        acc[1] *= keep;
-        const int n = min(kAttnThreads, len - t0);
-        for (int i = 0; i < n; ++i) {
-            if (s_blk[i] < 0) continue;
-            sum += s_p[i];
-            const int lb = kv.block.div(t0 + i);
-            const T* v = static_cast<const T*>(kv.v) + kv.at(s_blk[i], kvh, t0 + i - lb * kv.block_size());
-            if (tid < dim) acc[0] = fmaf(s_p[i], KvType<T>::load(v[tid]), acc[0]);
-            if (tid + kAttnThreads < dim) acc[1] = fmaf(s_p[i], KvType<T>::load(v[tid + kAttnThreads]), acc[1]);
+#pragma unroll
+        for (int w = 0; w < (KT + 31) / 32; ++w)
+            if (s_hole[i & 3][w]) status |= KV_BLOCK;
+        const int t0 = cur.tile * KT, base = cur.len - a.rows;
+        const bool edge = t0 + KT > base;  // positions that not every row sees
+        if (edge && cur.len > 0) {
+            // values of the pass's rows that are not finite are taken out of
+            // the product, where a weight of zero would not hide them; they
+            // are added to the rows that see them at the segment's end
+            for (int x = tid; x < KT * kPieces; x += S::kThreads) {
+                const int r = x / kPieces, t = t0 + r;
+                if (t < base || t >= cur.len) continue;
+                KvVec<T>* p = reinterpret_cast<KvVec<T>*>(smem + (sv - base_s) + attn_at<S>(r, x % kPieces));
+                bool wild = false;
+#pragma unroll
+                for (int e = 0; e < kVec; ++e)
+                    if (!finite(KvType<T>::load(p->x[e]))) {
+                        p->x[e] = KvType<T>::store(0.0f);
+                        wild = true;
+                    }
+                if (wild) atomicOr(&s_wild[seg & 1], 1u << (t - base));
+            }
+            __syncthreads();
         }
-        __syncthreads();
+        // scores of this warp's positions
+        constexpr int ST = KW / 8;
+        float s[RG][ST][4];
+#pragma unroll
+        for (int g = 0; g < RG; ++g)
+#pragma unroll
+            for (int t = 0; t < ST; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[g][t][e] = 0.0f;
+        if constexpr (S::kBf16) {
+#pragma unroll
+            for (int kk = 0; kk < DP / 16; ++kk) {
+                uint32_t kf[4];
+                ldsm4(sk + attn_at<S>(wk * KW + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)), kf);
+#pragma unroll
+                for (int g = 0; g < RG; ++g) {
+                    if constexpr (S::kQRegs) {
+                        mma_bf16(s[g][0], qf[g][kk], kf[0], kf[1]);
+                        mma_bf16(s[g][ST - 1], qf[g][kk], kf[2], kf[3]);
+                    } else {
+                        uint32_t qx[4];
+                        ldsm4(sq + attn_at<S>((wr * RG + g) * 16 + (lane & 15), kk * 2 + (lane >> 4)), qx);
+                        mma_bf16(s[g][0], qx, kf[0], kf[1]);
+                        mma_bf16(s[g][ST - 1], qx, kf[2], kf[3]);
+                    }
+                }
+            }
+        } else {
+#pragma unroll 4
+            for (int kk = 0; kk < DP / 8; ++kk) {
+                uint32_t bh[2], bl[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    split_tf32(ld_shared_f32(sk + attn_at<S>(wk * KW + quad, kk * 2 + e) + (lane & 3) * 4), bh[e], bl[e]);
+#pragma unroll
+                for (int g = 0; g < RG; ++g) {
+                    uint32_t ah[4], al[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        split_tf32(ld_shared_f32(sq + attn_at<S>((wr * RG + g) * 16 + quad + 8 * (e & 1), kk * 2 + (e >> 1)) +
+                                                 (lane & 3) * 4),
+                                   ah[e], al[e]);
+                    mma_tf32(s[g][0], al, bh[0], bh[1]);
+                    mma_tf32(s[g][0], ah, bl[0], bl[1]);
+                    mma_tf32(s[g][0], ah, bh[0], bh[1]);
+                }
+            }
+        }
+        // weights: the running maximum moves only when a score passes it by
+        // 8 (weights stay below 2^8), so that the sums are seldom rescaled
+#pragma unroll
+        for (int g = 0; g < RG; ++g) {
+            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int t = 0; t < ST; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float x = s[g][t][e] * c_scale;
+                    if (edge) {
+                        const int pos = t0 + wk * KW + t * 8 + two + (e & 1);
+                        if (pos >= base && !(pos < cur.len && (anc[g][e >> 1] >> (pos - base) & 1))) x = -INFINITY;
+                    }
+                    s[g][t][e] = x;
+                    top[e >> 1] = fmaxf(top[e >> 1], x);
+                }
+            bool move = false;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+                top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+                move |= top[e] > m_run[g][e] + 8.0f;
+            }
+            if (__any_sync(0xffffffffu, move)) {
+                float keep[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float m_new = fmaxf(m_run[g][e], top[e]);
+                    keep[e] = m_new == -INFINITY ? 1.0f : ex2(m_run[g][e] - m_new);
+                    m_run[g][e] = m_new;
+                    l_run[g][e] *= keep[e];
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[g][t][e] *= keep[e >> 1];
+            }
+            const float m_use[2] = {m_run[g][0] == -INFINITY ? 0.0f : m_run[g][0],
+                                    m_run[g][1] == -INFINITY ? 0.0f : m_run[g][1]};
+#pragma unroll
+            for (int t = 0; t < ST; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[g][t][e] = ex2(s[g][t][e] - m_use[e >> 1]);
+                    l_run[g][e >> 1] += s[g][t][e];
+                }
+        }
+        // weights times values; bf16 weights are rounded to bf16 for the
+        // product (relative 2^-8 each, random in sign; the sum l is not)
+        if constexpr (S::kBf16) {
+            uint32_t pf[RG][4];
+#pragma unroll
+            for (int g = 0; g < RG; ++g) {
+                pf[g][0] = pack_bf16(s[g][0][0], s[g][0][1]);
+                pf[g][1] = pack_bf16(s[g][0][2], s[g][0][3]);
+                pf[g][2] = pack_bf16(s[g][ST - 1][0], s[g][ST - 1][1]);
+                pf[g][3] = pack_bf16(s[g][ST - 1][2], s[g][ST - 1][3]);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; t += 2) {
+                uint32_t vf[4];
+                ldsm4t(sv + attn_at<S>(wk * KW + (lane & 15), t + (lane >> 4)), vf);
+#pragma unroll
+                for (int g = 0; g < RG; ++g) {
+                    mma_bf16(o[g][t], pf[g], vf[0], vf[1]);
+                    mma_bf16(o[g][t + 1], pf[g], vf[2], vf[3]);
+                }
+            }
+        } else {
+            uint32_t ph[RG][4], pl[RG][4];  // k of the instruction: position 2 (lane & 3), then the odd ones
+#pragma unroll
+            for (int g = 0; g < RG; ++g) {
+                split_tf32(s[g][0][0], ph[g][0], pl[g][0]);
+                split_tf32(s[g][0][2], ph[g][1], pl[g][1]);
+                split_tf32(s[g][0][1], ph[g][2], pl[g][2]);
+                split_tf32(s[g][0][3], ph[g][3], pl[g][3]);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                uint32_t bh[2], bl[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    split_tf32(ld_shared_f32(sv + attn_at<S>(wk * KW + two + e, t * 2 + (quad >> 2)) + (quad & 3) * 4),
+                               bh[e], bl[e]);
+#pragma unroll
+                for (int g = 0; g < RG; ++g) {
+                    mma_tf32(o[g][t], pl[g], bh[0], bh[1]);
+                    mma_tf32(o[g][t], ph[g], bl[0], bl[1]);
+                    mma_tf32(o[g][t], ph[g], bh[0], bh[1]);
+                }
+            }
+        }
+        const bool ends = cur.tile + 1 == cur.tiles;
+        if (ends || i + 1 == n) {
+            // the segment's part ends: the four position warps' results join
+            // in the tile just consumed, one warp after the other
+#pragma unroll
+            for (int g = 0; g < RG; ++g)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    l_run[g][e] += __shfl_xor_sync(0xffffffffu, l_run[g][e], 1);
+                    l_run[g][e] += __shfl_xor_sync(0xffffffffu, l_run[g][e], 2);
+                    if ((lane & 3) == 0)
+                        s_ml[wk][(wr * RG + g) * 16 + quad + 8 * e] = make_float2(m_run[g][e], l_run[g][e]);
+                }
+            __syncthreads();
+            float* red = reinterpret_cast<float*>(smem + (sk - base_s));
+            float keep[RG][2];
+#pragma unroll
+            for (int g = 0; g < RG; ++g)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int row = (wr * RG + g) * 16 + quad + 8 * e;
+                    float m = -INFINITY;
+                    for (int w = 0; w < 4; ++w) m = fmaxf(m, s_ml[w][row].x);
+                    keep[g][e] = m == -INFINITY ? 1.0f : ex2(m_run[g][e] - m);
+                }
+            for (int w = 0; w < 4; ++w) {
+                if (wk == w) {
+#pragma unroll
+                    for (int g = 0; g < RG; ++g)
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float2* p = reinterpret_cast<float2*>(
+                                    red + ((wr * RG + g) * 16 + quad + 8 * e) * DP + ((t * 8 + two) ^ ((quad & 3) * 8)));
+                                float2 x = w == 0 ? make_float2(0.0f, 0.0f) : *p;
+                                x.x += o[g][t][2 * e] * keep[g][e];
+                                x.y += o[g][t][2 * e + 1] * keep[g][e];
+                                *p = x;
+                            }
+                }
+                __syncthreads();
+            }
+            const bool whole = first_tile == 0 && ends;
+            const int piece = 2 * cta + (first_tile == 0 ? 1 : 0);
+            const uint32_t wild = s_wild[seg & 1];
+            constexpr int kGroup = S::kThreads / TM;  // threads of a row
+            const int row = tid / kGroup, lane_r = tid % kGroup;
+            float m = -INFINITY, l = 0.0f;
+            for (int w = 0; w < 4; ++w) m = fmaxf(m, s_ml[w][row].x);
+            for (int w = 0; w < 4; ++w) l += s_ml[w][row].y * (m == -INFINITY ? 1.0f : ex2(s_ml[w][row].x - m));
+            const int grow = rt * TM + row;
+            const int r = a.group.div(grow), gq = grow - r * static_cast<int>(a.group.d);
+            const int64_t token = static_cast<int64_t>(cur.b) * a.rows + r;
+            const int64_t head = token * a.q_heads + static_cast<int64_t>(h) * a.group.d + gq;
+            const uint32_t seen = wild ? [&] {
+                uint32_t line;
+                int depth;
+                warp_tree(a.parents ? s_parents[slot] : nullptr, a.rows, lane, line, depth);
+                uint32_t mine = 0;
+                for (int x = 0; x < 32; ++x) {
+                    const uint32_t y = __shfl_sync(0xffffffffu, line, x);
+                    if (x == r) mine = y;
+                }
+                return mine & wild;
+            }()
+                                       : 0;
+            const bool zero = cur.len <= 0 || status != 0;
+            if (grow < m_rows) {
+                const float inv = 1.0f / l;
+                for (int d = lane_r * 4; d < kv.dim; d += kGroup * 4) {
+                    const float4 x4 = *reinterpret_cast<const float4*>(red + row * DP + (d ^ ((row & 3) * 8)));
+                    float x[4] = {x4.x, x4.y, x4.z, x4.w};
+                    if (seen) {
+                        for (int j = 0; j < a.rows; ++j) {
+                            if (!(seen >> j & 1)) continue;
+                            const int t = base + j, lb = kv.block.div(t);
+                            const int blk = kv.tables[static_cast<int64_t>(cur.b) * kv.max_blocks + lb];
+                            if (!kv.valid(blk)) continue;
+                            const T* v = static_cast<const T*>(kv.v) + kv.at(blk, h, t - lb * kv.block_size()) + d;
+                            for (int e = 0; e < 4; ++e) {
+                                const float y = KvType<T>::load(v[e]);
+                                if (!finite(y)) x[e] += y;
+                            }
+                        }
+                    }
+                    if (whole) {
+                        T* out = static_cast<T*>(a.out) + head * kv.dim + d;
+                        attn_store4(out, zero ? 0.0f : x[0] * inv, zero ? 0.0f : x[1] * inv, zero ? 0.0f : x[2] * inv,
+                                    zero ? 0.0f : x[3] * inv);
+                    } else {
+                        *reinterpret_cast<float4*>(work.acc + (static_cast<int64_t>(piece) * TM + row) * DP + d) =
+                            make_float4(x[0], x[1], x[2], x[3]);
+                    }
+                }
+                if (lane_r == 0) {
+                    if (whole) {
+                        if (a.lse) a.lse[head] = zero ? -INFINITY : m * 0.693147181f + logf(l);
+                    } else {
+                        work.ml[static_cast<int64_t>(piece) * TM + row] = make_float2(m, l);
+                    }
+                }
+            }
+            if (tid == 0) {
+                if (whole) {
+                    if (cur.s == 0 && a.row_status) a.row_status[cur.b] = status;
+                } else {
+                    work.status[piece] = status;
+                    if (first_tile == 0) {
+                        const int64_t end = lo + i + (cur.tiles - cur.tile);  // the unit behind the segment's last
+                        AttnNote note;
+                        note.b = cur.b;
+                        note.s = cur.s;
+                        note.last = attn_owner(units, end - 1, used);
+                        note.pad = 0;
+                        work.notes[cta] = note;
+                    }
+                }
+            }
+            ++seg;
+        }
+        cur.next(a, KT);
     }
-    const bool fine = go && s_status == 0;
-    if (h == 0 && r == 0 && tid == 0 && a.row_status) a.row_status[b] = s_status;
-    for (int i = 0; i < 2; ++i)
-        if (tid + i * kAttnThreads < dim) out[tid + i * kAttnThreads] = KvType<T>::store(fine ? acc[i] / sum : 0.0f);
-    if (tid == 0 && a.lse) a.lse[token * a.q_heads + h] = fine ? m + logf(sum) : -INFINITY;
+}
+
+// ------------------------------------------------------------------ the join
+constexpr int kJoinThreads = 128;
+
+// Row tile rows blockIdx.y * 4 .. + 3 of the segment that CTA blockIdx.x of
+// the kernel before noted: a warp a row.
+template <typename S>
+__global__ void __launch_bounds__(kJoinThreads) tree_attention_join(const AttnArgs a, int ctas) {
+    using T = typename S::Type;
+    constexpr int TM = S::TM, DP = S::DP;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const AttnWork work = attn_work(a.workspace, ctas, TM, DP);
+    const int cta = blockIdx.x, lane = threadIdx.x & 31;
+    const AttnNote note = work.notes[cta];
+    if (note.b < 0) return;
+    const int row = blockIdx.y * 4 + (threadIdx.x >> 5);
+    const KvView& kv = a.kv;
+    const int h = note.s / a.row_tiles, rt = note.s - h * a.row_tiles;
+    const int grow = rt * TM + row;
+    int status = 0;
+    for (int c = cta; c <= note.last; ++c) status |= work.status[2 * c + (c == cta)];
+    if (row == 0 && note.s == 0 && lane == 0 && a.row_status) a.row_status[note.b] = status;
+    if (grow >= a.rows * static_cast<int>(a.group.d)) return;
+    float m = -INFINITY;
+    for (int c = cta; c <= note.last; ++c) m = fmaxf(m, work.ml[(2ll * c + (c == cta)) * TM + row].x);
+    const float m_use = m == -INFINITY ? 0.0f : m;
+    float l = 0.0f, x[DP / 32] = {};
+    for (int c = cta; c <= note.last; ++c) {
+        const int64_t piece = 2ll * c + (c == cta);
+        const float2 ml = work.ml[piece * TM + row];
+        const float keep = ex2(ml.x - m_use);
+        l += ml.y * keep;
+        const float* acc = work.acc + (piece * TM + row) * DP;
+#pragma unroll
+        for (int j = 0; j < DP / 32; ++j)
+            if (j * 32 + lane < kv.dim) x[j] += acc[j * 32 + lane] * keep;
+    }
+    const int r = a.group.div(grow), g = grow - r * static_cast<int>(a.group.d);
+    const int64_t token = static_cast<int64_t>(note.b) * a.rows + r;
+    const int64_t head = token * a.q_heads + static_cast<int64_t>(h) * a.group.d + g;
+    T* out = static_cast<T*>(a.out) + head * kv.dim;
+    const float inv = 1.0f / l;
+#pragma unroll
+    for (int j = 0; j < DP / 32; ++j)
+        if (j * 32 + lane < kv.dim) out[j * 32 + lane] = KvType<T>::store(status ? 0.0f : x[j] * inv);
+    if (lane == 0 && a.lse) a.lse[head] = status ? -INFINITY : m * 0.693147181f + logf(l);
 }
 
 }  // namespace specv

@@ -306,12 +306,32 @@ def specv_rollback(h: Handle, num_accepted, k, seq_lens, block_tables, num_block
 
 
 # ------------------------------------------------------------------ paged KV cache
+# A serving loop makes these calls once a layer: what a call checks is a few
+# attribute reads a tensor, and what is wrong is found out only if they fail.
+_cache_dtypes = None
+
+
+def _cache_setup():
+    """torch's names that every call needs, looked up once."""
+    global _cache_dtypes, _i32, _f32, _raw_stream
+    import torch
+
+    _i32, _f32 = torch.int32, torch.float32
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _cache_dtypes = {torch.bfloat16: SPECV_BF16, torch.float32: SPECV_F32}
+
+
 def _on(h, t, dtype, name, shape=None):
-    """A contiguous CUDA tensor on the handle's device."""
-    p = _dev(t, dtype, name, shape)
-    if t.device.index != h.device:
-        raise ValueError(f"{name} is on {t.device}, the handle on cuda:{h.device}")
-    return p
+    """Pointer of a contiguous CUDA tensor on the handle's device."""
+    try:
+        if (t.dtype is dtype and t.get_device() == h.device and t.is_contiguous()
+                and (shape is None or t.shape == shape)):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, dtype, name, shape)
+    raise ValueError(f"{name} is on {t.device}, the handle on cuda:{h.device}")
 
 
 def _inner(t, n):
@@ -325,70 +345,72 @@ def _inner(t, n):
     return want
 
 
+def _strides_match(a, b):
+    return all(x == y for x, y, n in zip(a.stride(), b.stride(), a.shape) if n > 1)
+
+
 def _kv_cache(h, k_cache, v_cache, block_tables, seq_lens, layered=False):
     """The descriptor of a cache; with ``layered`` the pools may have a
     leading dimension of layers.  Returns (descriptor, layers, layer_stride)."""
-    torch = _torch()
-    dt = _cache_dtype(k_cache)
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if not t.is_cuda or t.device.index != h.device:
-            raise ValueError(f"{name} must be on the handle's device, cuda:{h.device}")
-    if v_cache.dtype != k_cache.dtype:
+    if _cache_dtypes is None:
+        _cache_setup()
+    try:
+        dt = _cache_dtypes[k_cache.dtype]
+    except (AttributeError, KeyError):
+        raise TypeError("the cache pools must be bfloat16 or float32 tensors") from None
+    if k_cache.get_device() != h.device or v_cache.get_device() != h.device:
+        raise ValueError(f"k_cache and v_cache must be on the handle's device, cuda:{h.device}")
+    if v_cache.dtype is not k_cache.dtype:
         raise TypeError(f"v_cache must be {k_cache.dtype}, got {v_cache.dtype}")
-    if k_cache.dim() != 4 and not (layered and k_cache.dim() == 5):
+    shape = k_cache.shape
+    if len(shape) != 4 and not (layered and len(shape) == 5):
         raise ValueError("the cache pools have the shape "
                          + ("[layers, blocks, heads, block_size, head_dim] or " if layered else "")
                          + "[blocks, heads, block_size, head_dim]")
-    if v_cache.shape != k_cache.shape:
-        raise ValueError(f"v_cache has shape {tuple(v_cache.shape)}, expected {tuple(k_cache.shape)}")
-    blocks, heads, block_size, head_dim = k_cache.shape[-4:]
-    inner = _inner(k_cache, 3)
-    if inner is None or _inner(v_cache, 3) is None:
-        raise ValueError("the cache pools must be contiguous inside a block")
-    layers = k_cache.shape[0] if k_cache.dim() == 5 else 1
-    for i in range(k_cache.dim() - 3):
-        if k_cache.shape[i] > 1 and k_cache.stride(i) != v_cache.stride(i):
+    if v_cache.shape != shape:
+        raise ValueError(f"v_cache has shape {tuple(v_cache.shape)}, expected {tuple(shape)}")
+    blocks, heads, block_size, head_dim = shape[-4:]
+    inner = heads * block_size * head_dim
+    layers = shape[0] if len(shape) == 5 else 1
+    block_stride, layer_stride = inner, blocks * inner
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        if _inner(k_cache, 3) is None or _inner(v_cache, 3) is None:
+            raise ValueError("the cache pools must be contiguous inside a block")
+        if not _strides_match(k_cache, v_cache):
             raise ValueError("k_cache and v_cache must have the same strides")
-    block_stride = k_cache.stride(-4) if blocks > 1 else inner
-    layer_stride = k_cache.stride(0) if layers > 1 else 0
-    tables = _on(h, block_tables, torch.int32, "block_tables")
+        block_stride = k_cache.stride(-4) if blocks > 1 else inner
+        layer_stride = k_cache.stride(0) if layers > 1 else 0
+    tables = _on(h, block_tables, _i32, "block_tables")
     if block_tables.dim() != 2:
         raise ValueError("block_tables must have the shape [B, max_blocks]")
-    lens = _on(h, seq_lens, torch.int32, "seq_lens", (block_tables.shape[0],))
-    c = _lib.SpecvKvCache(dt, heads, head_dim, block_size, block_tables.shape[1], k_cache.data_ptr(),
-                          v_cache.data_ptr(), blocks, block_stride, tables, lens)
+    batch, max_blocks = block_tables.shape
+    lens = _on(h, seq_lens, _i32, "seq_lens", (batch,))
+    c = _lib.SpecvKvCache(dt, heads, head_dim, block_size, max_blocks, k_cache.data_ptr(), v_cache.data_ptr(), blocks,
+                          block_stride, tables, lens)
     return c, layers, layer_stride
-
-
-def _cache_dtype(t):
-    torch = _torch()
-    if isinstance(t, torch.Tensor):
-        if t.dtype == torch.bfloat16:
-            return SPECV_BF16
-        if t.dtype == torch.float32:
-            return SPECV_F32
-    raise TypeError("the cache pools must be bfloat16 or float32 tensors")
 
 
 def _token_rows(h, t, name, like, shape):
     """Pointer and row stride of a [B, rows, heads, head_dim] tensor whose
     rows are evenly spaced (a slice of a fused projection will do)."""
-    if not t.is_cuda or t.device.index != h.device:
+    if t.get_device() != h.device:
         raise ValueError(f"{name} must be on the handle's device, cuda:{h.device}")
-    if t.dtype != like.dtype:
+    if t.dtype is not like.dtype:
         raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-    if t.dim() != 4 or tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    B, rows = shape[:2]
-    inner = _inner(t, 2)
-    stride = t.stride(1) if rows > 1 else t.stride(0) if B > 1 else inner
-    if inner is None or (B > 1 and rows > 1 and t.stride(0) != rows * stride):
+    B, rows, heads, dim = shape
+    if t.is_contiguous():
+        return t.data_ptr(), heads * dim
+    s = t.stride()
+    stride = s[1] if rows > 1 else s[0] if B > 1 else heads * dim
+    if not (s[3] == 1 and (s[2] == dim or heads == 1)) or (B > 1 and rows > 1 and s[0] != rows * stride):
         raise ValueError(f"{name} must have contiguous heads and evenly spaced rows")
     return t.data_ptr(), stride
 
 
-def _device_stream(h, stream):
-    return stream if stream is not None else _torch().cuda.current_stream(h.device)
+def _stream_of(h, stream):
+    return _raw_stream(h.device) if stream is None else stream.cuda_stream
 
 
 def _empty(h, shape, dtype, stream):
@@ -413,7 +435,6 @@ def specv_cache_append(h: Handle, k_cache, v_cache, block_tables, seq_lens, k, v
     (None: chains, or prompts); row_counts [B] int32 (None: all rows are
     tokens).  Returns a dict: q_out (with q) and row_status [B]; ``out`` may
     supply them."""
-    torch = _torch()
     c, _, _ = _kv_cache(h, k_cache, v_cache, block_tables, seq_lens)
     if k.dim() != 4:
         raise ValueError("k must have the shape [B, rows, kv_heads, head_dim]")
@@ -424,10 +445,10 @@ def specv_cache_append(h: Handle, k_cache, v_cache, block_tables, seq_lens, k, v
     pv, v_stride = _token_rows(h, v, "v", k_cache, (B, rows, c.kv_heads, c.head_dim))
     pf, rot = None, 0
     if inv_freq is not None:
-        pf = _on(h, inv_freq, torch.float32, "inv_freq")
+        pf = _on(h, inv_freq, _f32, "inv_freq")
         rot = 2 * inv_freq.numel()
-    pp = None if parents is None else _on(h, parents, torch.int32, "parents", (B, rows - 1))
-    pc = None if row_counts is None else _on(h, row_counts, torch.int32, "row_counts", (B,))
+    pp = None if parents is None else _on(h, parents, _i32, "parents", (B, rows - 1))
+    pc = None if row_counts is None else _on(h, row_counts, _i32, "row_counts", (B,))
     out = {} if out is None else out
     pq, q_stride, q_heads, po = None, 0, 0, None
     if q is not None:
@@ -439,11 +460,11 @@ def specv_cache_append(h: Handle, k_cache, v_cache, block_tables, seq_lens, k, v
             out["q_out"] = _empty(h, (B, rows, q_heads, c.head_dim), k_cache.dtype, stream)
         po = _on(h, out["q_out"], k_cache.dtype, "q_out", (B, rows, q_heads, c.head_dim))
     if "row_status" not in out:
-        out["row_status"] = _empty(h, (B,), torch.int32, stream)
-    ps = _on(h, out["row_status"], torch.int32, "row_status", (B,))
+        out["row_status"] = _empty(h, (B,), _i32, stream)
+    ps = _on(h, out["row_status"], _i32, "row_status", (B,))
     st = _lib.load().specv_cache_append(
         h.ptr, c, pq, q_stride, q_heads, pk, k_stride, pv, v_stride, pf, rot, 1 if interleaved else 0, pp, pc, B, rows,
-        po, ps, _device_stream(h, stream).cuda_stream)
+        po, ps, _stream_of(h, stream))
     _check(st, "specv_cache_append")
     return out
 
@@ -458,7 +479,6 @@ def specv_tree_attention(h: Handle, q, k_cache, v_cache, block_tables, seq_lens,
     with ``lse``, lse [B, rows, q_heads] fp32; ``out`` may supply them.
     ``workspace`` may supply a CUDA uint8 tensor of at least
     specv_tree_attention_workspace bytes that no other call uses meanwhile."""
-    torch = _torch()
     c, _, _ = _kv_cache(h, k_cache, v_cache, block_tables, seq_lens)
     if q.dim() != 4:
         raise ValueError("q must have the shape [B, rows, q_heads, head_dim]")
@@ -466,27 +486,27 @@ def specv_tree_attention(h: Handle, q, k_cache, v_cache, block_tables, seq_lens,
     if B != block_tables.shape[0]:
         raise ValueError(f"q holds {B} sequences, block_tables {block_tables.shape[0]}")
     pq, q_stride = _token_rows(h, q, "q", k_cache, (B, rows, q_heads, c.head_dim))
-    pp = None if parents is None else _on(h, parents, torch.int32, "parents", (B, rows - 1))
+    pp = None if parents is None else _on(h, parents, _i32, "parents", (B, rows - 1))
     out = {} if out is None else out
     if "out" not in out:
         out["out"] = _empty(h, (B, rows, q_heads, c.head_dim), k_cache.dtype, stream)
     po = _on(h, out["out"], k_cache.dtype, "out", (B, rows, q_heads, c.head_dim))
     if "row_status" not in out:
-        out["row_status"] = _empty(h, (B,), torch.int32, stream)
-    ps = _on(h, out["row_status"], torch.int32, "row_status", (B,))
+        out["row_status"] = _empty(h, (B,), _i32, stream)
+    ps = _on(h, out["row_status"], _i32, "row_status", (B,))
     pl = None
     if lse:
         if "lse" not in out:
-            out["lse"] = _empty(h, (B, rows, q_heads), torch.float32, stream)
-        pl = _on(h, out["lse"], torch.float32, "lse", (B, rows, q_heads))
+            out["lse"] = _empty(h, (B, rows, q_heads), _f32, stream)
+        pl = _on(h, out["lse"], _f32, "lse", (B, rows, q_heads))
     lib = _lib.load()
     if workspace is None:
         need = lib.specv_tree_attention_workspace(h.ptr, c.dtype, c.kv_heads, c.head_dim, q_heads, B, rows)
-        workspace = _empty(h, (need,), torch.uint8, stream) if need else None
-    pw = None if workspace is None else _on(h, workspace, torch.uint8, "workspace")
+        workspace = _empty(h, (need,), _torch().uint8, stream) if need else None
+    pw = None if workspace is None else _on(h, workspace, _torch().uint8, "workspace")
     st = lib.specv_tree_attention(
         h.ptr, c, pq, q_stride, q_heads, pp, B, rows, c.head_dim ** -0.5 if scale is None else scale, po, pl, ps, pw,
-        0 if workspace is None else workspace.numel(), _device_stream(h, stream).cuda_stream)
+        0 if workspace is None else workspace.numel(), _stream_of(h, stream))
     _check(st, "specv_tree_attention")
     return out
 
@@ -505,17 +525,16 @@ def specv_cache_compact(h: Handle, k_cache, v_cache, block_tables, seq_lens, pat
     block_size, head_dim] or [layers, blocks, ...] for all layers at once,
     seq_lens [B] with the tree's nodes the last M.  row_status [B] (optional)
     receives 0 or the bits of a refused sequence."""
-    torch = _torch()
     c, layers, layer_stride = _kv_cache(h, k_cache, v_cache, block_tables, seq_lens, layered=True)
     B = block_tables.shape[0]
     if path.dim() != 2:
         raise ValueError("path must have the shape [B, M]")
     M = path.shape[1]
-    pp = _on(h, path, torch.int32, "path", (B, M))
-    pn = _on(h, num_accepted, torch.int32, "num_accepted", (B,))
-    ps = None if row_status is None else _on(h, row_status, torch.int32, "row_status", (B,))
+    pp = _on(h, path, _i32, "path", (B, M))
+    pn = _on(h, num_accepted, _i32, "num_accepted", (B,))
+    ps = None if row_status is None else _on(h, row_status, _i32, "row_status", (B,))
     st = _lib.load().specv_cache_compact(h.ptr, c, layers, layer_stride, pp, pn, B, M, ps,
-                                         _device_stream(h, stream).cuda_stream)
+                                         _stream_of(h, stream))
     _check(st, "specv_cache_compact")
 
 

@@ -5,6 +5,7 @@
 #include "cache_append.cuh"
 #include "cache_compact.cuh"
 #include "tree_attention.cuh"
+#include "tree_attention_tc.cuh"
 
 namespace {
 
@@ -57,13 +58,7 @@ specv_status launched(specv_ctx* h, const char* what) {
 // join's CTAs may be placed while the kernel before still runs (they wait for
 // its end), so that they do not add a launch to the call.
 template <typename S>
-cudaError_t launch_attention(const AttnArgs& a, int ctas, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(tree_attention_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         S::kSmem);
-    if (e != cudaSuccess) return e;
-    tree_attention_kernel<S><<<ctas, S::kThreads, S::kSmem, stream>>>(a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+cudaError_t launch_join(const AttnArgs& a, int ctas, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas), S::TM / 4, 1);
     cfg.blockDim = dim3(kJoinThreads, 1, 1);
@@ -76,6 +71,41 @@ cudaError_t launch_attention(const AttnArgs& a, int ctas, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, tree_attention_join<S>, a, ctas);
 }
 
+// Lets a kernel have `bytes` of dynamic shared memory; once a device (a bit
+// of `done` each) is enough.
+cudaError_t allow_smem(std::atomic<uint64_t>& done, const void* kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
+template <typename S>
+cudaError_t launch_attention(const AttnArgs& a, int ctas, cudaStream_t stream) {
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(done, reinterpret_cast<const void*>(tree_attention_kernel<S>), S::kSmem);
+    if (e != cudaSuccess) return e;
+    tree_attention_kernel<S><<<ctas, S::kThreads, S::kSmem, stream>>>(a);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_join<S>(a, ctas, stream);
+}
+
+template <typename S>
+cudaError_t launch_attention_tc(const AttnArgs& a, int ctas, cudaStream_t stream) {
+    constexpr int kBytes = sizeof(TcShared<S>);
+    static_assert(kBytes <= 227 * 1024, "a CTA's shared memory");
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(done, reinterpret_cast<const void*>(tree_attention_tc_kernel<S>), kBytes);
+    if (e != cudaSuccess) return e;
+    tree_attention_tc_kernel<S><<<ctas, S::kThreads, kBytes, stream>>>(a);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_join<S>(a, ctas, stream);
+}
+
 struct AttnPlan {
     int dp, tm, ctas;  // padded head_dim, rows of a tile, CTAs an SM
     cudaError_t (*launch)(const AttnArgs&, int, cudaStream_t);
@@ -86,8 +116,20 @@ constexpr AttnPlan plan_of() {
     return AttnPlan{S::DP, S::TM, S::kCtas, launch_attention<S>};
 }
 
-// The narrowest row tile that holds the rows * group rows of a kv head, or
-// the widest: a tile's keys and values are read once for all of its rows.
+template <typename S>
+constexpr AttnPlan plan_of_tc() {
+    return AttnPlan{S::DP, S::TM, S::kCtas, launch_attention_tc<S>};
+}
+
+// bf16 rows up to head_dim 128 and more than 16 rows a kv head (rows * group)
+// go to the tcgen05 kernel, whose row tile of 128 costs the tensor cores less
+// time than its positions cost the memory: 64 chains of 6 rows (24 a kv head)
+// over 2000 positions take 124 us there and 147 us on the other, 8 single
+// rows (4) over 1000 take 23 us there and 19 us on the other, whose pipeline
+// is shorter.  There, the narrowest row tile that holds the rows, or the
+// widest: a tile's keys and values are read once for all of its rows.
+constexpr int kTcLeast = 17;
+
 const AttnPlan& attn_plan(specv_dtype dt, int dim, int m) {
     using B = __nv_bfloat16;
     static constexpr AttnPlan plans[2][3][3] = {
@@ -101,6 +143,9 @@ const AttnPlan& attn_plan(specv_dtype dt, int dim, int m) {
          {plan_of<AttnShape<B, 128, 1, 1>>(), plan_of<AttnShape<B, 128, 1, 2>>(), plan_of<AttnShape<B, 128, 2, 2>>()},
          {plan_of<AttnShape<B, 256, 1, 1>>(), plan_of<AttnShape<B, 256, 1, 2>>(),
           plan_of<AttnShape<B, 256, 1, 2>>()}}};
+    static constexpr AttnPlan tc[2][2] = {{plan_of_tc<TcShape<64, false>>(), plan_of_tc<TcShape<64, true>>()},
+                                          {plan_of_tc<TcShape<128, false>>(), plan_of_tc<TcShape<128, true>>()}};
+    if (dt == SPECV_BF16 && dim <= 128 && m >= kTcLeast) return tc[dim <= 64 ? 0 : 1][m <= 128 ? 0 : 1];
     return plans[dt == SPECV_BF16 ? 1 : 0][dim <= 64 ? 0 : dim <= 128 ? 1 : 2][m <= 16 ? 0 : m <= 32 ? 1 : 2];
 }
 

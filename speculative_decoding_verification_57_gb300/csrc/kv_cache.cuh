@@ -9,7 +9,7 @@
 
 namespace specv {
 
-enum : int { KV_PARENT = 512, KV_LENGTH = 2048, KV_BLOCK = 4096, KV_PATH = 8192, KV_ACCEPTED = 128 };
+enum : int { KV_TIMEOUT = 64, KV_PARENT = 512, KV_LENGTH = 2048, KV_BLOCK = 4096, KV_PATH = 8192, KV_ACCEPTED = 128 };
 
 // Quotients n / d of 0 <= n < 2^31 by one multiplication: with p = 31 +
 // ceil(log2 d), m = ceil(2^p / d) is below 2^32 and off by less than d, so
@@ -49,18 +49,14 @@ struct KvView {
 };
 
 // The tree of one sequence's rows, by one converged warp; lane r holds row r
-// (row 0 the root, row 1 + i node i; `parents` NULL: a chain).  anc: bit j
-// set if row j is row r or above it.  Pointers are doubled, so five steps
-// reach the root of any tree of 32 rows.  Returns false (in every lane) if a
-// parent is outside [-1, i); rows past `rows` hold nothing.
-__device__ __forceinline__ bool warp_tree(const int32_t* parents, int rows, int lane, uint32_t& anc, int& depth) {
-    int up = lane - 1;  // the row above; the root's is itself
-    bool ok = true;
-    if (parents && lane > 0 && lane < rows) {
-        up = parents[lane - 1] + 1;
-        ok = up >= 0 && up < lane;
-    }
-    if (lane == 0 || lane >= rows || !ok) up = 0;
+// (row 0 the root, row 1 + i node i) and, as `parent`, parents[r - 1].  anc:
+// bit j set if row j is row r or above it.  Pointers are doubled, so five
+// steps reach the root of any tree of 32 rows.  Returns false (in every lane)
+// if a parent is outside [-1, i); lanes past `rows` hold nothing.
+__device__ __forceinline__ bool warp_tree_of(int parent, int rows, int lane, uint32_t& anc, int& depth) {
+    const bool node = lane > 0 && lane < rows;
+    const bool ok = !node || (parent >= -1 && parent < lane - 1);
+    int up = node && ok ? parent + 1 : 0;  // the row above; the root's is itself
     const bool all_ok = __all_sync(0xffffffffu, ok);
     anc = lane < rows ? (1u << lane) | (1u << up) : 0;
 #pragma unroll
@@ -71,6 +67,12 @@ __device__ __forceinline__ bool warp_tree(const int32_t* parents, int rows, int 
     if (lane >= rows) anc = 0;
     depth = __popc(anc) - 1;
     return all_ok;
+}
+
+// The same from the sequence's parents in memory (NULL: a chain).
+__device__ __forceinline__ bool warp_tree(const int32_t* parents, int rows, int lane, uint32_t& anc, int& depth) {
+    const int parent = parents && lane > 0 && lane < rows ? parents[lane - 1] : lane - 2;
+    return warp_tree_of(parent, rows, lane, anc, depth);
 }
 
 template <typename T>

@@ -81,14 +81,18 @@ struct AttnCursor {
     }
 };
 
+// Shared memory of attn_cut.
+struct AttnCut {
+    int64_t sum[32];
+    int64_t at;
+    int b;
+};
+
 // The line's length, the number of CTAs that share it and the start of this
 // CTA's run, by the whole CTA (THREADS threads, a multiple of 32).
 template <int THREADS>
-__device__ void attn_cut(const AttnArgs& a, int tile_keys, int cta, int ctas, int64_t& units, int& used, int64_t& lo,
-                         int64_t& hi, AttnCursor& cur) {
-    __shared__ int64_t s_sum[THREADS / 32];
-    __shared__ int64_t s_at;
-    __shared__ int s_b;
+__device__ void attn_cut(const AttnArgs& a, AttnCut& sh, int tile_keys, int cta, int ctas, int64_t& units, int& used,
+                         int64_t& lo, int64_t& hi, AttnCursor& cur) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int segs = a.kv.heads * a.row_tiles;
     // the total, then the sequence that holds `lo`: a pass over the lengths
@@ -99,10 +103,10 @@ __device__ void attn_cut(const AttnArgs& a, int tile_keys, int cta, int ctas, in
         sum += mine;
     }
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (lane == 0) s_sum[warp] = sum;
+    if (lane == 0) sh.sum[warp] = sum;
     __syncthreads();
     int64_t total = 0;
-    for (int w = 0; w < THREADS / 32; ++w) total += s_sum[w];
+    for (int w = 0; w < THREADS / 32; ++w) total += sh.sum[w];
     units = total * segs;
     const int64_t most = (units + kAttnLeast - 1) / kAttnLeast;
     used = static_cast<int>(most < ctas ? most : ctas);
@@ -123,24 +127,24 @@ __device__ void attn_cut(const AttnArgs& a, int tile_keys, int cta, int ctas, in
             if (lane >= off) incl += o;
         }
         __syncthreads();
-        if (lane == 31) s_sum[warp] = incl;
+        if (lane == 31) sh.sum[warp] = incl;
         __syncthreads();
         int64_t ahead = before;
-        for (int w = 0; w < warp; ++w) ahead += s_sum[w];
+        for (int w = 0; w < warp; ++w) ahead += sh.sum[w];
         const int64_t start = (ahead + incl - mine) * segs, end = (ahead + incl) * segs;
         if (mine > 0 && start <= lo && lo < end) {
-            s_b = b;
-            s_at = start;
+            sh.b = b;
+            sh.at = start;
         }
-        for (int w = warp; w < THREADS / 32; ++w) ahead += s_sum[w];
+        for (int w = warp; w < THREADS / 32; ++w) ahead += sh.sum[w];
         before = ahead;
         if (before * segs > lo) break;
     }
     __syncthreads();
-    cur.b = s_b;
+    cur.b = sh.b;
     cur.len = attn_len(a, cur.b);
     cur.tiles = attn_tiles(cur.len, tile_keys);
-    const int64_t off = lo - s_at;
+    const int64_t off = lo - sh.at;
     cur.s = static_cast<int>(off / cur.tiles);
     cur.tile = static_cast<int>(off - static_cast<int64_t>(cur.s) * cur.tiles);
 }
@@ -293,6 +297,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
     __shared__ int s_hole[4][KT / 32 > 0 ? KT / 32 : 1];  // whether a position's block is outside the pool
     __shared__ int s_parents[kStages][32];
     __shared__ float2 s_ml[4][TM];
+    __shared__ AttnCut s_cut;
     __shared__ uint32_t s_wild[2];  // nodes with values that are not finite, of a segment and the next
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int wk = warp & 3, wr = warp >> 2;
@@ -307,7 +312,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
     int64_t units, lo, hi;
     int used;
     AttnCursor cur, ahead, ids;
-    attn_cut<S::kThreads>(a, KT, cta, ctas, units, used, lo, hi, cur);
+    attn_cut<S::kThreads>(a, s_cut, KT, cta, ctas, units, used, lo, hi, cur);
     if (tid == 0) {
         s_wild[0] = s_wild[1] = 0;
         work.notes[cta].b = -1;

@@ -1,0 +1,620 @@
+// tree_attention_tc.cuh -- tree attention in bf16 on the tcgen05 tensor cores,
+// head_dim up to 128.  Mathematics, work line and joining as in
+// tree_attention.cuh; a tile is 128 positions, a row tile 128 rows.
+//
+// One CTA an SM, 13 warps: two streams of four softmax warps, four warps that
+// copy, one that issues the products.  A stream has the scores of one row
+// tile and tile of positions (128 x 128 fp32) and its outputs (128 x DP fp32)
+// in tensor memory; a softmax thread owns a row, so that maxima and sums need
+// no exchange.  While one stream's weights are formed the tensor cores work
+// on the other's products.  With up to 128 rows a kv head the streams take
+// tiles of positions in turn and their outputs join at the segment's end;
+// with more (WIDE) each has a row tile of its own and both use every tile.
+//
+// Weights go back to tensor memory over the scores they came from, in bf16,
+// as the left operand of the product with the values; keys lie in shared
+// memory with head_dim along the contraction, values with the positions along
+// it, both as they lie in the cache, in 128-byte swizzled panels of 64
+// columns.
+#pragma once
+#include "tree_attention.cuh"
+
+namespace specv {
+
+// ------------------------------------------------------------------ tcgen05
+__device__ __forceinline__ void tc_alloc(uint32_t smem_dst, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_dealloc(uint32_t addr, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tc_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Arrives on `bar` when every product this thread issued so far is done.
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// d (+)= a b, a and b in shared memory
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+}
+// d (+)= a b, a in tensor memory
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+}
+
+// 32 columns of the warp's 32 lanes, a lane a thread
+__device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+        "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+        "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(
+            r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+        : "memory");
+}
+
+// Shared memory operands in 128-byte swizzled panels (64 columns of bf16; row
+// r at 128 r, eight rows an atom of 1024 bytes).
+// ... contraction along the columns: atoms 1024 bytes apart along the rows
+__device__ __forceinline__ uint64_t tc_desc_rows(uint32_t addr) {
+    return (2ull << 61) | (1ull << 46) | (64ull << 32) | (1ull << 16) | ((addr >> 4) & 0x3fff);
+}
+// ... contraction along the rows: atoms 1024 bytes apart along it, panels of 128 rows apart along the columns
+__device__ __forceinline__ uint64_t tc_desc_cols(uint32_t addr) {
+    return (2ull << 61) | (1ull << 46) | (64ull << 32) | (1024ull << 16) | ((addr >> 4) & 0x3fff);
+}
+
+// bf16 x bf16 -> fp32, 128 rows, n columns; cols: the right operand's contraction runs along its rows
+__host__ __device__ constexpr uint32_t tc_idesc(int n, bool cols) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (cols ? 1u << 16 : 0u) | (static_cast<uint32_t>(n / 8) << 17) |
+           (128u / 16 << 24);
+}
+
+// ------------------------------------------------------------------ shapes
+template <int DP_, bool WIDE_>
+struct TcShape {
+    using Type = __nv_bfloat16;
+    static constexpr int DP = DP_;
+    static constexpr bool WIDE = WIDE_;
+    static constexpr int kTiles = WIDE ? 2 : 1;  // row tiles of a segment
+    static constexpr int TM = 128 * kTiles;
+    static constexpr int KT = 128;
+    static constexpr int kPanel = 128 * 128;  // bytes of 128 rows of 64 columns
+    static constexpr int kPanels = DP / 64;
+    static constexpr int kSlot = kPanels * kPanel;  // keys, or values, of a tile
+    static constexpr int kQ = kTiles * kSlot;
+    // Slots for keys and values alike, filled and freed in the order of their
+    // use: keys of a part's first kLead tiles, then values of tile t and keys
+    // of tile t + kLead in turn.  160 to 192 KB: an SM's share of the memory's
+    // rate times its latency several times over.
+    static constexpr int kLead = WIDE ? 1 : 2;
+    static constexpr int kSlots = DP == 64 ? 10 : WIDE ? 5 : 6;
+    static constexpr int kThreads = 13 * 32;
+    static constexpr int kCtas = 1;
+    // place, in the order of use from its part's first slot on, of the values of tile t of nt
+    static __device__ __forceinline__ int values_at(int t, int nt) {
+        const int more = nt > kLead ? nt - kLead : 0;
+        return (nt < kLead ? nt : kLead) + t + (t < more ? t : more);
+    }
+};
+
+template <typename S>
+struct TcShared {
+    unsigned char q[S::kQ];
+    unsigned char slot[S::kSlots][S::kSlot];
+    float2 ml[S::WIDE ? 1 : 2][S::WIDE ? 1 : 128];  // the streams' maxima and sums, as they join
+    AttnCut cut;
+    uint64_t full[S::kSlots], empty[S::kSlots];
+    uint64_t q_full, q_empty, s_full[2], p_ready[2], o_done[2], end;
+    uint32_t wild[16];  // by segment: nodes with values that are not finite ...
+    int hole[16];       // ... and whether a block is outside the pool
+    uint32_t tmem;
+    int fail;  // a wait ran out: no role waits any more
+};
+
+// A wait of a role: bounded, and none after one ran out.
+__device__ __forceinline__ void tc_wait(uint32_t bar, uint32_t phase, int* fail) {
+    if (mbar_test_wait(bar, phase)) return;
+    if (*static_cast<volatile int*>(fail)) return;
+    if (!mbar_wait_bounded(bar, phase, 1u << 30)) *static_cast<volatile int*>(fail) = 1;
+}
+__device__ __forceinline__ bool tc_failed(const int* fail) { return *static_cast<const volatile int*>(fail) != 0; }
+
+// Where a segment's part in a run ends: its tiles from cur.tile on, `left` tiles of the run to go.
+__device__ __forceinline__ int tc_part(const AttnCursor& cur, int left) {
+    return cur.tiles - cur.tile < left ? cur.tiles - cur.tile : left;
+}
+
+// The copies this thread issued so far arrive on `bar` when they have landed.
+__device__ __forceinline__ void tc_copies_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// ------------------------------------------------------------------ copies
+// Four warps.  A warp copies 32 rows of every tile; lane l finds the place of
+// one of them in the pool (while the slot it goes to is still in use) and
+// hands it to the lanes that copy the row's 16-byte pieces.
+template <typename S>
+__device__ void tc_copy_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor cur, int n, int p) {
+    using T = typename S::Type;
+    constexpr int kPieces = S::DP / 8;    // 16-byte pieces of a row
+    constexpr int kStep = 128 / kPieces;  // rows a pass of the 128 threads
+    constexpr int kOwn = 32 / kPieces;    // rows a pass of a warp
+    const KvView& kv = a.kv;
+    const int lane = p & 31, warp = p >> 5;
+    const int c = p % kPieces, r0 = p / kPieces;
+    const int mine = (lane / kOwn) * kStep + warp * kOwn + lane % kOwn;  // the row whose place this lane finds
+    const bool col = c * 8 < kv.dim;
+    const int m_rows = a.rows * static_cast<int>(a.group.d);
+    // place of this thread's piece of row r in a panelled buffer
+    auto place = [&](int r) { return (c >> 3) * S::kPanel + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
+    int use = 0, seg = 0;
+    auto copy_tile = [&](const void* pool, int tile, int h) {
+        int64_t at = -1;
+        const int t = tile * S::KT + mine;
+        if (t < cur.len) {
+            const int lb = kv.block.div(t);
+            const int blk = __ldg(kv.tables + static_cast<int64_t>(cur.b) * kv.max_blocks + lb);
+            if (kv.valid(blk))
+                at = kv.at(blk, h, t - lb * kv.block_size());
+            else
+                sh.hole[seg & 15] = 1;
+        }
+        const int slot = use % S::kSlots;
+        if (use >= S::kSlots) tc_wait(smem_u32(&sh.empty[slot]), (use / S::kSlots - 1) & 1, &sh.fail);
+        __syncwarp();
+        const uint32_t dst = smem_u32(sh.slot[slot]);
+#pragma unroll
+        for (int i = 0; i < S::KT / kStep; ++i) {
+            const int64_t from = __shfl_sync(0xffffffffu, at, i * kOwn + lane / kPieces);
+            const bool take = from >= 0 && col;
+            cp_async16(dst + place(r0 + i * kStep), static_cast<const T*>(pool) + (take ? from + c * 8 : 0), take);
+        }
+        tc_copies_arrive(smem_u32(&sh.full[slot]));
+        ++use;
+    };
+    for (int j = 0; j < n; ++seg) {
+        const int nt = tc_part(cur, n - j), h = cur.s / a.row_tiles, rt = cur.s - h * a.row_tiles;
+        if (p == 0) {  // flags of a later segment; the roles are never that far apart
+            sh.wild[(seg + 8) & 15] = 0;
+            sh.hole[(seg + 8) & 15] = 0;
+        }
+        if (seg > 0) tc_wait(smem_u32(&sh.q_empty), (seg - 1) & 1, &sh.fail);
+        const T* q = static_cast<const T*>(a.q);
+#pragma unroll 4
+        for (int m = r0; m < S::TM; m += kStep) {
+            const int row = rt * S::TM + m;
+            const bool take = row < m_rows && col;
+            const int r = a.group.div(row), g = row - r * static_cast<int>(a.group.d);
+            const int64_t off = (static_cast<int64_t>(cur.b) * a.rows + r) * a.q_stride +
+                                (static_cast<int64_t>(h) * a.group.d + g) * kv.dim + c * 8;
+            cp_async16(smem_u32(sh.q) + (m >> 7) * S::kSlot + place(m & 127), q + (take ? off : 0), take);
+        }
+        tc_copies_arrive(smem_u32(&sh.q_full));
+        for (int t = 0; t < nt && t < S::kLead; ++t) copy_tile(kv.k, cur.tile + t, h);
+        for (int t = 0; t < nt; ++t) {
+            copy_tile(kv.v, cur.tile + t, h);
+            if (t + S::kLead < nt) copy_tile(kv.k, cur.tile + t + S::kLead, h);
+        }
+        j += nt;
+        cur.tile += nt - 1;
+        cur.next(a, S::KT);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// ------------------------------------------------------------------ products
+// One thread.  Item i of a segment's part: stream i & 1, tile i >> 1 (WIDE) or
+// i.  The scores of item i + 2 follow the output product of item i, whose
+// weights lie where they go: products of one thread run in order.  What the
+// copies wrote is shown to the tensor cores' proxy by the fence behind the
+// wait for them.
+template <typename S>
+__device__ void tc_mma_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor cur, int n) {
+    const uint32_t tm = sh.tmem;
+    constexpr uint32_t kScores = tc_idesc(S::KT, false), kOutputs = tc_idesc(S::DP, true);
+    uint32_t p_seen[2] = {0, 0};
+    int j0 = 0, seg = 0, use = 0, k_use = 0, v_use = 0;
+    while (j0 < n) {
+        const int nt = tc_part(cur, n - j0);
+        const int items = nt * S::kTiles;
+        auto scores = [&](int i) {
+            const int x = i & 1;
+            if (!S::WIDE || x == 0) {
+                k_use = use++;
+                tc_wait(smem_u32(&sh.full[k_use % S::kSlots]), (k_use / S::kSlots) & 1, &sh.fail);
+            }
+            if (tc_failed(&sh.fail)) return;
+            fence_proxy_async_smem();
+            tc_after_sync();
+            const uint32_t qa = smem_u32(sh.q) + (S::WIDE ? x * S::kSlot : 0);
+            const uint32_t ka = smem_u32(sh.slot[k_use % S::kSlots]);
+#pragma unroll
+            for (int kk = 0; kk < S::DP / 16; ++kk) {
+                const uint32_t off = (kk >> 2) * S::kPanel + (kk & 3) * 32;
+                tc_mma_ss(tm + x * 128, tc_desc_rows(qa + off), tc_desc_rows(ka + off), kScores, kk > 0);
+            }
+            tc_commit(smem_u32(&sh.s_full[x]));
+            if (!S::WIDE || x == 1) tc_commit(smem_u32(&sh.empty[k_use % S::kSlots]));
+            if (i == items - 1) tc_commit(smem_u32(&sh.q_empty));
+        };
+        tc_wait(smem_u32(&sh.q_full), seg & 1, &sh.fail);
+        scores(0);
+        if (items > 1) scores(1);
+        for (int i = 0; i < items; ++i) {
+            const int x = i & 1;
+            tc_wait(smem_u32(&sh.p_ready[x]), p_seen[x] & 1, &sh.fail);
+            ++p_seen[x];
+            if (!S::WIDE || x == 0) {
+                v_use = use++;
+                tc_wait(smem_u32(&sh.full[v_use % S::kSlots]), (v_use / S::kSlots) & 1, &sh.fail);
+            }
+            if (tc_failed(&sh.fail)) continue;
+            fence_proxy_async_smem();
+            tc_after_sync();
+            const uint32_t va = smem_u32(sh.slot[v_use % S::kSlots]);
+#pragma unroll
+            for (int kk = 0; kk < S::KT / 16; ++kk)
+                tc_mma_ts(tm + 256 + x * S::DP, tm + x * 128 + kk * 8, tc_desc_cols(va + kk * 2048), kOutputs,
+                          i >= 2 || kk > 0);
+            if (!S::WIDE || x == 1) tc_commit(smem_u32(&sh.empty[v_use % S::kSlots]));
+            if (i + 2 < items)
+                scores(i + 2);
+            else
+                tc_commit(smem_u32(&sh.o_done[x]));
+        }
+        j0 += nt;
+        cur.tile += nt - 1;
+        cur.next(a, S::KT);
+        ++seg;
+    }
+    // nothing of this thread's is in flight when tensor memory is freed
+    tc_commit(smem_u32(&sh.end));
+    mbar_wait_bounded(smem_u32(&sh.end), 0, 1u << 30);
+}
+
+// ------------------------------------------------------------------ softmax
+template <typename S>
+__device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor cur, int n, int64_t units, int64_t lo,
+                                int used, int x, int row) {
+    using T = typename S::Type;
+    const KvView& kv = a.kv;
+    const int lane = row & 31, cta = blockIdx.x;
+    const AttnWork work = attn_work(a.workspace, gridDim.x, S::TM, S::DP);
+    const int m_rows = a.rows * static_cast<int>(a.group.d);
+    const uint32_t lanes = static_cast<uint32_t>(row & ~31) << 16;
+    const uint32_t ts = sh.tmem + x * 128 + lanes;
+    // a scale of zero still has to tell hidden positions (an infinite score) from the others
+    const float scale = a.scale == 0.0f ? 1e-30f : a.scale * 1.44269504f;
+    const float hidden = scale < 0.0f ? INFINITY : -INFINITY;
+    uint32_t s_seen = 0, o_seen = 0;
+    int j0 = 0, seg = 0, use0 = 0;
+    while (j0 < n) {
+        const int nt = tc_part(cur, n - j0);
+        const int items = nt * S::kTiles;
+        const int first_tile = cur.tile;
+        const int h = cur.s / a.row_tiles, rt = cur.s - h * a.row_tiles;
+        const int grow = rt * S::TM + (S::WIDE ? x * 128 : 0) + row;
+        const bool warp_in = grow - lane < m_rows;  // the warp has rows
+        const int r = a.group.div(grow), gq = grow - r * static_cast<int>(a.group.d);
+        const int base = cur.len - a.rows;
+        int parent = lane - 2;
+        if (a.parents && lane > 0 && lane < a.rows)
+            parent = a.parents[static_cast<int64_t>(cur.b) * (a.rows - 1) + lane - 1];
+        uint32_t line = 0;
+        bool tree_ok = true;
+        if ((first_tile + nt) * S::KT > base) {
+            int depth;
+            tree_ok = warp_tree_of(parent, a.rows, lane, line, depth);
+        }
+        const uint32_t anc = __shfl_sync(0xffffffffu, line, r < a.rows ? r : 0);
+        float m_run = -INFINITY, l_run = 0.0f;
+        for (int i = x; i < items; i += 2) {
+            const int t = S::WIDE ? i >> 1 : i, t0 = (first_tile + t) * S::KT;
+            tc_wait(smem_u32(&sh.s_full[x]), s_seen & 1, &sh.fail);
+            ++s_seen;
+            __syncwarp();
+            tc_after_sync();
+            if (warp_in) {
+                uint32_t s[32];
+                if (t0 + S::KT > base) {  // positions that not every row sees
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        tc_ld32(ts + c * 32, s);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const int pos = t0 + c * 32 + e;
+                            if (pos >= base && !(pos < cur.len && (anc >> (pos - base) & 1))) s[e] = __float_as_uint(hidden);
+                        }
+                        tc_st32(ts + c * 32, s);
+                    }
+                    tc_wait_st();
+                }
+                float top = hidden;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    tc_ld32(ts + c * 32, s);
+                    tc_wait_ld();
+                    if (scale >= 0.0f) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(s[e]));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) top = fminf(top, __uint_as_float(s[e]));
+                    }
+                }
+                top *= scale;
+                // the running maximum moves only when a score passes it by 8 (weights stay below 2^8)
+                if (__any_sync(0xffffffffu, top > m_run + 8.0f)) {
+                    const float m_new = fmaxf(m_run, top);
+                    const float keep = m_new == -INFINITY ? 1.0f : ex2(m_run - m_new);
+                    m_run = m_new;
+                    l_run *= keep;
+                    if (i != x) {
+                        const uint32_t to = sh.tmem + 256 + x * S::DP + lanes;
+#pragma unroll 1
+                        for (int c = 0; c < S::DP / 32; ++c) {
+                            tc_ld32(to + c * 32, s);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) * keep);
+                            tc_st32(to + c * 32, s);
+                        }
+                    }
+                }
+                const float m_use = m_run == -INFINITY ? 0.0f : m_run;
+                float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    tc_ld32(ts + c * 32, s);
+                    tc_wait_ld();
+                    // weights in bf16 for the product (relative 2^-8 each, random in sign); their sum is of the fp32 ones
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float w0 = ex2(fmaf(__uint_as_float(s[2 * e]), scale, -m_use));
+                        const float w1 = ex2(fmaf(__uint_as_float(s[2 * e + 1]), scale, -m_use));
+                        sum[0] += w0;
+                        sum[1] += w1;
+                        w[e] = pack_bf16(w0, w1);
+                    }
+                    tc_st16(ts + c * 16, w);
+                }
+                l_run += sum[0] + sum[1];
+                tc_wait_st();
+            }
+            if (cur.len > 0 && t0 + S::KT > base) {
+                // values of the pass's rows that are not finite are taken out of the product, where a weight of zero
+                // would not hide them; they are added to the rows that see them at the segment's end
+                const int slot = (use0 + S::values_at(t, nt)) % S::kSlots;
+                tc_wait(smem_u32(&sh.full[slot]), (use0 + S::values_at(t, nt)) / S::kSlots & 1, &sh.fail);
+                const int lo_r = base > t0 ? base - t0 : 0, hi_r = cur.len - t0 < S::KT ? cur.len - t0 : S::KT;
+                for (int y = lo_r * (S::DP / 8) + row; y < hi_r * (S::DP / 8); y += 128) {
+                    const int vr = y / (S::DP / 8), vc = y % (S::DP / 8);
+                    KvVec<T>* vx = reinterpret_cast<KvVec<T>*>(sh.slot[slot] + (vc >> 3) * S::kPanel + vr * 128 +
+                                                               (((vc & 7) ^ (vr & 7)) << 4));
+                    bool wild = false;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (!finite(KvType<T>::load(vx->x[e]))) {
+                            vx->x[e] = KvType<T>::store(0.0f);
+                            wild = true;
+                        }
+                    if (wild) atomicOr(&sh.wild[seg & 15], 1u << (t0 + vr - base));
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            tc_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.p_ready[x]));
+        }
+        // the segment's part ends
+        if (items > x) {
+            tc_wait(smem_u32(&sh.o_done[x]), o_seen & 1, &sh.fail);
+            ++o_seen;
+        }
+        __syncwarp();
+        tc_after_sync();
+        float e0 = 1.0f, e1 = 0.0f;  // factors of the two streams' outputs
+        if constexpr (!S::WIDE) {
+            sh.ml[x][row] = make_float2(m_run, l_run);
+            __syncwarp();
+            asm volatile("bar.sync 2, 256;" ::: "memory");
+            tc_after_sync();
+            const float2 one = sh.ml[0][row], two = sh.ml[1][row];
+            m_run = fmaxf(one.x, two.x);
+            const float m_use = m_run == -INFINITY ? 0.0f : m_run;
+            e0 = ex2(one.x - m_use);
+            e1 = ex2(two.x - m_use);
+            l_run = one.y * e0 + two.y * e1;
+        }
+        const bool ends = first_tile + nt == cur.tiles;
+        const bool whole = first_tile == 0 && ends;
+        const int piece = 2 * cta + (first_tile == 0 ? 1 : 0);
+        int status = cur.len < 0 ? KV_LENGTH : cur.len == 0 ? 0 : tree_ok ? 0 : KV_PARENT;
+        if (sh.hole[seg & 15]) status |= KV_BLOCK;
+        if (tc_failed(&sh.fail)) status |= KV_TIMEOUT;
+        const bool zero = cur.len <= 0 || status != 0;
+        const uint32_t seen = anc & sh.wild[seg & 15];
+        const int64_t head = (static_cast<int64_t>(cur.b) * a.rows + r) * a.q_heads + static_cast<int64_t>(h) * a.group.d + gq;
+        const float inv = 1.0f / l_run;
+        if (warp_in) {
+            // one row tile: each stream writes half of the columns
+            constexpr int kCols = S::WIDE ? S::DP : S::DP / 2;
+            const uint32_t to = sh.tmem + 256 + lanes;
+#pragma unroll 1
+            for (int c = 0; c < kCols / 32; ++c) {
+                const int d0 = (S::WIDE ? 0 : x * kCols) + c * 32;
+                if (d0 >= kv.dim) break;
+                __syncwarp();
+                float o[32];
+                uint32_t t[32];
+                tc_ld32(to + (S::WIDE ? x * S::DP : 0) + d0, t);
+                tc_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(t[e]);
+                if constexpr (!S::WIDE) {
+                    if (items > 1) {
+                        tc_ld32(to + S::DP + d0, t);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = o[e] * e0 + __uint_as_float(t[e]) * e1;
+                    }
+                }
+                if (grow < m_rows) {
+                    for (uint32_t left = seen; left; left &= left - 1) {
+                        const int pos = base + __ffs(left) - 1, lb = kv.block.div(pos);
+                        const int blk = kv.tables[static_cast<int64_t>(cur.b) * kv.max_blocks + lb];
+                        if (!kv.valid(blk)) continue;
+                        const T* v = static_cast<const T*>(kv.v) + kv.at(blk, h, pos - lb * kv.block_size()) + d0;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float y = d0 + e < kv.dim ? KvType<T>::load(v[e]) : 0.0f;
+                            if (!finite(y)) o[e] += y;
+                        }
+                    }
+                    if (whole) {
+                        T* out = static_cast<T*>(a.out) + head * kv.dim + d0;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            if (d0 + e >= kv.dim) break;
+                            float y[8];
+#pragma unroll
+                            for (int f = 0; f < 8; ++f) y[f] = zero ? 0.0f : o[e + f] * inv;
+                            *reinterpret_cast<uint4*>(out + e) = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]),
+                                                                            pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+                        }
+                    } else {
+                        float* acc = work.acc +
+                                     (static_cast<int64_t>(piece) * S::TM + (S::WIDE ? x * 128 : 0) + row) * S::DP + d0;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4*>(acc + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    }
+                }
+            }
+            if (grow < m_rows && (S::WIDE || x == 0)) {
+                if (!whole)
+                    work.ml[static_cast<int64_t>(piece) * S::TM + (S::WIDE ? x * 128 : 0) + row] = make_float2(m_run, l_run);
+                else if (a.lse)
+                    a.lse[head] = zero ? -INFINITY : m_run * 0.693147181f + logf(l_run);
+            }
+        }
+        if (x == 0 && row == 0) {
+            if (whole) {
+                if (cur.s == 0 && a.row_status) a.row_status[cur.b] = status;
+            } else {
+                work.status[piece] = status;
+                if (first_tile == 0) {
+                    AttnNote note;
+                    note.b = cur.b;
+                    note.s = cur.s;
+                    note.last = attn_owner(units, lo + j0 + cur.tiles - 1, used);
+                    note.pad = 0;
+                    work.notes[cta] = note;
+                }
+            }
+        }
+        if constexpr (!S::WIDE) {
+            __syncwarp();
+            tc_before_sync();
+            asm volatile("bar.sync 2, 256;" ::: "memory");  // both streams' outputs are read
+        }
+        j0 += nt;
+        use0 += 2 * nt;
+        cur.tile += nt - 1;
+        cur.next(a, S::KT);
+        ++seg;
+    }
+}
+
+// ------------------------------------------------------------------ the kernel
+template <typename S>
+__global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const AttnArgs a) {
+    extern __shared__ __align__(1024) unsigned char tc_smem[];
+    TcShared<S>& sh = *reinterpret_cast<TcShared<S>*>(tc_smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int64_t units, lo, hi;
+    int used;
+    AttnCursor cur;
+    attn_cut<S::kThreads>(a, sh.cut, S::KT, blockIdx.x, gridDim.x, units, used, lo, hi, cur);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this grid's end
+    if (tid == 0) attn_work(a.workspace, gridDim.x, S::TM, S::DP).notes[blockIdx.x].b = -1;
+    if (static_cast<int>(blockIdx.x) >= used) return;
+    const int n = static_cast<int>(hi - lo);
+    if (tid == 0) {
+        for (int i = 0; i < S::kSlots; ++i) {
+            mbar_init(smem_u32(&sh.full[i]), 128);
+            mbar_init(smem_u32(&sh.empty[i]), 1);
+        }
+        mbar_init(smem_u32(&sh.q_full), 128);
+        mbar_init(smem_u32(&sh.q_empty), 1);
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(smem_u32(&sh.s_full[x]), 1);
+            mbar_init(smem_u32(&sh.p_ready[x]), 4);
+            mbar_init(smem_u32(&sh.o_done[x]), 1);
+        }
+        mbar_init(smem_u32(&sh.end), 1);
+        fence_mbar_init();
+        sh.fail = (smem_u32(tc_smem) & 1023) != 0;  // the swizzle goes by address bits: no product from another alignment
+    }
+    if (tid < 16) {
+        sh.wild[tid] = 0;
+        sh.hole[tid] = 0;
+    }
+    __syncwarp();
+    if (warp == 12) tc_alloc(smem_u32(&sh.tmem), 512);
+    tc_before_sync();
+    __syncthreads();
+    tc_after_sync();
+    if (warp < 8)
+        tc_softmax_role<S>(a, sh, cur, n, units, lo, used, warp >> 2, tid & 127);
+    else if (warp < 12)
+        tc_copy_role<S>(a, sh, cur, n, tid - 256);
+    else if (lane == 0)
+        tc_mma_role<S>(a, sh, cur, n);
+    __syncwarp();
+    tc_before_sync();
+    __syncthreads();
+    tc_after_sync();
+    if (warp == 12) tc_dealloc(sh.tmem, 512);
+}
+
+}  // namespace specv

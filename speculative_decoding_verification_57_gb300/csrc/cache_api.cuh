@@ -60,7 +60,8 @@ specv_status launched(specv_ctx* h, const char* what) {
 template <typename S>
 cudaError_t launch_join(const AttnArgs& a, int ctas, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas), S::TM / 4, 1);
+    const int m = a.rows * static_cast<int>(a.group.d);  // rows of a kv head
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(((m < S::TM ? m : S::TM) + 3) / 4), 1);
     cfg.blockDim = dim3(kJoinThreads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

@@ -737,12 +737,13 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
 // ------------------------------------------------------------------ the join
 constexpr int kJoinThreads = 128;
 
-// Row tile rows blockIdx.y * 4 .. + 3 of the segment that CTA blockIdx.x of
-// the kernel before noted: a warp a row.
+// Rows blockIdx.y * 4 .. + 3 of the row tile whose segment CTA blockIdx.x of
+// the kernel before noted: a warp a row.  Lanes take the pieces' maxima and
+// sums side by side, 32 at a time; the outputs come four pieces at a time.
 template <typename S>
 __global__ void __launch_bounds__(kJoinThreads) tree_attention_join(const AttnArgs a, int ctas) {
     using T = typename S::Type;
-    constexpr int TM = S::TM, DP = S::DP;
+    constexpr int TM = S::TM, DP = S::DP, kOut = DP / 32;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const AttnWork work = attn_work(a.workspace, ctas, TM, DP);
     const int cta = blockIdx.x, lane = threadIdx.x & 31;
@@ -752,31 +753,55 @@ __global__ void __launch_bounds__(kJoinThreads) tree_attention_join(const AttnAr
     const KvView& kv = a.kv;
     const int h = note.s / a.row_tiles, rt = note.s - h * a.row_tiles;
     const int grow = rt * TM + row;
-    int status = 0;
-    for (int c = cta; c <= note.last; ++c) status |= work.status[2 * c + (c == cta)];
-    if (row == 0 && note.s == 0 && lane == 0 && a.row_status) a.row_status[note.b] = status;
     if (grow >= a.rows * static_cast<int>(a.group.d)) return;
-    float m = -INFINITY;
-    for (int c = cta; c <= note.last; ++c) m = fmaxf(m, work.ml[(2ll * c + (c == cta)) * TM + row].x);
-    const float m_use = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f, x[DP / 32] = {};
-    for (int c = cta; c <= note.last; ++c) {
-        const int64_t piece = 2ll * c + (c == cta);
-        const float2 ml = work.ml[piece * TM + row];
+    const int n = note.last - cta + 1;
+    // piece i: [1] of the CTA that starts the segment, then [0] of the next ones
+    auto piece = [&](int i) { return 2ll * (cta + i) + (i == 0); };
+    int status = 0;
+    float m = -INFINITY, l = 0.0f, x[kOut] = {};
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const bool in = i0 + lane < n;
+        const float2 ml = in ? work.ml[piece(i0 + lane) * TM + row] : make_float2(-INFINITY, 0.0f);
+        const int st = in ? work.status[piece(i0 + lane)] : 0;
+        status |= static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(st)));
+        const float m_new = fmaxf(m, warp_max_f32(ml.x));
+        const float m_use = m_new == -INFINITY ? 0.0f : m_new;
+        const float before = ex2(m - m_use);
+        m = m_new;
         const float keep = ex2(ml.x - m_use);
-        l += ml.y * keep;
-        const float* acc = work.acc + (piece * TM + row) * DP;
+        float part = ml.y * keep;
+        for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
+        l = l * before + part;
 #pragma unroll
-        for (int j = 0; j < DP / 32; ++j)
-            if (j * 32 + lane < kv.dim) x[j] += acc[j * 32 + lane] * keep;
+        for (int j = 0; j < kOut; ++j) x[j] *= before;
+        const int here = n - i0 < 32 ? n - i0 : 32;
+        for (int i = 0; i < here; i += 4) {
+            float y[4][kOut];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int j = 0; j < kOut; ++j)
+                    y[u][j] = i + u < here && j * 32 + lane < kv.dim
+                                  ? work.acc[(piece(i0 + i + u) * TM + row) * DP + j * 32 + lane]
+                                  : 0.0f;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float w = __shfl_sync(0xffffffffu, keep, i + u < 32 ? i + u : 31);
+                if (i + u < here) {
+#pragma unroll
+                    for (int j = 0; j < kOut; ++j) x[j] += y[u][j] * w;
+                }
+            }
+        }
     }
+    if (row == 0 && note.s == 0 && lane == 0 && a.row_status) a.row_status[note.b] = status;
     const int r = a.group.div(grow), g = grow - r * static_cast<int>(a.group.d);
     const int64_t token = static_cast<int64_t>(note.b) * a.rows + r;
     const int64_t head = token * a.q_heads + static_cast<int64_t>(h) * a.group.d + g;
     T* out = static_cast<T*>(a.out) + head * kv.dim;
     const float inv = 1.0f / l;
 #pragma unroll
-    for (int j = 0; j < DP / 32; ++j)
+    for (int j = 0; j < kOut; ++j)
         if (j * 32 + lane < kv.dim) out[j * 32 + lane] = KvType<T>::store(status ? 0.0f : x[j] * inv);
     if (lane == 0 && a.lse) a.lse[head] = status ? -INFINITY : m * 0.693147181f + logf(l);
 }

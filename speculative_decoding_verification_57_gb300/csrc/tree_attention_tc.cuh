@@ -2,8 +2,9 @@
 // head_dim up to 128.  Mathematics, work line and joining as in
 // tree_attention.cuh; a tile is 128 positions, a row tile 128 rows.
 //
-// One CTA an SM, 13 warps: two streams of four softmax warps, four warps that
-// copy, one that issues the products.  A stream has the scores of one row
+// One CTA an SM, 16 warps: two streams of four softmax warps, four warps that
+// copy, one that issues the products (and three that only make up its
+// warpgroup, so that registers can be moved to the softmax warps).  A stream has the scores of one row
 // tile and tile of positions (128 x 128 fp32) and its outputs (128 x DP fp32)
 // in tensor memory; a softmax thread owns a row, so that maxima and sums need
 // no exchange.  While one stream's weights are formed the tensor cores work
@@ -79,6 +80,14 @@ __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) 
         "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
         : "memory");
 }
+__device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+}
 __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(
@@ -124,7 +133,9 @@ struct TcShape {
     // rate times its latency several times over.
     static constexpr int kLead = WIDE ? 1 : 2;
     static constexpr int kSlots = DP == 64 ? 10 : WIDE ? 5 : 6;
-    static constexpr int kThreads = 13 * 32;
+    static constexpr int kThreads = 16 * 32;
+    // registers of a softmax thread, and of the others: together the 128 a thread that the launch has
+    static constexpr int kMany = 184, kFew = 72;
     static constexpr int kCtas = 1;
     // place, in the order of use from its part's first slot on, of the values of tile t of nt
     static __device__ __forceinline__ int values_at(int t, int nt) {
@@ -351,72 +362,80 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
             __syncwarp();
             tc_after_sync();
             if (warp_in) {
-                uint32_t s[32];
+                uint32_t s[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tc_ld32(ts + c * 32, s[c]);
+                tc_wait_ld();
                 if (t0 + S::KT > base) {  // positions that not every row sees
-#pragma unroll 1
+#pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        tc_ld32(ts + c * 32, s);
-                        tc_wait_ld();
+                        // bit e: position t0 + 32 c + e is before the pass's rows, or one that this row sees
+                        const int gap = base - (t0 + c * 32);
+                        const uint32_t open = gap >= 32 ? ~0u
+                                              : gap >= 0 ? (anc << gap) | ((1u << gap) - 1)
+                                              : gap > -32 ? anc >> -gap
+                                                          : 0u;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const int pos = t0 + c * 32 + e;
-                            if (pos >= base && !(pos < cur.len && (anc >> (pos - base) & 1))) s[e] = __float_as_uint(hidden);
-                        }
-                        tc_st32(ts + c * 32, s);
-                    }
-                    tc_wait_st();
-                }
-                float top = hidden;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tc_ld32(ts + c * 32, s);
-                    tc_wait_ld();
-                    if (scale >= 0.0f) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(s[e]));
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) top = fminf(top, __uint_as_float(s[e]));
+                        for (int e = 0; e < 32; ++e)
+                            if (!(open >> e & 1)) s[c][e] = __float_as_uint(hidden);
                     }
                 }
-                top *= scale;
+                float top[4] = {hidden, hidden, hidden, hidden};
+                if (scale >= 0.0f) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) top[c] = fmaxf(top[c], __uint_as_float(s[c][e]));
+                    top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) top[c] = fminf(top[c], __uint_as_float(s[c][e]));
+                    top[0] = fminf(fminf(top[0], top[1]), fminf(top[2], top[3]));
+                }
+                top[0] *= scale;
                 // the running maximum moves only when a score passes it by 8 (weights stay below 2^8)
-                if (__any_sync(0xffffffffu, top > m_run + 8.0f)) {
-                    const float m_new = fmaxf(m_run, top);
+                if (__any_sync(0xffffffffu, top[0] > m_run + 8.0f)) {
+                    const float m_new = fmaxf(m_run, top[0]);
                     const float keep = m_new == -INFINITY ? 1.0f : ex2(m_run - m_new);
                     m_run = m_new;
                     l_run *= keep;
                     if (i != x) {
                         const uint32_t to = sh.tmem + 256 + x * S::DP + lanes;
 #pragma unroll 1
-                        for (int c = 0; c < S::DP / 32; ++c) {
-                            tc_ld32(to + c * 32, s);
+                        for (int c = 0; c < S::DP / 16; ++c) {
+                            uint32_t o[16];
+                            tc_ld16(to + c * 16, o);
                             tc_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) * keep);
-                            tc_st32(to + c * 32, s);
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                            tc_st16(to + c * 16, o);
                         }
                     }
                 }
                 const float m_use = m_run == -INFINITY ? 0.0f : m_run;
-                float sum[2] = {0.0f, 0.0f};
+                const f2 sc = pack2(scale, scale), nm = pack2(-m_use, -m_use);
+                f2 sum[2] = {pack2(0.0f, 0.0f), pack2(0.0f, 0.0f)};
+                // weights in bf16 for the product (relative 2^-8 each, random in sign); their sum is of the fp32 ones
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tc_ld32(ts + c * 32, s);
-                    tc_wait_ld();
-                    // weights in bf16 for the product (relative 2^-8 each, random in sign); their sum is of the fp32 ones
-                    uint32_t w[16];
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t w[32];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float w0 = ex2(fmaf(__uint_as_float(s[2 * e]), scale, -m_use));
-                        const float w1 = ex2(fmaf(__uint_as_float(s[2 * e + 1]), scale, -m_use));
-                        sum[0] += w0;
-                        sum[1] += w1;
+                    for (int e = 0; e < 32; ++e) {
+                        const uint32_t* p = &s[2 * half + (e >> 4)][2 * (e & 15)];
+                        float w0, w1;
+                        unpack2(fma2(pack2(__uint_as_float(p[0]), __uint_as_float(p[1])), sc, nm), w0, w1);
+                        w0 = ex2(w0);
+                        w1 = ex2(w1);
+                        sum[e & 1] = add2(sum[e & 1], pack2(w0, w1));
                         w[e] = pack_bf16(w0, w1);
                     }
-                    tc_st16(ts + c * 16, w);
+                    tc_st32(ts + half * 32, w);
                 }
-                l_run += sum[0] + sum[1];
+                float l0, l1;
+                unpack2(add2(sum[0], sum[1]), l0, l1);
+                l_run += l0 + l1;
                 tc_wait_st();
             }
             if (cur.len > 0 && t0 + S::KT > base) {
@@ -604,12 +623,16 @@ __global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
-    if (warp < 8)
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kMany));
         tc_softmax_role<S>(a, sh, cur, n, units, lo, used, warp >> 2, tid & 127);
-    else if (warp < 12)
-        tc_copy_role<S>(a, sh, cur, n, tid - 256);
-    else if (lane == 0)
-        tc_mma_role<S>(a, sh, cur, n);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kFew));
+        if (warp < 12)
+            tc_copy_role<S>(a, sh, cur, n, tid - 256);
+        else if (warp == 12 && lane == 0)
+            tc_mma_role<S>(a, sh, cur, n);
+    }
     __syncwarp();
     tc_before_sync();
     __syncthreads();

@@ -95,16 +95,53 @@ cudaError_t launch_attention(const AttnArgs& a, int ctas, cudaStream_t stream) {
     return e != cudaSuccess ? e : launch_join<S>(a, ctas, stream);
 }
 
+// Boxes for the cache's blocks, if they fill tiles of 128 rows evenly; false:
+// they do not, or the pool is outside what a tensor map can say.
+bool make_maps(const KvView& kv, TcMaps& maps) {
+    const int bs = static_cast<int>(kv.block.d);
+    if (bs % 8 || (128 % bs && bs % 128) || kv.blocks < 1 || kv.block_stride >= (1ll << 38)) return false;
+    static const auto encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                                             CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                             CUtensorMapFloatOOBfill)>(f);
+    }();
+    if (!encode) return false;
+    maps.rows = bs < 128 ? bs : 128;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(kv.dim), static_cast<cuuint64_t>(bs),
+                                static_cast<cuuint64_t>(kv.heads), static_cast<cuuint64_t>(kv.blocks)};
+    const cuuint64_t strides[3] = {dims[0] * 2, dims[0] * dims[1] * 2, static_cast<cuuint64_t>(kv.block_stride) * 2};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(maps.rows), 1, 1}, ones[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 2; ++i)
+        if (encode(i ? &maps.v : &maps.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, i ? kv.v : kv.k, dims, strides, box, ones,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return false;
+    return true;
+}
+
 template <typename S>
-cudaError_t launch_attention_tc(const AttnArgs& a, int ctas, cudaStream_t stream) {
+cudaError_t launch_tc(const AttnArgs& a, const TcMaps& maps, int ctas, cudaStream_t stream) {
     constexpr int kBytes = sizeof(TcShared<S>);
     static_assert(kBytes <= 227 * 1024, "a CTA's shared memory");
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(done, reinterpret_cast<const void*>(tree_attention_tc_kernel<S>), kBytes);
     if (e != cudaSuccess) return e;
-    tree_attention_tc_kernel<S><<<ctas, S::kThreads, kBytes, stream>>>(a);
+    tree_attention_tc_kernel<S><<<ctas, S::kThreads, kBytes, stream>>>(a, maps);
     e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_join<S>(a, ctas, stream);
+}
+
+template <int DP, bool WIDE>
+cudaError_t launch_attention_tc(const AttnArgs& a, int ctas, cudaStream_t stream) {
+    TcMaps maps = {};
+    if (make_maps(a.kv, maps)) return launch_tc<TcShape<DP, WIDE, true>>(a, maps, ctas, stream);
+    return launch_tc<TcShape<DP, WIDE, false>>(a, maps, ctas, stream);
 }
 
 struct AttnPlan {
@@ -117,9 +154,9 @@ constexpr AttnPlan plan_of() {
     return AttnPlan{S::DP, S::TM, S::kCtas, launch_attention<S>};
 }
 
-template <typename S>
+template <int DP, bool WIDE>
 constexpr AttnPlan plan_of_tc() {
-    return AttnPlan{S::DP, S::TM, S::kCtas, launch_attention_tc<S>};
+    return AttnPlan{DP, TcShape<DP, WIDE, true>::TM, 1, launch_attention_tc<DP, WIDE>};
 }
 
 // bf16 rows up to head_dim 128 and more than 16 rows a kv head (rows * group)
@@ -144,8 +181,8 @@ const AttnPlan& attn_plan(specv_dtype dt, int dim, int m) {
          {plan_of<AttnShape<B, 128, 1, 1>>(), plan_of<AttnShape<B, 128, 1, 2>>(), plan_of<AttnShape<B, 128, 2, 2>>()},
          {plan_of<AttnShape<B, 256, 1, 1>>(), plan_of<AttnShape<B, 256, 1, 2>>(),
           plan_of<AttnShape<B, 256, 1, 2>>()}}};
-    static constexpr AttnPlan tc[2][2] = {{plan_of_tc<TcShape<64, false>>(), plan_of_tc<TcShape<64, true>>()},
-                                          {plan_of_tc<TcShape<128, false>>(), plan_of_tc<TcShape<128, true>>()}};
+    static constexpr AttnPlan tc[2][2] = {{plan_of_tc<64, false>(), plan_of_tc<64, true>()},
+                                          {plan_of_tc<128, false>(), plan_of_tc<128, true>()}};
     if (dt == SPECV_BF16 && dim <= 128 && m >= kTcLeast) return tc[dim <= 64 ? 0 : 1][m <= 128 ? 0 : 1];
     return plans[dt == SPECV_BF16 ? 1 : 0][dim <= 64 ? 0 : dim <= 128 ? 1 : 2][m <= 16 ? 0 : m <= 32 ? 1 : 2];
 }

@@ -3,8 +3,8 @@
 // tree_attention.cuh; a tile is 128 positions, a row tile 128 rows.
 //
 // One CTA an SM, 16 warps: two streams of four softmax warps, four warps that
-// copy, one that issues the products (and three that only make up its
-// warpgroup, so that registers can be moved to the softmax warps).  A stream has the scores of one row
+// copy, two that issue the products, and some that help or only make up their
+// warpgroup, so that registers can be moved to the softmax warps.  A stream has the scores of one row
 // tile and tile of positions (128 x 128 fp32) and its outputs (128 x DP fp32)
 // in tensor memory; a softmax thread owns a row, so that maxima and sums need
 // no exchange.  While one stream's weights are formed the tensor cores work
@@ -17,7 +17,14 @@
 // memory with head_dim along the contraction, values with the positions along
 // it, both as they lie in the cache, in 128-byte swizzled panels of 64
 // columns.
+//
+// Blocks whose rows fill tiles evenly (a multiple of eight that divides 128,
+// or a multiple of 128) come as tensor boxes, a box a block and panel; others
+// by 16-byte copies.  The boxes take one warp a tenth of the instructions and
+// land where the tensor cores see them at once: TIMES.
 #pragma once
+#include <cuda.h>
+
 #include "tree_attention.cuh"
 
 namespace specv {
@@ -36,25 +43,32 @@ __device__ __forceinline__ void tc_after_sync() { asm volatile("tcgen05.fence::a
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Arrives on `bar` when every product this thread issued so far is done.
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+// The issuing warp runs as one and one lane of it (`lead` not 0) issues.
+// Arrives on `bar` when every product that lane issued so far is done.
+__device__ __forceinline__ void tc_commit(uint32_t bar, uint32_t lead) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.u32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+        "r"(lead)
+        : "memory");
 }
 
 // d (+)= a b, a and b in shared memory
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add,
+                                          uint32_t lead) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(add)
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add), "r"(lead)
         : "memory");
 }
 // d (+)= a b, a in tensor memory
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add,
+                                          uint32_t lead) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(add)
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add), "r"(lead)
         : "memory");
 }
 
@@ -115,11 +129,12 @@ __host__ __device__ constexpr uint32_t tc_idesc(int n, bool cols) {
 }
 
 // ------------------------------------------------------------------ shapes
-template <int DP_, bool WIDE_>
+template <int DP_, bool WIDE_, bool TMA_>
 struct TcShape {
     using Type = __nv_bfloat16;
     static constexpr int DP = DP_;
     static constexpr bool WIDE = WIDE_;
+    static constexpr bool TMA = TMA_;  // blocks come as tensor boxes; else by 16-byte copies
     static constexpr int kTiles = WIDE ? 2 : 1;  // row tiles of a segment
     static constexpr int TM = 128 * kTiles;
     static constexpr int KT = 128;
@@ -133,6 +148,7 @@ struct TcShape {
     // rate times its latency several times over.
     static constexpr int kLead = WIDE ? 1 : 2;
     static constexpr int kSlots = DP == 64 ? 10 : WIDE ? 5 : 6;
+    static constexpr int kBoxWarps = 3;
     static constexpr int kThreads = 16 * 32;
     // registers of a softmax thread, and of the others: together the 128 a thread that the launch has
     static constexpr int kMany = 184, kFew = 72;
@@ -142,6 +158,17 @@ struct TcShape {
         const int more = nt > kLead ? nt - kLead : 0;
         return (nt < kLead ? nt : kLead) + t + (t < more ? t : more);
     }
+    // ... and of its keys
+    static __device__ __forceinline__ int keys_at(int t, int nt) {
+        return t < kLead ? t : values_at(t - kLead, nt) + 1;
+    }
+};
+
+// Tensor maps of the two pools ([blocks, heads, block_size, head_dim], boxes
+// of `rows` rows of 64 columns), where boxes are used.
+struct TcMaps {
+    CUtensorMap k, v;
+    int rows;
 };
 
 template <typename S>
@@ -150,8 +177,9 @@ struct TcShared {
     unsigned char slot[S::kSlots][S::kSlot];
     float2 ml[S::WIDE ? 1 : 2][S::WIDE ? 1 : 128];  // the streams' maxima and sums, as they join
     AttnCut cut;
-    uint64_t full[S::kSlots], empty[S::kSlots];
-    uint64_t q_full, q_empty, s_full[2], p_ready[2], o_done[2], end;
+    // a slot's copies have landed, are visible to the tensor cores, are used up
+    uint64_t full[S::kSlots], shown[S::kSlots], empty[S::kSlots];
+    uint64_t q_full, q_shown, q_empty, s_full[2], p_ready[2], o_done[2], turn[2], end[2];
     uint32_t wild[16];  // by segment: nodes with values that are not finite ...
     int hole[16];       // ... and whether a block is outside the pool
     uint32_t tmem;
@@ -166,6 +194,7 @@ __device__ __forceinline__ void tc_wait(uint32_t bar, uint32_t phase, int* fail)
 }
 __device__ __forceinline__ bool tc_failed(const int* fail) { return *static_cast<const volatile int*>(fail) != 0; }
 
+
 // Where a segment's part in a run ends: its tiles from cur.tile on, `left` tiles of the run to go.
 __device__ __forceinline__ int tc_part(const AttnCursor& cur, int left) {
     return cur.tiles - cur.tile < left ? cur.tiles - cur.tile : left;
@@ -176,12 +205,151 @@ __device__ __forceinline__ void tc_copies_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// ------------------------------------------------------------------ copies
-// Four warps.  A warp copies 32 rows of every tile; lane l finds the place of
-// one of them in the pool (while the slot it goes to is still in use) and
-// hands it to the lanes that copy the row's 16-byte pieces.
+// A box of a block: 64 columns from `col` on of rows `row`.. of a head.
+__device__ __forceinline__ void tc_box(uint32_t dst, const CUtensorMap* map, int col, int row, int h, int blk,
+                                       uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst),
+        "l"(map), "r"(col), "r"(row), "r"(h), "r"(blk), "r"(bar)
+        : "memory");
+}
+
+// The slots of a run in the order of their use.
 template <typename S>
-__device__ void tc_copy_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor cur, int n, int p) {
+struct TcUses {
+    AttnCursor cur;  // at a part's first tile
+    int n, nt;       // tiles from it on to the run's end, and of the part
+    int u = 0, seg = 0;
+
+    __device__ __forceinline__ TcUses(const AttnCursor& c, int n_) : cur(c), n(n_), nt(tc_part(c, n_)) {}
+    __device__ __forceinline__ void next(const AttnArgs& a) {
+        if (++u < 2 * nt) return;
+        u = 0;
+        ++seg;
+        n -= nt;
+        cur.tile += nt - 1;
+        cur.next(a, S::KT);
+        nt = tc_part(cur, n);
+    }
+    // whether the use is of values, and its tile
+    __device__ __forceinline__ bool what(int& tile) const {
+        const int lead = nt < S::kLead ? nt : S::kLead, w = u - lead, pairs = 2 * (nt - lead);
+        const bool values = w >= 0 && (w >= pairs || !(w & 1));
+        tile = cur.tile + (w < 0 ? u : w >= pairs ? w - (nt - lead) : (w >> 1) + (w & 1 ? lead : 0));
+        return values;
+    }
+};
+
+// ------------------------------------------------------------------ copies
+// Queries of a segment's row tiles, by THREADS threads (a multiple of a row's
+// pieces apart), p of them this one.
+template <typename S, int THREADS>
+__device__ __forceinline__ void tc_copy_queries(const AttnArgs& a, TcShared<S>& sh, const AttnCursor& cur, int p) {
+    using T = typename S::Type;
+    constexpr int kPieces = S::DP / 8, kStep = THREADS / kPieces;
+    const KvView& kv = a.kv;
+    const int c = p % kPieces, h = cur.s / a.row_tiles, rt = cur.s - h * a.row_tiles;
+    const int m_rows = a.rows * static_cast<int>(a.group.d);
+    const T* q = static_cast<const T*>(a.q);
+#pragma unroll 4
+    for (int m = p / kPieces; m < S::TM; m += kStep) {
+        const int row = rt * S::TM + m;
+        const bool take = row < m_rows && c * 8 < kv.dim;
+        const int r = a.group.div(row), g = row - r * static_cast<int>(a.group.d);
+        const int64_t off = (static_cast<int64_t>(cur.b) * a.rows + r) * a.q_stride +
+                            (static_cast<int64_t>(h) * a.group.d + g) * kv.dim + c * 8;
+        cp_async16(smem_u32(sh.q) + (m >> 7) * S::kSlot + (c >> 3) * S::kPanel + (m & 127) * 128 + (((c & 7) ^ (m & 7)) << 4),
+                   q + (take ? off : 0), take);
+    }
+}
+
+// Boxes (TMA): kBoxWarps warps, a slot each in turn (a box takes a warp some 90
+// cycles to issue, and a slot is up to 32 of them).  Lane l brings a panel of
+// one of the tile's blocks; its block number is read a slot ahead.  A block
+// that is outside the pool or past the sequence's end is asked for at block
+// number `blocks`, which reads as zeros.
+template <typename S>
+__device__ void tc_box_role(const AttnArgs& a, const TcMaps& maps, TcShared<S>& sh, const AttnCursor& cur, int n,
+                            int warp, int lane) {
+    const KvView& kv = a.kv;
+    const int part = lane / S::kPanels, panel = lane % S::kPanels;  // block of the tile, and columns
+    const int rows = maps.rows;                                    // of a box
+    const bool mine = part * rows < S::KT;
+    TcUses<S> it(cur, n);
+    // what this lane asks for: block number (0: nothing to ask), and where in it
+    struct Box {
+        int blk, row, h, seg;
+        bool values, in;
+    };
+    auto read = [&]() {
+        Box x;
+        int tile;
+        x.values = it.what(tile);
+        const int t = tile * S::KT + part * rows;
+        x.in = mine && t < it.cur.len;
+        const int lb = kv.block.div(x.in ? t : 0);
+        x.blk = x.in ? __ldg(kv.tables + static_cast<int64_t>(it.cur.b) * kv.max_blocks + lb) : 0;
+        x.row = t - lb * kv.block_size();
+        x.h = it.cur.s / a.row_tiles;
+        x.seg = it.seg;
+        return x;
+    };
+    // to use `to` of the run, from use `at`
+    auto go = [&](int at, int to) {
+        for (; at < to && at < 2 * n; ++at) {
+            if (it.u == 0 && warp == 0 && lane == 0) {  // flags of a later segment; the roles are never that far apart
+                sh.wild[(it.seg + 8) & 15] = 0;
+                sh.hole[(it.seg + 8) & 15] = 0;
+            }
+            it.next(a);
+        }
+    };
+    go(0, warp);
+    Box next = read();
+    for (int use = warp; use < 2 * n; use += S::kBoxWarps) {
+        const Box x = next;
+        go(use, use + S::kBoxWarps);
+        if (use + S::kBoxWarps < 2 * n) next = read();
+        const int slot = use % S::kSlots;
+        if (use >= S::kSlots) tc_wait(smem_u32(&sh.empty[slot]), (use / S::kSlots - 1) & 1, &sh.fail);
+        __syncwarp();
+        const uint32_t bar = smem_u32(&sh.full[slot]);
+        if (lane == 0) mbar_arrive_expect_tx(bar, S::kSlot);
+        __syncwarp();
+        const bool valid = x.in && kv.valid(x.blk);
+        if (x.in && !valid) sh.hole[x.seg & 15] = 1;
+        if (mine)
+            tc_box(smem_u32(sh.slot[slot]) + panel * S::kPanel + part * rows * 128, x.values ? &maps.v : &maps.k,
+                   panel * 64, valid ? x.row : 0, x.h, valid ? x.blk : kv.blocks, bar);
+    }
+    // no box is in flight when the CTA ends, not even after a wait that ran out
+    if (warp == 0)
+        for (int use = 2 * n > S::kSlots ? 2 * n - S::kSlots : 0; use < 2 * n; ++use)
+            mbar_wait_bounded(smem_u32(&sh.full[use % S::kSlots]), (use / S::kSlots) & 1, 1u << 30);
+}
+
+// Queries where the keys and values are boxes: one warp.
+template <typename S>
+__device__ void tc_query_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor cur, int n, int p) {
+    for (int j = 0, seg = 0; j < n; ++seg) {
+        const int nt = tc_part(cur, n - j);
+        if (seg > 0) tc_wait(smem_u32(&sh.q_empty), (seg - 1) & 1, &sh.fail);
+        tc_copy_queries<S, 32>(a, sh, cur, p);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        mbar_arrive(smem_u32(&sh.q_shown));
+        j += nt;
+        cur.tile += nt - 1;
+        cur.next(a, S::KT);
+    }
+}
+
+// 16-byte copies: four warps.  A warp copies 32 rows of every tile; lane l
+// finds the place of one of them in the pool (while the slot it goes to is
+// still in use) and hands it to the lanes that copy the row's pieces.
+template <typename S>
+__device__ void tc_copy_role(const AttnArgs& a, TcShared<S>& sh, const AttnCursor& cur, int n, int p) {
     using T = typename S::Type;
     constexpr int kPieces = S::DP / 8;    // 16-byte pieces of a row
     constexpr int kStep = 128 / kPieces;  // rows a pass of the 128 threads
@@ -191,132 +359,141 @@ __device__ void tc_copy_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor cur,
     const int c = p % kPieces, r0 = p / kPieces;
     const int mine = (lane / kOwn) * kStep + warp * kOwn + lane % kOwn;  // the row whose place this lane finds
     const bool col = c * 8 < kv.dim;
-    const int m_rows = a.rows * static_cast<int>(a.group.d);
-    // place of this thread's piece of row r in a panelled buffer
-    auto place = [&](int r) { return (c >> 3) * S::kPanel + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
-    int use = 0, seg = 0;
-    auto copy_tile = [&](const void* pool, int tile, int h) {
+    TcUses<S> it(cur, n);
+    for (int use = 0; use < 2 * n; ++use, it.next(a)) {
+        if (it.u == 0) {
+            if (p == 0) {  // flags of a later segment; the roles are never that far apart
+                sh.wild[(it.seg + 8) & 15] = 0;
+                sh.hole[(it.seg + 8) & 15] = 0;
+            }
+            if (it.seg > 0) tc_wait(smem_u32(&sh.q_empty), (it.seg - 1) & 1, &sh.fail);
+            tc_copy_queries<S, 128>(a, sh, it.cur, p);
+            tc_copies_arrive(smem_u32(&sh.q_full));
+        }
+        int tile;
+        const bool values = it.what(tile);
         int64_t at = -1;
         const int t = tile * S::KT + mine;
-        if (t < cur.len) {
+        if (t < it.cur.len) {
             const int lb = kv.block.div(t);
-            const int blk = __ldg(kv.tables + static_cast<int64_t>(cur.b) * kv.max_blocks + lb);
+            const int blk = __ldg(kv.tables + static_cast<int64_t>(it.cur.b) * kv.max_blocks + lb);
             if (kv.valid(blk))
-                at = kv.at(blk, h, t - lb * kv.block_size());
+                at = kv.at(blk, it.cur.s / a.row_tiles, t - lb * kv.block_size());
             else
-                sh.hole[seg & 15] = 1;
+                sh.hole[it.seg & 15] = 1;
         }
         const int slot = use % S::kSlots;
         if (use >= S::kSlots) tc_wait(smem_u32(&sh.empty[slot]), (use / S::kSlots - 1) & 1, &sh.fail);
         __syncwarp();
         const uint32_t dst = smem_u32(sh.slot[slot]);
+        const T* pool = static_cast<const T*>(values ? kv.v : kv.k);
 #pragma unroll
         for (int i = 0; i < S::KT / kStep; ++i) {
             const int64_t from = __shfl_sync(0xffffffffu, at, i * kOwn + lane / kPieces);
             const bool take = from >= 0 && col;
-            cp_async16(dst + place(r0 + i * kStep), static_cast<const T*>(pool) + (take ? from + c * 8 : 0), take);
+            const int r = r0 + i * kStep;
+            cp_async16(dst + (c >> 3) * S::kPanel + r * 128 + (((c & 7) ^ (r & 7)) << 4), pool + (take ? from + c * 8 : 0),
+                       take);
         }
         tc_copies_arrive(smem_u32(&sh.full[slot]));
-        ++use;
-    };
-    for (int j = 0; j < n; ++seg) {
-        const int nt = tc_part(cur, n - j), h = cur.s / a.row_tiles, rt = cur.s - h * a.row_tiles;
-        if (p == 0) {  // flags of a later segment; the roles are never that far apart
-            sh.wild[(seg + 8) & 15] = 0;
-            sh.hole[(seg + 8) & 15] = 0;
-        }
-        if (seg > 0) tc_wait(smem_u32(&sh.q_empty), (seg - 1) & 1, &sh.fail);
-        const T* q = static_cast<const T*>(a.q);
-#pragma unroll 4
-        for (int m = r0; m < S::TM; m += kStep) {
-            const int row = rt * S::TM + m;
-            const bool take = row < m_rows && col;
-            const int r = a.group.div(row), g = row - r * static_cast<int>(a.group.d);
-            const int64_t off = (static_cast<int64_t>(cur.b) * a.rows + r) * a.q_stride +
-                                (static_cast<int64_t>(h) * a.group.d + g) * kv.dim + c * 8;
-            cp_async16(smem_u32(sh.q) + (m >> 7) * S::kSlot + place(m & 127), q + (take ? off : 0), take);
-        }
-        tc_copies_arrive(smem_u32(&sh.q_full));
-        for (int t = 0; t < nt && t < S::kLead; ++t) copy_tile(kv.k, cur.tile + t, h);
-        for (int t = 0; t < nt; ++t) {
-            copy_tile(kv.v, cur.tile + t, h);
-            if (t + S::kLead < nt) copy_tile(kv.k, cur.tile + t + S::kLead, h);
-        }
-        j += nt;
-        cur.tile += nt - 1;
-        cur.next(a, S::KT);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// ------------------------------------------------------------------ products
-// One thread.  Item i of a segment's part: stream i & 1, tile i >> 1 (WIDE) or
-// i.  The scores of item i + 2 follow the output product of item i, whose
-// weights lie where they go: products of one thread run in order.  What the
-// copies wrote is shown to the tensor cores' proxy by the fence behind the
-// wait for them.
+// What the copies wrote is shown to the tensor cores' proxy by a thread of its
+// own: the fence takes some 300 cycles, which would otherwise stand between
+// the products.
 template <typename S>
-__device__ void tc_mma_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor cur, int n) {
+__device__ void tc_show_role(const AttnArgs& a, TcShared<S>& sh, const AttnCursor& cur, int n) {
+    TcUses<S> it(cur, n);
+    for (int use = 0; use < 2 * n; ++use, it.next(a)) {
+        if (it.u == 0) {
+            tc_wait(smem_u32(&sh.q_full), it.seg & 1, &sh.fail);
+            fence_proxy_async_smem();
+            mbar_arrive(smem_u32(&sh.q_shown));
+        }
+        tc_wait(smem_u32(&sh.full[use % S::kSlots]), (use / S::kSlots) & 1, &sh.fail);
+        fence_proxy_async_smem();
+        mbar_arrive(smem_u32(&sh.shown[use % S::kSlots]));
+    }
+}
+
+// ------------------------------------------------------------------ products
+// One warp a stream.  A product's issue waits for the one before it, so that
+// one warp's waits and commits would all be idle time of the tensor cores; and
+// the two take turns, an output product and the next scores at a time, because
+// streams that share the tensor cores fall into step and then form their
+// weights at the same time, while these idle (16 trees of 32 rows over 8192
+// positions: TIMES).  Item i of a segment's part belongs to stream i & 1 and
+// tile i >> 1 (WIDE) or i.  A stream's next scores follow its output product,
+// whose weights lie where they go: products of one thread run in order.
+template <typename S>
+__device__ void tc_mma_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor cur, int n, int x, uint32_t lead) {
     const uint32_t tm = sh.tmem;
+    const uint32_t ts = tm + x * 128, to = tm + 256 + x * S::DP;
     constexpr uint32_t kScores = tc_idesc(S::KT, false), kOutputs = tc_idesc(S::DP, true);
-    uint32_t p_seen[2] = {0, 0};
-    int j0 = 0, seg = 0, use = 0, k_use = 0, v_use = 0;
+    uint32_t p_seen = 0, turns = 0;
+    int j0 = 0, seg = 0, use0 = 0;
+    auto wait_slot = [&](int use) {
+        const int slot = use % S::kSlots;
+        tc_wait(smem_u32(S::TMA ? &sh.full[slot] : &sh.shown[slot]), (use / S::kSlots) & 1, &sh.fail);
+        return slot;
+    };
     while (j0 < n) {
         const int nt = tc_part(cur, n - j0);
         const int items = nt * S::kTiles;
-        auto scores = [&](int i) {
-            const int x = i & 1;
-            if (!S::WIDE || x == 0) {
-                k_use = use++;
-                tc_wait(smem_u32(&sh.full[k_use % S::kSlots]), (k_use / S::kSlots) & 1, &sh.fail);
-            }
-            if (tc_failed(&sh.fail)) return;
-            fence_proxy_async_smem();
-            tc_after_sync();
-            const uint32_t qa = smem_u32(sh.q) + (S::WIDE ? x * S::kSlot : 0);
-            const uint32_t ka = smem_u32(sh.slot[k_use % S::kSlots]);
+        const uint64_t qd = tc_desc_rows(smem_u32(sh.q) + (S::WIDE ? x * S::kSlot : 0));
+        auto scores = [&](int slot) {
+            const uint64_t kd = tc_desc_rows(smem_u32(sh.slot[slot]));
 #pragma unroll
             for (int kk = 0; kk < S::DP / 16; ++kk) {
-                const uint32_t off = (kk >> 2) * S::kPanel + (kk & 3) * 32;
-                tc_mma_ss(tm + x * 128, tc_desc_rows(qa + off), tc_desc_rows(ka + off), kScores, kk > 0);
+                const uint32_t off = ((kk >> 2) * S::kPanel + (kk & 3) * 32) >> 4;
+                tc_mma_ss(ts, qd + off, kd + off, kScores, kk > 0, lead);
             }
-            tc_commit(smem_u32(&sh.s_full[x]));
-            if (!S::WIDE || x == 1) tc_commit(smem_u32(&sh.empty[k_use % S::kSlots]));
-            if (i == items - 1) tc_commit(smem_u32(&sh.q_empty));
         };
-        tc_wait(smem_u32(&sh.q_full), seg & 1, &sh.fail);
-        scores(0);
-        if (items > 1) scores(1);
-        for (int i = 0; i < items; ++i) {
-            const int x = i & 1;
-            tc_wait(smem_u32(&sh.p_ready[x]), p_seen[x] & 1, &sh.fail);
-            ++p_seen[x];
-            if (!S::WIDE || x == 0) {
-                v_use = use++;
-                tc_wait(smem_u32(&sh.full[v_use % S::kSlots]), (v_use / S::kSlots) & 1, &sh.fail);
-            }
-            if (tc_failed(&sh.fail)) continue;
-            fence_proxy_async_smem();
+        tc_wait(smem_u32(&sh.q_shown), seg & 1, &sh.fail);
+        if (x < items) {
+            const int slot = wait_slot(use0 + S::keys_at(S::WIDE ? 0 : x, nt));
+            __syncwarp();
             tc_after_sync();
-            const uint32_t va = smem_u32(sh.slot[v_use % S::kSlots]);
+            scores(slot);
+            tc_commit(smem_u32(&sh.s_full[x]), lead);
+            tc_commit(smem_u32(&sh.empty[slot]), lead);
+        }
+        for (int i = x; i < items; i += 2) {
+            const int t = S::WIDE ? i >> 1 : i;
+            const bool more = i + 2 < items;
+            const int v_slot = wait_slot(use0 + S::values_at(t, nt));
+            const int k_slot = more ? wait_slot(use0 + S::keys_at(t + (S::WIDE ? 1 : 2), nt)) : 0;
+            tc_wait(smem_u32(&sh.p_ready[x]), p_seen & 1, &sh.fail);
+            ++p_seen;
+            if (i > 0) {
+                tc_wait(smem_u32(&sh.turn[x]), turns & 1, &sh.fail);
+                ++turns;
+            }
+            __syncwarp();
+            tc_after_sync();
+            const uint64_t vd = tc_desc_cols(smem_u32(sh.slot[v_slot]));
 #pragma unroll
             for (int kk = 0; kk < S::KT / 16; ++kk)
-                tc_mma_ts(tm + 256 + x * S::DP, tm + x * 128 + kk * 8, tc_desc_cols(va + kk * 2048), kOutputs,
-                          i >= 2 || kk > 0);
-            if (!S::WIDE || x == 1) tc_commit(smem_u32(&sh.empty[v_use % S::kSlots]));
-            if (i + 2 < items)
-                scores(i + 2);
-            else
-                tc_commit(smem_u32(&sh.o_done[x]));
+                tc_mma_ts(to, ts + kk * 8, vd + kk * (2048 >> 4), kOutputs, i >= 2 || kk > 0, lead);
+            if (more) scores(k_slot);
+            if (lead && i + 1 < items) mbar_arrive(smem_u32(&sh.turn[x ^ 1]));
+            __syncwarp();
+            tc_commit(smem_u32(more ? &sh.s_full[x] : &sh.o_done[x]), lead);
+            tc_commit(smem_u32(&sh.empty[v_slot]), lead);
+            if (more) tc_commit(smem_u32(&sh.empty[k_slot]), lead);
         }
+        tc_commit(smem_u32(&sh.q_empty), lead);
         j0 += nt;
+        use0 += 2 * nt;
         cur.tile += nt - 1;
         cur.next(a, S::KT);
         ++seg;
     }
-    // nothing of this thread's is in flight when tensor memory is freed
-    tc_commit(smem_u32(&sh.end));
-    mbar_wait_bounded(smem_u32(&sh.end), 0, 1u << 30);
+    // nothing of this warp's is in flight when tensor memory is freed
+    tc_commit(smem_u32(&sh.end[x]), lead);
+    mbar_wait_bounded(smem_u32(&sh.end[x]), 0, 1u << 30);
 }
 
 // ------------------------------------------------------------------ softmax
@@ -443,11 +620,17 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
                 // would not hide them; they are added to the rows that see them at the segment's end
                 const int slot = (use0 + S::values_at(t, nt)) % S::kSlots;
                 tc_wait(smem_u32(&sh.full[slot]), (use0 + S::values_at(t, nt)) / S::kSlots & 1, &sh.fail);
-                const int lo_r = base > t0 ? base - t0 : 0, hi_r = cur.len - t0 < S::KT ? cur.len - t0 : S::KT;
+                // (boxes bring the rest of the last block too, whatever it holds: zeros in its place)
+                const int lo_r = base > t0 ? base - t0 : 0, end_r = cur.len - t0 < S::KT ? cur.len - t0 : S::KT;
+                const int hi_r = S::TMA ? S::KT : end_r;
                 for (int y = lo_r * (S::DP / 8) + row; y < hi_r * (S::DP / 8); y += 128) {
                     const int vr = y / (S::DP / 8), vc = y % (S::DP / 8);
                     KvVec<T>* vx = reinterpret_cast<KvVec<T>*>(sh.slot[slot] + (vc >> 3) * S::kPanel + vr * 128 +
                                                                (((vc & 7) ^ (vr & 7)) << 4));
+                    if (vr >= end_r) {
+                        *reinterpret_cast<uint4*>(vx) = make_uint4(0, 0, 0, 0);
+                        continue;
+                    }
                     bool wild = false;
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
@@ -586,7 +769,7 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
 
 // ------------------------------------------------------------------ the kernel
 template <typename S>
-__global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
     extern __shared__ __align__(1024) unsigned char tc_smem[];
     TcShared<S>& sh = *reinterpret_cast<TcShared<S>*>(tc_smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -600,17 +783,20 @@ __global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const
     const int n = static_cast<int>(hi - lo);
     if (tid == 0) {
         for (int i = 0; i < S::kSlots; ++i) {
-            mbar_init(smem_u32(&sh.full[i]), 128);
-            mbar_init(smem_u32(&sh.empty[i]), 1);
+            mbar_init(smem_u32(&sh.full[i]), S::TMA ? 1 : 128);
+            mbar_init(smem_u32(&sh.shown[i]), 1);
+            mbar_init(smem_u32(&sh.empty[i]), S::kTiles);  // the streams that use it
         }
         mbar_init(smem_u32(&sh.q_full), 128);
-        mbar_init(smem_u32(&sh.q_empty), 1);
+        mbar_init(smem_u32(&sh.q_shown), S::TMA ? 32 : 1);
+        mbar_init(smem_u32(&sh.q_empty), 2);
         for (int x = 0; x < 2; ++x) {
             mbar_init(smem_u32(&sh.s_full[x]), 1);
             mbar_init(smem_u32(&sh.p_ready[x]), 4);
             mbar_init(smem_u32(&sh.o_done[x]), 1);
+            mbar_init(smem_u32(&sh.turn[x]), 1);
+            mbar_init(smem_u32(&sh.end[x]), 1);
         }
-        mbar_init(smem_u32(&sh.end), 1);
         fence_mbar_init();
         sh.fail = (smem_u32(tc_smem) & 1023) != 0;  // the swizzle goes by address bits: no product from another alignment
     }
@@ -628,10 +814,19 @@ __global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const
         tc_softmax_role<S>(a, sh, cur, n, units, lo, used, warp >> 2, tid & 127);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kFew));
-        if (warp < 12)
-            tc_copy_role<S>(a, sh, cur, n, tid - 256);
-        else if (warp == 12 && lane == 0)
-            tc_mma_role<S>(a, sh, cur, n);
+        if (warp == 12 || warp == 13) {
+            tc_mma_role<S>(a, sh, cur, n, warp - 12, lane == 0);
+        } else if constexpr (S::TMA) {
+            if (warp < 8 + S::kBoxWarps)
+                tc_box_role<S>(a, maps, sh, cur, n, warp - 8, lane);
+            else if (warp < 12)
+                tc_query_role<S>(a, sh, cur, n, lane);
+        } else {
+            if (warp < 12)
+                tc_copy_role<S>(a, sh, cur, n, tid - 256);
+            else if (warp == 14 && lane == 0)
+                tc_show_role<S>(a, sh, cur, n);
+        }
     }
     __syncwarp();
     tc_before_sync();

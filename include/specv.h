@@ -336,8 +336,8 @@ specv_status specv_cache_append(specv_handle h, const specv_kv_cache *cache, con
  *   out         [B, rows, q_heads, head_dim] out, without gaps
  *   lse         [B, rows, q_heads] fp32 out (nullable): log of the sum of
  *               the exponentials of the scaled scores
- *   row_status  [B] out (nullable): 0, or bits 512, 2048, 4096.  out of an
- *               idle or refused sequence is 0, lse -infinity
+ *   row_status  [B] out (nullable): 0, or bits 512, 2048, 4096, 64.  out of
+ *               an idle or refused sequence is 0, lse -infinity
  *   workspace   device memory of specv_tree_attention_workspace(...) bytes,
  *               256-byte aligned, the call's own until it has run
  * Positions that a row does not see take no part, whatever they hold (NaN and
@@ -371,8 +371,10 @@ specv_status specv_cache_compact(specv_handle h, const specv_kv_cache *cache, in
 int specv_plan_cluster(specv_handle h, specv_dtype logits_dtype, int batch, int k, int64_t V);
 
 /* Test hook, off unless called: arms the next launch of the split-vocabulary
- * kernel (V > 2048) on this handle so that CTA 0 of the grid never issues
- * the bulk copy of its pass-1 stage use number `stage_use` (counted from 0
+ * kernel (V > 2048) or of the tcgen05 tree-attention kernel (bf16, head_dim up
+ * to 128, more than 16 rows a kv head) on this handle so that CTA 0 of the
+ * grid never issues the bulk copy of its pass-1 stage use (the copies of its
+ * slot use) number `stage_use` (counted from 0
  * in issue order) nor signals it, and every wait of that launch gives up
  * after `polls` polls.  The waits that run out end the row's work: it
  * reports row_status bit 64 (num_accepted 0, out_tokens -1) and the call

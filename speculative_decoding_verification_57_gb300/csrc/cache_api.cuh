@@ -60,8 +60,8 @@ specv_status launched(specv_ctx* h, const char* what) {
 template <typename S>
 cudaError_t launch_join(const AttnArgs& a, int ctas, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    const int m = a.rows * static_cast<int>(a.group.d);  // rows of a kv head
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(((m < S::TM ? m : S::TM) + 3) / 4), 1);
+    const int pieces = static_cast<int>(a.filled.d) * (a.kv.dim / 4);  // of four columns
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>((pieces + kJoinThreads - 1) / kJoinThreads), 1);
     cfg.blockDim = dim3(kJoinThreads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -146,17 +146,18 @@ cudaError_t launch_attention_tc(const AttnArgs& a, int ctas, cudaStream_t stream
 
 struct AttnPlan {
     int dp, tm, ctas;  // padded head_dim, rows of a tile, CTAs an SM
+    bool tc;           // the tcgen05 kernel
     cudaError_t (*launch)(const AttnArgs&, int, cudaStream_t);
 };
 
 template <typename S>
 constexpr AttnPlan plan_of() {
-    return AttnPlan{S::DP, S::TM, S::kCtas, launch_attention<S>};
+    return AttnPlan{S::DP, S::TM, S::kCtas, false, launch_attention<S>};
 }
 
 template <int DP, bool WIDE>
 constexpr AttnPlan plan_of_tc() {
-    return AttnPlan{DP, TcShape<DP, WIDE, true>::TM, 1, launch_attention_tc<DP, WIDE>};
+    return AttnPlan{DP, TcShape<DP, WIDE, true>::TM, 1, true, launch_attention_tc<DP, WIDE>};
 }
 
 // bf16 rows up to head_dim 128 and more than 16 rows a kv head (rows * group)
@@ -268,11 +269,19 @@ specv_status specv_tree_attention(specv_handle h, const specv_kv_cache* cache, c
     a.row_status = row_status;
     a.workspace = static_cast<unsigned char*>(workspace);
     a.group = FastDiv(static_cast<uint32_t>(group));
+    a.filled = FastDiv(static_cast<uint32_t>(rows * group < p.tm ? rows * group : p.tm));
     a.q_heads = q_heads;
     a.rows = rows;
     a.batch = batch;
     a.row_tiles = (rows * group + p.tm - 1) / p.tm;
     a.scale = scale;
+    a.withhold = -1;
+    a.polls = 1u << 30;
+    if (p.tc && h->test_withhold >= 0) {  // the test hook arms one launch
+        a.withhold = h->test_withhold;
+        a.polls = h->test_polls;
+        h->test_withhold = -1;
+    }
     DeviceGuard g(h->device);
     if (!g.ok) return cuda_fail(cudaErrorInvalidDevice, "cudaSetDevice");
     const cudaError_t e = p.launch(a, ctas, static_cast<cudaStream_t>(stream));

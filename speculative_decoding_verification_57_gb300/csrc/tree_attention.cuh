@@ -38,10 +38,13 @@ struct AttnArgs {
     float* lse;
     int32_t* row_status;
     unsigned char* workspace;
-    FastDiv group;  // query heads of a kv head
+    FastDiv group;   // query heads of a kv head
+    FastDiv filled;  // rows of a row tile that hold any (the first tile has the most)
     int q_heads, rows, batch;
     int row_tiles;
     float scale;
+    int withhold;    // test hook (tcgen05 kernel): this slot use of CTA 0's run is not copied (-1: none)
+    uint32_t polls;  // most polls of a wait
 };
 
 // ------------------------------------------------------------------ the cut
@@ -153,17 +156,18 @@ __device__ void attn_cut(const AttnArgs& a, AttnCut& sh, int tile_keys, int cta,
 // For every CTA a note on the segment that starts in its run and goes on
 // past it, and two partial results: [0] of the segment its run starts in the
 // middle of, [1] of the segment it starts and does not finish.
-struct AttnNote {
-    int b, s;      // b < 0: none
-    int last;      // the CTA with the segment's last tile
-    int pad;
+struct alignas(16) AttnNote {
+    int b, s;    // b < 0: none
+    int last;    // the CTA with the segment's last tile
+    int failed;  // a wait of the CTA ran out: sequences b0 .. b1 may be wrong
+    int b0, b1;
 };
 
 struct AttnWork {
     AttnNote* notes;   // [ctas]
     int* status;       // [ctas * 2]
     float2* ml;        // [ctas * 2][TM]: maximum and sum of the weights
-    float* acc;        // [ctas * 2][TM][DP]
+    float4* acc;       // [ctas * 2][DP / 4][TM]: four columns of a row, rows side by side
 };
 
 __host__ __device__ inline int64_t attn_work_bytes(int ctas, int tm, int dp) {
@@ -175,8 +179,8 @@ __host__ __device__ inline AttnWork attn_work(unsigned char* p, int ctas, int tm
     AttnWork w;
     w.notes = reinterpret_cast<AttnNote*>(p);
     w.ml = reinterpret_cast<float2*>(w.notes + ctas);
-    w.acc = reinterpret_cast<float*>(w.ml + static_cast<int64_t>(ctas) * 2 * tm);
-    w.status = reinterpret_cast<int*>(w.acc + static_cast<int64_t>(ctas) * 2 * tm * dp);
+    w.acc = reinterpret_cast<float4*>(w.ml + static_cast<int64_t>(ctas) * 2 * tm);
+    w.status = reinterpret_cast<int*>(w.acc + static_cast<int64_t>(ctas) * 2 * tm * (dp / 4));
     return w;
 }
 
@@ -316,6 +320,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
     if (tid == 0) {
         s_wild[0] = s_wild[1] = 0;
         work.notes[cta].b = -1;
+        work.notes[cta].failed = 0;
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this grid's end
     if (cta >= used) return;
@@ -700,7 +705,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
                         attn_store4(out, zero ? 0.0f : x[0] * inv, zero ? 0.0f : x[1] * inv, zero ? 0.0f : x[2] * inv,
                                     zero ? 0.0f : x[3] * inv);
                     } else {
-                        *reinterpret_cast<float4*>(work.acc + (static_cast<int64_t>(piece) * TM + row) * DP + d) =
+                        work.acc[(static_cast<int64_t>(piece) * (DP / 4) + d / 4) * TM + row] =
                             make_float4(x[0], x[1], x[2], x[3]);
                     }
                 }
@@ -713,18 +718,13 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
                 }
             }
             if (tid == 0) {
-                if (whole) {
-                    if (cur.s == 0 && a.row_status) a.row_status[cur.b] = status;
-                } else {
+                if (first_tile == 0 && cur.s == 0 && a.row_status) a.row_status[cur.b] = status;
+                if (!whole) {
                     work.status[piece] = status;
                     if (first_tile == 0) {
-                        const int64_t end = lo + i + (cur.tiles - cur.tile);  // the unit behind the segment's last
-                        AttnNote note;
-                        note.b = cur.b;
-                        note.s = cur.s;
-                        note.last = attn_owner(units, end - 1, used);
-                        note.pad = 0;
-                        work.notes[cta] = note;
+                        work.notes[cta].b = cur.b;
+                        work.notes[cta].s = cur.s;
+                        work.notes[cta].last = attn_owner(units, lo + i + (cur.tiles - cur.tile) - 1, used);
                     }
                 }
             }
@@ -736,74 +736,68 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
 
 // ------------------------------------------------------------------ the join
 constexpr int kJoinThreads = 128;
+constexpr int kJoinPieces = 8;  // loads in flight a thread
 
-// Rows blockIdx.y * 4 .. + 3 of the row tile whose segment CTA blockIdx.x of
-// the kernel before noted: a warp a row.  Lanes take the pieces' maxima and
-// sums side by side, 32 at a time; the outputs come four pieces at a time.
+// Four columns of a row a thread, rows side by side, of the segment that CTA
+// blockIdx.x of the kernel before noted; kJoinPieces pieces at a time.
 template <typename S>
 __global__ void __launch_bounds__(kJoinThreads) tree_attention_join(const AttnArgs a, int ctas) {
     using T = typename S::Type;
-    constexpr int TM = S::TM, DP = S::DP, kOut = DP / 32;
+    constexpr int TM = S::TM, DP = S::DP;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const AttnWork work = attn_work(a.workspace, ctas, TM, DP);
-    const int cta = blockIdx.x, lane = threadIdx.x & 31;
+    const int cta = blockIdx.x;
     const AttnNote note = work.notes[cta];
+    if (note.failed && blockIdx.y == 0 && a.row_status)
+        for (int b = note.b0 + static_cast<int>(threadIdx.x); b <= note.b1; b += kJoinThreads)
+            atomicOr(a.row_status + b, KV_TIMEOUT);
     if (note.b < 0) return;
-    const int row = blockIdx.y * 4 + (threadIdx.x >> 5);
     const KvView& kv = a.kv;
+    const int at = blockIdx.y * kJoinThreads + threadIdx.x;
+    const int col = a.filled.div(at), row = at - col * static_cast<int>(a.filled.d);  // col: a group of four
     const int h = note.s / a.row_tiles, rt = note.s - h * a.row_tiles;
     const int grow = rt * TM + row;
-    if (grow >= a.rows * static_cast<int>(a.group.d)) return;
-    const int n = note.last - cta + 1;
-    // piece i: [1] of the CTA that starts the segment, then [0] of the next ones
-    auto piece = [&](int i) { return 2ll * (cta + i) + (i == 0); };
+    if (col * 4 >= kv.dim || grow >= a.rows * static_cast<int>(a.group.d)) return;
     int status = 0;
-    float m = -INFINITY, l = 0.0f, x[kOut] = {};
-    for (int i0 = 0; i0 < n; i0 += 32) {
-        const bool in = i0 + lane < n;
-        const float2 ml = in ? work.ml[piece(i0 + lane) * TM + row] : make_float2(-INFINITY, 0.0f);
-        const int st = in ? work.status[piece(i0 + lane)] : 0;
-        status |= static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(st)));
-        const float m_new = fmaxf(m, warp_max_f32(ml.x));
+    float m = -INFINITY, l = 0.0f;
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int c = cta; c <= note.last; c += kJoinPieces) {
+        float2 ml[kJoinPieces];
+        float4 y[kJoinPieces];
+#pragma unroll
+        for (int u = 0; u < kJoinPieces; ++u) {
+            const bool in = c + u <= note.last;
+            // [1] of the CTA that starts the segment, then [0] of the next ones
+            const int64_t piece = 2ll * (in ? c + u : cta) + (!in || c + u == cta);
+            status |= work.status[piece];
+            ml[u] = work.ml[piece * TM + row];
+            y[u] = work.acc[(piece * (DP / 4) + col) * TM + row];
+            if (!in) ml[u] = make_float2(-INFINITY, 0.0f);
+        }
+        float m_new = m;
+#pragma unroll
+        for (int u = 0; u < kJoinPieces; ++u) m_new = fmaxf(m_new, ml[u].x);
         const float m_use = m_new == -INFINITY ? 0.0f : m_new;
         const float before = ex2(m - m_use);
         m = m_new;
-        const float keep = ex2(ml.x - m_use);
-        float part = ml.y * keep;
-        for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
-        l = l * before + part;
+        l *= before;
+        x = make_float4(x.x * before, x.y * before, x.z * before, x.w * before);
 #pragma unroll
-        for (int j = 0; j < kOut; ++j) x[j] *= before;
-        const int here = n - i0 < 32 ? n - i0 : 32;
-        for (int i = 0; i < here; i += 4) {
-            float y[4][kOut];
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-#pragma unroll
-                for (int j = 0; j < kOut; ++j)
-                    y[u][j] = i + u < here && j * 32 + lane < kv.dim
-                                  ? work.acc[(piece(i0 + i + u) * TM + row) * DP + j * 32 + lane]
-                                  : 0.0f;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const float w = __shfl_sync(0xffffffffu, keep, i + u < 32 ? i + u : 31);
-                if (i + u < here) {
-#pragma unroll
-                    for (int j = 0; j < kOut; ++j) x[j] += y[u][j] * w;
-                }
-            }
+        for (int u = 0; u < kJoinPieces; ++u) {
+            if (c + u > note.last) break;
+            const float w = ex2(ml[u].x - m_use);
+            l = fmaf(ml[u].y, w, l);
+            x = make_float4(fmaf(y[u].x, w, x.x), fmaf(y[u].y, w, x.y), fmaf(y[u].z, w, x.z), fmaf(y[u].w, w, x.w));
         }
     }
-    if (row == 0 && note.s == 0 && lane == 0 && a.row_status) a.row_status[note.b] = status;
+    if (at == 0 && note.s == 0 && status && a.row_status) atomicOr(a.row_status + note.b, status);
     const int r = a.group.div(grow), g = grow - r * static_cast<int>(a.group.d);
     const int64_t token = static_cast<int64_t>(note.b) * a.rows + r;
     const int64_t head = token * a.q_heads + static_cast<int64_t>(h) * a.group.d + g;
-    T* out = static_cast<T*>(a.out) + head * kv.dim;
-    const float inv = 1.0f / l;
-#pragma unroll
-    for (int j = 0; j < kOut; ++j)
-        if (j * 32 + lane < kv.dim) out[j * 32 + lane] = KvType<T>::store(status ? 0.0f : x[j] * inv);
-    if (lane == 0 && a.lse) a.lse[head] = status ? -INFINITY : m * 0.693147181f + logf(l);
+    const float inv = status ? 0.0f : 1.0f / l;
+    if (status) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    attn_store4(static_cast<T*>(a.out) + head * kv.dim + col * 4, x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+    if (col == 0 && a.lse) a.lse[head] = status ? -INFINITY : m * 0.693147181f + logf(l);
 }
 
 }  // namespace specv

@@ -186,14 +186,18 @@ struct TcShared {
     int fail;  // a wait ran out: no role waits any more
 };
 
-// A wait of a role: bounded, and none after one ran out.
-__device__ __forceinline__ void tc_wait(uint32_t bar, uint32_t phase, int* fail) {
-    if (mbar_test_wait(bar, phase)) return;
-    if (*static_cast<volatile int*>(fail)) return;
-    if (!mbar_wait_bounded(bar, phase, 1u << 30)) *static_cast<volatile int*>(fail) = 1;
+// A wait of a role: bounded, and none after one ran out.  False: it, or
+// another, ran out; the role copies and issues nothing more.  A parity tells
+// two successive phases apart and no more: who waits for a phase has to know
+// that the one before it is complete.
+__device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t phase, int* fail, uint32_t polls) {
+    if (mbar_test_wait(bar, phase)) return true;
+    if (*static_cast<volatile int*>(fail)) return false;
+    if (mbar_wait_bounded(bar, phase, polls)) return true;
+    *static_cast<volatile int*>(fail) = 1;
+    return false;
 }
 __device__ __forceinline__ bool tc_failed(const int* fail) { return *static_cast<const volatile int*>(fail) != 0; }
-
 
 // Where a segment's part in a run ends: its tiles from cur.tile on, `left` tiles of the run to go.
 __device__ __forceinline__ int tc_part(const AttnCursor& cur, int left) {
@@ -252,10 +256,12 @@ __device__ __forceinline__ void tc_copy_queries(const AttnArgs& a, TcShared<S>& 
     const int c = p % kPieces, h = cur.s / a.row_tiles, rt = cur.s - h * a.row_tiles;
     const int m_rows = a.rows * static_cast<int>(a.group.d);
     const T* q = static_cast<const T*>(a.q);
+    // (rows behind the last keep what shared memory held: nobody reads their results)
+    const int last = m_rows - rt * S::TM < S::TM ? m_rows - rt * S::TM : S::TM;
 #pragma unroll 4
-    for (int m = p / kPieces; m < S::TM; m += kStep) {
+    for (int m = p / kPieces; m < last; m += kStep) {
         const int row = rt * S::TM + m;
-        const bool take = row < m_rows && c * 8 < kv.dim;
+        const bool take = c * 8 < kv.dim;
         const int r = a.group.div(row), g = row - r * static_cast<int>(a.group.d);
         const int64_t off = (static_cast<int64_t>(cur.b) * a.rows + r) * a.q_stride +
                             (static_cast<int64_t>(h) * a.group.d + g) * kv.dim + c * 8;
@@ -306,14 +312,19 @@ __device__ void tc_box_role(const AttnArgs& a, const TcMaps& maps, TcShared<S>& 
         }
     };
     go(0, warp);
-    Box next = read();
-    for (int use = warp; use < 2 * n; use += S::kBoxWarps) {
+    const int withhold = blockIdx.x == 0 ? a.withhold : -1;
+    Box next = {};
+    if (warp < 2 * n) next = read();
+    int use = warp;
+    for (; use < 2 * n; use += S::kBoxWarps) {
         const Box x = next;
         go(use, use + S::kBoxWarps);
         if (use + S::kBoxWarps < 2 * n) next = read();
         const int slot = use % S::kSlots;
-        if (use >= S::kSlots) tc_wait(smem_u32(&sh.empty[slot]), (use / S::kSlots - 1) & 1, &sh.fail);
-        __syncwarp();
+        // (whose phase before, kSlots uses earlier, this warp's last wait implies: slots are used up in order)
+        bool go_on = use < S::kSlots || tc_wait(smem_u32(&sh.empty[slot]), (use / S::kSlots - 1) & 1, &sh.fail, a.polls);
+        go_on = __all_sync(0xffffffffu, go_on);
+        if (!go_on || use == withhold) break;
         const uint32_t bar = smem_u32(&sh.full[slot]);
         if (lane == 0) mbar_arrive_expect_tx(bar, S::kSlot);
         __syncwarp();
@@ -323,10 +334,11 @@ __device__ void tc_box_role(const AttnArgs& a, const TcMaps& maps, TcShared<S>& 
             tc_box(smem_u32(sh.slot[slot]) + panel * S::kPanel + part * rows * 128, x.values ? &maps.v : &maps.k,
                    panel * 64, valid ? x.row : 0, x.h, valid ? x.blk : kv.blocks, bar);
     }
-    // no box is in flight when the CTA ends, not even after a wait that ran out
-    if (warp == 0)
-        for (int use = 2 * n > S::kSlots ? 2 * n - S::kSlots : 0; use < 2 * n; ++use)
-            mbar_wait_bounded(smem_u32(&sh.full[use % S::kSlots]), (use / S::kSlots) & 1, 1u << 30);
+    // no box of this warp's is in flight when the CTA ends, not even after a wait that ran out (earlier ones had landed
+    // when their slots were filled again)
+    const int end = use;
+    for (use = end - S::kBoxWarps; use >= 0 && use > end - S::kSlots; use -= S::kBoxWarps)
+        mbar_wait_bounded(smem_u32(&sh.full[use % S::kSlots]), (use / S::kSlots) & 1, 1u << 30);
 }
 
 // Queries where the keys and values are boxes: one warp.
@@ -334,7 +346,7 @@ template <typename S>
 __device__ void tc_query_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor cur, int n, int p) {
     for (int j = 0, seg = 0; j < n; ++seg) {
         const int nt = tc_part(cur, n - j);
-        if (seg > 0) tc_wait(smem_u32(&sh.q_empty), (seg - 1) & 1, &sh.fail);
+        if (seg > 0 && !tc_wait(smem_u32(&sh.q_empty), (seg - 1) & 1, &sh.fail, a.polls)) break;
         tc_copy_queries<S, 32>(a, sh, cur, p);
         asm volatile("cp.async.wait_all;" ::: "memory");
         fence_proxy_async_smem();
@@ -359,6 +371,7 @@ __device__ void tc_copy_role(const AttnArgs& a, TcShared<S>& sh, const AttnCurso
     const int c = p % kPieces, r0 = p / kPieces;
     const int mine = (lane / kOwn) * kStep + warp * kOwn + lane % kOwn;  // the row whose place this lane finds
     const bool col = c * 8 < kv.dim;
+    const int withhold = blockIdx.x == 0 ? a.withhold : -1;
     TcUses<S> it(cur, n);
     for (int use = 0; use < 2 * n; ++use, it.next(a)) {
         if (it.u == 0) {
@@ -366,7 +379,8 @@ __device__ void tc_copy_role(const AttnArgs& a, TcShared<S>& sh, const AttnCurso
                 sh.wild[(it.seg + 8) & 15] = 0;
                 sh.hole[(it.seg + 8) & 15] = 0;
             }
-            if (it.seg > 0) tc_wait(smem_u32(&sh.q_empty), (it.seg - 1) & 1, &sh.fail);
+            const bool go_on = it.seg == 0 || tc_wait(smem_u32(&sh.q_empty), (it.seg - 1) & 1, &sh.fail, a.polls);
+            if (!__all_sync(0xffffffffu, go_on)) break;
             tc_copy_queries<S, 128>(a, sh, it.cur, p);
             tc_copies_arrive(smem_u32(&sh.q_full));
         }
@@ -383,8 +397,9 @@ __device__ void tc_copy_role(const AttnArgs& a, TcShared<S>& sh, const AttnCurso
                 sh.hole[it.seg & 15] = 1;
         }
         const int slot = use % S::kSlots;
-        if (use >= S::kSlots) tc_wait(smem_u32(&sh.empty[slot]), (use / S::kSlots - 1) & 1, &sh.fail);
-        __syncwarp();
+        const bool go_on =
+            use < S::kSlots || tc_wait(smem_u32(&sh.empty[slot]), (use / S::kSlots - 1) & 1, &sh.fail, a.polls);
+        if (!__all_sync(0xffffffffu, go_on) || use == withhold) break;
         const uint32_t dst = smem_u32(sh.slot[slot]);
         const T* pool = static_cast<const T*>(values ? kv.v : kv.k);
 #pragma unroll
@@ -408,11 +423,11 @@ __device__ void tc_show_role(const AttnArgs& a, TcShared<S>& sh, const AttnCurso
     TcUses<S> it(cur, n);
     for (int use = 0; use < 2 * n; ++use, it.next(a)) {
         if (it.u == 0) {
-            tc_wait(smem_u32(&sh.q_full), it.seg & 1, &sh.fail);
+            if (!tc_wait(smem_u32(&sh.q_full), it.seg & 1, &sh.fail, a.polls)) return;
             fence_proxy_async_smem();
             mbar_arrive(smem_u32(&sh.q_shown));
         }
-        tc_wait(smem_u32(&sh.full[use % S::kSlots]), (use / S::kSlots) & 1, &sh.fail);
+        if (!tc_wait(smem_u32(&sh.full[use % S::kSlots]), (use / S::kSlots) & 1, &sh.fail, a.polls)) return;
         fence_proxy_async_smem();
         mbar_arrive(smem_u32(&sh.shown[use % S::kSlots]));
     }
@@ -434,12 +449,19 @@ __device__ void tc_mma_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor cur, 
     constexpr uint32_t kScores = tc_idesc(S::KT, false), kOutputs = tc_idesc(S::DP, true);
     uint32_t p_seen = 0, turns = 0;
     int j0 = 0, seg = 0, use0 = 0;
+    bool fine = true;  // no wait ran out; the same in all lanes
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        fine = __all_sync(0xffffffffu, fine && tc_wait(smem_u32(bar), parity, &sh.fail, a.polls));
+    };
+    // A slot is waited for in the order of use: its filling before (kSlots uses earlier) was then waited for too, so that
+    // the parity tells the right one.  WIDE, a warp waits for every slot itself; else the other warp has waited for those
+    // between, and this one has to be in its turn.
     auto wait_slot = [&](int use) {
         const int slot = use % S::kSlots;
-        tc_wait(smem_u32(S::TMA ? &sh.full[slot] : &sh.shown[slot]), (use / S::kSlots) & 1, &sh.fail);
+        wait(S::TMA ? &sh.full[slot] : &sh.shown[slot], (use / S::kSlots) & 1);
         return slot;
     };
-    while (j0 < n) {
+    while (fine && j0 < n) {
         const int nt = tc_part(cur, n - j0);
         const int items = nt * S::kTiles;
         const uint64_t qd = tc_desc_rows(smem_u32(sh.q) + (S::WIDE ? x * S::kSlot : 0));
@@ -451,10 +473,10 @@ __device__ void tc_mma_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor cur, 
                 tc_mma_ss(ts, qd + off, kd + off, kScores, kk > 0, lead);
             }
         };
-        tc_wait(smem_u32(&sh.q_shown), seg & 1, &sh.fail);
+        wait(&sh.q_shown, seg & 1);  // (both warps are through with the part before)
         if (x < items) {
             const int slot = wait_slot(use0 + S::keys_at(S::WIDE ? 0 : x, nt));
-            __syncwarp();
+            if (!fine) break;
             tc_after_sync();
             scores(slot);
             tc_commit(smem_u32(&sh.s_full[x]), lead);
@@ -463,15 +485,20 @@ __device__ void tc_mma_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor cur, 
         for (int i = x; i < items; i += 2) {
             const int t = S::WIDE ? i >> 1 : i;
             const bool more = i + 2 < items;
-            const int v_slot = wait_slot(use0 + S::values_at(t, nt));
-            const int k_slot = more ? wait_slot(use0 + S::keys_at(t + (S::WIDE ? 1 : 2), nt)) : 0;
-            tc_wait(smem_u32(&sh.p_ready[x]), p_seen & 1, &sh.fail);
+            int v_slot = 0, k_slot = 0;
+            auto wait_slots = [&] {
+                v_slot = wait_slot(use0 + S::values_at(t, nt));
+                if (more) k_slot = wait_slot(use0 + S::keys_at(t + S::kLead, nt));
+            };
+            if (S::WIDE) wait_slots();
+            wait(&sh.p_ready[x], p_seen & 1);
             ++p_seen;
             if (i > 0) {
-                tc_wait(smem_u32(&sh.turn[x]), turns & 1, &sh.fail);
+                wait(&sh.turn[x], turns & 1);
                 ++turns;
             }
-            __syncwarp();
+            if (!S::WIDE) wait_slots();
+            if (!fine) break;
             tc_after_sync();
             const uint64_t vd = tc_desc_cols(smem_u32(sh.slot[v_slot]));
 #pragma unroll
@@ -534,9 +561,9 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
         float m_run = -INFINITY, l_run = 0.0f;
         for (int i = x; i < items; i += 2) {
             const int t = S::WIDE ? i >> 1 : i, t0 = (first_tile + t) * S::KT;
-            tc_wait(smem_u32(&sh.s_full[x]), s_seen & 1, &sh.fail);
+            const bool fine = tc_wait(smem_u32(&sh.s_full[x]), s_seen & 1, &sh.fail, a.polls);
             ++s_seen;
-            __syncwarp();
+            if (!__all_sync(0xffffffffu, fine)) break;
             tc_after_sync();
             if (warp_in) {
                 uint32_t s[4][32];
@@ -572,8 +599,9 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
                     top[0] = fminf(fminf(top[0], top[1]), fminf(top[2], top[3]));
                 }
                 top[0] *= scale;
-                // the running maximum moves only when a score passes it by 8 (weights stay below 2^8)
-                if (__any_sync(0xffffffffu, top[0] > m_run + 8.0f)) {
+                // the running maximum moves only when a score passes it by 8 (weights stay below 2^8); rows behind the
+                // last, whose queries are whatever shared memory held, have no say in it
+                if (__any_sync(0xffffffffu, grow < m_rows && top[0] > m_run + 8.0f)) {
                     const float m_new = fmaxf(m_run, top[0]);
                     const float keep = m_new == -INFINITY ? 1.0f : ex2(m_run - m_new);
                     m_run = m_new;
@@ -619,7 +647,8 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
                 // values of the pass's rows that are not finite are taken out of the product, where a weight of zero
                 // would not hide them; they are added to the rows that see them at the segment's end
                 const int slot = (use0 + S::values_at(t, nt)) % S::kSlots;
-                tc_wait(smem_u32(&sh.full[slot]), (use0 + S::values_at(t, nt)) / S::kSlots & 1, &sh.fail);
+                // (the filling before was used up: scores of this tile follow it)
+                tc_wait(smem_u32(&sh.full[slot]), (use0 + S::values_at(t, nt)) / S::kSlots & 1, &sh.fail, a.polls);
                 // (boxes bring the rest of the last block too, whatever it holds: zeros in its place)
                 const int lo_r = base > t0 ? base - t0 : 0, end_r = cur.len - t0 < S::KT ? cur.len - t0 : S::KT;
                 const int hi_r = S::TMA ? S::KT : end_r;
@@ -649,7 +678,7 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
         }
         // the segment's part ends
         if (items > x) {
-            tc_wait(smem_u32(&sh.o_done[x]), o_seen & 1, &sh.fail);
+            tc_wait(smem_u32(&sh.o_done[x]), o_seen & 1, &sh.fail, a.polls);
             ++o_seen;
         }
         __syncwarp();
@@ -724,11 +753,11 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
                                                                             pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
                         }
                     } else {
-                        float* acc = work.acc +
-                                     (static_cast<int64_t>(piece) * S::TM + (S::WIDE ? x * 128 : 0) + row) * S::DP + d0;
+                        float4* acc = work.acc + (static_cast<int64_t>(piece) * (S::DP / 4) + d0 / 4) * S::TM +
+                                      (S::WIDE ? x * 128 : 0) + row;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4*>(acc + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        for (int e = 0; e < 8; ++e)
+                            acc[e * S::TM] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                     }
                 }
             }
@@ -740,18 +769,18 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
             }
         }
         if (x == 0 && row == 0) {
-            if (whole) {
-                if (cur.s == 0 && a.row_status) a.row_status[cur.b] = status;
-            } else {
+            if (first_tile == 0 && cur.s == 0 && a.row_status) a.row_status[cur.b] = status;
+            if (!whole) {
                 work.status[piece] = status;
                 if (first_tile == 0) {
-                    AttnNote note;
-                    note.b = cur.b;
-                    note.s = cur.s;
-                    note.last = attn_owner(units, lo + j0 + cur.tiles - 1, used);
-                    note.pad = 0;
-                    work.notes[cta] = note;
+                    work.notes[cta].b = cur.b;
+                    work.notes[cta].s = cur.s;
+                    work.notes[cta].last = attn_owner(units, lo + j0 + cur.tiles - 1, used);
                 }
+            }
+            if (status & KV_TIMEOUT) {
+                work.notes[cta].failed = 1;
+                work.notes[cta].b1 = cur.b;
             }
         }
         if constexpr (!S::WIDE) {
@@ -773,12 +802,21 @@ __global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const
     extern __shared__ __align__(1024) unsigned char tc_smem[];
     TcShared<S>& sh = *reinterpret_cast<TcShared<S>*>(tc_smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if constexpr (S::TMA) {
+        if (tid < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(tid ? &maps.v : &maps.k) : "memory");
+    }
     int64_t units, lo, hi;
     int used;
     AttnCursor cur;
+    cur.b = 0;
     attn_cut<S::kThreads>(a, sh.cut, S::KT, blockIdx.x, gridDim.x, units, used, lo, hi, cur);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this grid's end
-    if (tid == 0) attn_work(a.workspace, gridDim.x, S::TM, S::DP).notes[blockIdx.x].b = -1;
+    if (tid == 0) {
+        AttnNote* note = attn_work(a.workspace, gridDim.x, S::TM, S::DP).notes + blockIdx.x;
+        note->b = -1;
+        note->failed = 0;
+        note->b0 = cur.b;
+    }
     if (static_cast<int>(blockIdx.x) >= used) return;
     const int n = static_cast<int>(hi - lo);
     if (tid == 0) {

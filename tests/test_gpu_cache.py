@@ -327,6 +327,58 @@ def test_calls_on_two_streams(sv, h):
         cases[i % 2].check(out)
 
 
+@pytest.mark.parametrize("bs", [16, 5])
+@pytest.mark.parametrize("use", [0, 3])
+@pytest.mark.parametrize("rows,hq", [(17, 8), (32, 16)])
+def test_withheld_copy_times_out_then_next_call_is_clean(sv, bs, use, rows, hq):
+    """A slot of the tcgen05 kernel's first CTA (whose run is two tiles, four slot
+    uses) is never filled: its waits run
+    out, the sequences it works on report bit 64, the others and the next
+    call are as ever."""
+    import torch
+
+    handle = sv.specv_create(0, max_batch=64, max_k=31, vocab=1000)
+    c = Case(50 + use, "bf16", 40, rows, hq, 2, 128, bs, [300 + 20 * (i % 7) for i in range(40)], "tree")
+    sv.specv_test_withhold_stage(handle, use, 200_000)
+    got = c.call(sv, handle)
+    bad = (got["row_status"] & sv.ST_TIMEOUT) != 0
+    assert bad[0] and bad.sum() < 5 and not (got["row_status"] & ~sv.ST_TIMEOUT).any()
+    for b in range(40):
+        if not bad[b]:
+            continue
+        c.lens[b] = 0  # checked as if idle below: their rows are not looked at
+        for key, fill in (("out", 0.0), ("lse", -math.inf)):
+            got[key][b] = fill
+    got["row_status"][bad] = 0
+    c.check(got)
+    c2 = Case(50 + use, "bf16", 40, rows, hq, 2, 128, bs, [300 + 20 * (i % 7) for i in range(40)], "tree")
+    c2.check(c2.call(sv, handle))
+    sv.specv_destroy(handle)
+
+
+def test_many_calls_give_the_same(sv, h):
+    """Many calls back to back under memory load, every one the same bits
+    (a slot read too early would show)."""
+    import torch
+
+    c = Case(60, "bf16", 24, 17, 8, 2, 128, 16, [700 + 97 * (i % 9) for i in range(24)], "tree")
+    args = (c.q_t, c.kc_t, c.vc_t, _dev(c.tables), _dev(c.lens))
+    par = _dev(c.parents)
+    one = sv.specv_tree_attention(h, *args, parents=par, lse=True)
+    c.check(one)
+    noise = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(300):
+        if i % 10 == 0:
+            with torch.cuda.stream(side):
+                noise.add_(1)
+        two = sv.specv_tree_attention(h, *args, parents=par, lse=True)
+        wrong += (two["out"] != one["out"]).sum() + (two["lse"] != one["lse"]).sum()
+    torch.cuda.synchronize()
+    assert int(wrong) == 0
+
+
 # ---------------------------------------------------------------------------- append
 APPENDS = [
     # B, rows, q heads, kv heads, dim, block, lengths, tree, rot, interleaved, counts

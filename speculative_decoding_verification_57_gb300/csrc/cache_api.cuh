@@ -222,15 +222,21 @@ specv_status specv_cache_append(specv_handle h, const specv_kv_cache* cache, con
     a.q_heads = q ? q_heads : 0;
     a.rot = rot_dim;
     a.interleaved = interleaved != 0;
-    a.rows = rows;
+    a.rows = FastDiv(static_cast<uint32_t>(rows));
+    const int vec = cache->dtype == SPECV_BF16 ? 8 : 4;
+    a.units = FastDiv(static_cast<uint32_t>(cache->head_dim / vec / 2));
     DeviceGuard g(h->device);
     if (!g.ok) return cuda_fail(cudaErrorInvalidDevice, "cudaSetDevice");
     const unsigned grid = static_cast<unsigned>(batch) * static_cast<unsigned>(rows);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (cache->dtype == SPECV_BF16)
-        cache_append_kernel<__nv_bfloat16><<<grid, kAppendThreads, 0, s>>>(a);
-    else
-        cache_append_kernel<float><<<grid, kAppendThreads, 0, s>>>(a);
+    // pieces of 16 bytes turn whole, apart or within, where rot_dim fills them
+    const int mode = rot_dim % (interleaved ? vec : 2 * vec) ? kValues : interleaved && rot_dim ? kNeighbours : kApart;
+    using B = __nv_bfloat16;
+    using Kernel = void (*)(AppendArgs);
+    static constexpr Kernel kernels[2][3] = {
+        {cache_append_kernel<float, kApart>, cache_append_kernel<float, kNeighbours>, cache_append_kernel<float, kValues>},
+        {cache_append_kernel<B, kApart>, cache_append_kernel<B, kNeighbours>, cache_append_kernel<B, kValues>}};
+    kernels[cache->dtype == SPECV_BF16][mode]<<<grid, kAppendThreads, 0, s>>>(a);
     return launched(h, "cache_append launch");
 }
 
@@ -311,13 +317,16 @@ specv_status specv_cache_compact(specv_handle h, const specv_kv_cache* cache, in
     c.M = M;
     c.layers = layers;
     c.vec_elems = vec;
-    c.vecs = cache->head_dim / vec;
     DeviceGuard g(h->device);
     if (!g.ok) return cuda_fail(cudaErrorInvalidDevice, "cudaSetDevice");
-    const int64_t pieces = static_cast<int64_t>(layers) * 2 * cache->kv_heads * c.vecs;
+    const int64_t per_head = cache->head_dim / vec, per_layer = 2 * cache->kv_heads * per_head;
+    const int64_t pieces = layers * per_layer;
     if (pieces > INT32_MAX / 2) return SPECV_ERR_INVALID_ARGUMENT;
+    c.per_head = FastDiv(static_cast<uint32_t>(per_head));
+    c.per_cache = FastDiv(static_cast<uint32_t>(per_layer / 2));
+    c.per_layer = FastDiv(static_cast<uint32_t>(per_layer));
     const int64_t want = (pieces + kCompactThreads - 1) / kCompactThreads;
-    const dim3 grid(static_cast<unsigned>(batch), static_cast<unsigned>(want < 1 ? 1 : want > 64 ? 64 : want), 1);
+    const dim3 grid(static_cast<unsigned>(batch), static_cast<unsigned>(want < 1 ? 1 : want > kCompactCtas ? kCompactCtas : want), 1);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (cache->dtype == SPECV_BF16)
         cache_compact_kernel<__nv_bfloat16><<<grid, kCompactThreads, 0, s>>>(c);

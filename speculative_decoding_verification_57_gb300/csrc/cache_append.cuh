@@ -2,16 +2,28 @@
 // and keys turned by their rotary positions on the way.
 //
 // A token is a CTA: its position's angles are formed once in shared memory
-// and serve every head.  Angles are formed in float64 (position * inv_freq
-// passes 2^24 for far positions, where fp32 would lose the fraction of a
-// turn), brought into [-pi, pi] there, and the sine and cosine are taken in
-// fp32.
+// and serve every head.  Bound by memory for prompts and by a chain of three
+// loads (length, block, row) for a few tokens; so a thread asks for its rows
+// of q, k and v, whose places depend on nothing, before it looks at anything
+// else, and what it gets is 16 bytes each: pieces of a head that turn
+// together (j and j + rot / 2, or two neighbours).
+// MEASURED
+//
+// Angles are formed in float64 (position * inv_freq passes 2^24 for far
+// positions, where fp32 would lose the fraction of a turn), brought into
+// [-pi, pi] there, and the sine and cosine are taken in fp32.
 #pragma once
 #include "kv_cache.cuh"
+#include "ptx.cuh"
 
 namespace specv {
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 192;
+constexpr int kAppendHeads = 2;  // whose pieces a thread has in flight
+
+// How the pairs lie: pieces apart, neighbours in a piece, or (where rot does
+// not fill pieces) by values.
+enum AppendMode { kApart = 0, kNeighbours = 1, kValues = 2 };
 
 struct AppendArgs {
     KvView kv;
@@ -23,7 +35,8 @@ struct AppendArgs {
     const int32_t* row_counts;
     int32_t* row_status;
     int q_heads, rot, interleaved;
-    int rows;
+    FastDiv rows;   // of a sequence
+    FastDiv units;  // pairs of pieces of a head
 };
 
 // cos and sin of the angle pos * f.
@@ -37,77 +50,175 @@ __device__ __forceinline__ float2 append_turn(int pos, float f) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendArgs a) {
-    __shared__ float2 turn[128];
-    __shared__ int s_status;
-    const int b = blockIdx.x / a.rows, r = blockIdx.x % a.rows;
+__device__ __forceinline__ void append_pair(T& x0, T& x1, float c, float s) {
+    const float a = KvType<T>::load(x0), b = KvType<T>::load(x1);
+    x0 = KvType<T>::store(a * c - b * s);
+    x1 = KvType<T>::store(a * s + b * c);
+}
+
+// Pairs x[e], y[e] of two pieces, two at a time in packed arithmetic.
+__device__ __forceinline__ void append_apart(f2& x, f2& y, f2 c, f2 s) {
+    const f2 a = x, b = y;
+    x = sub2(mul2(a, c), mul2(b, s));
+    y = fma2(a, s, mul2(b, c));
+}
+__device__ __forceinline__ void append_pieces(KvVec<float>& x, KvVec<float>& y, const float* c, const float* s) {
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+        f2 a = pack2(x.x[e], x.x[e + 1]), b = pack2(y.x[e], y.x[e + 1]);
+        append_apart(a, b, pack2(c[e], c[e + 1]), pack2(s[e], s[e + 1]));
+        unpack2(a, x.x[e], x.x[e + 1]);
+        unpack2(b, y.x[e], y.x[e + 1]);
+    }
+}
+__device__ __forceinline__ void append_pieces(KvVec<__nv_bfloat16>& x, KvVec<__nv_bfloat16>& y, const float* c,
+                                              const float* s) {
+    uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
+    uint32_t* yw = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        f2 a = pack2(bf16_lo(xw[e]), bf16_hi(xw[e])), b = pack2(bf16_lo(yw[e]), bf16_hi(yw[e]));
+        append_apart(a, b, pack2(c[2 * e], c[2 * e + 1]), pack2(s[2 * e], s[2 * e + 1]));
+        float lo, hi;
+        unpack2(a, lo, hi);
+        xw[e] = kv_pack_bf16(lo, hi);
+        unpack2(b, lo, hi);
+        yw[e] = kv_pack_bf16(lo, hi);
+    }
+}
+
+// A thread has the same two pieces (a unit) of every hstep-th head, so that it
+// keeps the angles that turn them.  Heads are counted through q, k and v.
+template <typename T, int MODE>
+__global__ void __launch_bounds__(kAppendThreads, 5) cache_append_kernel(const AppendArgs a) {
+    constexpr int kVec = KvType<T>::kVec;
+    using Vec = KvVec<T>;
+    __shared__ __align__(16) float s_cos[128], s_sin[128];
+    const int rows = static_cast<int>(a.rows.d);
+    const int b = a.rows.div(blockIdx.x), r = blockIdx.x - b * rows;
     const int tid = threadIdx.x;
     const KvView& kv = a.kv;
+    const int turning = a.q_heads + kv.heads, heads = turning + kv.heads;
+    const int per = static_cast<int>(a.units.d), hstep = kAppendThreads / per;
+    const int h0 = a.units.div(tid), u = tid - h0 * per;
+    const int half = a.rot / 2;
+    // the unit's pieces of a head that turns, and of a value's
+    const bool apart = MODE == kApart && u < half / kVec;
+    const int x0 = apart ? u * kVec : MODE == kApart ? a.rot + 2 * (u * kVec - half) : 2 * u * kVec;
+    const int y0 = apart ? x0 + half : x0 + kVec;
+    // the token's queries, keys and values, at the first head as heads are counted
+    const int64_t token = blockIdx.x;
+    const T* q = static_cast<const T*>(a.q) + token * a.q_stride;
+    const T* k = static_cast<const T*>(a.k) + token * a.k_stride - a.q_heads * kv.dim;
+    const T* v = static_cast<const T*>(a.v) + token * a.v_stride - turning * kv.dim;
+    T* q_out = static_cast<T*>(a.q_out) + token * a.q_heads * kv.dim;
+    Vec x[kAppendHeads], y[kAppendHeads];
+    auto load = [&](int h, int j) {
+        if (h >= heads) return;
+        const T* p = (h < a.q_heads ? q : h < turning ? k : v) + h * kv.dim;
+        x[j] = *reinterpret_cast<const Vec*>(p + (h < turning ? x0 : 2 * u * kVec));
+        y[j] = *reinterpret_cast<const Vec*>(p + (h < turning ? y0 : 2 * u * kVec + kVec));
+    };
+    auto load_all = [&](int h1) {
+        if (h0 >= hstep) return;
+#pragma unroll
+        for (int j = 0; j < kAppendHeads; ++j) load(h1 + j * hstep, j);
+    };
+    if (MODE != kValues) load_all(h0);
+    // the token's sequence: its length, its tree, the blocks it writes to.  Every token of a sequence looks at all of
+    // them, so that of a refused sequence nothing is written
     const int len = kv.lens[b];
-    const int count = a.row_counts ? a.row_counts[b] : (len == 0 ? 0 : a.rows);
-    int status = 0;
-    if (count < 0 || count > a.rows || len < 0 || (count > 0 && (len < count || !kv.fits(len)))) status = KV_LENGTH;
-    const int base = len - count;
-    // every token of a sequence looks at all its blocks: a refused sequence writes nothing
-    if (tid == 0) s_status = 0;
-    __syncthreads();
-    int depth = r;
+    const int count = a.row_counts ? a.row_counts[b] : (len == 0 ? 0 : rows);
+    const int base = len - count, slot = base + r;
+    const int32_t* table = kv.tables + static_cast<int64_t>(b) * kv.max_blocks;
+    int status = 0, blk = 0;
+    if (count < 0 || count > rows || len < 0 || (count > 0 && (len < count || !kv.fits(len)))) status = KV_LENGTH;
     if (status == 0 && count > 0) {
-        if (a.parents && tid < 32) {
+        bool parent_bad = false, block_bad = false;
+        int depth = r;
+        if (a.parents) {
             uint32_t anc;
             int d;
-            const bool ok = warp_tree(a.parents + static_cast<int64_t>(b) * (a.rows - 1), count, tid, anc, d);
-            if (!ok && tid == 0) atomicOr(&s_status, KV_PARENT);
-            if (tid == r) turn[0].x = __int_as_float(d);
+            parent_bad = !warp_tree(a.parents + static_cast<int64_t>(b) * (rows - 1), count, tid & 31, anc, d);
+            depth = __shfl_sync(0xffffffffu, d, r);
         }
-        const int first = kv.block.div(base), last = kv.block.div(len - 1);
-        for (int i = first + tid; i <= last; i += kAppendThreads)
-            if (!kv.valid(kv.tables[static_cast<int64_t>(b) * kv.max_blocks + i])) atomicOr(&s_status, KV_BLOCK);
-        __syncthreads();
-        status = s_status;
-        if (a.parents) depth = __float_as_int(turn[0].x);
-        __syncthreads();
+        if (r < count) blk = table[kv.block.div(slot)];
+        for (int i = kv.block.div(base) + tid, last = kv.block.div(len - 1); i <= last; i += kAppendThreads)
+            block_bad |= !kv.valid(table[i]);
+        for (int j = tid; j < half; j += kAppendThreads) {
+            const float2 cs = append_turn(base + depth, a.inv_freq[j]);
+            s_cos[j] = cs.x;
+            s_sin[j] = cs.y;
+        }
+        if (__syncthreads_or(parent_bad || block_bad))
+            status = (__syncthreads_or(parent_bad) ? KV_PARENT : 0) | (__syncthreads_or(block_bad) ? KV_BLOCK : 0);
     }
     if (r == 0 && tid == 0 && a.row_status) a.row_status[b] = status;
-    const int64_t token = static_cast<int64_t>(b) * a.rows + r;
-    const T* q = static_cast<const T*>(a.q) + token * a.q_stride;
-    T* q_out = static_cast<T*>(a.q_out) + token * a.q_heads * kv.dim;
     if (status != 0 || r >= count) {
         if (a.q)
-            for (int i = tid; i < a.q_heads * kv.dim; i += kAppendThreads) q_out[i] = KvType<T>::store(0.0f);
+            for (int i = tid; i < a.q_heads * per * 2; i += kAppendThreads)
+                reinterpret_cast<uint4*>(q_out)[i] = make_uint4(0, 0, 0, 0);
         return;
     }
-    const int half = a.rot / 2;
-    for (int j = tid; j < half; j += kAppendThreads) turn[j] = append_turn(base + depth, a.inv_freq[j]);
-    __syncthreads();
-    const int slot = base + r;
-    const int lb = kv.block.div(slot), in = slot - lb * kv.block_size();
-    const int blk = kv.tables[static_cast<int64_t>(b) * kv.max_blocks + lb];
-    const T* k = static_cast<const T*>(a.k) + token * a.k_stride;
-    const T* v = static_cast<const T*>(a.v) + token * a.v_stride;
-    const int q_n = a.q ? a.q_heads : 0;
-    const int pairs = kv.dim / 2;  // of a head: half rotated pairs, then the rest by twos
-    for (int i = tid; i < (q_n + kv.heads) * pairs; i += kAppendThreads) {
-        int h = i / pairs, j = i - h * pairs;
-        const bool is_q = h < q_n;
-        if (!is_q) h -= q_n;
-        const T* x = is_q ? q + h * kv.dim : k + h * kv.dim;
-        T* y = is_q ? q_out + h * kv.dim : static_cast<T*>(kv.k) + kv.at(blk, h, in);
-        const int i0 = j >= half || a.interleaved ? 2 * j : j;
-        const int i1 = j >= half || a.interleaved ? 2 * j + 1 : j + half;
-        if (j >= half) {
-            y[i0] = x[i0];
-            y[i1] = x[i1];
-        } else {
-            const float x0 = KvType<T>::load(x[i0]), x1 = KvType<T>::load(x[i1]);
-            const float2 cs = turn[j];
-            y[i0] = KvType<T>::store(x0 * cs.x - x1 * cs.y);
-            y[i1] = KvType<T>::store(x0 * cs.y + x1 * cs.x);
+    const int64_t at = kv.at(blk, 0, slot - kv.block.div(slot) * kv.block_size());
+    const int64_t next = static_cast<int64_t>(kv.block_size()) * kv.dim;  // from a head of a block to the next
+    T* k_out = static_cast<T*>(kv.k) + at;
+    T* v_out = static_cast<T*>(kv.v) + at;
+    if constexpr (MODE == kValues) {
+        const int pairs = kv.dim / 2;  // of a head: the turning ones, then the rest by twos
+        for (int i = tid; i < heads * pairs; i += kAppendThreads) {
+            const int h = i / pairs, j = i - h * pairs;
+            const T* p = (h < a.q_heads ? q : h < turning ? k : v) + h * kv.dim;
+            T* to = h < a.q_heads ? q_out + h * kv.dim
+                    : h < turning ? k_out + (h - a.q_heads) * next
+                                  : v_out + (h - turning) * next;
+            const bool turns = h < turning && j < half, far = turns && !a.interleaved;
+            const int d0 = far ? j : 2 * j, d1 = far ? j + half : 2 * j + 1;
+            T e0 = p[d0], e1 = p[d1];
+            if (turns) append_pair(e0, e1, s_cos[j], s_sin[j]);
+            to[d0] = e0;
+            to[d1] = e1;
         }
-    }
-    for (int i = tid; i < kv.heads * kv.dim; i += kAppendThreads) {
-        const int h = i / kv.dim, d = i - h * kv.dim;
-        static_cast<T*>(kv.v)[kv.at(blk, h, in) + d] = v[i];
+    } else {
+        if (h0 >= hstep) return;
+        // angles of the unit: of pairs x[e], y[e], or of the neighbours in x and then in y
+        const int first = MODE == kApart ? x0 : x0 / 2;
+        const bool turns = MODE == kApart ? apart : x0 < a.rot;
+        const bool both = MODE == kApart || y0 < a.rot;  // (neighbours: whether the second piece turns too)
+        float c[kVec], s[kVec];
+        if (turns) {
+#pragma unroll
+            for (int e = 0; e < kVec; e += 4) {
+                *reinterpret_cast<float4*>(c + e) = *reinterpret_cast<const float4*>(s_cos + first + e);
+                *reinterpret_cast<float4*>(s + e) = *reinterpret_cast<const float4*>(s_sin + first + e);
+            }
+        }
+        for (int h1 = h0; h1 < heads; h1 += kAppendHeads * hstep) {
+            if (h1 != h0) load_all(h1);
+#pragma unroll
+            for (int j = 0; j < kAppendHeads; ++j) {
+                const int h = h1 + j * hstep;
+                if (h >= heads) continue;
+                if (h < turning && turns) {
+                    if constexpr (MODE == kApart) {
+                        append_pieces(x[j], y[j], c, s);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < kVec; e += 2) append_pair(x[j].x[e], x[j].x[e + 1], c[e / 2], s[e / 2]);
+                        if (both) {
+#pragma unroll
+                            for (int e = 0; e < kVec; e += 2)
+                                append_pair(y[j].x[e], y[j].x[e + 1], c[(kVec + e) / 2], s[(kVec + e) / 2]);
+                        }
+                    }
+                }
+                T* to = h < a.q_heads ? q_out + h * kv.dim
+                        : h < turning ? k_out + (h - a.q_heads) * next
+                                      : v_out + (h - turning) * next;
+                *reinterpret_cast<Vec*>(to + (h < turning ? x0 : 2 * u * kVec)) = x[j];
+                *reinterpret_cast<Vec*>(to + (h < turning ? y0 : 2 * u * kVec + kVec)) = y[j];
+            }
+        }
     }
 }
 

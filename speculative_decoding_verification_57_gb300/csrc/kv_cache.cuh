@@ -91,6 +91,12 @@ struct KvType<__nv_bfloat16> {
     static __device__ __forceinline__ __nv_bfloat16 store(float x) { return __float2bfloat16_rn(x); }
 };
 
+__device__ __forceinline__ uint32_t kv_pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // 16 bytes of elements.
 template <typename T>
 struct alignas(16) KvVec {

@@ -235,17 +235,11 @@ __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 __device__ __forceinline__ void attn_store4(float* p, float a, float b, float c, float d) {
     *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
 }
 __device__ __forceinline__ void attn_store4(__nv_bfloat16* p, float a, float b, float c, float d) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(a, b), pack_bf16(c, d));
+    *reinterpret_cast<uint2*>(p) = make_uint2(kv_pack_bf16(a, b), kv_pack_bf16(c, d));
 }
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
@@ -575,10 +569,10 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
             uint32_t pf[RG][4];
 #pragma unroll
             for (int g = 0; g < RG; ++g) {
-                pf[g][0] = pack_bf16(s[g][0][0], s[g][0][1]);
-                pf[g][1] = pack_bf16(s[g][0][2], s[g][0][3]);
-                pf[g][2] = pack_bf16(s[g][ST - 1][0], s[g][ST - 1][1]);
-                pf[g][3] = pack_bf16(s[g][ST - 1][2], s[g][ST - 1][3]);
+                pf[g][0] = kv_pack_bf16(s[g][0][0], s[g][0][1]);
+                pf[g][1] = kv_pack_bf16(s[g][0][2], s[g][0][3]);
+                pf[g][2] = kv_pack_bf16(s[g][ST - 1][0], s[g][ST - 1][1]);
+                pf[g][3] = kv_pack_bf16(s[g][ST - 1][2], s[g][ST - 1][3]);
             }
 #pragma unroll
             for (int t = 0; t < NT; t += 2) {

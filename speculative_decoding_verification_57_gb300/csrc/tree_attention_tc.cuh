@@ -634,7 +634,7 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
                         w0 = ex2(w0);
                         w1 = ex2(w1);
                         sum[e & 1] = add2(sum[e & 1], pack2(w0, w1));
-                        w[e] = pack_bf16(w0, w1);
+                        w[e] = kv_pack_bf16(w0, w1);
                     }
                     tc_st32(ts + half * 32, w);
                 }
@@ -749,8 +749,8 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
                             float y[8];
 #pragma unroll
                             for (int f = 0; f < 8; ++f) y[f] = zero ? 0.0f : o[e + f] * inv;
-                            *reinterpret_cast<uint4*>(out + e) = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]),
-                                                                            pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+                            *reinterpret_cast<uint4*>(out + e) = make_uint4(kv_pack_bf16(y[0], y[1]), kv_pack_bf16(y[2], y[3]),
+                                                                            kv_pack_bf16(y[4], y[5]), kv_pack_bf16(y[6], y[7]));
                         }
                     } else {
                         float4* acc = work.acc + (static_cast<int64_t>(piece) * (S::DP / 4) + d0 / 4) * S::TM +

@@ -54,22 +54,32 @@ specv_status launched(specv_ctx* h, const char* what) {
     return SPECV_OK;
 }
 
-// Tree attention of one shape: its kernel and, behind it, the join.  The
-// join's CTAs may be placed while the kernel before still runs (they wait for
-// its end), so that they do not add a launch to the call.
-template <typename S>
-cudaError_t launch_join(const AttnArgs& a, int ctas, cudaStream_t stream) {
+// Tree attention of one shape: its kernel and, behind it, the join.  The CTAs
+// of both may be placed while the kernel before still runs (they wait for its
+// end on the device), so that launches overlap what runs before them.
+template <typename... Params>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t stream,
+                         const Params&... params) {
     cudaLaunchConfig_t cfg = {};
-    const int pieces = static_cast<int>(a.filled.d) * (a.kv.dim / 4);  // of four columns
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>((pieces + kJoinThreads - 1) / kJoinThreads), 1);
-    cfg.blockDim = dim3(kJoinThreads, 1, 1);
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_attention_join<S>, a, ctas);
+    return cudaLaunchKernelEx(&cfg, kernel, params...);
+}
+
+template <typename S>
+cudaError_t launch_join(const AttnArgs& a, int ctas, cudaStream_t stream) {
+    const int pieces = static_cast<int>(a.filled.d) * (a.kv.dim / 4);  // of four columns
+    return launch_early(tree_attention_join<S>,
+                        dim3(static_cast<unsigned>(ctas),
+                             static_cast<unsigned>((pieces + kJoinThreads - 1) / kJoinThreads)),
+                        kJoinThreads, 0, stream, a, ctas);
 }
 
 // Lets a kernel have `bytes` of dynamic shared memory; once a device (a bit
@@ -90,14 +100,14 @@ cudaError_t launch_attention(const AttnArgs& a, int ctas, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(done, reinterpret_cast<const void*>(tree_attention_kernel<S>), S::kSmem);
     if (e != cudaSuccess) return e;
-    tree_attention_kernel<S><<<ctas, S::kThreads, S::kSmem, stream>>>(a);
-    e = cudaGetLastError();
+    e = launch_early(tree_attention_kernel<S>, dim3(static_cast<unsigned>(ctas)), S::kThreads, S::kSmem, stream, a);
     return e != cudaSuccess ? e : launch_join<S>(a, ctas, stream);
 }
 
 // Boxes for the cache's blocks, if they fill tiles of 128 rows evenly; false:
 // they do not, or the pool is outside what a tensor map can say.
-bool make_maps(const KvView& kv, TcMaps& maps) {
+bool make_maps(const AttnArgs& a, TcMaps& maps) {
+    const KvView& kv = a.kv;
     const int bs = static_cast<int>(kv.block.d);
     if (bs % 8 || (128 % bs && bs % 128) || kv.blocks < 1 || kv.block_stride >= (1ll << 38)) return false;
     static const auto encode = [] {
@@ -122,6 +132,20 @@ bool make_maps(const KvView& kv, TcMaps& maps) {
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return false;
+    // the queries, a row tile a box and panel, where groups of heads fill row tiles
+    const int group = static_cast<int>(a.group.d);
+    maps.q_rows = 0;
+    if (128 % group == 0 && a.q_stride > 0 && a.q_stride * a.rows < (1ll << 38)) {
+        const cuuint64_t q_dims[4] = {dims[0], static_cast<cuuint64_t>(a.q_heads), static_cast<cuuint64_t>(a.rows),
+                                      static_cast<cuuint64_t>(a.batch)};
+        const cuuint64_t q_strides[3] = {dims[0] * 2, static_cast<cuuint64_t>(a.q_stride) * 2,
+                                         static_cast<cuuint64_t>(a.q_stride) * a.rows * 2};
+        const cuuint32_t q_box[4] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(128 / group), 1};
+        if (encode(&maps.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(a.q), q_dims, q_strides, q_box, ones,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS)
+            maps.q_rows = 128 / group;
+    }
     return true;
 }
 
@@ -132,15 +156,14 @@ cudaError_t launch_tc(const AttnArgs& a, const TcMaps& maps, int ctas, cudaStrea
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(done, reinterpret_cast<const void*>(tree_attention_tc_kernel<S>), kBytes);
     if (e != cudaSuccess) return e;
-    tree_attention_tc_kernel<S><<<ctas, S::kThreads, kBytes, stream>>>(a, maps);
-    e = cudaGetLastError();
+    e = launch_early(tree_attention_tc_kernel<S>, dim3(static_cast<unsigned>(ctas)), S::kThreads, kBytes, stream, a, maps);
     return e != cudaSuccess ? e : launch_join<S>(a, ctas, stream);
 }
 
 template <int DP, bool WIDE>
 cudaError_t launch_attention_tc(const AttnArgs& a, int ctas, cudaStream_t stream) {
     TcMaps maps = {};
-    if (make_maps(a.kv, maps)) return launch_tc<TcShape<DP, WIDE, true>>(a, maps, ctas, stream);
+    if (make_maps(a, maps)) return launch_tc<TcShape<DP, WIDE, true>>(a, maps, ctas, stream);
     return launch_tc<TcShape<DP, WIDE, false>>(a, maps, ctas, stream);
 }
 

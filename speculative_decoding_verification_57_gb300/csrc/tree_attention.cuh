@@ -310,6 +310,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
     int64_t units, lo, hi;
     int used;
     AttnCursor cur, ahead, ids;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // what the kernels before wrote
     attn_cut<S::kThreads>(a, s_cut, KT, cta, ctas, units, used, lo, hi, cur);
     if (tid == 0) {
         s_wild[0] = s_wild[1] = 0;
@@ -321,31 +322,32 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
     const int n = static_cast<int>(hi - lo);
     ids = ahead = cur;
 
-    // block numbers of tile `i` of the run, whose cursor `ids` is: into a register ...
-    int64_t my_row = -1;
-    bool my_hole = false;
+    // block number of this thread's position in tile `i` of the run, whose cursor `ids` is: into a register ...
+    struct Place {
+        int blk, in, h;  // in: position in the block, < 0 for none
+    };
     int ids_i = 0;
     auto fetch_row = [&]() {
-        my_row = -1;
-        my_hole = false;
+        Place p = {0, -1, 0};
         if (ids_i < n) {
             const int t = ids.tile * KT + tid;
             if (tid < KT && t < ids.len) {
                 const int lb = kv.block.div(t);
-                const int blk = __ldg(kv.tables + static_cast<int64_t>(ids.b) * kv.max_blocks + lb);
-                my_hole = !kv.valid(blk);
-                const int h = ids.s / a.row_tiles;
-                if (!my_hole) my_row = kv.at(blk, h, t - lb * kv.block_size());
+                p.blk = __ldg(kv.tables + static_cast<int64_t>(ids.b) * kv.max_blocks + lb);
+                p.in = t - lb * kv.block_size();
+                p.h = ids.s / a.row_tiles;
             }
             ids.next(a, KT);
         }
         ++ids_i;
+        return p;
     };
-    // ... and from there to shared memory, for the copies of tile i
-    auto post_row = [&](int i) {
+    // ... and from there its place to shared memory, for the copies of tile i
+    auto post_row = [&](int i, const Place& p) {
         if (tid < KT) {
-            s_row[i & 1][tid] = my_row;
-            const bool any = __any_sync(0xffffffffu, my_hole);
+            const bool valid = p.in >= 0 && kv.valid(p.blk);
+            s_row[i & 1][tid] = valid ? kv.at(p.blk, p.h, p.in) : -1;
+            const bool any = __any_sync(0xffffffffu, p.in >= 0 && !valid);
             if (lane == 0) s_hole[i & 3][warp] = any;
         }
     };
@@ -391,13 +393,16 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
     };
 
     // fill the pipeline
+    Place places[kAhead + 1];
+#pragma unroll
+    for (int i = 0; i <= kAhead; ++i) places[i] = fetch_row();
+#pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-        fetch_row();
-        post_row(i);
+        post_row(i, places[i]);
         __syncthreads();
         copy_tile(i);
     }
-    fetch_row();
+    Place place = places[kAhead];
 
     float o[RG][NT][4];
     float m_run[RG][2], l_run[RG][2];
@@ -406,8 +411,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
     int seg = 0, status = 0, first_tile = 0;
 
     for (int i = 0; i < n; ++i) {
-        post_row(i + kAhead);
-        fetch_row();
+        post_row(i + kAhead, place);
+        place = fetch_row();
         cp_wait<kAhead - 1>();
         __syncthreads();
         copy_tile(i + kAhead);

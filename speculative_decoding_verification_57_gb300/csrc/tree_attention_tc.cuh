@@ -165,10 +165,12 @@ struct TcShape {
 };
 
 // Tensor maps of the two pools ([blocks, heads, block_size, head_dim], boxes
-// of `rows` rows of 64 columns), where boxes are used.
+// of `rows` rows of 64 columns), where boxes are used, and of the queries
+// ([batch, rows, heads, head_dim], boxes of a group of heads of q_rows rows,
+// 128 rows of a row tile) where groups fill row tiles (q_rows 0: they do not).
 struct TcMaps {
-    CUtensorMap k, v;
-    int rows;
+    CUtensorMap k, v, q;
+    int rows, q_rows;
 };
 
 template <typename S>
@@ -271,7 +273,8 @@ __device__ __forceinline__ void tc_copy_queries(const AttnArgs& a, TcShared<S>& 
 }
 
 // Boxes (TMA): kBoxWarps warps, a slot each in turn (a box takes a warp some 90
-// cycles to issue, and a slot is up to 32 of them).  Lane l brings a panel of
+// cycles to issue, and a slot is up to 32 of them; sharing each slot's boxes
+// instead was slower, 64 trees of 17 rows over 4096 positions 173 us for 160).  Lane l brings a panel of
 // one of the tile's blocks; its block number is read a slot ahead.  A block
 // that is outside the pool or past the sequence's end is asked for at block
 // number `blocks`, which reads as zeros.
@@ -341,20 +344,40 @@ __device__ void tc_box_role(const AttnArgs& a, const TcMaps& maps, TcShared<S>& 
         mbar_wait_bounded(smem_u32(&sh.full[use % S::kSlots]), (use / S::kSlots) & 1, 1u << 30);
 }
 
-// Queries where the keys and values are boxes: one warp.
+// Queries where the keys and values are boxes: one warp, by boxes of its own
+// or, where groups of heads do not fill row tiles, by 16-byte copies.
 template <typename S>
-__device__ void tc_query_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor cur, int n, int p) {
+__device__ void tc_query_role(const AttnArgs& a, const TcMaps& maps, TcShared<S>& sh, AttnCursor cur, int n, int p) {
+    const uint32_t bar = smem_u32(&sh.q_shown);
+    int sent = -1;
     for (int j = 0, seg = 0; j < n; ++seg) {
         const int nt = tc_part(cur, n - j);
-        if (seg > 0 && !tc_wait(smem_u32(&sh.q_empty), (seg - 1) & 1, &sh.fail, a.polls)) break;
-        tc_copy_queries<S, 32>(a, sh, cur, p);
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_proxy_async_smem();
-        mbar_arrive(smem_u32(&sh.q_shown));
+        const bool go_on = seg == 0 || tc_wait(smem_u32(&sh.q_empty), (seg - 1) & 1, &sh.fail, a.polls);
+        if (!__all_sync(0xffffffffu, go_on)) break;
+        if (maps.q_rows) {
+            // box p: panel p % kPanels of row tile p / kPanels; tiles behind the last row are left out
+            const int h = cur.s / a.row_tiles, rt = cur.s - h * a.row_tiles;
+            const int tile = p / S::kPanels, panel = p % S::kPanels;
+            const int r = (rt * S::kTiles + tile) * maps.q_rows;
+            const bool mine = tile < S::kTiles && r < a.rows;
+            const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, mine));
+            if (p == 0) mbar_arrive_expect_tx(bar, boxes * S::kPanel);
+            __syncwarp();
+            if (mine)
+                tc_box(smem_u32(sh.q) + tile * S::kSlot + panel * S::kPanel, &maps.q, panel * 64,
+                       h * static_cast<int>(a.group.d), r, cur.b, bar);
+        } else {
+            tc_copy_queries<S, 32>(a, sh, cur, p);
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_proxy_async_smem();
+            mbar_arrive(bar);
+        }
         j += nt;
         cur.tile += nt - 1;
         cur.next(a, S::KT);
+        sent = seg;
     }
+    if (maps.q_rows && sent >= 0) mbar_wait_bounded(bar, sent & 1, 1u << 30);  // no box is in flight when the CTA ends
 }
 
 // 16-byte copies: four warps.  A warp copies 32 rows of every tile; lane l
@@ -539,6 +562,11 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
     const float hidden = scale < 0.0f ? INFINITY : -INFINITY;
     uint32_t s_seen = 0, o_seen = 0;
     int j0 = 0, seg = 0, use0 = 0;
+    auto parent_of = [&](int b) {
+        return a.parents && lane > 0 && lane < a.rows ? a.parents[static_cast<int64_t>(b) * (a.rows - 1) + lane - 1]
+                                                      : lane - 2;
+    };
+    int next_parent = parent_of(cur.b);
     while (j0 < n) {
         const int nt = tc_part(cur, n - j0);
         const int items = nt * S::kTiles;
@@ -548,9 +576,12 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
         const bool warp_in = grow - lane < m_rows;  // the warp has rows
         const int r = a.group.div(grow), gq = grow - r * static_cast<int>(a.group.d);
         const int base = cur.len - a.rows;
-        int parent = lane - 2;
-        if (a.parents && lane > 0 && lane < a.rows)
-            parent = a.parents[static_cast<int64_t>(cur.b) * (a.rows - 1) + lane - 1];
+        // the next part's sequence is read while this one is worked on
+        AttnCursor ahead = cur;
+        ahead.tile += nt - 1;
+        if (j0 + nt < n) ahead.next(a, S::KT);
+        const int parent = next_parent;
+        next_parent = parent_of(ahead.b);
         uint32_t line = 0;
         bool tree_ok = true;
         if ((first_tile + nt) * S::KT > base) {
@@ -651,7 +682,11 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
                 tc_wait(smem_u32(&sh.full[slot]), (use0 + S::values_at(t, nt)) / S::kSlots & 1, &sh.fail, a.polls);
                 // (boxes bring the rest of the last block too, whatever it holds: zeros in its place)
                 const int lo_r = base > t0 ? base - t0 : 0, end_r = cur.len - t0 < S::KT ? cur.len - t0 : S::KT;
-                const int hi_r = S::TMA ? S::KT : end_r;
+                int hi_r = end_r;
+                if (S::TMA && end_r < S::KT) {
+                    hi_r = (kv.block.div(cur.len - 1) + 1) * kv.block_size() - t0;
+                    if (hi_r > S::KT) hi_r = S::KT;
+                }
                 for (int y = lo_r * (S::DP / 8) + row; y < hi_r * (S::DP / 8); y += 128) {
                     const int vr = y / (S::DP / 8), vc = y % (S::DP / 8);
                     KvVec<T>* vx = reinterpret_cast<KvVec<T>*>(sh.slot[slot] + (vc >> 3) * S::kPanel + vr * 128 +
@@ -790,8 +825,7 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
         }
         j0 += nt;
         use0 += 2 * nt;
-        cur.tile += nt - 1;
-        cur.next(a, S::KT);
+        cur = ahead;
         ++seg;
     }
 }
@@ -809,6 +843,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const
     int used;
     AttnCursor cur;
     cur.b = 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // what the kernels before wrote
     attn_cut<S::kThreads>(a, sh.cut, S::KT, blockIdx.x, gridDim.x, units, used, lo, hi, cur);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this grid's end
     if (tid == 0) {
@@ -826,7 +861,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const
             mbar_init(smem_u32(&sh.empty[i]), S::kTiles);  // the streams that use it
         }
         mbar_init(smem_u32(&sh.q_full), 128);
-        mbar_init(smem_u32(&sh.q_shown), S::TMA ? 32 : 1);
+        mbar_init(smem_u32(&sh.q_shown), S::TMA && !maps.q_rows ? 32 : 1);
         mbar_init(smem_u32(&sh.q_empty), 2);
         for (int x = 0; x < 2; ++x) {
             mbar_init(smem_u32(&sh.s_full[x]), 1);
@@ -858,7 +893,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const
             if (warp < 8 + S::kBoxWarps)
                 tc_box_role<S>(a, maps, sh, cur, n, warp - 8, lane);
             else if (warp < 12)
-                tc_query_role<S>(a, sh, cur, n, lane);
+                tc_query_role<S>(a, maps, sh, cur, n, lane);
         } else {
             if (warp < 12)
                 tc_copy_role<S>(a, sh, cur, n, tid - 256);

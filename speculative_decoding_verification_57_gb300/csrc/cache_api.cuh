@@ -75,11 +75,14 @@ cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, int 
 
 template <typename S>
 cudaError_t launch_join(const AttnArgs& a, int ctas, cudaStream_t stream) {
-    const int pieces = static_cast<int>(a.filled.d) * (a.kv.dim / 4);  // of four columns
-    return launch_early(tree_attention_join<S>,
-                        dim3(static_cast<unsigned>(ctas),
-                             static_cast<unsigned>((pieces + kJoinThreads - 1) / kJoinThreads)),
-                        kJoinThreads, 0, stream, a, ctas);
+    // Many segments, at most two or three pieces each, if there are half as many as CTAs; sixteen columns a thread pay
+    // for row tiles of 256 (16 trees of 32 rows with 64 heads: 113 us for 118), and cost chains of 6 rows 83 us for 80
+    const bool few = static_cast<int64_t>(a.batch) * a.kv.heads * a.row_tiles < ctas / 2;
+    constexpr int kCols = S::TM == 256 ? 4 : 1;
+    const int threads = static_cast<int>(a.filled.d) * (a.kv.dim / (few ? 4 : 4 * kCols));  // of a segment
+    const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>((threads + kJoinThreads - 1) / kJoinThreads));
+    return launch_early(few ? tree_attention_join<S, 8, 1> : tree_attention_join<S, 2, kCols>, grid, kJoinThreads, 0, stream,
+                        a, ctas);
 }
 
 // Lets a kernel have `bytes` of dynamic shared memory; once a device (a bit

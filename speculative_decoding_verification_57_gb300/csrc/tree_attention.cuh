@@ -735,11 +735,13 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
 
 // ------------------------------------------------------------------ the join
 constexpr int kJoinThreads = 128;
-constexpr int kJoinPieces = 8;  // loads in flight a thread
 
-// Four columns of a row a thread, rows side by side, of the segment that CTA
-// blockIdx.x of the kernel before noted; kJoinPieces pieces at a time.
-template <typename S>
+// COLS times four columns of a row a thread, rows side by side, of the segment
+// that CTA blockIdx.x of the kernel before noted; PIECES pieces of it at a
+// time.  Bound by latency, so that a thread has several loads in flight: of
+// many columns where there are many segments, each cut in two or three, of
+// many pieces where there are few, each spread over many CTAs.
+template <typename S, int PIECES, int COLS>
 __global__ void __launch_bounds__(kJoinThreads) tree_attention_join(const AttnArgs a, int ctas) {
     using T = typename S::Type;
     constexpr int TM = S::TM, DP = S::DP;
@@ -753,40 +755,50 @@ __global__ void __launch_bounds__(kJoinThreads) tree_attention_join(const AttnAr
     if (note.b < 0) return;
     const KvView& kv = a.kv;
     const int at = blockIdx.y * kJoinThreads + threadIdx.x;
-    const int col = a.filled.div(at), row = at - col * static_cast<int>(a.filled.d);  // col: a group of four
+    const int part = a.filled.div(at), row = at - part * static_cast<int>(a.filled.d);
+    const int col = part * COLS;  // the first group of four columns
     const int h = note.s / a.row_tiles, rt = note.s - h * a.row_tiles;
     const int grow = rt * TM + row;
     if (col * 4 >= kv.dim || grow >= a.rows * static_cast<int>(a.group.d)) return;
     int status = 0;
     float m = -INFINITY, l = 0.0f;
-    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int c = cta; c <= note.last; c += kJoinPieces) {
-        float2 ml[kJoinPieces];
-        float4 y[kJoinPieces];
+    float4 x[COLS];
 #pragma unroll
-        for (int u = 0; u < kJoinPieces; ++u) {
-            const bool in = c + u <= note.last;
-            // [1] of the CTA that starts the segment, then [0] of the next ones
-            const int64_t piece = 2ll * (in ? c + u : cta) + (!in || c + u == cta);
-            status |= work.status[piece];
-            ml[u] = work.ml[piece * TM + row];
-            y[u] = work.acc[(piece * (DP / 4) + col) * TM + row];
-            if (!in) ml[u] = make_float2(-INFINITY, 0.0f);
+    for (int k = 0; k < COLS; ++k) x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int c = cta; c <= note.last; c += PIECES) {
+        float2 ml[PIECES];
+        float4 y[PIECES][COLS];
+#pragma unroll
+        for (int u = 0; u < PIECES; ++u) {
+            ml[u] = make_float2(-INFINITY, 0.0f);
+            if (c + u <= note.last) {
+                // [1] of the CTA that starts the segment, then [0] of the next ones
+                const int64_t piece = 2ll * (c + u) + (c + u == cta);
+                status |= work.status[piece];
+                ml[u] = work.ml[piece * TM + row];
+#pragma unroll
+                for (int k = 0; k < COLS; ++k) y[u][k] = work.acc[(piece * (DP / 4) + col + k) * TM + row];
+            }
         }
         float m_new = m;
 #pragma unroll
-        for (int u = 0; u < kJoinPieces; ++u) m_new = fmaxf(m_new, ml[u].x);
+        for (int u = 0; u < PIECES; ++u) m_new = fmaxf(m_new, ml[u].x);
         const float m_use = m_new == -INFINITY ? 0.0f : m_new;
         const float before = ex2(m - m_use);
         m = m_new;
         l *= before;
-        x = make_float4(x.x * before, x.y * before, x.z * before, x.w * before);
 #pragma unroll
-        for (int u = 0; u < kJoinPieces; ++u) {
+        for (int k = 0; k < COLS; ++k)
+            x[k] = make_float4(x[k].x * before, x[k].y * before, x[k].z * before, x[k].w * before);
+#pragma unroll
+        for (int u = 0; u < PIECES; ++u) {
             if (c + u > note.last) break;
             const float w = ex2(ml[u].x - m_use);
             l = fmaf(ml[u].y, w, l);
-            x = make_float4(fmaf(y[u].x, w, x.x), fmaf(y[u].y, w, x.y), fmaf(y[u].z, w, x.z), fmaf(y[u].w, w, x.w));
+#pragma unroll
+            for (int k = 0; k < COLS; ++k)
+                x[k] = make_float4(fmaf(y[u][k].x, w, x[k].x), fmaf(y[u][k].y, w, x[k].y), fmaf(y[u][k].z, w, x[k].z),
+                                   fmaf(y[u][k].w, w, x[k].w));
         }
     }
     if (at == 0 && note.s == 0 && status && a.row_status) atomicOr(a.row_status + note.b, status);
@@ -794,8 +806,12 @@ __global__ void __launch_bounds__(kJoinThreads) tree_attention_join(const AttnAr
     const int64_t token = static_cast<int64_t>(note.b) * a.rows + r;
     const int64_t head = token * a.q_heads + static_cast<int64_t>(h) * a.group.d + g;
     const float inv = status ? 0.0f : 1.0f / l;
-    if (status) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    attn_store4(static_cast<T*>(a.out) + head * kv.dim + col * 4, x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+#pragma unroll
+    for (int k = 0; k < COLS; ++k) {
+        if (status) x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        attn_store4(static_cast<T*>(a.out) + head * kv.dim + (col + k) * 4, x[k].x * inv, x[k].y * inv, x[k].z * inv,
+                    x[k].w * inv);
+    }
     if (col == 0 && a.lse) a.lse[head] = status ? -INFINITY : m * 0.693147181f + logf(l);
 }
 

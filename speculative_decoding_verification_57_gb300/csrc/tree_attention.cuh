@@ -63,10 +63,6 @@ __device__ __forceinline__ int attn_owner(int64_t units, int64_t x, int n) {
     return static_cast<int>(((x + 1) * n - 1) / units);
 }
 
-// A CTA takes at least this many tiles (while there are fewer than CTAs *
-// this, fewer CTAs run): a run's start costs about as much as two tiles.
-constexpr int kAttnLeast = 2;
-
 // Where a run stands on the line of tiles.
 struct AttnCursor {
     int b, s, tile;  // sequence, segment of it (kv head * row_tiles + row tile), tile
@@ -111,8 +107,7 @@ __device__ void attn_cut(const AttnArgs& a, AttnCut& sh, int tile_keys, int cta,
     int64_t total = 0;
     for (int w = 0; w < THREADS / 32; ++w) total += sh.sum[w];
     units = total * segs;
-    const int64_t most = (units + kAttnLeast - 1) / kAttnLeast;
-    used = static_cast<int>(most < ctas ? most : ctas);
+    used = static_cast<int>(units < ctas ? units : ctas);
     if (cta >= used) {
         lo = hi = 0;
         return;
@@ -265,14 +260,16 @@ struct AttnShape {
     static constexpr int kSmem = kStages * (2 * kHalf + kQ);
     // queries in registers for as long as a segment, unless the outputs need these
     static constexpr bool kQRegs = kBf16 && RG * DP <= 128;
+    static constexpr bool kQSplit = !kBf16 && RG * DP <= 64;  // ... as their two tf32 parts
     // resident CTAs: by shared memory (227 KB, 1 KB a CTA taken, about 3 KB
     // static) and by registers (outputs, queries, and about 100 others)
     static constexpr int kFit = 227 * 1024 / (kSmem + 4096);
-    static constexpr int kRegs = RG * DP / 2 + (kQRegs ? RG * DP / 4 : 0) + 100;
+    static constexpr int kRegs = RG * DP / 2 + (kQRegs ? RG * DP / 4 : kQSplit ? RG * DP : 0) + 100;
     static constexpr int kMost = 65536 / (kRegs * kThreads) > 1 ? 65536 / (kRegs * kThreads) : 1;
     static constexpr int kCtas = kFit > kMost ? kMost : kFit;
-    // a segment's end reduces the warps' results in the tile last consumed
-    static_assert(TM * DP * 4 <= 2 * kHalf, "the reduction fits a stage");
+    // a segment's end adds up the position warps' results in the tile last consumed, so many of them side by side
+    static constexpr int kSide = 2 * kHalf / (TM * DP * 4) > 4 ? 4 : 2 * kHalf / (TM * DP * 4);
+    static_assert(kSide == 1 || kSide == 2 || kSide == 4, "the reduction fits a stage");
 };
 
 // Byte offset of 16-byte piece c of row r: pieces change places within a row
@@ -408,6 +405,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
     float m_run[RG][2], l_run[RG][2];
     uint32_t anc[RG][2];
     uint32_t qf[S::kQRegs ? RG : 1][S::kQRegs ? DP / 16 : 1][4];
+    uint32_t qh[S::kQSplit ? RG : 1][S::kQSplit ? DP / 8 : 1][4], ql[S::kQSplit ? RG : 1][S::kQSplit ? DP / 8 : 1][4];
     int seg = 0, status = 0, first_tile = 0;
 
     for (int i = 0; i < n; ++i) {
@@ -441,6 +439,16 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[g][t][e] = 0.0f;
+                if constexpr (S::kQSplit) {
+#pragma unroll
+                    for (int kk = 0; kk < DP / 8; ++kk)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            split_tf32(ld_shared_f32(sq + attn_at<S>((wr * RG + g) * 16 + quad + 8 * (e & 1),
+                                                                     kk * 2 + (e >> 1)) +
+                                                     (lane & 3) * 4),
+                                       qh[g][kk][e], ql[g][kk][e]);
+                }
                 if constexpr (S::kQRegs) {
 #pragma unroll
                     for (int kk = 0; kk < DP / 16; ++kk)
@@ -500,7 +508,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
                 }
             }
         } else {
-#pragma unroll 4
+#pragma unroll(S::kQSplit ? DP / 8 : 4)
             for (int kk = 0; kk < DP / 8; ++kk) {
                 uint32_t bh[2], bl[2];
 #pragma unroll
@@ -510,10 +518,17 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
                 for (int g = 0; g < RG; ++g) {
                     uint32_t ah[4], al[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        split_tf32(ld_shared_f32(sq + attn_at<S>((wr * RG + g) * 16 + quad + 8 * (e & 1), kk * 2 + (e >> 1)) +
-                                                 (lane & 3) * 4),
-                                   ah[e], al[e]);
+                    for (int e = 0; e < 4; ++e) {
+                        if constexpr (S::kQSplit) {
+                            ah[e] = qh[g][kk][e];
+                            al[e] = ql[g][kk][e];
+                        } else {
+                            split_tf32(ld_shared_f32(sq + attn_at<S>((wr * RG + g) * 16 + quad + 8 * (e & 1),
+                                                                     kk * 2 + (e >> 1)) +
+                                                     (lane & 3) * 4),
+                                       ah[e], al[e]);
+                        }
+                    }
                     mma_tf32(s[g][0], al, bh[0], bh[1]);
                     mma_tf32(s[g][0], ah, bl[0], bl[1]);
                     mma_tf32(s[g][0], ah, bh[0], bh[1]);
@@ -616,7 +631,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
         const bool ends = cur.tile + 1 == cur.tiles;
         if (ends || i + 1 == n) {
             // the segment's part ends: the four position warps' results join
-            // in the tile just consumed, one warp after the other
+            // in the tile just consumed
 #pragma unroll
             for (int g = 0; g < RG; ++g)
 #pragma unroll
@@ -638,8 +653,10 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
                     for (int w = 0; w < 4; ++w) m = fmaxf(m, s_ml[w][row].x);
                     keep[g][e] = m == -INFINITY ? 1.0f : ex2(m_run[g][e] - m);
                 }
-            for (int w = 0; w < 4; ++w) {
-                if (wk == w) {
+            float* mine = red + (wk % S::kSide) * TM * DP;
+#pragma unroll
+            for (int w = 0; w < 4 / S::kSide; ++w) {
+                if (wk / S::kSide == w) {
 #pragma unroll
                     for (int g = 0; g < RG; ++g)
 #pragma unroll
@@ -647,7 +664,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 float2* p = reinterpret_cast<float2*>(
-                                    red + ((wr * RG + g) * 16 + quad + 8 * e) * DP + ((t * 8 + two) ^ ((quad & 3) * 8)));
+                                    mine + ((wr * RG + g) * 16 + quad + 8 * e) * DP + ((t * 8 + two) ^ ((quad & 3) * 8)));
                                 float2 x = w == 0 ? make_float2(0.0f, 0.0f) : *p;
                                 x.x += o[g][t][2 * e] * keep[g][e];
                                 x.y += o[g][t][2 * e + 1] * keep[g][e];
@@ -684,8 +701,16 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
             if (grow < m_rows) {
                 const float inv = 1.0f / l;
                 for (int d = lane_r * 4; d < kv.dim; d += kGroup * 4) {
-                    const float4 x4 = *reinterpret_cast<const float4*>(red + row * DP + (d ^ ((row & 3) * 8)));
-                    float x[4] = {x4.x, x4.y, x4.z, x4.w};
+                    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int w = 0; w < S::kSide; ++w) {
+                        const float4 x4 =
+                            *reinterpret_cast<const float4*>(red + (w * TM + row) * DP + (d ^ ((row & 3) * 8)));
+                        x[0] += x4.x;
+                        x[1] += x4.y;
+                        x[2] += x4.z;
+                        x[3] += x4.w;
+                    }
                     if (seen) {
                         for (int j = 0; j < a.rows; ++j) {
                             if (!(seen >> j & 1)) continue;

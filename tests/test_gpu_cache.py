@@ -331,19 +331,19 @@ def test_calls_on_two_streams(sv, h):
 @pytest.mark.parametrize("use", [0, 3])
 @pytest.mark.parametrize("rows,hq", [(17, 8), (32, 16)])
 def test_withheld_copy_times_out_then_next_call_is_clean(sv, bs, use, rows, hq):
-    """A slot of the tcgen05 kernel's first CTA (whose run is two tiles, four slot
-    uses) is never filled: its waits run
+    """A slot of the tcgen05 kernel's first CTA is never filled: its waits run
     out, the sequences it works on report bit 64, the others and the next
-    call are as ever."""
+    call are as ever.  (570 tiles and more for 152 CTAs: a run is three tiles at
+    least, six slot uses.)"""
     import torch
 
     handle = sv.specv_create(0, max_batch=64, max_k=31, vocab=1000)
-    c = Case(50 + use, "bf16", 40, rows, hq, 2, 128, bs, [300 + 20 * (i % 7) for i in range(40)], "tree")
+    c = Case(50 + use, "bf16", 12, rows, hq, 2, 128, bs, [3000 + 20 * i for i in range(12)], "tree")
     sv.specv_test_withhold_stage(handle, use, 200_000)
     got = c.call(sv, handle)
     bad = (got["row_status"] & sv.ST_TIMEOUT) != 0
     assert bad[0] and bad.sum() < 5 and not (got["row_status"] & ~sv.ST_TIMEOUT).any()
-    for b in range(40):
+    for b in range(12):
         if not bad[b]:
             continue
         c.lens[b] = 0  # checked as if idle below: their rows are not looked at
@@ -351,7 +351,7 @@ def test_withheld_copy_times_out_then_next_call_is_clean(sv, bs, use, rows, hq):
             got[key][b] = fill
     got["row_status"][bad] = 0
     c.check(got)
-    c2 = Case(50 + use, "bf16", 40, rows, hq, 2, 128, bs, [300 + 20 * (i % 7) for i in range(40)], "tree")
+    c2 = Case(50 + use, "bf16", 12, rows, hq, 2, 128, bs, [3000 + 20 * i for i in range(12)], "tree")
     c2.check(c2.call(sv, handle))
     sv.specv_destroy(handle)
 

@@ -57,8 +57,16 @@ __device__ __forceinline__ int attn_len(const AttnArgs& a, int b) {
 // An idle or refused sequence counts as a tile, whose CTA writes its zeros.
 __device__ __forceinline__ int attn_tiles(int len, int tile) { return len <= 0 ? 1 : (len + tile - 1) / tile; }
 
-// Run of CTA c of n over `units` tiles, and the CTA that has unit x.
-__device__ __forceinline__ int64_t attn_run(int64_t units, int c, int n) { return units * c / n; }
+// a / b for a >= 0, b > 0; by the 32-bit division, an eighth of the other's time, wherever it will do.
+__device__ __forceinline__ int64_t attn_div(int64_t a, int b) {
+    return a >> 31 ? a / b : static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+}
+
+// Run of CTA c of n over a line of `units`, floor(units c / n), and the CTA that has unit x.
+__device__ __forceinline__ int64_t attn_run(int64_t units, int c, int n) {
+    const int64_t each = attn_div(units, n);
+    return each * c + attn_div((units - each * n) * c, n);
+}
 __device__ __forceinline__ int attn_owner(int64_t units, int64_t x, int n) {
     return static_cast<int>(((x + 1) * n - 1) / units);
 }
@@ -83,68 +91,142 @@ struct AttnCursor {
 // Shared memory of attn_cut.
 struct AttnCut {
     int64_t sum[32];
-    int64_t at;
-    int b;
+    int64_t tiles[2];  // of the sequences before that at the run's start, and end
+    int b[2];
 };
 
-// The line's length, the number of CTAs that share it and the start of this
-// CTA's run, by the whole CTA (THREADS threads, a multiple of 32).
-template <int THREADS>
-__device__ void attn_cut(const AttnArgs& a, AttnCut& sh, int tile_keys, int cta, int ctas, int64_t& units, int& used,
-                         int64_t& lo, int64_t& hi, AttnCursor& cur) {
+// A CTA's run.  The line is of units: the tiles, and behind each segment's
+// last, where runs are long, some that stand for what a segment costs besides
+// its tiles (its queries, its end) and hold nothing.
+struct AttnRun {
+    int64_t units;  // of the line
+    int64_t first;  // the unit of the run's first tile
+    int used;       // CTAs that have runs
+    int n;          // tiles of the run
+    int extra;      // units behind a segment's last tile
+
+    // unit of a tile `tiles` tiles and `segments` segments on from the first
+    __device__ __forceinline__ int64_t unit(int tiles, int segments) const {
+        return first + tiles + static_cast<int64_t>(extra) * segments;
+    }
+};
+
+// The run of CTA `cta` of `ctas` and the cursor at its first tile, by the
+// whole CTA (THREADS threads, a multiple of 32).  COST: a segment's extra
+// units, in tiles, where a run has eight tiles or more.  Up to 32 sequences
+// every warp finds out by itself; with more, each thread has some of them.
+template <int THREADS, int COST>
+__device__ AttnRun attn_cut(const AttnArgs& a, AttnCut& sh, int tile_keys, int cta, int ctas, AttnCursor& cur) {
+    constexpr int kEnds = COST > 0 ? 2 : 1;  // of the run, looked for among the sequences
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int segs = a.kv.heads * a.row_tiles;
-    // the total, then the sequence that holds `lo`: a pass over the lengths
-    // for each (one load a thread serves both for up to THREADS sequences)
-    int64_t sum = 0, mine = 0;
-    for (int b = tid; b < a.batch; b += THREADS) {
-        mine = attn_tiles(attn_len(a, b), tile_keys);
-        sum += mine;
-    }
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (lane == 0) sh.sum[warp] = sum;
-    __syncthreads();
-    int64_t total = 0;
-    for (int w = 0; w < THREADS / 32; ++w) total += sh.sum[w];
-    units = total * segs;
-    used = static_cast<int>(units < ctas ? units : ctas);
-    if (cta >= used) {
-        lo = hi = 0;
-        return;
-    }
-    lo = attn_run(units, cta, used);
-    hi = attn_run(units, cta + 1, used);
-    int64_t before = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += THREADS) {
-        const int b = b0 + tid;
-        if (a.batch > THREADS) mine = b < a.batch ? attn_tiles(attn_len(a, b), tile_keys) : 0;
-        if (b >= a.batch) mine = 0;
-        int64_t incl = mine;
+    const bool small = a.batch <= 32;
+    // the total
+    int64_t sum = 0, mine = 0, incl = 0;
+    int my_len = 0;
+    if (small) {
+        if (lane < a.batch) {
+            my_len = attn_len(a, lane);
+            mine = attn_tiles(my_len, tile_keys);
+        }
+        incl = mine;
         for (int off = 1; off < 32; off <<= 1) {
             const int64_t o = __shfl_up_sync(0xffffffffu, incl, off);
             if (lane >= off) incl += o;
         }
-        __syncthreads();
-        if (lane == 31) sh.sum[warp] = incl;
-        __syncthreads();
-        int64_t ahead = before;
-        for (int w = 0; w < warp; ++w) ahead += sh.sum[w];
-        const int64_t start = (ahead + incl - mine) * segs, end = (ahead + incl) * segs;
-        if (mine > 0 && start <= lo && lo < end) {
-            sh.b = b;
-            sh.at = start;
+        sum = __shfl_sync(0xffffffffu, incl, 31);
+    } else {
+        for (int b = tid; b < a.batch; b += THREADS) {
+            mine = attn_tiles(attn_len(a, b), tile_keys);
+            sum += mine;
         }
-        for (int w = warp; w < THREADS / 32; ++w) ahead += sh.sum[w];
-        before = ahead;
-        if (before * segs > lo) break;
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        if (lane == 0) sh.sum[warp] = sum;
+        __syncthreads();
+        sum = 0;
+        for (int w = 0; w < THREADS / 32; ++w) sum += sh.sum[w];
     }
-    __syncthreads();
-    cur.b = sh.b;
-    cur.len = attn_len(a, cur.b);
-    cur.tiles = attn_tiles(cur.len, tile_keys);
-    const int64_t off = lo - sh.at;
-    cur.s = static_cast<int>(off / cur.tiles);
-    cur.tile = static_cast<int>(off - static_cast<int64_t>(cur.s) * cur.tiles);
+    AttnRun run;
+    run.extra = COST > 0 && sum * segs >= 8ll * ctas ? COST : 0;
+    run.units = (sum + static_cast<int64_t>(run.extra) * a.batch) * segs;
+    run.used = static_cast<int>(run.units < ctas ? run.units : ctas);
+    run.first = 0;
+    run.n = 0;
+    if (cta >= run.used) return run;
+    const int64_t ends[2] = {attn_run(run.units, cta, run.used), attn_run(run.units, cta + 1, run.used)};
+    // the sequences that hold the run's ends, and the tiles of those before them
+    int at_b[kEnds], at_len[kEnds];
+    int64_t at_before[kEnds];
+    if (small) {
+        const int64_t start = (incl - mine + static_cast<int64_t>(run.extra) * lane) * segs;
+        const int64_t end = start + (mine + run.extra) * segs;
+#pragma unroll
+        for (int i = 0; i < kEnds; ++i) {
+            const uint32_t hit = __ballot_sync(0xffffffffu, mine > 0 && start <= ends[i] && ends[i] < end);
+            at_b[i] = hit ? __ffs(hit) - 1 : 0;  // (none: the line's end)
+            at_len[i] = __shfl_sync(0xffffffffu, my_len, at_b[i]);
+            at_before[i] = __shfl_sync(0xffffffffu, incl - mine, at_b[i]);
+        }
+    } else {
+        int64_t before = 0;
+        for (int b0 = 0; b0 < a.batch; b0 += THREADS) {
+            const int b = b0 + tid;
+            // (one load a thread serves both passes for up to THREADS sequences)
+            if (a.batch > THREADS) mine = b < a.batch ? attn_tiles(attn_len(a, b), tile_keys) : 0;
+            if (b >= a.batch) mine = 0;
+            incl = mine;
+            for (int off = 1; off < 32; off <<= 1) {
+                const int64_t o = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += o;
+            }
+            __syncthreads();
+            if (lane == 31) sh.sum[warp] = incl;
+            __syncthreads();
+            int64_t ahead = before;
+            for (int w = 0; w < warp; ++w) ahead += sh.sum[w];
+            const int64_t start = (ahead + incl - mine + static_cast<int64_t>(run.extra) * b) * segs;
+            const int64_t end = start + (mine + run.extra) * segs;
+#pragma unroll
+            for (int i = 0; i < kEnds; ++i)
+                if (mine > 0 && start <= ends[i] && ends[i] < end) {
+                    sh.b[i] = b;
+                    sh.tiles[i] = ahead + incl - mine;
+                }
+            for (int w = warp; w < THREADS / 32; ++w) ahead += sh.sum[w];
+            before = ahead;
+            if ((before + static_cast<int64_t>(run.extra) * (b0 + THREADS)) * segs > ends[kEnds - 1]) break;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kEnds; ++i) {
+            at_b[i] = ends[i] < run.units ? sh.b[i] : 0;
+            at_len[i] = attn_len(a, at_b[i]);
+            at_before[i] = sh.tiles[i];
+        }
+    }
+    // tiles before each end; the cursor at the first
+    int64_t tiles[kEnds];
+#pragma unroll
+    for (int i = 0; i < kEnds; ++i) {
+        const int t = attn_tiles(at_len[i], tile_keys);
+        const int64_t off = ends[i] - (at_before[i] + static_cast<int64_t>(run.extra) * at_b[i]) * segs;
+        const int s = static_cast<int>(attn_div(ends[i] < run.units ? off : 0, t + run.extra));
+        const int at = static_cast<int>(off - static_cast<int64_t>(s) * (t + run.extra));
+        tiles[i] = ends[i] < run.units ? at_before[i] * segs + static_cast<int64_t>(s) * t + (at < t ? at : t) : sum * segs;
+        if (i > 0) continue;
+        run.first = ends[0];
+        cur.b = at_b[0];
+        cur.s = s;
+        cur.len = at_len[0];
+        cur.tiles = t;
+        cur.tile = at < t ? at : t - 1;
+        if (at >= t) {  // in the units behind a segment's last tile: on to the next segment
+            run.first += t + run.extra - at;
+            cur.next(a, tile_keys);
+        }
+    }
+    run.n = static_cast<int>(kEnds == 2 ? tiles[kEnds - 1] - tiles[0] : ends[1] - ends[0]);
+    return run;
 }
 
 // ------------------------------------------------------------------ workspace
@@ -264,7 +346,7 @@ struct AttnShape {
     // resident CTAs: by shared memory (227 KB, 1 KB a CTA taken, about 3 KB
     // static) and by registers (outputs, queries, and about 100 others)
     static constexpr int kFit = 227 * 1024 / (kSmem + 4096);
-    static constexpr int kRegs = RG * DP / 2 + (kQRegs ? RG * DP / 4 : kQSplit ? RG * DP : 0) + 100;
+    static constexpr int kRegs = RG * DP / 2 + (kQRegs ? RG * DP / 4 : kQSplit ? RG * DP - 30 : 0) + 100;
     static constexpr int kMost = 65536 / (kRegs * kThreads) > 1 ? 65536 / (kRegs * kThreads) : 1;
     static constexpr int kCtas = kFit > kMost ? kMost : kFit;
     // a segment's end adds up the position warps' results in the tile last consumed, so many of them side by side
@@ -304,19 +386,17 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
     const int m_rows = a.rows * static_cast<int>(a.group.d);  // rows of a kv head
     const float c_scale = a.scale * 1.44269504f;
 
-    int64_t units, lo, hi;
-    int used;
     AttnCursor cur, ahead, ids;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // what the kernels before wrote
-    attn_cut<S::kThreads>(a, s_cut, KT, cta, ctas, units, used, lo, hi, cur);
+    const AttnRun run = attn_cut<S::kThreads, 0>(a, s_cut, KT, cta, ctas, cur);
     if (tid == 0) {
         s_wild[0] = s_wild[1] = 0;
         work.notes[cta].b = -1;
         work.notes[cta].failed = 0;
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this grid's end
-    if (cta >= used) return;
-    const int n = static_cast<int>(hi - lo);
+    const int n = run.n;
+    if (n == 0) return;
     ids = ahead = cur;
 
     // block number of this thread's position in tile `i` of the run, whose cursor `ids` is: into a register ...
@@ -748,7 +828,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
                     if (first_tile == 0) {
                         work.notes[cta].b = cur.b;
                         work.notes[cta].s = cur.s;
-                        work.notes[cta].last = attn_owner(units, lo + i + (cur.tiles - cur.tile) - 1, used);
+                        work.notes[cta].last =
+                            attn_owner(run.units, run.unit(i + cur.tiles - cur.tile - 1, seg), run.used);
                     }
                 }
             }

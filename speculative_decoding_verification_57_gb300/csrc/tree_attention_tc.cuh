@@ -149,6 +149,9 @@ struct TcShape {
     static constexpr int kLead = WIDE ? 1 : 2;
     static constexpr int kSlots = DP == 64 ? 10 : WIDE ? 5 : 6;
     static constexpr int kBoxWarps = 3;
+    // of a segment, besides its tiles, in tiles (64 trees of 17 rows over 4096 positions: 0 152 us, 2 149, 4 147; 64 chains
+    // of 6 over 2000: 80.5, 77.2, 76.7; WIDE, 16 trees of 32 rows with 64 heads over 8192: 0 114, 2 109.4, 3 109.2, 4 109.5)
+    static constexpr int kCost = WIDE ? 3 : 4;
     static constexpr int kThreads = 16 * 32;
     // registers of a softmax thread, and of the others: together the 128 a thread that the launch has
     static constexpr int kMany = 184, kFew = 72;
@@ -548,8 +551,8 @@ __device__ void tc_mma_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor cur, 
 
 // ------------------------------------------------------------------ softmax
 template <typename S>
-__device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor cur, int n, int64_t units, int64_t lo,
-                                int used, int x, int row) {
+__device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor cur, const AttnRun& run, int x, int row) {
+    const int n = run.n;
     using T = typename S::Type;
     const KvView& kv = a.kv;
     const int lane = row & 31, cta = blockIdx.x;
@@ -810,7 +813,7 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
                 if (first_tile == 0) {
                     work.notes[cta].b = cur.b;
                     work.notes[cta].s = cur.s;
-                    work.notes[cta].last = attn_owner(units, lo + j0 + cur.tiles - 1, used);
+                    work.notes[cta].last = attn_owner(run.units, run.unit(j0 + cur.tiles - 1, seg), run.used);
                 }
             }
             if (status & KV_TIMEOUT) {
@@ -839,12 +842,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const
     if constexpr (S::TMA) {
         if (tid < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(tid ? &maps.v : &maps.k) : "memory");
     }
-    int64_t units, lo, hi;
-    int used;
     AttnCursor cur;
     cur.b = 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // what the kernels before wrote
-    attn_cut<S::kThreads>(a, sh.cut, S::KT, blockIdx.x, gridDim.x, units, used, lo, hi, cur);
+    const AttnRun run = attn_cut<S::kThreads, S::kCost>(a, sh.cut, S::KT, blockIdx.x, gridDim.x, cur);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this grid's end
     if (tid == 0) {
         AttnNote* note = attn_work(a.workspace, gridDim.x, S::TM, S::DP).notes + blockIdx.x;
@@ -852,8 +853,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const
         note->failed = 0;
         note->b0 = cur.b;
     }
-    if (static_cast<int>(blockIdx.x) >= used) return;
-    const int n = static_cast<int>(hi - lo);
+    const int n = run.n;
+    if (n == 0) return;
     if (tid == 0) {
         for (int i = 0; i < S::kSlots; ++i) {
             mbar_init(smem_u32(&sh.full[i]), S::TMA ? 1 : 128);
@@ -884,7 +885,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const
     tc_after_sync();
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kMany));
-        tc_softmax_role<S>(a, sh, cur, n, units, lo, used, warp >> 2, tid & 127);
+        tc_softmax_role<S>(a, sh, cur, run, warp >> 2, tid & 127);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kFew));
         if (warp == 12 || warp == 13) {

@@ -272,8 +272,8 @@ specv_status specv_rollback(specv_handle h, const int32_t *num_accepted, int bat
  * and so is block_stride in bytes.  Sizes outside these, or a block_stride
  * below kv_heads * block_size * head_dim: SPECV_ERR_INVALID_ARGUMENT.
  * A sequence is refused, with its row_status saying why, if its length is
- * negative, below the rows of the pass (0 aside) or above max_blocks *
- * block_size (bit 2048), or if an entry of its table that the call needs is
+ * negative, below the rows of the pass (0 aside), above max_blocks *
+ * block_size or above 2^31 - 513 (bit 2048), or if an entry of its table that the call needs is
  * outside [0, blocks) (bit 4096). */
 typedef struct {
     specv_dtype dtype;
@@ -361,7 +361,7 @@ int64_t specv_tree_attention_workspace(specv_handle h, specv_dtype dtype, int kv
  *   row_status          [B] out (nullable): 0, or bits 128 (num_accepted
  *                       outside [0, M]), 2048 (a length below M, 0 aside),
  *                       4096, 8192.  A refused sequence is left as it is
- * Positions behind the path keep what they held.  1 <= M <= max_k. */
+ * Positions behind the path keep what they held.  1 <= M <= max_k, layers >= 1. */
 specv_status specv_cache_compact(specv_handle h, const specv_kv_cache *cache, int layers, int64_t layer_stride,
                                  const int32_t *path, const int32_t *num_accepted, int batch, int M,
                                  int32_t *row_status, void *stream);

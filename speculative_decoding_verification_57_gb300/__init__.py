@@ -24,6 +24,7 @@ __all__ = [
     "specv_verify_sample_host",
     "specv_cache_append",
     "specv_tree_attention",
+    "specv_tree_attention_workspace",
     "specv_cache_compact",
     "specv_plan_cluster",
     "specv_test_withhold_stage",

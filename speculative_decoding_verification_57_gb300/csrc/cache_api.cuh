@@ -328,12 +328,12 @@ specv_status specv_cache_compact(specv_handle h, const specv_kv_cache* cache, in
     CompactArgs c = {};
     if (!make_view(h, cache, batch, c.kv)) return SPECV_ERR_INVALID_ARGUMENT;
     const int vec = cache->dtype == SPECV_BF16 ? 8 : 4;
-    if (M < 1 || M > h->max_k || layers < 0 || layers > 65536 || layer_stride < 0 || layer_stride % vec)
+    if (M < 1 || M > h->max_k || layers < 1 || layers > 65536 || layer_stride < 0 || layer_stride % vec)
         return SPECV_ERR_INVALID_ARGUMENT;
     // (layers overlap unless the pools or the blocks of one lie apart; either order of the two strides is fine)
     if (layers > 1 && layer_stride < static_cast<int64_t>(cache->kv_heads) * cache->block_size * cache->head_dim)
         return SPECV_ERR_INVALID_ARGUMENT;
-    if (layers > 0 && layer_stride > INT64_MAX / 16 / layers) return SPECV_ERR_INVALID_ARGUMENT;
+    if (layer_stride > INT64_MAX / 16 / layers) return SPECV_ERR_INVALID_ARGUMENT;
     if (batch == 0) return SPECV_OK;
     if (!path || !num_accepted) return SPECV_ERR_INVALID_ARGUMENT;
     c.path = path;

@@ -41,9 +41,9 @@ struct KvView {
     __device__ __forceinline__ int64_t at(int blk, int h, int slot) const {
         return blk * block_stride + (static_cast<int64_t>(h) * block_size() + slot) * dim;
     }
-    // whether n positions fit the table
+    // whether n positions fit the table (and a tile beyond them an int)
     __device__ __forceinline__ bool fits(int n) const {
-        return n <= static_cast<int64_t>(max_blocks) * block_size();
+        return n <= static_cast<int64_t>(max_blocks) * block_size() && n <= INT32_MAX - 512;
     }
     __device__ __forceinline__ bool valid(int blk) const { return blk >= 0 && blk < blocks; }
 };

@@ -384,7 +384,9 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
     const AttnWork work = attn_work(a.workspace, ctas, TM, DP);
     const uint32_t base_s = smem_u32(smem);
     const int m_rows = a.rows * static_cast<int>(a.group.d);  // rows of a kv head
-    const float c_scale = a.scale * 1.44269504f;
+    // a scale of zero still has to tell hidden positions (an infinite score) from the others
+    const float c_scale = a.scale == 0.0f ? 1e-30f : a.scale * 1.44269504f;
+    const float hidden = c_scale < 0.0f ? INFINITY : -INFINITY;
 
     AttnCursor cur, ahead, ids;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // what the kernels before wrote
@@ -588,6 +590,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
                 }
             }
         } else {
+            float s_low[RG][4] = {};
 #pragma unroll(S::kQSplit ? DP / 8 : 4)
             for (int kk = 0; kk < DP / 8; ++kk) {
                 uint32_t bh[2], bl[2];
@@ -609,11 +612,16 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
                                        ah[e], al[e]);
                         }
                     }
-                    mma_tf32(s[g][0], al, bh[0], bh[1]);
-                    mma_tf32(s[g][0], ah, bl[0], bl[1]);
+                    // (the small products add up by themselves: a sum of the tensor cores loses bits of its size a step)
+                    mma_tf32(s_low[g], al, bh[0], bh[1]);
+                    mma_tf32(s_low[g], ah, bl[0], bl[1]);
                     mma_tf32(s[g][0], ah, bh[0], bh[1]);
                 }
             }
+#pragma unroll
+            for (int g = 0; g < RG; ++g)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[g][0][e] += s_low[g][e];
         }
         // weights: the running maximum moves only when a score passes it by
         // 8 (weights stay below 2^8), so that the sums are seldom rescaled
@@ -624,13 +632,11 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
             for (int t = 0; t < ST; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    float x = s[g][t][e] * c_scale;
                     if (edge) {
                         const int pos = t0 + wk * KW + t * 8 + two + (e & 1);
-                        if (pos >= base && !(pos < cur.len && (anc[g][e >> 1] >> (pos - base) & 1))) x = -INFINITY;
+                        if (pos >= base && !(pos < cur.len && (anc[g][e >> 1] >> (pos - base) & 1))) s[g][t][e] = hidden;
                     }
-                    s[g][t][e] = x;
-                    top[e >> 1] = fmaxf(top[e >> 1], x);
+                    top[e >> 1] = fmaxf(top[e >> 1], s[g][t][e] * c_scale);
                 }
             bool move = false;
 #pragma unroll
@@ -659,7 +665,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
             for (int t = 0; t < ST; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    s[g][t][e] = ex2(s[g][t][e] - m_use[e >> 1]);
+                    s[g][t][e] = ex2(fmaf(s[g][t][e], c_scale, -m_use[e >> 1]));
                     l_run[g][e >> 1] += s[g][t][e];
                 }
         }
@@ -702,9 +708,12 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
                                bh[e], bl[e]);
 #pragma unroll
                 for (int g = 0; g < RG; ++g) {
-                    mma_tf32(o[g][t], pl[g], bh[0], bh[1]);
-                    mma_tf32(o[g][t], ph[g], bl[0], bl[1]);
-                    mma_tf32(o[g][t], ph[g], bh[0], bh[1]);
+                    float part[4] = {};  // the tile's, added in fp32 proper
+                    mma_tf32(part, pl[g], bh[0], bh[1]);
+                    mma_tf32(part, ph[g], bl[0], bl[1]);
+                    mma_tf32(part, ph[g], bh[0], bh[1]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[g][t][e] += part[e];
                 }
             }
         }

@@ -69,6 +69,7 @@ class Handle:
         self.max_batch = max_batch
         self.max_k = max_k
         self.vocab = vocab
+        self._workspace = {}  # bytes of workspace by the sizes of a call
 
     def __del__(self):
         try:
@@ -502,7 +503,10 @@ def specv_tree_attention(h: Handle, q, k_cache, v_cache, block_tables, seq_lens,
         pl = _on(h, out["lse"], _f32, "lse", (B, rows, q_heads))
     lib = _lib.load()
     if workspace is None:
-        need = lib.specv_tree_attention_workspace(h.ptr, c.dtype, c.kv_heads, c.head_dim, q_heads, B, rows)
+        sizes = (c.dtype, c.kv_heads, c.head_dim, q_heads, B, rows)
+        need = h._workspace.get(sizes)
+        if need is None:
+            need = h._workspace[sizes] = lib.specv_tree_attention_workspace(h.ptr, *sizes)
         workspace = _empty(h, (need,), _torch().uint8, stream) if need else None
     pw = None if workspace is None else _on(h, workspace, _torch().uint8, "workspace")
     st = lib.specv_tree_attention(

@@ -189,29 +189,29 @@ constexpr AttnPlan plan_of_tc() {
 // bf16 rows up to head_dim 128 and more than 16 rows a kv head (rows * group)
 // go to the tcgen05 kernel, whose row tile of 128 costs the tensor cores less
 // time than its positions cost the memory: 64 chains of 6 rows (24 a kv head)
-// over 2000 positions take 124 us there and 147 us on the other, 8 single
-// rows (4) over 1000 take 23 us there and 19 us on the other, whose pipeline
-// is shorter.  There, the narrowest row tile that holds the rows, or the
-// widest: a tile's keys and values are read once for all of its rows.
+// over 2000 positions took 124 us there and 147 us on the other when both were
+// new.  Up to 16 the other's shorter pipeline is even or ahead: 128 single
+// rows of 16 heads of 64 over 1000 positions 100 us for 162, 64 times 4 rows
+// over 300 34 us for 39, 64 single rows over 2000 87 us for 79.  In each, the
+// narrowest row tile that holds the rows, or the widest: a tile's keys and
+// values are read once for all of its rows.
 constexpr int kTcLeast = 17;
 
 const AttnPlan& attn_plan(specv_dtype dt, int dim, int m) {
     using B = __nv_bfloat16;
-    static constexpr AttnPlan plans[2][3][3] = {
-        {{plan_of<AttnShape<float, 64, 1, 1>>(), plan_of<AttnShape<float, 64, 1, 2>>(),
-          plan_of<AttnShape<float, 64, 2, 2>>()},
-         {plan_of<AttnShape<float, 128, 1, 1>>(), plan_of<AttnShape<float, 128, 1, 2>>(),
-          plan_of<AttnShape<float, 128, 2, 2>>()},
-         {plan_of<AttnShape<float, 256, 1, 1>>(), plan_of<AttnShape<float, 256, 1, 2>>(),
-          plan_of<AttnShape<float, 256, 1, 2>>()}},
-        {{plan_of<AttnShape<B, 64, 1, 1>>(), plan_of<AttnShape<B, 64, 1, 2>>(), plan_of<AttnShape<B, 64, 2, 2>>()},
-         {plan_of<AttnShape<B, 128, 1, 1>>(), plan_of<AttnShape<B, 128, 1, 2>>(), plan_of<AttnShape<B, 128, 2, 2>>()},
-         {plan_of<AttnShape<B, 256, 1, 1>>(), plan_of<AttnShape<B, 256, 1, 2>>(),
-          plan_of<AttnShape<B, 256, 1, 2>>()}}};
-    static constexpr AttnPlan tc[2][2] = {{plan_of_tc<64, false>(), plan_of_tc<64, true>()},
-                                          {plan_of_tc<128, false>(), plan_of_tc<128, true>()}};
-    if (dt == SPECV_BF16 && dim <= 128 && m >= kTcLeast) return tc[dim <= 64 ? 0 : 1][m <= 128 ? 0 : 1];
-    return plans[dt == SPECV_BF16 ? 1 : 0][dim <= 64 ? 0 : dim <= 128 ? 1 : 2][m <= 16 ? 0 : m <= 32 ? 1 : 2];
+    using F = float;
+    static constexpr AttnPlan f32[3][3] = {
+        {plan_of<AttnShape<F, 64, 1, 1>>(), plan_of<AttnShape<F, 64, 1, 2>>(), plan_of<AttnShape<F, 64, 2, 2>>()},
+        {plan_of<AttnShape<F, 128, 1, 1>>(), plan_of<AttnShape<F, 128, 1, 2>>(), plan_of<AttnShape<F, 128, 2, 2>>()},
+        {plan_of<AttnShape<F, 256, 1, 1>>(), plan_of<AttnShape<F, 256, 1, 2>>(), plan_of<AttnShape<F, 256, 1, 2>>()}};
+    static constexpr AttnPlan few[2] = {plan_of<AttnShape<B, 64, 1, 1>>(), plan_of<AttnShape<B, 128, 1, 1>>()};
+    static constexpr AttnPlan many[2][2] = {{plan_of_tc<64, false>(), plan_of_tc<64, true>()},
+                                            {plan_of_tc<128, false>(), plan_of_tc<128, true>()}};
+    static constexpr AttnPlan big[2] = {plan_of<AttnShape<B, 256, 1, 1>>(), plan_of<AttnShape<B, 256, 1, 2>>()};
+    const int d = dim <= 64 ? 0 : dim <= 128 ? 1 : 2;
+    if (dt == SPECV_F32) return f32[d][m <= 16 ? 0 : m <= 32 ? 1 : 2];
+    if (d == 2) return big[m <= 16 ? 0 : 1];
+    return m < kTcLeast ? few[d] : many[d][m <= 128 ? 0 : 1];
 }
 
 }  // namespace

@@ -3,12 +3,12 @@
 // tree_attention.cuh; a tile is 128 positions, a row tile 128 rows.
 //
 // One CTA an SM, 16 warps: two streams of four softmax warps, four warps that
-// copy, two that issue the products, and some that help or only make up their
-// warpgroup, so that registers can be moved to the softmax warps.  A stream has the scores of one row
-// tile and tile of positions (128 x 128 fp32) and its outputs (128 x DP fp32)
-// in tensor memory; a softmax thread owns a row, so that maxima and sums need
-// no exchange.  While one stream's weights are formed the tensor cores work
-// on the other's products.  With up to 128 rows a kv head the streams take
+// copy, two that issue the products, and two that help or only make up their
+// warpgroup, so that registers can be moved to the softmax warps.  A stream
+// has the scores of one row tile and tile of positions (128 x 128 fp32) and
+// its outputs (128 x DP fp32) in tensor memory; a softmax thread owns a row,
+// so that maxima and sums need no exchange.  While one stream's weights are
+// formed the tensor cores work on the other's products.  With up to 128 rows a kv head the streams take
 // tiles of positions in turn and their outputs join at the segment's end;
 // with more (WIDE) each has a row tile of its own and both use every tile.
 //
@@ -20,8 +20,23 @@
 //
 // Blocks whose rows fill tiles evenly (a multiple of eight that divides 128,
 // or a multiple of 128) come as tensor boxes, a box a block and panel; others
-// by 16-byte copies.  The boxes take one warp a tenth of the instructions and
-// land where the tensor cores see them at once: TIMES.
+// by 16-byte copies.  Boxes land where the tensor cores see them at once and
+// cost the softmax warps' schedulers next to nothing (with the issuing warps'
+// turns, they took the trees and the wide trees of the list below from 178 and
+// 149 us to 156 and 129).
+//
+// Measured (GB300, 2070 MHz, graph replays over 3 sets of inputs; bytes and
+// operations counted once; of 6691 GB/s and 1926 TFLOP/s measured):
+//   64 chains of 6 rows, 32/8 heads of 128, 1000..2000 positions    77 us  78%
+//   64 trees of 17 rows, same heads, 2048..4096                    147 us  84%
+//   one tree of 17 rows, same heads, 131072                         93 us  86%
+//   16 trees of 32 rows, 64/8 heads, 4096..8192 (WIDE)             109 us  59%,
+//     967 TFLOP/s, 50%
+// With one row tile the memory bounds it, short of it by each run's start
+// (5 us), its segments' ends and the join (5 to 10 us).  WIDE, a tile takes a
+// stream 3500 cycles: 1300 for its products (16 instructions of 64 cycles and
+// their issue), 1900 for its weights, the rest to tell one of the other; two
+// streams hide half of that.
 #pragma once
 #include <cuda.h>
 
@@ -155,7 +170,6 @@ struct TcShape {
     static constexpr int kThreads = 16 * 32;
     // registers of a softmax thread, and of the others: together the 128 a thread that the launch has
     static constexpr int kMany = 184, kFew = 72;
-    static constexpr int kCtas = 1;
     // place, in the order of use from its part's first slot on, of the values of tile t of nt
     static __device__ __forceinline__ int values_at(int t, int nt) {
         const int more = nt > kLead ? nt - kLead : 0;
@@ -465,7 +479,8 @@ __device__ void tc_show_role(const AttnArgs& a, TcShared<S>& sh, const AttnCurso
 // the two take turns, an output product and the next scores at a time, because
 // streams that share the tensor cores fall into step and then form their
 // weights at the same time, while these idle (16 trees of 32 rows over 8192
-// positions: TIMES).  Item i of a segment's part belongs to stream i & 1 and
+// positions: one warp for both 134 us, two 153, two in turns 129).  Item i of
+// a segment's part belongs to stream i & 1 and
 // tile i >> 1 (WIDE) or i.  A stream's next scores follow its output product,
 // whose weights lie where they go: products of one thread run in order.
 template <typename S>

@@ -333,7 +333,7 @@ specv_status specv_cache_append(specv_handle h, const specv_kv_cache *cache, con
  *   parents     [B, rows - 1] int32; NULL: chains.  1 <= rows <= max_k + 1;
  *               rows = 1 is plain decoding
  *   scale       factor of the scores before the softmax, finite
- *   out         [B, rows, q_heads, head_dim] out, without gaps
+ *   out         [B, rows, q_heads, head_dim] out, without gaps; not q's memory
  *   lse         [B, rows, q_heads] fp32 out (nullable): log of the sum of
  *               the exponentials of the scaled scores
  *   row_status  [B] out (nullable): 0, or bits 512, 2048, 4096, 64.  out of

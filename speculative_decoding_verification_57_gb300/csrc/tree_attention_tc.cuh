@@ -346,10 +346,11 @@ __device__ void tc_box_role(const AttnArgs& a, const TcMaps& maps, TcShared<S>& 
         go_on = __all_sync(0xffffffffu, go_on);
         if (!go_on || use == withhold) break;
         const uint32_t bar = smem_u32(&sh.full[slot]);
-        if (lane == 0) mbar_arrive_expect_tx(bar, S::kSlot);
-        __syncwarp();
         const bool valid = x.in && kv.valid(x.blk);
         if (x.in && !valid) sh.hole[x.seg & 15] = 1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(bar, S::kSlot);
+        __syncwarp();
         if (mine)
             tc_box(smem_u32(sh.slot[slot]) + panel * S::kPanel + part * rows * 128, x.values ? &maps.v : &maps.k,
                    panel * 64, valid ? x.row : 0, x.h, valid ? x.blk : kv.blocks, bar);
@@ -713,14 +714,20 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
                         *reinterpret_cast<uint4*>(vx) = make_uint4(0, 0, 0, 0);
                         continue;
                     }
+                    KvVec<T> v = *vx;
                     bool wild = false;
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        if (!finite(KvType<T>::load(vx->x[e]))) {
-                            vx->x[e] = KvType<T>::store(0.0f);
+                        if (!finite(KvType<T>::load(v.x[e]))) {
+                            v.x[e] = KvType<T>::store(0.0f);
                             wild = true;
                         }
-                    if (wild) atomicOr(&sh.wild[seg & 15], 1u << (t0 + vr - base));
+                    if (wild) {
+                        // (noted before it is gone: with WIDE the other stream looks at the same values)
+                        atomicOr(&sh.wild[seg & 15], 1u << (t0 + vr - base));
+                        __threadfence_block();
+                        *vx = v;
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();

@@ -286,7 +286,8 @@ specv_status specv_tree_attention(specv_handle h, const specv_kv_cache* cache, c
         !std::isfinite(scale))
         return SPECV_ERR_INVALID_ARGUMENT;
     if (batch == 0) return SPECV_OK;
-    if (!rows_ok(cache, q, q_stride) || !out || !aligned16(out)) return SPECV_ERR_INVALID_ARGUMENT;
+    // (a segment's end writes its rows of out while others still read their queries)
+    if (!rows_ok(cache, q, q_stride) || !out || !aligned16(out) || out == q) return SPECV_ERR_INVALID_ARGUMENT;
     const int group = q_heads / cache->kv_heads;
     const AttnPlan& p = attn_plan(cache->dtype, cache->head_dim, rows * group);
     const int ctas = h->sm_count * p.ctas;

@@ -729,6 +729,15 @@ def test_calls_are_refused_without_launching(sv, h):
     assert sv.specv_launch_count(h) == before
 
 
+def test_attention_is_refused_in_place(sv, h):
+    """out that is q itself: rows would be written while others read theirs."""
+    c = Case(41, "bf16", 2, 3, 4, 2, 64, 16, [20, 9], "tree")
+    before = sv.specv_launch_count(h)
+    with pytest.raises(sv.SpecvError):
+        sv.specv_tree_attention(h, c.q_t, c.kc_t, c.vc_t, _dev(c.tables), _dev(c.lens), out=dict(out=c.q_t))
+    assert sv.specv_launch_count(h) == before
+
+
 def test_empty_batches_and_empty_pools(sv, h):
     import torch
 

@@ -54,6 +54,21 @@ specv_status launched(specv_ctx* h, const char* what) {
     return SPECV_OK;
 }
 
+using AppendKernel = void (*)(AppendArgs);
+
+template <typename T, int THREADS>
+AppendKernel append_kernel_of(int mode) {
+    return mode == kApart        ? cache_append_kernel<T, kApart, THREADS>
+           : mode == kNeighbours ? cache_append_kernel<T, kNeighbours, THREADS>
+                                 : cache_append_kernel<T, kValues, THREADS>;
+}
+
+AppendKernel append_kernel(specv_dtype dt, int mode, bool many) {
+    using B = __nv_bfloat16;
+    if (dt == SPECV_BF16) return many ? append_kernel_of<B, kAppendMany>(mode) : append_kernel_of<B, kAppendFew>(mode);
+    return many ? append_kernel_of<float, kAppendMany>(mode) : append_kernel_of<float, kAppendFew>(mode);
+}
+
 // Tree attention of one shape: its kernel and, behind it, the join.  The CTAs
 // of both may be placed while the kernel before still runs (they wait for its
 // end on the device), so that launches overlap what runs before them.
@@ -255,14 +270,11 @@ specv_status specv_cache_append(specv_handle h, const specv_kv_cache* cache, con
     if (!g.ok) return cuda_fail(cudaErrorInvalidDevice, "cudaSetDevice");
     const unsigned grid = static_cast<unsigned>(batch) * static_cast<unsigned>(rows);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool many = grid > static_cast<unsigned>(h->sm_count) * (kAppendResident / kAppendFew);
     // pieces of 16 bytes turn whole, apart or within, where rot_dim fills them
     const int mode = rot_dim % (interleaved ? vec : 2 * vec) ? kValues : interleaved && rot_dim ? kNeighbours : kApart;
-    using B = __nv_bfloat16;
-    using Kernel = void (*)(AppendArgs);
-    static constexpr Kernel kernels[2][3] = {
-        {cache_append_kernel<float, kApart>, cache_append_kernel<float, kNeighbours>, cache_append_kernel<float, kValues>},
-        {cache_append_kernel<B, kApart>, cache_append_kernel<B, kNeighbours>, cache_append_kernel<B, kValues>}};
-    kernels[cache->dtype == SPECV_BF16][mode]<<<grid, kAppendThreads, 0, s>>>(a);
+    const AppendKernel kernel = append_kernel(cache->dtype, mode, many);
+    kernel<<<grid, many ? kAppendMany : kAppendFew, 0, s>>>(a);
     return launched(h, "cache_append launch");
 }
 

@@ -9,11 +9,12 @@
 // together (j and j + rot / 2, or two neighbours).
 //
 // Measured (GB300; bytes counted once, of 6691 GB/s measured): 4 ragged
-// prompts of up to 2048 tokens, 32/8 heads of 128 in bf16, 31 us, 73%; 64
-// trees of 17 rows 6.7 us, 60%; one token for 8 sequences 2.6 us (launch and
+// prompts of up to 2048 tokens, 32/8 heads of 128 in bf16, 28.6 us, 79%; 64
+// trees of 17 rows 5.6 us, 71%; one token for 8 sequences 2.6 us (launch and
 // the chain of loads).  Prompts issue an instruction in two of three cycles:
 // rotation in packed pairs and angles that stay in registers took them from
-// 51 us to 31.
+// 51 us to 31, CTAs of half the threads (a token that waits holds less of the
+// SM) to 28.6.
 //
 // Angles are formed in float64 (position * inv_freq passes 2^24 for far
 // positions, where fp32 would lose the fraction of a turn), brought into
@@ -24,7 +25,11 @@
 
 namespace specv {
 
-constexpr int kAppendThreads = 192;
+// Threads of a CTA: as many for a few tokens, half of them where the tokens
+// are more than the SMs hold at once.  Prompts as above 30.9 us with 192, 28.6
+// with 96 (64: 28.1), trees 6.7 and 5.6, one token for 8 sequences 2.6 and 3.0.
+constexpr int kAppendFew = 192, kAppendMany = 96;
+constexpr int kAppendResident = 960;  // threads of an SM
 constexpr int kAppendHeads = 2;  // whose pieces a thread has in flight
 
 // How the pairs lie: pieces apart, neighbours in a piece, or (where rot does
@@ -95,8 +100,8 @@ __device__ __forceinline__ void append_pieces(KvVec<__nv_bfloat16>& x, KvVec<__n
 
 // A thread has the same two pieces (a unit) of every hstep-th head, so that it
 // keeps the angles that turn them.  Heads are counted through q, k and v.
-template <typename T, int MODE>
-__global__ void __launch_bounds__(kAppendThreads, 5) cache_append_kernel(const AppendArgs a) {
+template <typename T, int MODE, int THREADS>
+__global__ void __launch_bounds__(THREADS, kAppendResident / THREADS) cache_append_kernel(const AppendArgs a) {
     constexpr int kVec = KvType<T>::kVec;
     using Vec = KvVec<T>;
     __shared__ __align__(16) float s_cos[128], s_sin[128];
@@ -105,7 +110,7 @@ __global__ void __launch_bounds__(kAppendThreads, 5) cache_append_kernel(const A
     const int tid = threadIdx.x;
     const KvView& kv = a.kv;
     const int turning = a.q_heads + kv.heads, heads = turning + kv.heads;
-    const int per = static_cast<int>(a.units.d), hstep = kAppendThreads / per;
+    const int per = static_cast<int>(a.units.d), hstep = THREADS / per;
     const int h0 = a.units.div(tid), u = tid - h0 * per;
     const int half = a.rot / 2;
     // the unit's pieces of a head that turns, and of a value's
@@ -149,9 +154,9 @@ __global__ void __launch_bounds__(kAppendThreads, 5) cache_append_kernel(const A
             depth = __shfl_sync(0xffffffffu, d, r);
         }
         if (r < count) blk = table[kv.block.div(slot)];
-        for (int i = kv.block.div(base) + tid, last = kv.block.div(len - 1); i <= last; i += kAppendThreads)
+        for (int i = kv.block.div(base) + tid, last = kv.block.div(len - 1); i <= last; i += THREADS)
             block_bad |= !kv.valid(table[i]);
-        for (int j = tid; j < half; j += kAppendThreads) {
+        for (int j = tid; j < half; j += THREADS) {
             const float2 cs = append_turn(base + depth, a.inv_freq[j]);
             s_cos[j] = cs.x;
             s_sin[j] = cs.y;
@@ -162,7 +167,7 @@ __global__ void __launch_bounds__(kAppendThreads, 5) cache_append_kernel(const A
     if (r == 0 && tid == 0 && a.row_status) a.row_status[b] = status;
     if (status != 0 || r >= count) {
         if (a.q)
-            for (int i = tid; i < a.q_heads * per * 2; i += kAppendThreads)
+            for (int i = tid; i < a.q_heads * per * 2; i += THREADS)
                 reinterpret_cast<uint4*>(q_out)[i] = make_uint4(0, 0, 0, 0);
         return;
     }
@@ -172,7 +177,7 @@ __global__ void __launch_bounds__(kAppendThreads, 5) cache_append_kernel(const A
     T* v_out = static_cast<T*>(kv.v) + at;
     if constexpr (MODE == kValues) {
         const int pairs = kv.dim / 2;  // of a head: the turning ones, then the rest by twos
-        for (int i = tid; i < heads * pairs; i += kAppendThreads) {
+        for (int i = tid; i < heads * pairs; i += THREADS) {
             const int h = i / pairs, j = i - h * pairs;
             const T* p = (h < a.q_heads ? q : h < turning ? k : v) + h * kv.dim;
             T* to = h < a.q_heads ? q_out + h * kv.dim

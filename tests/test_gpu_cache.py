@@ -541,6 +541,22 @@ def test_append_matches_the_formula(sv, h, dtype, shape):
         assert np.all(_np(got["q_out"])[b, m:] == 0)
 
 
+# more tokens than the SMs hold at once: CTAs of fewer threads
+MANY_APPENDS = [
+    (60, 17, 4, 2, 64, 16, [17 + i if i % 7 else 0 for i in range(60)], "tree", 64, False, None),
+    (3, 300, 6, 3, 80, 5, [300, 417, 299], "chain", 40, True, [300, 291, 0]),
+    (300, 3, 2, 1, 16, 1, [3 + i % 5 for i in range(300)], "tree", 6, False, [i % 4 for i in range(300)]),
+    (100, 9, 2, 1, 256, 16, [9 + i for i in range(100)], "star", 256, False, None),
+    (1, 777, 8, 4, 48, 64, [1000], "chain", 0, False, [770]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", MANY_APPENDS, ids=lambda s: "B%d_R%d_H%d-%d_D%d_bs%d_%s" % (s[:6] + (s[7],)))
+def test_append_of_many_tokens(sv, h, dtype, shape):
+    test_append_matches_the_formula(sv, h, dtype, shape)
+
+
 def test_append_without_queries_in_place_and_in_slices(sv, h):
     import torch
 

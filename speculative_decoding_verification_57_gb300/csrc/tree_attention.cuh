@@ -303,11 +303,20 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
 }
 
 // x = hi + lo with both in tf32 (11 significant bits each): a product of two
-// such pairs without lo * lo is off by 3 * 2^-22 of its size.
+// such pairs without lo * lo is off by 3 * 2^-22 of its size.  hi is never
+// infinite: what would round to infinity is the largest tf32 number instead, so
+// that a finite x has two finite parts, and an infinite one an infinite lo
+// only (an infinite hi would make lo, a difference, no number).  CUT: lo is cut
+// off instead of rounded (x off by 2^-22, not 2^-23), so that the parts do not
+// add up to more than the largest float either.
+template <bool CUT = false>
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+    asm("cvt.rna.satfinite.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
     const float rest = x - __uint_as_float(hi);
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(rest));
+    if (CUT)
+        lo = __float_as_uint(rest) & 0xffffe000u;
+    else
+        asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(rest));
 }
 
 // 16 bytes global -> shared; zeros if !take (src is then not read)
@@ -371,6 +380,18 @@ struct AttnShape {
 template <typename S>
 __device__ __forceinline__ uint32_t attn_at(int r, int c) {
     return static_cast<uint32_t>(r * S::kRow + ((c ^ (r & 7)) << 4));
+}
+
+// Product of query row m (at sq) and position n (at sk) of fp32 tiles, summed
+// in float64, whose range no sum of such products leaves.
+template <typename S>
+__device__ float attn_dot(uint32_t sq, int m, uint32_t sk, int n) {
+    double sum = 0.0;
+#pragma unroll 1
+    for (int c = 0; c < S::DP; ++c)
+        sum += static_cast<double>(ld_shared_f32(sq + attn_at<S>(m, c >> 2) + (c & 3) * 4)) *
+               static_cast<double>(ld_shared_f32(sk + attn_at<S>(n, c >> 2) + (c & 3) * 4));
+    return static_cast<float>(sum);
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -634,6 +655,16 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
             for (int g = 0; g < RG; ++g)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[g][0][e] += s_low[g][e];
+            // a score that is not finite: infinities and values near the ends of the type may have met with opposite
+            // signs in the parts though not in the score
+#pragma unroll
+            for (int g = 0; g < RG; ++g) {
+                if (finite(fabsf(s[g][0][0]) + fabsf(s[g][0][1]) + fabsf(s[g][0][2]) + fabsf(s[g][0][3]))) continue;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (!finite(s[g][0][e]))
+                        s[g][0][e] = attn_dot<S>(sq, (wr * RG + g) * 16 + quad + 8 * (e >> 1), sk, wk * KW + two + (e & 1));
+            }
         }
         // weights: the running maximum moves only when a score passes it by
         // 8 (weights stay below 2^8), so that the sums are seldom rescaled
@@ -716,8 +747,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
                 uint32_t bh[2], bl[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    split_tf32(ld_shared_f32(sv + attn_at<S>(wk * KW + two + e, t * 2 + (quad >> 2)) + (quad & 3) * 4),
-                               bh[e], bl[e]);
+                    split_tf32<true>(ld_shared_f32(sv + attn_at<S>(wk * KW + two + e, t * 2 + (quad >> 2)) + (quad & 3) * 4),
+                                     bh[e], bl[e]);
 #pragma unroll
                 for (int g = 0; g < RG; ++g) {
                     float part[4] = {};  // the tile's, added in fp32 proper

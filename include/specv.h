@@ -337,7 +337,8 @@ specv_status specv_cache_append(specv_handle h, const specv_kv_cache *cache, con
  *   lse         [B, rows, q_heads] fp32 out (nullable): log of the sum of
  *               the exponentials of the scaled scores
  *   row_status  [B] out (nullable): 0, or bits 512, 2048, 4096, 64.  out of
- *               an idle or refused sequence is 0, lse -infinity
+ *               an idle or refused sequence is 0, lse -infinity; with bit 64
+ *               what they hold of the sequence is not determined
  *   workspace   device memory of specv_tree_attention_workspace(...) bytes,
  *               256-byte aligned, the call's own until it has run
  * Positions that a row does not see take no part, whatever they hold (NaN and

@@ -248,7 +248,7 @@ __device__ AttnRun attn_cut(const AttnArgs& a, AttnCut& sh, int tile_keys, int c
 struct alignas(16) AttnNote {
     int b, s;    // b < 0: none
     int last;    // the CTA with the segment's last tile
-    int failed;  // a wait of the CTA ran out: sequences b0 .. b1 may be wrong
+    int failed;  // a wait of the CTA ran out: sequences b0 .. b1, all that its run touches, may be wrong
     int b0, b1;
 };
 

@@ -202,7 +202,8 @@ struct TcShared {
     uint32_t wild[16];  // by segment: nodes with values that are not finite ...
     int hole[16];       // ... and whether a block is outside the pool
     uint32_t tmem;
-    int fail;  // a wait ran out: no role waits any more
+    int fail;          // a wait ran out: no role waits any more
+    AttnCursor start;  // of the run
 };
 
 // A wait of a role: bounded, and none after one ran out.  False: it, or
@@ -838,10 +839,6 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
                     work.notes[cta].last = attn_owner(run.units, run.unit(j0 + cur.tiles - 1, seg), run.used);
                 }
             }
-            if (status & KV_TIMEOUT) {
-                work.notes[cta].failed = 1;
-                work.notes[cta].b1 = cur.b;
-            }
         }
         if constexpr (!S::WIDE) {
             __syncwarp();
@@ -874,6 +871,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const
         note->b = -1;
         note->failed = 0;
         note->b0 = cur.b;
+        sh.start = cur;
     }
     const int n = run.n;
     if (n == 0) return;
@@ -929,6 +927,17 @@ __global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const
     __syncthreads();
     tc_after_sync();
     if (warp == 12) tc_dealloc(sh.tmem, 512);
+    // told when every role is done: a wait may run out after the threads that end a segment have looked at the flag
+    if (tid == 0 && tc_failed(&sh.fail)) {
+        AttnCursor at = sh.start;
+        for (int left = n, nt; (nt = tc_part(at, left)) < left; left -= nt) {
+            at.tile += nt - 1;
+            at.next(a, S::KT);
+        }
+        AttnNote* note = attn_work(a.workspace, gridDim.x, S::TM, S::DP).notes + blockIdx.x;
+        note->b1 = at.b;
+        note->failed = 1;
+    }
 }
 
 }  // namespace specv

@@ -356,11 +356,17 @@ __device__ void tc_box_role(const AttnArgs& a, const TcMaps& maps, TcShared<S>& 
             tc_box(smem_u32(sh.slot[slot]) + panel * S::kPanel + part * rows * 128, x.values ? &maps.v : &maps.k,
                    panel * 64, valid ? x.row : 0, x.h, valid ? x.blk : kv.blocks, bar);
     }
-    // no box of this warp's is in flight when the CTA ends, not even after a wait that ran out (earlier ones had landed
-    // when their slots were filled again)
+    // no box of this warp's is in flight when the CTA ends, not even after a wait that ran out (those of kSlots uses
+    // before the last and earlier had landed: their slots were used up).  Another warp may have filled a slot again since,
+    // so that its parity is back where it was: then the slot had been used up, which its other barrier tells
     const int end = use;
-    for (use = end - S::kBoxWarps; use >= 0 && use > end - S::kSlots; use -= S::kBoxWarps)
-        mbar_wait_bounded(smem_u32(&sh.full[use % S::kSlots]), (use / S::kSlots) & 1, 1u << 30);
+    const unsigned long long since = gtimer();
+    for (use = end - S::kBoxWarps; use >= 0 && use > end - S::kSlots; use -= S::kBoxWarps) {
+        const uint32_t bar = smem_u32(&sh.full[use % S::kSlots]), used = smem_u32(&sh.empty[use % S::kSlots]);
+        const uint32_t phase = (use / S::kSlots) & 1;
+        while (!mbar_test_wait(used, phase) && !mbar_wait_bounded(bar, phase, 256) && gtimer() - since < kWaitNs) {
+        }
+    }
 }
 
 // Queries where the keys and values are boxes: one warp, by boxes of its own

@@ -32,3 +32,26 @@ def test_whatever_a_missing_copy_changes_is_told(sv, bs, dim, rows, hq):  # noqa
     for key in ("out", "lse"):
         assert torch.equal(again[key], want[key])
     sv.specv_destroy(handle)
+
+
+@pytest.mark.parametrize("bs", [16, 5])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("rows,hq", [(17, 8), (32, 16)])
+def test_a_missing_copy_costs_its_own_waits_only(sv, bs, dim, rows, hq):  # noqa: F811
+    """No role of a call that ran out waits for something that is over already
+    (such a wait would run for 200 ms; 2000 polls take less than 10)."""
+    import torch
+
+    handle = sv.specv_create(0, max_batch=64, max_k=31, vocab=1000)
+    c = Case(rows + dim, "bf16", 7, rows, hq, 2, dim, bs, [11000 + 37 * i for i in range(7)], "tree", poison=False)
+    c.call(sv, handle)
+    for use in (0, 1, 2, 3, 7):
+        sv.specv_test_withhold_stage(handle, use, 2000)
+        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        start.record()
+        got = c.call(sv, handle)
+        end.record()
+        torch.cuda.synchronize()
+        assert got["row_status"].tolist()[0] == sv.ST_TIMEOUT
+        assert start.elapsed_time(end) < 150, use
+    sv.specv_destroy(handle)

@@ -266,7 +266,9 @@ specv_status specv_rollback(specv_handle h, const int32_t *num_accepted, int bat
  *   seq_lens      [B] int32: positions held, the rows of the current pass the
  *                 last of them (position t is in block t / block_size of the
  *                 table, at t % block_size).  0: an idle sequence (padding of
- *                 a batch): nothing of it is read, its status is 0
+ *                 a batch): nothing of it is read from the cache, its status
+ *                 is 0, and what its rows in the calls' tensors hold (they
+ *                 have to be readable all the same) has no effect
  * head_dim is a multiple of 16 from 16 to 256, block_size 1..65536, blocks at
  * most 2^31 - 1; k, v and the tensors of the calls below are 16-byte aligned,
  * and so is block_stride in bytes.  Sizes outside these, or a block_stride

@@ -5,16 +5,17 @@
 // and serve every head.  Bound by memory for prompts and by a chain of three
 // loads (length, block, row) for a few tokens; so a thread asks for its rows
 // of q, k and v, whose places depend on nothing, before it looks at anything
-// else, and what it gets is 16 bytes each: pieces of a head that turn
-// together (j and j + rot / 2, or two neighbours).
+// else (but the row count, where there is one: padding is not read), and what
+// it gets is 16 bytes each: pieces of a head that turn together (j and
+// j + rot / 2, or two neighbours).
 //
 // Measured (GB300; bytes counted once, of 6691 GB/s measured): 4 ragged
-// prompts of up to 2048 tokens, 32/8 heads of 128 in bf16, 28.6 us, 79%; 64
+// prompts of up to 2048 tokens, 32/8 heads of 128 in bf16, 26.2 us, 86%; 64
 // trees of 17 rows 5.6 us, 71%; one token for 8 sequences 2.6 us (launch and
 // the chain of loads).  Prompts issue an instruction in two of three cycles:
 // rotation in packed pairs and angles that stay in registers took them from
 // 51 us to 31, CTAs of half the threads (a token that waits holds less of the
-// SM) to 28.6.
+// SM) to 28.6, leaving padding unread to 26.2.
 //
 // Angles are formed in float64 (position * inv_freq passes 2^24 for far
 // positions, where fp32 would lose the fraction of a turn), brought into
@@ -135,11 +136,13 @@ __global__ void __launch_bounds__(THREADS, kAppendResident / THREADS) cache_appe
 #pragma unroll
         for (int j = 0; j < kAppendHeads; ++j) load(h1 + j * hstep, j);
     };
-    if (MODE != kValues) load_all(h0);
+    // (where rows are counted, a row that is padding is not read)
+    const int counted = a.row_counts ? a.row_counts[b] : rows;
+    if (MODE != kValues && r < counted) load_all(h0);
     // the token's sequence: its length, its tree, the blocks it writes to.  Every token of a sequence looks at all of
     // them, so that of a refused sequence nothing is written
     const int len = kv.lens[b];
-    const int count = a.row_counts ? a.row_counts[b] : (len == 0 ? 0 : rows);
+    const int count = a.row_counts || len != 0 ? counted : 0;
     const int base = len - count, slot = base + r;
     const int32_t* table = kv.tables + static_cast<int64_t>(b) * kv.max_blocks;
     int status = 0, blk = 0;

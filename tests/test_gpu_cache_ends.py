@@ -1,5 +1,5 @@
 """The calls on the paged KV cache at the ends of the type: infinities and
-the largest finite values in keys and values, seen and hidden, and scales at
+the largest finite values in keys and values, seen and hidden, padding, and scales at
 the ends of fp32."""
 import math
 
@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 
 import cache_plain as P
-from test_gpu_cache import Case, _np, h, sv  # noqa: F401  (h and sv are fixtures)
+from test_gpu_cache import Case, _dev, _dtype, _np, _rounded, _tables, h, sv  # noqa: F401  (h and sv are fixtures)
 
 pytestmark = pytest.mark.gpu
 
@@ -111,3 +111,31 @@ def _flat(c, t, key):
         k[tables[b, t]] = key * (np.arange(kc.shape[3]) == 7)
         v[tables[b, t]] = 0.0
     return k, v, tables
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,rows,rot,inter", [(3, 9, 64, False), (40, 50, 64, False), (40, 50, 32, True), (3, 9, 6, False)])
+def test_append_leaves_padding_alone(sv, h, dtype, B, rows, rot, inter):  # noqa: F811
+    """Whatever the rows behind a sequence's count hold, the cache and the
+    queries are the same bits; padding's queries are zero."""
+    import torch
+
+    dt = _dtype(dtype)
+    rng = np.random.default_rng(B)
+    counts = rng.integers(0, rows + 1, size=B).astype(np.int32)
+    lens = counts + rng.integers(0, 30, size=B).astype(np.int32) * (counts > 0)
+    tables, blocks = _tables(rng, lens, 16)
+    inv = _dev((10000.0 ** (-np.arange(rot // 2) * 2 / rot)).astype(np.float32))
+    x, _ = _rounded(rng, (B, rows, 8, 64), dt)
+    pad = torch.from_numpy(np.arange(rows)[None] >= counts[:, None]).cuda()
+    results = []
+    for fill in (0.0, math.nan, float(torch.finfo(dt).max), -math.inf):
+        y = x.clone()
+        y[pad] = fill
+        kc, vc = (torch.zeros((blocks, 2, 16, 64), dtype=dt, device="cuda") for _ in range(2))
+        got = sv.specv_cache_append(h, kc, vc, _dev(tables), _dev(lens.astype(np.int32)), y[:, :, 4:6], y[:, :, 6:],
+                                    q=y[:, :, :4], inv_freq=inv, interleaved=inter, row_counts=_dev(counts))
+        assert not got["row_status"].any() and not got["q_out"][pad].any()
+        results.append((got["q_out"], kc, vc))
+    for other in results[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(results[0], other))

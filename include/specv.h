@@ -65,7 +65,10 @@
  *                                   infinite at an examined entry
  *                               64  an internal wait timed out (the result of
  *                                   this row is not valid)
- *                              512  (tree verification) a parent index
+ *                              128  (rollback, KV cache compaction) an
+ *                                   accepted count out of range
+ *                              256  (rollback) no room in the free list
+ *                              512  (trees) a parent index
  *                                   outside [-1, node)
  *                             1024  (top-k / top-p verification) top_k
  *                                   outside [1, 4096] or top_p outside (0, 1]

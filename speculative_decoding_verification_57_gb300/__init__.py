@@ -11,8 +11,9 @@ from __future__ import annotations
 import ctypes
 
 from . import _lib
-from ._lib import (ST_BLOCK, ST_ERROR_MASK, ST_LENGTH, ST_NONFINITE, ST_PARENT, ST_PATH, ST_Q_INVALID, ST_TEMPERATURE,
-                   ST_TIMEOUT, ST_TOKEN_RANGE, ST_UNIFORM_RANGE, ST_ZERO_RESIDUAL, SPECV_BF16, SPECV_F32)
+from ._lib import (ST_ACCEPTED, ST_BLOCK, ST_ERROR_MASK, ST_FILTER, ST_LENGTH, ST_NO_ROOM, ST_NONFINITE, ST_PARENT, ST_PATH,
+                   ST_Q_INVALID, ST_TEMPERATURE, ST_TIMEOUT, ST_TOKEN_RANGE, ST_UNIFORM_RANGE, ST_ZERO_RESIDUAL,
+                   SPECV_BF16, SPECV_F32)
 
 __all__ = [
     "SpecvError",
@@ -37,7 +38,10 @@ __all__ = [
     "ST_ZERO_RESIDUAL",
     "ST_Q_INVALID",
     "ST_TIMEOUT",
+    "ST_ACCEPTED",
+    "ST_NO_ROOM",
     "ST_PARENT",
+    "ST_FILTER",
     "ST_LENGTH",
     "ST_BLOCK",
     "ST_PATH",

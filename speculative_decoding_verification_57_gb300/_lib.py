@@ -21,13 +21,16 @@ ST_TEMPERATURE = 8
 ST_ZERO_RESIDUAL = 16
 ST_Q_INVALID = 32
 ST_TIMEOUT = 64
+ST_ACCEPTED = 128
+ST_NO_ROOM = 256
 ST_PARENT = 512
 ST_FILTER = 1024
 ST_LENGTH = 2048
 ST_BLOCK = 4096
 ST_PATH = 8192
+# every bit but ST_ZERO_RESIDUAL, which is information: the row's result is not one to use
 ST_ERROR_MASK = (ST_NONFINITE | ST_TOKEN_RANGE | ST_UNIFORM_RANGE | ST_TEMPERATURE | ST_Q_INVALID | ST_TIMEOUT
-                 | ST_PARENT | ST_FILTER)
+                 | ST_ACCEPTED | ST_NO_ROOM | ST_PARENT | ST_FILTER | ST_LENGTH | ST_BLOCK | ST_PATH)
 
 
 class SpecvDebug(ctypes.Structure):

@@ -337,7 +337,9 @@ specv_status specv_cache_append(specv_handle h, const specv_kv_cache *cache, con
  *               h / (q_heads / kv_heads)
  *   parents     [B, rows - 1] int32; NULL: chains.  1 <= rows <= max_k + 1;
  *               rows = 1 is plain decoding
- *   scale       factor of the scores before the softmax, finite
+ *   scale       factor of the scores before the softmax; it and scale *
+ *               log2(e), the factor of the scores in base 2, finite.  Scores
+ *               are fp32: one that these take out of its range is infinite
  *   out         [B, rows, q_heads, head_dim] out, without gaps; not q's memory
  *   lse         [B, rows, q_heads] fp32 out (nullable): log of the sum of
  *               the exponentials of the scaled scores

@@ -295,7 +295,7 @@ specv_status specv_tree_attention(specv_handle h, const specv_kv_cache* cache, c
     AttnArgs a = {};
     if (!make_view(h, cache, batch, a.kv)) return SPECV_ERR_INVALID_ARGUMENT;
     if (rows < 1 || rows - 1 > h->max_k || q_heads < 1 || q_heads > 65536 || q_heads % cache->kv_heads ||
-        !std::isfinite(scale))
+        !std::isfinite(scale) || !std::isfinite(attn_scale(scale)))
         return SPECV_ERR_INVALID_ARGUMENT;
     if (batch == 0) return SPECV_OK;
     // (a segment's end writes its rows of out while others still read their queries)

@@ -59,6 +59,13 @@ struct AttnArgs {
     uint32_t polls;  // most polls of a wait
 };
 
+// Factor of the scores in base 2.  A scale of zero still has to tell hidden
+// positions (an infinite score) from the others: the smallest number there is,
+// so that the largest scores differ by less than 2^-20 of a weight.
+__host__ __device__ __forceinline__ float attn_scale(float scale) {
+    return scale == 0.0f ? 1.40129846e-45f : scale * 1.44269504f;
+}
+
 // ------------------------------------------------------------------ the cut
 // Positions of sequence b that are attended to; -1 if it is refused by its length.
 __device__ __forceinline__ int attn_len(const AttnArgs& a, int b) {
@@ -417,8 +424,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
     const AttnWork work = attn_work(a.workspace, ctas, TM, DP);
     const uint32_t base_s = smem_u32(smem);
     const int m_rows = a.rows * static_cast<int>(a.group.d);  // rows of a kv head
-    // a scale of zero still has to tell hidden positions (an infinite score) from the others
-    const float c_scale = a.scale == 0.0f ? 1e-30f : a.scale * 1.44269504f;
+    const float c_scale = attn_scale(a.scale);
     const float hidden = c_scale < 0.0f ? INFINITY : -INFINITY;
 
     AttnCursor cur, ahead, ids;

@@ -583,8 +583,7 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
     const int m_rows = a.rows * static_cast<int>(a.group.d);
     const uint32_t lanes = static_cast<uint32_t>(row & ~31) << 16;
     const uint32_t ts = sh.tmem + x * 128 + lanes;
-    // a scale of zero still has to tell hidden positions (an infinite score) from the others
-    const float scale = a.scale == 0.0f ? 1e-30f : a.scale * 1.44269504f;
+    const float scale = attn_scale(a.scale);
     const float hidden = scale < 0.0f ? INFINITY : -INFINITY;
     uint32_t s_seen = 0, o_seen = 0;
     int j0 = 0, seg = 0, use0 = 0;

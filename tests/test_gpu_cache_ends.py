@@ -139,3 +139,26 @@ def test_append_leaves_padding_alone(sv, h, dtype, B, rows, rot, inter):  # noqa
         results.append((got["q_out"], kc, vc))
     for other in results[1:]:
         assert all(torch.equal(a, b) for a, b in zip(results[0], other))
+
+
+@pytest.mark.parametrize("rows,hq", MANY)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_scale_of_zero_weighs_evenly(sv, h, dtype, rows, hq):  # noqa: F811
+    """Whatever the scores' size: here 1e31."""
+    c = Case(rows + 3, dtype, 2, rows, hq, 2, 64, 16, [90, rows + 5], "tree", q_scale=1e30)
+    c.check(c.call(sv, h, scale=0.0), scale=0.0)
+    c.check(c.call(sv, h, scale=-0.0), scale=0.0)
+
+
+def test_scales_out_of_range_are_refused(sv, h):  # noqa: F811
+    """A scale has to be finite, and so has scale * log2(e), the factor of the
+    scores in base 2."""
+    c = Case(1, "f32", 1, 2, 2, 2, 64, 16, [20], "tree", q_scale=1e-30)
+    before = sv.specv_launch_count(h)
+    for scale in (3e38, -2.4e38, math.inf, -math.inf, math.nan, 1e40):
+        with pytest.raises(sv.SpecvError):
+            c.call(sv, h, scale=scale)
+    assert sv.specv_launch_count(h) == before
+    got = c.call(sv, h, scale=2.3e38)
+    assert np.isfinite(_np(got["out"])).all() and np.isfinite(_np(got["lse"])).all()
+    c.check(c.call(sv, h, scale=1e-45), scale=1e-45)

@@ -306,14 +306,20 @@ typedef struct {
  *               values of each head of q and k turn in pairs by the angle
  *               position * inv_freq[j]; pair j is (j, j + rot_dim / 2), or
  *               (2j, 2j + 1) if interleaved.  rot_dim 0: no rotation
- *               (inv_freq may be NULL).  The angle is formed in float64, the
- *               products in fp32, rounded once
+ *               (inv_freq may be NULL).  The angle is formed and brought into
+ *               [-pi, pi] in float64; its sine and cosine and the products are
+ *               fp32 (together off by at most 2^-21 of |x0| + |x1|), rounded
+ *               once
  *   parents     [B, rows - 1] int32 as for specv_verify_tree_greedy; NULL:
  *               every sequence is a chain (then rows is not bounded by max_k,
  *               so that prompts can be appended)
  *   row_counts  [B] int32, 0..rows: the rows of each sequence that are tokens,
  *               the others being padding that is not read; NULL: all rows
- *               (none of an idle sequence).  Outside: bit 2048
+ *               (none of an idle sequence).  Outside: bit 2048.  This is for
+ *               prompts: specv_tree_attention and specv_cache_compact know no
+ *               counts and take a sequence's last `rows` positions (last M)
+ *               for the pass's, so that a pass whose counts are below rows is
+ *               not one for them (they cannot tell; use a call for each count)
  *   row_status  [B] out (nullable): 0, or bits 512 (a parent outside
  *               [-1, i)), 2048, 4096.  Of a refused sequence nothing is written
  *               to the cache
@@ -349,7 +355,15 @@ specv_status specv_cache_append(specv_handle h, const specv_kv_cache *cache, con
  *   workspace   device memory of specv_tree_attention_workspace(...) bytes,
  *               256-byte aligned, the call's own until it has run
  * Positions that a row does not see take no part, whatever they hold (NaN and
- * infinities among them). */
+ * infinities among them).  Sums are fp32.  Weights exp(score - m), with m at
+ * most 8 log 2 below the row's largest score so far, are rounded to bf16 for the
+ * product with the values of a bf16 cache (2^-9 each on average, 2^-8 at most,
+ * so that an output is off by up to 2^-8 of the weighted mean of |v|, besides
+ * its own rounding; their sum, and so lse, is not rounded); those of an fp32
+ * cache, and its values, go in as two tf32 parts (products off by 3 * 2^-22 at
+ * most).  Sums of weight * value are divided by the sum of the weights at the
+ * end: of values above 2^119 or so they may leave fp32's range though the
+ * result would not. */
 specv_status specv_tree_attention(specv_handle h, const specv_kv_cache *cache, const void *q, int64_t q_stride,
                                   int q_heads, const int32_t *parents, int batch, int rows, float scale, void *out,
                                   float *lse, int32_t *row_status, void *workspace, int64_t workspace_bytes,

@@ -439,7 +439,8 @@ def specv_cache_append(h: Handle, k_cache, v_cache, block_tables, seq_lens, k, v
     (optional) of the caches' type, rows evenly spaced; inv_freq
     [rot_dim / 2] fp32 (None: no rotation); parents [B, rows - 1] int32
     (None: chains, or prompts); row_counts [B] int32 (None: all rows are
-    tokens).  Returns a dict: q_out (with q) and row_status [B]; ``out`` may
+    tokens; counts below ``rows`` are for prompts, as specv_tree_attention and
+    specv_cache_compact know none).  Returns a dict: q_out (with q) and row_status [B]; ``out`` may
     supply them."""
     c, _, _ = _kv_cache(h, k_cache, v_cache, block_tables, seq_lens)
     if k.dim() != 4:
@@ -481,6 +482,8 @@ def specv_tree_attention(h: Handle, q, k_cache, v_cache, block_tables, seq_lens,
     q [B, rows, q_heads, head_dim], rows evenly spaced, rows <= max_k + 1;
     the caches, block_tables and seq_lens as for specv_cache_append; parents
     [B, rows - 1] int32 (None: chains); scale defaults to head_dim ** -0.5.
+    The pass's rows are the last ``rows`` positions of every sequence.  Weights
+    of a bf16 cache are rounded to bf16 for the product with the values.
     Returns a dict: out [B, rows, q_heads, head_dim], row_status [B] and,
     with ``lse``, lse [B, rows, q_heads] fp32; ``out`` may supply them.
     ``workspace`` may supply a CUDA uint8 tensor of at least

@@ -1,0 +1,89 @@
+"""The calls on the paged KV cache at shapes between their kernels' tiles:
+many query heads to a kv head, row tiles without rows, long prompts, blocks
+that sequences share."""
+import numpy as np
+import pytest
+
+import cache_plain as P
+from test_gpu_cache import Case, _dev, _np, _rounded, h, sv, test_append_matches_the_formula  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+check_append = test_append_matches_the_formula
+del test_append_matches_the_formula
+
+GROUPS = [
+    # B, rows, q heads, kv heads, dim, block, lengths, tree
+    (2, 32, 16, 1, 128, 16, [32, 300], "tree"),   # 512 rows a kv head: two row tiles of 256, queries as boxes of 8 rows
+    (1, 32, 32, 1, 64, 16, [200], "tree"),        # 1024 rows, boxes of 4
+    (2, 9, 32, 1, 128, 16, [9, 300], "tree"),     # 288 rows: the last tile's second half has none
+    (2, 5, 32, 1, 64, 32, [5, 140], "star"),      # 160 rows: 32 in the second half
+    (2, 17, 16, 2, 128, 16, [40, 290], "tree"),   # 136 rows: 8 in the second half
+    (2, 16, 16, 2, 128, 16, [16, 290], "line"),   # 256 rows: both halves full
+    (2, 8, 16, 1, 128, 16, [8, 129], "tree"),     # 128 rows: one half
+    (2, 12, 24, 2, 112, 64, [12, 200], "tree"),   # 144 rows, groups that fill no row tile
+    (1, 32, 128, 1, 128, 16, [180], "tree"),      # a row a box, 4096 rows
+    (1, 3, 256, 1, 64, 16, [150], "tree"),        # groups above a row tile
+    (1, 1, 256, 1, 128, 16, [300], "chain"),
+    (2, 2, 64, 1, 16, 128, [2, 260], "tree"),
+    (3, 32, 16, 2, 80, 8, [33, 127, 128], "star"),
+    (3, 25, 32, 4, 64, 256, [25, 256, 513], "tree"),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", GROUPS, ids=lambda s: "B%d_R%d_H%d-%d_D%d_bs%d_%s" % (s[:6] + (s[7],)))
+def test_many_query_heads_to_a_kv_head(sv, h, dtype, shape):  # noqa: F811
+    B, rows, hq, hkv, dim, bs, lens, kind = shape
+    c = Case(B * 900 + rows * 10 + dim, dtype, B, rows, hq, hkv, dim, bs, lens, kind)
+    c.check(c.call(sv, h))
+
+
+@pytest.mark.parametrize("rows,hq", [(3, 4), (17, 8), (32, 16)])
+def test_sequences_that_share_blocks(sv, h, rows, hq):  # noqa: F811
+    """A common prefix held once: block tables that name the same blocks."""
+    c = Case(rows, "bf16", 4, rows, hq, 2, 64, 16, [rows + 200, rows + 230, rows + 64, rows + 300], "tree", poison=False)
+    c.tables[1, :12], c.tables[2, :4], c.tables[3, :12] = c.tables[0, :12], c.tables[0, :4], c.tables[0, :12]
+    c.check(c.call(sv, h))
+
+
+PROMPTS = [
+    # B, rows, q heads, kv heads, dim, block, lengths, tree, rot, interleaved, counts
+    (2, 2500, 2, 1, 64, 16, [2600, 1999], "chain", 64, False, [2500, 1999]),
+    (1, 3500, 1, 1, 16, 1, [3501], "chain", 8, True, None),
+    (2, 2100, 3, 1, 32, 64, [0, 2100], "chain", 6, False, [0, 2100]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", PROMPTS, ids=lambda s: "B%d_R%d_H%d-%d_D%d_bs%d" % s[:6])
+def test_long_prompts(sv, h, dtype, shape):  # noqa: F811
+    check_append(sv, h, dtype, shape)
+
+
+@pytest.mark.parametrize("rows,hq", [(3, 4), (17, 8), (32, 16)])
+def test_append_then_attention_for_each_count(sv, h, rows, hq):  # noqa: F811
+    """A batch whose passes differ in rows, as the header has it: appended with
+    row counts, attended to by a call for each count."""
+    import torch
+
+    rng = np.random.default_rng(rows)
+    c = Case(rows, "f32", 4, rows, hq, 2, 64, 16, [rows + 40] * 4, "tree", poison=False)
+    counts = np.array([rows, 1 + rows // 2, rows, 1 + rows // 2], np.int32)
+    lens = 40 + counts
+    (k_t, k), (v_t, v) = (_rounded(rng, (4, rows, 2, 64), c.dtype) for _ in range(2))
+    tables, par = _dev(c.tables), _dev(c.parents)
+    kc, vc = c.kc.copy(), c.vc.copy()
+    got = sv.specv_cache_append(h, c.kc_t, c.vc_t, tables, _dev(lens), k_t, v_t, parents=par, row_counts=_dev(counts))
+    assert not got["row_status"].any()
+    P.append(kc, vc, c.tables, lens, k, v, parents=c.parents, counts=counts)
+    np.testing.assert_array_equal(_np(c.kc_t), kc)
+    for n in sorted(set(counts.tolist())):
+        pick = np.flatnonzero(counts == n)
+        at = torch.from_numpy(pick).cuda()
+        sub_par = c.parents[pick][:, :n - 1]
+        one = sv.specv_tree_attention(h, c.q_t[at][:, :n].contiguous(), c.kc_t, c.vc_t, tables[at].contiguous(),
+                                      _dev(lens[pick]), parents=_dev(sub_par), lse=True)
+        out, lse, status, avg, mag = P.attention(c.q[pick][:, :n], kc, vc, c.tables[pick], lens[pick], sub_par, c.scale)
+        t_out, t_lse = P.attention_bounds(out, lse, avg, mag, int(lens.max()), 64, False)
+        assert not one["row_status"].any() and not status.any()
+        assert (np.abs(_np(one["out"]) - out) <= t_out).all() and (np.abs(_np(one["lse"]) - lse) <= t_lse).all()

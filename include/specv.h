@@ -326,7 +326,8 @@ typedef struct {
  * Row r goes to cache position base + r, base = seq_lens - row count, and has
  * the rotary position base + depth(r): depth(0) = 0, a child one more than
  * its parent, so that a kept path keeps its rotation when specv_cache_compact
- * moves it.  Sequences of a batch must not share the blocks they write to. */
+ * moves it.  Sequences of a batch must not share the blocks they write to, nor
+ * a table name one of these twice. */
 specv_status specv_cache_append(specv_handle h, const specv_kv_cache *cache, const void *q, int64_t q_stride,
                                 int q_heads, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                                 const float *inv_freq, int rot_dim, int interleaved, const int32_t *parents,

@@ -281,8 +281,8 @@ specv_status specv_cache_append(specv_handle h, const specv_kv_cache* cache, con
 int64_t specv_tree_attention_workspace(specv_handle h, specv_dtype dtype, int kv_heads, int head_dim, int q_heads,
                                        int batch, int rows) {
     if (!h || (dtype != SPECV_F32 && dtype != SPECV_BF16) || kv_heads < 1 || head_dim < 16 || head_dim > 256 ||
-        head_dim % 16 || q_heads < 1 || q_heads % kv_heads || batch < 1 || batch > h->max_batch || rows < 1 ||
-        rows - 1 > h->max_k)
+        head_dim % 16 || q_heads < 1 || q_heads > 65536 || q_heads % kv_heads || batch < 1 ||
+        batch > h->max_batch || rows < 1 || rows - 1 > h->max_k)
         return 0;
     const AttnPlan& p = attn_plan(dtype, head_dim, rows * (q_heads / kv_heads));
     return attn_work_bytes(h->sm_count * p.ctas, p.tm, p.dp);

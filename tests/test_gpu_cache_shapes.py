@@ -87,3 +87,14 @@ def test_append_then_attention_for_each_count(sv, h, rows, hq):  # noqa: F811
         t_out, t_lse = P.attention_bounds(out, lse, avg, mag, int(lens.max()), 64, False)
         assert not one["row_status"].any() and not status.any()
         assert (np.abs(_np(one["out"]) - out) <= t_out).all() and (np.abs(_np(one["lse"]) - lse) <= t_lse).all()
+
+
+def test_workspace_of_invalid_sizes_is_none(sv, h):  # noqa: F811
+    """0 where specv_tree_attention refuses the sizes, at every end of them."""
+    need = lambda dt=sv.SPECV_BF16, kv=8, dim=128, q=32, batch=4, rows=17: (  # noqa: E731
+        sv.specv_tree_attention_workspace(h, dt, kv, dim, q, batch, rows))
+    assert need() > 0 and need(kv=65536, q=65536) > 0 and need(kv=1, q=65536, rows=32) > 0
+    for kw in (dict(dt=2), dict(kv=0), dict(dim=8), dict(dim=24), dict(dim=272), dict(q=0), dict(q=33),
+               dict(kv=1, q=65537), dict(kv=1, q=2 ** 30, rows=32), dict(kv=131072, q=131072), dict(batch=0),
+               dict(batch=513), dict(rows=0), dict(rows=33)):
+        assert need(**kw) == 0, kw

@@ -9,13 +9,16 @@
 // it gets is 16 bytes each: pieces of a head that turn together (j and
 // j + rot / 2, or two neighbours).
 //
-// Measured (GB300; bytes counted once, of 6691 GB/s measured): 4 ragged
-// prompts of up to 2048 tokens, 32/8 heads of 128 in bf16, 26.2 us, 86%; 64
-// trees of 17 rows 5.6 us, 71%; one token for 8 sequences 2.6 us (launch and
+// Measured (GB300, graph replays over sets of inputs of more than twice the L2;
+// bytes counted once, of 6691 GB/s measured): 4 ragged prompts of up to 2048
+// tokens, 32/8 heads of 128 in bf16, 26.1 us, 87%; 64 trees of 17 rows 7.7 us,
+// 52% (5.7 with inputs in the L2); one token for 8 sequences 2.4 us (launch and
 // the chain of loads).  Prompts issue an instruction in two of three cycles:
 // rotation in packed pairs and angles that stay in registers took them from
 // 51 us to 31, CTAs of half the threads (a token that waits holds less of the
-// SM) to 28.6, leaving padding unread to 26.2.
+// SM) to 28.6, leaving padding unread to 26.1.  One prompt of 32,768
+// tokens takes 120 us, all of the copy rate; in blocks of 1 it takes 285,
+// because every token looks at all blocks that its sequence writes to.
 //
 // Angles are formed in float64 (position * inv_freq passes 2^24 for far
 // positions, where fp32 would lose the fraction of a turn), brought into
@@ -27,8 +30,8 @@
 namespace specv {
 
 // Threads of a CTA: as many for a few tokens, half of them where the tokens
-// are more than the SMs hold at once.  Prompts as above 30.9 us with 192, 28.6
-// with 96 (64: 28.1), trees 6.7 and 5.6, one token for 8 sequences 2.6 and 3.0.
+// are more than the SMs hold at once.  Prompts as above 28.6 us with 192, 26.1
+// with 96 (64: 26.4), trees 8.9 and 7.7, one token for 8 sequences 2.4 and 2.7.
 constexpr int kAppendFew = 192, kAppendMany = 96;
 constexpr int kAppendResident = 960;  // threads of an SM
 constexpr int kAppendHeads = 2;  // whose pieces a thread has in flight

@@ -8,10 +8,11 @@
 // place stored to is never one that a later move reads).  Nodes that are in
 // place already are left out.
 //
-// Measured (GB300): 32 layers of 64 sequences, up to 4 nodes of 8 heads of 128
-// in bf16 each, 5.8 us, 89% of 6691 GB/s for 34 MB; one layer of 8 sequences
-// 2.2 us.  Bound by the chain length, table, node, which at most twelve CTAs a
-// sequence go through (64: 6.2 us).
+// Measured (GB300, graph replays over sets of inputs of more than twice the
+// L2): 32 layers of 64 sequences, up to 4 nodes of 8 heads of 128 in bf16 each,
+// 7.5 us, 68% of 6691 GB/s for 34 MB (5.8 with inputs in the L2); one layer of 8
+// sequences 2.0 us.  Bound by the chain length, table, node, which at most
+// twelve CTAs a sequence go through (64: 7.5 us too, 6.2 in the L2).
 #pragma once
 #include "kv_cache.cuh"
 

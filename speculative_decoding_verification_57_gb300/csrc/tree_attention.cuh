@@ -28,11 +28,14 @@
 // the rest is in tree_attention_tc.cuh.  fp32 values enter the tensor cores as
 // two tf32 parts, three products each.
 //
-// Measured (GB300, graph replays over 3 sets of inputs; bytes counted once, of
-// 6691 GB/s measured): single rows, 32/8 heads of 128 in bf16, for 8 sequences
-// over 500..1000 positions 14.6 us, 26%; for 64 over 1000..2000 75 us, 80%;
-// fp32 chains of 5, 12 heads of 64, for 8 sequences over 500..1000 23.5 us,
-// 25%.  The short ones are bound by the chain launch, length, block, tile
+// Measured (GB300, graph replays over sets of inputs of more than twice the L2;
+// bytes counted once, of 6691 GB/s measured): single rows, 32/8 heads of 128 in
+// bf16, for 8 sequences over 500..1000 positions 15.8 us, 24%; for 64 over
+// 1000..2000 75 us, 80%; heads of 256, 64 sequences: single rows over 1000..2000
+// (16/4 heads) 95 us, 63%, trees of 17 rows over 2048..4096 573 us, 22%, three
+// row tiles reading the cache each; fp32 chains of 5, 12 heads of 64, for 8
+// sequences over 500..1000 23.3 us, 25%, for 64 102 us, 44%, and 40 rows of a kv
+// head over 120,000 positions 152 us for a floor of 18.  The short ones are bound by the chain launch, length, block, tile
 // (about 8 us) and by the join (4.5 us); fp32 by instructions (to split keys
 // and values) with 12 warps an SM.
 #pragma once

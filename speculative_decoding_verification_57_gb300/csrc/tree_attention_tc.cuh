@@ -25,18 +25,20 @@
 // turns, they took the trees and the wide trees of the list below from 178 and
 // 149 us to 156 and 129).
 //
-// Measured (GB300, 2070 MHz, graph replays over 3 sets of inputs; bytes and
-// operations counted once; of 6691 GB/s and 1926 TFLOP/s measured):
+// Measured (GB300, 2070 MHz, graph replays over sets of inputs of more than
+// twice the L2; bytes and operations counted once; of 6691 GB/s and 1926 TFLOP/s measured):
 //   64 chains of 6 rows, 32/8 heads of 128, 1000..2000 positions    77 us  78%
 //   64 trees of 17 rows, same heads, 2048..4096                    147 us  84%
-//   one tree of 17 rows, same heads, 131072                         93 us  86%
-//   16 trees of 32 rows, 64/8 heads, 4096..8192 (WIDE)             109 us  59%,
-//     967 TFLOP/s, 50%
+//   one tree of 17 rows, same heads, 131072                         94 us  85%
+//   16 trees of 32 rows, 64/8 heads, 4096..8192 (WIDE)             108 us  59%,
+//     972 TFLOP/s, 50%
 // With one row tile the memory bounds it, short of it by each run's start
 // (5 us), its segments' ends and the join (5 to 10 us).  WIDE, a tile takes a
 // stream 3500 cycles: 1300 for its products (16 instructions of 64 cycles and
 // their issue), 1900 for its weights, the rest to tell one of the other; two
-// streams hide half of that.
+// streams hide half of that.  The compiler counts 128 registers a thread for all
+// roles (what the launch has, not what the softmax warps get) and spills 300 to
+// 560 bytes of them a thread.
 #pragma once
 #include <cuda.h>
 

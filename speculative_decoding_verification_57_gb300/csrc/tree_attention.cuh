@@ -454,7 +454,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
             const int t = ids.tile * KT + tid;
             if (tid < KT && t < ids.len) {
                 const int lb = kv.block.div(t);
-                p.blk = __ldg(kv.tables + static_cast<int64_t>(ids.b) * kv.max_blocks + lb);
+                // (no read-only load: the kernel may have started before the one that wrote the table ended)
+                p.blk = kv.tables[static_cast<int64_t>(ids.b) * kv.max_blocks + lb];
                 p.in = t - lb * kv.block_size();
                 p.h = ids.s / a.row_tiles;
             }

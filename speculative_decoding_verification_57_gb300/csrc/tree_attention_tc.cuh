@@ -318,7 +318,7 @@ __device__ void tc_box_role(const AttnArgs& a, const TcMaps& maps, TcShared<S>& 
         const int t = tile * S::KT + part * rows;
         x.in = mine && t < it.cur.len;
         const int lb = kv.block.div(x.in ? t : 0);
-        x.blk = x.in ? __ldg(kv.tables + static_cast<int64_t>(it.cur.b) * kv.max_blocks + lb) : 0;
+        x.blk = x.in ? kv.tables[static_cast<int64_t>(it.cur.b) * kv.max_blocks + lb] : 0;
         x.row = t - lb * kv.block_size();
         x.h = it.cur.s / a.row_tiles;
         x.seg = it.seg;
@@ -440,7 +440,7 @@ __device__ void tc_copy_role(const AttnArgs& a, TcShared<S>& sh, const AttnCurso
         const int t = tile * S::KT + mine;
         if (t < it.cur.len) {
             const int lb = kv.block.div(t);
-            const int blk = __ldg(kv.tables + static_cast<int64_t>(it.cur.b) * kv.max_blocks + lb);
+            const int blk = kv.tables[static_cast<int64_t>(it.cur.b) * kv.max_blocks + lb];
             if (kv.valid(blk))
                 at = kv.at(blk, it.cur.s / a.row_tiles, t - lb * kv.block_size());
             else

@@ -98,3 +98,34 @@ def test_workspace_of_invalid_sizes_is_none(sv, h):  # noqa: F811
                dict(kv=1, q=65537), dict(kv=1, q=2 ** 30, rows=32), dict(kv=131072, q=131072), dict(batch=0),
                dict(batch=513), dict(rows=0), dict(rows=33)):
         assert need(**kw) == 0, kw
+
+
+@pytest.mark.parametrize("rows,hq", [(1, 4), (3, 4), (17, 8), (32, 16)])
+def test_tables_and_lengths_written_just_before(sv, h, rows, hq):  # noqa: F811
+    """Kernels that write the tables, lengths, trees and queries, with the
+    call right behind them, many times over: every call sees its own."""
+    import torch
+
+    cases = [Case(rows + i, "bf16", 3, rows, hq, 2, 64, 16, lens, "tree", width=40, poison=False)
+             for i, lens in enumerate(([rows, 500, 90], [610, rows + 1, 33 + rows]))]
+    blocks = max(c.kc_t.shape[0] for c in cases)
+    kc = torch.zeros((2, blocks, 2, 16, 64), dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    src = []
+    for i, c in enumerate(cases):
+        kc[i, :c.kc_t.shape[0]], vc[i, :c.vc_t.shape[0]] = c.kc_t, c.vc_t
+        shift = np.where(c.tables >= 0, c.tables + i * blocks, -1).astype(np.int32)  # in one pool of both
+        src.append((_dev(shift), _dev(c.lens), _dev(c.parents), c.q_t))
+    pool_k, pool_v = kc.view(-1, 2, 16, 64), vc.view(-1, 2, 16, 64)
+    now = [torch.zeros_like(t) for t in src[0]]
+    outs = []
+    for i in range(40):
+        for t, s in zip(now, src[i % 2]):
+            t.copy_(s)
+        outs.append(sv.specv_tree_attention(h, now[3], pool_k, pool_v, now[0], now[1], parents=now[2], lse=True))
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        if i < 2:
+            cases[i].check(out)
+        else:
+            assert torch.equal(out["out"], outs[i % 2]["out"]) and torch.equal(out["lse"], outs[i % 2]["lse"])

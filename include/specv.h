@@ -389,6 +389,97 @@ specv_status specv_cache_compact(specv_handle h, const specv_kv_cache *cache, in
                                  const int32_t *path, const int32_t *num_accepted, int batch, int M,
                                  int32_t *row_status, void *stream);
 
+/* Norms of the heads of an append (each weight nullable: those heads are
+ * then not normed): a head x of queries or keys becomes x * rsqrt(mean(x^2) +
+ * eps) * (weight + weight_add) before its pairs turn.  Weights [head_dim] of
+ * the cache's type, device memory; weight_add 1 for models that keep weights as
+ * their difference from one, else 0.  eps >= 0 and weight_add finite. */
+typedef struct {
+    const void *q_weight, *k_weight;
+    float eps, weight_add;
+} specv_head_norm;
+
+/* Rotary positions of an append, where they are not base + depth.
+ *   positions  [B, rows, axes] int32 (nullable): the position of each row on
+ *              each axis (time, height and width of a patch of an image or
+ *              video, say), any number.  Then offsets and parents are NULL
+ *   axes       1..16
+ *   pair_axis  [rot_dim / 2], HOST memory, read by the call: the axis, below
+ *              axes, by whose position pair j turns (inv_freq[j] as ever).
+ *              NULL with one axis
+ *   offsets    [B] int32 (nullable; without positions): added to base + depth,
+ *              for sequences whose positions run ahead of the cache (behind
+ *              an eviction) or behind it (behind images) */
+typedef struct {
+    int axes;
+    const int32_t *positions;
+    const uint8_t *pair_axis;
+    const int32_t *offsets;
+} specv_positions;
+
+/* specv_cache_append for models that norm the heads of queries and keys
+ * and for positions on several axes: in addition `norm` and `positions`,
+ * both nullable (and then exactly that call).  Norms, turns and products are fp32
+ * with one rounding at the end; the mean of squares is fp32 too: a head
+ * with values beyond 2^63 has an infinite one and comes out as zeros.
+ * Everything else as there. */
+specv_status specv_cache_append_norm(specv_handle h, const specv_kv_cache *cache, const void *q, int64_t q_stride,
+                                     int q_heads, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                     const specv_head_norm *norm, const float *inv_freq, int rot_dim, int interleaved,
+                                     const specv_positions *positions, const int32_t *parents,
+                                     const int32_t *row_counts, int batch, int rows, void *q_out, int32_t *row_status,
+                                     void *stream);
+
+/* The attention weight that the positions of a cache gather from a pass, for
+ * specv_cache_evict: mass_out[b, h, t] = mass[b, h, t] + the sum, over the
+ * pass's rows r that see position t and the query heads g of kv head h, of
+ * exp(scale * q . k_t - lse[b, r, g]).
+ *   q, q_stride, q_heads, parents, rows, scale  as for specv_tree_attention
+ *   lse         [B, rows, q_heads] fp32, as specv_tree_attention (or
+ *               specv_prefix_attention) left it.  A row whose lse is infinite
+ *               takes no part (set it so for rows of rejected drafts)
+ *   mass        [B, kv_heads, width] fp32 (nullable: zeros).  The pass's own
+ *               positions start from 0: what it holds there is not read
+ *   mass_out    [B, kv_heads, width] fp32 out; mass itself, or other memory.
+ *               Written for positions first .. length - 1
+ *   first       positions before it are left alone (a shared prefix)
+ *   row_status  [B] out (nullable): 0, or bits 512, 2048 (also a length above
+ *               width), 4096.  Of a refused sequence nothing is written
+ * Sums are fp32 in a fixed order: results repeat.  The values of the cache are
+ * not read. */
+specv_status specv_attention_mass(specv_handle h, const specv_kv_cache *cache, const void *q, int64_t q_stride,
+                                  int q_heads, const int32_t *parents, int batch, int rows, float scale,
+                                  const float *lse, const float *mass, float *mass_out, int64_t width, int first,
+                                  int32_t *row_status, void *stream);
+
+/* Eviction: sequences longer than `budget` are brought back to it, in keys and
+ * values of `layers` layers at once (as specv_cache_compact counts them).  Of
+ * each layer and kv head the first `first` and the last `recent` positions
+ * stay, and of those between the budget - first - recent with the largest mass
+ * (equal ones: the lower position; NaN counts as the largest).  Below line =
+ * budget - recent kept positions stay where they are, the i-th hole there
+ * takes the i-th kept position above, and the recent ones follow from the line
+ * on in their order.  (Attention asks for no order among positions before a
+ * pass; rotary positions are in the keys, and go on with specv_positions.offsets
+ * raised by `evicted`.)
+ *   mass        [layers, B, kv_heads, width] fp32 as specv_attention_mass
+ *               gathers it
+ *   mass_out    [layers, B, kv_heads, width] out: the masses of the positions
+ *               that remain, at their places; not mass's memory.  Behind the new
+ *               length it is left alone
+ *   budget      1 or more, at least first + recent
+ *   lens_out    [B] out: the new lengths; not cache->seq_lens' memory
+ *   evicted     [B] out (nullable): old minus new length
+ *   row_status  [B] out (nullable): 0, or bits 2048 (also a length above
+ *               width), 4096 (an entry from position `first` on outside the
+ *               pool).  Of a refused sequence nothing moves, and its length stays
+ * Sequences must not share blocks from position `first` on.  Blocks that are
+ * no longer in use stay in the tables: specv_rollback with these lengths and
+ * num_accepted = k pops them into the free list. */
+specv_status specv_cache_evict(specv_handle h, const specv_kv_cache *cache, int layers, int64_t layer_stride,
+                               const float *mass, float *mass_out, int64_t width, int batch, int budget, int recent,
+                               int first, int32_t *lens_out, int32_t *evicted, int32_t *row_status, void *stream);
+
 /* Number of CTAs per sequence (thread-block cluster size, 1..16) that the
  * next call with these sizes would use; 0 if the sizes are invalid. */
 int specv_plan_cluster(specv_handle h, specv_dtype logits_dtype, int batch, int k, int64_t V);

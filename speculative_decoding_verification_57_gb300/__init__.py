@@ -27,6 +27,9 @@ __all__ = [
     "specv_tree_attention",
     "specv_tree_attention_workspace",
     "specv_cache_compact",
+    "specv_cache_append_norm",
+    "specv_attention_mass",
+    "specv_cache_evict",
     "specv_plan_cluster",
     "specv_test_withhold_stage",
     "specv_launch_count",
@@ -419,29 +422,20 @@ def _stream_of(h, stream):
     return _raw_stream(h.device) if stream is None else stream.cuda_stream
 
 
-def _empty(h, shape, dtype, stream):
+def _empty(h, shape, dtype, stream, zero=False):
     """A tensor for a call on ``stream``: allocated there, so that its memory
     is not handed on before the call has run."""
     torch = _torch()
+    make = torch.zeros if zero else torch.empty
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", h.device))
+        return make(shape, dtype=dtype, device=torch.device("cuda", h.device))
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", h.device))
+        return make(shape, dtype=dtype, device=torch.device("cuda", h.device))
 
 
-def specv_cache_append(h: Handle, k_cache, v_cache, block_tables, seq_lens, k, v, *, q=None, inv_freq=None,
-                       interleaved=False, parents=None, row_counts=None, out=None, stream=None):
-    """Append the keys and values of a pass to a paged cache, in place, and
-    rotate queries and keys by their positions on the way.  k_cache, v_cache
-    [blocks, kv_heads, block_size, head_dim] bf16 or fp32; block_tables
-    [B, max_blocks], seq_lens [B] int32, the lengths with the pass's rows;
-    k, v [B, rows, kv_heads, head_dim] and q [B, rows, q_heads, head_dim]
-    (optional) of the caches' type, rows evenly spaced; inv_freq
-    [rot_dim / 2] fp32 (None: no rotation); parents [B, rows - 1] int32
-    (None: chains, or prompts); row_counts [B] int32 (None: all rows are
-    tokens; counts below ``rows`` are for prompts, as specv_tree_attention and
-    specv_cache_compact know none).  Returns a dict: q_out (with q) and row_status [B]; ``out`` may
-    supply them."""
+def _append_args(h, k_cache, v_cache, block_tables, seq_lens, k, v, q, inv_freq, parents, row_counts, out, stream):
+    """What the two appends have in common: the arguments up to v's stride, the
+    rotation's, those from parents to rows, and the outputs'."""
     c, _, _ = _kv_cache(h, k_cache, v_cache, block_tables, seq_lens)
     if k.dim() != 4:
         raise ValueError("k must have the shape [B, rows, kv_heads, head_dim]")
@@ -469,10 +463,67 @@ def specv_cache_append(h: Handle, k_cache, v_cache, block_tables, seq_lens, k, v
     if "row_status" not in out:
         out["row_status"] = _empty(h, (B,), _i32, stream)
     ps = _on(h, out["row_status"], _i32, "row_status", (B,))
-    st = _lib.load().specv_cache_append(
-        h.ptr, c, pq, q_stride, q_heads, pk, k_stride, pv, v_stride, pf, rot, 1 if interleaved else 0, pp, pc, B, rows,
-        po, ps, _stream_of(h, stream))
+    return (h.ptr, c, pq, q_stride, q_heads, pk, k_stride, pv, v_stride), (pf, rot), (pp, pc, B, rows), (po, ps), out
+
+
+def specv_cache_append(h: Handle, k_cache, v_cache, block_tables, seq_lens, k, v, *, q=None, inv_freq=None,
+                       interleaved=False, parents=None, row_counts=None, out=None, stream=None):
+    """Append the keys and values of a pass to a paged cache, in place, and
+    rotate queries and keys by their positions on the way.  k_cache, v_cache
+    [blocks, kv_heads, block_size, head_dim] bf16 or fp32; block_tables
+    [B, max_blocks], seq_lens [B] int32, the lengths with the pass's rows;
+    k, v [B, rows, kv_heads, head_dim] and q [B, rows, q_heads, head_dim]
+    (optional) of the caches' type, rows evenly spaced; inv_freq
+    [rot_dim / 2] fp32 (None: no rotation); parents [B, rows - 1] int32
+    (None: chains, or prompts); row_counts [B] int32 (None: all rows are
+    tokens; counts below ``rows`` are for prompts, as specv_tree_attention and
+    specv_cache_compact know none).  Returns a dict: q_out (with q) and row_status [B]; ``out`` may
+    supply them."""
+    head, turn, rows, to, out = _append_args(h, k_cache, v_cache, block_tables, seq_lens, k, v, q, inv_freq, parents,
+                                             row_counts, out, stream)
+    st = _lib.load().specv_cache_append(*head, *turn, 1 if interleaved else 0, *rows, *to, _stream_of(h, stream))
     _check(st, "specv_cache_append")
+    return out
+
+
+def specv_cache_append_norm(h: Handle, k_cache, v_cache, block_tables, seq_lens, k, v, *, q=None, q_norm=None,
+                            k_norm=None, eps=1e-6, weight_add=0.0, inv_freq=None, interleaved=False, positions=None,
+                            pair_axis=None, offsets=None, parents=None, row_counts=None, out=None, stream=None):
+    """specv_cache_append for models that norm the heads of queries and keys,
+    and for positions on several axes.  q_norm, k_norm [head_dim] of the
+    caches' type (None: not normed): a head x becomes x * rsqrt(mean(x^2) +
+    eps) * (weight + weight_add) before it turns.  positions [B, rows, axes]
+    int32: each row's position on each axis, with pair_axis, bytes (or a
+    sequence) of rot_dim / 2 numbers, the axis that turns each pair (None with
+    one axis); or offsets [B] int32, added to base + depth.  The rest, and the
+    result, as for specv_cache_append."""
+    head, turn, rows, to, out = _append_args(h, k_cache, v_cache, block_tables, seq_lens, k, v, q, inv_freq, parents,
+                                             row_counts, out, stream)
+    norm = places = None
+    if q_norm is not None or k_norm is not None:
+        shape = k_cache.shape[-1:]
+        norm = _lib.SpecvHeadNorm(None if q_norm is None else _on(h, q_norm, k_cache.dtype, "q_norm", shape),
+                                  None if k_norm is None else _on(h, k_norm, k_cache.dtype, "k_norm", shape), eps,
+                                  weight_add)
+    if positions is not None:
+        if positions.dim() != 3:
+            raise ValueError("positions must have the shape [B, rows, axes]")
+        axes = positions.shape[2]
+        if axes < 1:
+            raise ValueError("positions need an axis")
+        pa = None if pair_axis is None else bytes(pair_axis)
+        if pa is not None and len(pa) != turn[1] // 2:
+            raise ValueError(f"pair_axis has {len(pa)} entries, expected {turn[1] // 2}")
+        if offsets is not None or parents is not None:
+            raise ValueError("positions go with neither offsets nor parents")
+        places = _lib.SpecvPositions(axes, _on(h, positions, _i32, "positions", (*k.shape[:2], axes)), pa, None)
+    elif pair_axis is not None:
+        raise ValueError("pair_axis needs positions")
+    elif offsets is not None:
+        places = _lib.SpecvPositions(1, None, None, _on(h, offsets, _i32, "offsets", (k.shape[0],)))
+    st = _lib.load().specv_cache_append_norm(*head, norm, *turn, 1 if interleaved else 0, places, *rows, *to,
+                                             _stream_of(h, stream))
+    _check(st, "specv_cache_append_norm")
     return out
 
 
@@ -548,6 +599,78 @@ def specv_cache_compact(h: Handle, k_cache, v_cache, block_tables, seq_lens, pat
     st = _lib.load().specv_cache_compact(h.ptr, c, layers, layer_stride, pp, pn, B, M, ps,
                                          _stream_of(h, stream))
     _check(st, "specv_cache_compact")
+
+
+def specv_attention_mass(h: Handle, q, k_cache, v_cache, block_tables, seq_lens, lse, *, mass=None, first=0,
+                         parents=None, scale=None, out=None, stream=None):
+    """The attention weight that the cache's positions gather from a pass:
+    mass[b, h, t] plus the sum of exp(scale * q . k_t - lse) over the pass's
+    rows that see position t and the query heads of kv head h.  q, the cache,
+    parents and scale as for specv_tree_attention, lse [B, rows, q_heads] fp32
+    as it left it (rows of an infinite lse take no part); mass [B, kv_heads,
+    width] fp32 (None: zeros; the pass's own positions start from zero);
+    positions before ``first`` are left alone.  Returns a dict: mass [B,
+    kv_heads, width] and row_status [B]; ``out`` may supply them (mass itself
+    among them).  Without it mass is new, zero where nothing is written, and
+    as wide as ``mass`` or the table."""
+    c, _, _ = _kv_cache(h, k_cache, v_cache, block_tables, seq_lens)
+    if q.dim() != 4:
+        raise ValueError("q must have the shape [B, rows, q_heads, head_dim]")
+    B, rows, q_heads = q.shape[:3]
+    if B != block_tables.shape[0]:
+        raise ValueError(f"q holds {B} sequences, block_tables {block_tables.shape[0]}")
+    pq, q_stride = _token_rows(h, q, "q", k_cache, (B, rows, q_heads, c.head_dim))
+    pp = None if parents is None else _on(h, parents, _i32, "parents", (B, rows - 1))
+    pl = _on(h, lse, _f32, "lse", (B, rows, q_heads))
+    out = {} if out is None else out
+    if "mass" not in out:
+        width = c.max_blocks * c.block_size if mass is None else mass.shape[-1]
+        out["mass"] = _empty(h, (B, c.kv_heads, width), _f32, stream, zero=True)
+    width = out["mass"].shape[-1]
+    po = _on(h, out["mass"], _f32, "out['mass']", (B, c.kv_heads, width))
+    pm = None if mass is None else _on(h, mass, _f32, "mass", (B, c.kv_heads, width))
+    if "row_status" not in out:
+        out["row_status"] = _empty(h, (B,), _i32, stream)
+    ps = _on(h, out["row_status"], _i32, "row_status", (B,))
+    st = _lib.load().specv_attention_mass(
+        h.ptr, c, pq, q_stride, q_heads, pp, B, rows, c.head_dim ** -0.5 if scale is None else scale, pl, pm, po, width,
+        int(first), ps, _stream_of(h, stream))
+    _check(st, "specv_attention_mass")
+    return out
+
+
+def specv_cache_evict(h: Handle, k_cache, v_cache, block_tables, seq_lens, mass, budget, *, recent=0, first=0, out=None,
+                      stream=None):
+    """Bring sequences longer than ``budget`` back to it, in place in the
+    caches [blocks, kv_heads, block_size, head_dim] or [layers, blocks, ...]:
+    of each layer and kv head the first ``first`` and the last ``recent``
+    positions stay, and of those between the ones of the largest mass; kept
+    ones above budget - recent fill the holes below it in order, the recent
+    ones follow.  mass [B, kv_heads, width] or [layers, B, kv_heads, width]
+    fp32.  Returns a dict: mass (new memory: the remaining positions' masses, zero
+    behind them), seq_lens [B] (the new lengths), evicted [B] and row_status
+    [B]; ``out`` may supply them, none of them the inputs' memory.  Rotary
+    positions go on with offsets raised by ``evicted``; specv_rollback with the
+    new lengths and num_accepted = k frees the blocks behind them."""
+    c, layers, layer_stride = _kv_cache(h, k_cache, v_cache, block_tables, seq_lens, layered=True)
+    B = block_tables.shape[0]
+    shape = (B, c.kv_heads) if k_cache.dim() == 4 else (layers, B, c.kv_heads)
+    pm = _on(h, mass, _f32, "mass", (*shape, mass.shape[-1]) if mass.dim() else None)
+    if mass.dim() == 0:
+        raise ValueError("mass must have the shape [B, kv_heads, width] or [layers, B, kv_heads, width]")
+    width = mass.shape[-1]
+    out = {} if out is None else out
+    if "mass" not in out:
+        out["mass"] = _empty(h, mass.shape, _f32, stream, zero=True)
+    for name in ("seq_lens", "evicted", "row_status"):
+        if name not in out:
+            out[name] = _empty(h, (B,), _i32, stream)
+    po = _on(h, out["mass"], _f32, "out['mass']", mass.shape)
+    pn, pe, ps = (_on(h, out[name], _i32, name, (B,)) for name in ("seq_lens", "evicted", "row_status"))
+    st = _lib.load().specv_cache_evict(h.ptr, c, layers, layer_stride, pm, po, width, B, int(budget), int(recent),
+                                       int(first), pn, pe, ps, _stream_of(h, stream))
+    _check(st, "specv_cache_evict")
+    return out
 
 
 def specv_plan_cluster(h: Handle, logits_dtype, B, k, V) -> int:

@@ -59,6 +59,24 @@ class SpecvKvCache(ctypes.Structure):
     ]
 
 
+class SpecvHeadNorm(ctypes.Structure):
+    _fields_ = [
+        ("q_weight", ctypes.c_void_p),
+        ("k_weight", ctypes.c_void_p),
+        ("eps", ctypes.c_float),
+        ("weight_add", ctypes.c_float),
+    ]
+
+
+class SpecvPositions(ctypes.Structure):
+    _fields_ = [
+        ("axes", ctypes.c_int),
+        ("positions", ctypes.c_void_p),
+        ("pair_axis", ctypes.c_char_p),
+        ("offsets", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -95,6 +113,14 @@ def load(build_if_missing=True):
     lib.specv_cache_append.restype = i32
     lib.specv_cache_append.argtypes = [vp, cache, vp, i64, i32, vp, i64, vp, i64, vp, i32, i32, vp, vp, i32, i32, vp,
                                        vp, vp]
+    lib.specv_cache_append_norm.restype = i32
+    lib.specv_cache_append_norm.argtypes = [vp, cache, vp, i64, i32, vp, i64, vp, i64, ctypes.POINTER(SpecvHeadNorm), vp,
+                                            i32, i32, ctypes.POINTER(SpecvPositions), vp, vp, i32, i32, vp, vp, vp]
+    lib.specv_attention_mass.restype = i32
+    lib.specv_attention_mass.argtypes = [vp, cache, vp, i64, i32, vp, i32, i32, ctypes.c_float, vp, vp, vp, i64, i32, vp,
+                                         vp]
+    lib.specv_cache_evict.restype = i32
+    lib.specv_cache_evict.argtypes = [vp, cache, i32, i64, vp, vp, i64, i32, i32, i32, i32, vp, vp, vp, vp]
     lib.specv_tree_attention.restype = i32
     lib.specv_tree_attention.argtypes = [vp, cache, vp, i64, i32, vp, i32, i32, ctypes.c_float, vp, vp, vp, vp, i64,
                                          vp]

@@ -1,18 +1,21 @@
 """In-tree build of the CUDA library (``libspecv.so``) for sm_103a.
 
-One translation unit (``csrc/library.cu``) compiled by nvcc with the CUDA
-runtime linked statically; the result sits next to this file, where the
+Translation units (``UNITS``) compiled by nvcc side by side and linked with
+the CUDA runtime statically; the result sits next to this file, where the
 binding loads it.  Rebuilt when any source or the public header is newer.
 """
+import concurrent.futures
 import glob
 import os
 import shutil
 import subprocess
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libspecv.so")
 SOURCES = sorted(glob.glob(os.path.join(PKG, "csrc", "*.cu")) + glob.glob(os.path.join(PKG, "csrc", "*.cuh")))
+UNITS = ("library.cu", "serving.cu")
 HEADER = os.path.join(ROOT, "include", "specv.h")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
@@ -38,16 +41,24 @@ def build(force=False, verbose=False):
     """Compile libspecv.so if missing or stale; return its path."""
     if not force and not needs_build():
         return LIB
-    tmp = LIB + ".tmp"
-    cmd = [
-        nvcc_path(), ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
-        "-o", tmp, os.path.join(PKG, "csrc", "library.cu"),
-    ]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + res.stdout + res.stderr)
+    flags = [ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC"]
     if verbose:
-        print(res.stdout + res.stderr)
+        flags += ["-Xptxas", "-v"]
+    tmp = LIB + ".tmp"
+
+    def run(cmd):
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError("nvcc failed:\n" + res.stdout + res.stderr)
+        if verbose:
+            print(res.stdout + res.stderr)
+
+    nvcc = nvcc_path()
+    with tempfile.TemporaryDirectory() as work:
+        objects = [os.path.join(work, u + ".o") for u in UNITS]
+        with concurrent.futures.ThreadPoolExecutor() as pool:
+            list(pool.map(lambda u, o: run([nvcc, *flags, "-c", "-o", o, os.path.join(PKG, "csrc", u)]), UNITS, objects))
+        run([nvcc, ARCH, "-shared", "-o", tmp, *objects])
     os.replace(tmp, LIB)
     return LIB
 

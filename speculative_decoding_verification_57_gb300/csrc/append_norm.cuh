@@ -1,0 +1,282 @@
+// append_norm.cuh -- the append of cache_append.cuh for models that norm the
+// heads of queries and keys, and for positions on several axes: a head x
+// becomes x * rsqrt(mean(x^2) + eps) * (weight + weight_add), and its pairs
+// turn by position * inv_freq as there, the position being that of the pair's
+// axis (positions[b, r, axis]) or, with one axis, base + depth(r) + offset[b].
+// Everything between the loads and the one rounding at the end is fp32 (the
+// angle float64).
+//
+// Layout, loads ahead of the length and the rest as in cache_append.cuh.  A
+// head belongs to a group of 1, 2, 4, .. 32 neighbouring lanes, the least that
+// hold its pieces, so that its sum of squares is added up by shuffles; lanes
+// behind the head's pieces (heads of 96: two of eight) are idle.  Weights
+// lie in shared memory in fp32, read as often as the data: in registers they
+// would cost resident CTAs.
+#pragma once
+#include "cache_append.cuh"
+
+namespace specv {
+
+struct AppendNormArgs {
+    AppendArgs a;
+    const void *q_weight, *k_weight;  // [head_dim] of the cache's type; NULL: not normed
+    const int32_t* positions;         // [B, rows, axes]; NULL: base + depth + offset
+    const int32_t* offsets;           // [B]; NULL: 0
+    float eps, weight_add, inv_dim;
+    int axes;
+    int group;  // lanes of a head
+    uint8_t axis[128];  // of each pair
+};
+
+// cos and sin of the angle pos * f, formed as append_turn forms it.
+__device__ __forceinline__ float2 append_turn_at(double pos, float f) {
+    const double a = pos * static_cast<double>(f);
+    const double two_pi = 6.283185307179586476925286766559;
+    const double turns = rint(a * 0.15915494309189533576888376337251);
+    float s, c;
+    sincosf(static_cast<float>(fma(-turns, two_pi, a)), &s, &c);
+    return make_float2(c, s);
+}
+
+// 16 bytes as floats, two at a time, and back.
+template <typename T>
+__device__ __forceinline__ void append_open(const KvVec<T>& x, f2 (&f)[KvType<T>::kVec / 2]) {
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = pack2(bf16_lo(w[e]), bf16_hi(w[e]));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) f[e] = pack2(x.x[2 * e], x.x[2 * e + 1]);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void append_close(const f2 (&f)[KvType<T>::kVec / 2], KvVec<T>& x) {
+#pragma unroll
+    for (int e = 0; e < KvType<T>::kVec / 2; ++e) {
+        float lo, hi;
+        unpack2(f[e], lo, hi);
+        if constexpr (sizeof(T) == 2) {
+            reinterpret_cast<uint32_t*>(&x)[e] = kv_pack_bf16(lo, hi);
+        } else {
+            x.x[2 * e] = lo;
+            x.x[2 * e + 1] = hi;
+        }
+    }
+}
+
+// Neighbours f[e] turned by the angle of pair e.
+template <int N>
+__device__ __forceinline__ void append_neighbours(f2 (&f)[N], const float* c, const float* s) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        float x, y;
+        unpack2(f[e], x, y);
+        f[e] = pack2(x * c[e] - y * s[e], x * s[e] + y * c[e]);
+    }
+}
+
+template <typename T, int MODE, int THREADS>
+__global__ void __launch_bounds__(THREADS, kAppendResident / THREADS)
+cache_append_norm_kernel(const __grid_constant__ AppendNormArgs n) {
+    constexpr int kVec = KvType<T>::kVec, kTwos = kVec / 2;
+    using Vec = KvVec<T>;
+    __shared__ __align__(16) float s_cos[128], s_sin[128], s_weight[2][256];
+    __shared__ float s_head[MODE == kValues ? THREADS / 32 : 1][MODE == kValues ? 256 : 1];
+    const AppendArgs& a = n.a;
+    const int rows = static_cast<int>(a.rows.d);
+    const int b = a.rows.div(blockIdx.x), r = blockIdx.x - b * rows;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const KvView& kv = a.kv;
+    const int turning = a.q_heads + kv.heads, heads = turning + kv.heads;
+    const int per = static_cast<int>(a.units.d), hstep = THREADS / n.group;
+    const int h0 = tid / n.group, u = tid - h0 * n.group;
+    const bool piece = u < per;  // the lane has pieces of its head
+    const int half = a.rot / 2;
+    // the unit's pieces of a head that turns, and of a value's
+    const bool apart = MODE == kApart && u < half / kVec;
+    const int x0 = apart ? u * kVec : MODE == kApart ? a.rot + 2 * (u * kVec - half) : 2 * u * kVec;
+    const int y0 = apart ? x0 + half : x0 + kVec;
+    // the token's queries, keys and values, at the first head as heads are counted
+    const int64_t token = blockIdx.x;
+    const T* q = static_cast<const T*>(a.q) + token * a.q_stride;
+    const T* k = static_cast<const T*>(a.k) + token * a.k_stride - a.q_heads * kv.dim;
+    const T* v = static_cast<const T*>(a.v) + token * a.v_stride - turning * kv.dim;
+    T* q_out = static_cast<T*>(a.q_out) + token * a.q_heads * kv.dim;
+    Vec x[kAppendHeads], y[kAppendHeads];
+    auto load_all = [&](int h1) {
+#pragma unroll
+        for (int j = 0; j < kAppendHeads; ++j) {
+            const int h = h1 + h0 + j * hstep;
+            if (!piece || h >= heads) continue;
+            const T* p = (h < a.q_heads ? q : h < turning ? k : v) + h * kv.dim;
+            x[j] = *reinterpret_cast<const Vec*>(p + (h < turning ? x0 : 2 * u * kVec));
+            y[j] = *reinterpret_cast<const Vec*>(p + (h < turning ? y0 : 2 * u * kVec + kVec));
+        }
+    };
+    // (where rows are counted, a row that is padding is not read)
+    const int counted = a.row_counts ? a.row_counts[b] : rows;
+    if (MODE != kValues && r < counted) load_all(0);
+    // the token's sequence, as in cache_append_kernel
+    const int len = kv.lens[b];
+    const int count = a.row_counts || len != 0 ? counted : 0;
+    const int base = len - count, slot = base + r;
+    const int32_t* table = kv.tables + static_cast<int64_t>(b) * kv.max_blocks;
+    int status = 0, blk = 0;
+    if (count < 0 || count > rows || len < 0 || (count > 0 && (len < count || !kv.fits(len)))) status = KV_LENGTH;
+    if (status == 0 && count > 0) {
+        bool parent_bad = false, block_bad = false;
+        int depth = r;
+        if (a.parents) {
+            uint32_t anc;
+            int d;
+            parent_bad = !warp_tree(a.parents + static_cast<int64_t>(b) * (rows - 1), count, lane, anc, d);
+            depth = __shfl_sync(0xffffffffu, d, r);
+        }
+        if (r < count) {
+            blk = table[kv.block.div(slot)];
+            const int64_t at = static_cast<int64_t>(base) + depth + (n.offsets ? n.offsets[b] : 0);
+            for (int j = tid; j < half; j += THREADS) {
+                const double pos = n.positions ? static_cast<double>(n.positions[token * n.axes + n.axis[j]])
+                                               : static_cast<double>(at);
+                const float2 cs = append_turn_at(pos, a.inv_freq[j]);
+                s_cos[j] = cs.x;
+                s_sin[j] = cs.y;
+            }
+            for (int d = tid; d < kv.dim; d += THREADS) {
+                const T *wq = static_cast<const T*>(n.q_weight), *wk = static_cast<const T*>(n.k_weight);
+                s_weight[0][d] = wq ? KvType<T>::load(wq[d]) + n.weight_add : 1.0f;
+                s_weight[1][d] = wk ? KvType<T>::load(wk[d]) + n.weight_add : 1.0f;
+            }
+        }
+        for (int i = kv.block.div(base) + tid, last = kv.block.div(len - 1); i <= last; i += THREADS)
+            block_bad |= !kv.valid(table[i]);
+        if (__syncthreads_or(parent_bad || block_bad))
+            status = (__syncthreads_or(parent_bad) ? KV_PARENT : 0) | (__syncthreads_or(block_bad) ? KV_BLOCK : 0);
+    }
+    if (r == 0 && tid == 0 && a.row_status) a.row_status[b] = status;
+    if (status != 0 || r >= count) {
+        if (a.q)
+            for (int i = tid; i < a.q_heads * per * 2; i += THREADS)
+                reinterpret_cast<uint4*>(q_out)[i] = make_uint4(0, 0, 0, 0);
+        return;
+    }
+    const int64_t at = kv.at(blk, 0, slot - kv.block.div(slot) * kv.block_size());
+    const int64_t next = static_cast<int64_t>(kv.block_size()) * kv.dim;  // from a head of a block to the next
+    T* k_out = static_cast<T*>(kv.k) + at;
+    T* v_out = static_cast<T*>(kv.v) + at;
+    if constexpr (MODE == kValues) {
+        // a head a warp, through shared memory: pairs that do not fill pieces
+        float* head = s_head[tid >> 5];
+        for (int h = tid >> 5; h < heads; h += THREADS / 32) {
+            const T* p = (h < a.q_heads ? q : h < turning ? k : v) + h * kv.dim;
+            const bool normed = h < a.q_heads ? n.q_weight != nullptr : h < turning && n.k_weight;
+            float sum = 0.0f;
+            for (int d = lane; d < kv.dim; d += 32) {
+                const float f = KvType<T>::load(p[d]);
+                head[d] = f;
+                sum = fmaf(f, f, sum);
+            }
+            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            __syncwarp();
+            const float inv = normed ? rsqrtf(fmaf(sum, n.inv_dim, n.eps)) : 1.0f;
+            const float* w = s_weight[h < a.q_heads ? 0 : 1];
+            T* to = h < a.q_heads ? q_out + h * kv.dim
+                    : h < turning ? k_out + (h - a.q_heads) * next
+                                  : v_out + (h - turning) * next;
+            for (int j = lane; j < kv.dim / 2; j += 32) {  // the turning pairs, then the rest by twos
+                const bool turns = h < turning && j < half, far = turns && !a.interleaved;
+                const int d0 = far ? j : 2 * j, d1 = far ? j + half : 2 * j + 1;
+                float e0 = head[d0], e1 = head[d1];
+                if (normed) {
+                    e0 *= inv * w[d0];
+                    e1 *= inv * w[d1];
+                }
+                if (turns) {
+                    const float c = s_cos[j], s = s_sin[j], f = e0;
+                    e0 = f * c - e1 * s;
+                    e1 = f * s + e1 * c;
+                }
+                to[d0] = KvType<T>::store(e0);
+                to[d1] = KvType<T>::store(e1);
+            }
+            __syncwarp();
+        }
+    } else {
+        // angles of the unit: of pairs x[e], y[e], or of the neighbours in x and then in y
+        const int first = MODE == kApart ? x0 : x0 / 2;
+        const bool turns = piece && (MODE == kApart ? apart : x0 < a.rot);
+        const bool both = MODE == kApart || y0 < a.rot;  // (neighbours: whether the second piece turns too)
+        float c[kVec], s[kVec];
+        if (turns) {
+#pragma unroll
+            for (int e = 0; e < kVec; e += 4) {
+                *reinterpret_cast<float4*>(c + e) = *reinterpret_cast<const float4*>(s_cos + first + e);
+                *reinterpret_cast<float4*>(s + e) = *reinterpret_cast<const float4*>(s_sin + first + e);
+            }
+        }
+        for (int h1 = 0; h1 < heads; h1 += kAppendHeads * hstep) {
+            if (h1 > 0) load_all(h1);
+#pragma unroll
+            for (int j = 0; j < kAppendHeads; ++j) {
+                const int h = h1 + h0 + j * hstep;
+                const bool mine = piece && h < heads;
+                const bool normed = mine && (h < a.q_heads ? n.q_weight != nullptr : h < turning && n.k_weight);
+                f2 fx[kTwos], fy[kTwos];
+                float inv = 1.0f;
+                if (mine && h < turning) {
+                    append_open<T>(x[j], fx);
+                    append_open<T>(y[j], fy);
+                }
+                if (__any_sync(0xffffffffu, normed)) {
+                    float all = 0.0f;
+                    if (normed) {
+                        f2 sum = pack2(0.0f, 0.0f);
+#pragma unroll
+                        for (int e = 0; e < kTwos; ++e) sum = fma2(fx[e], fx[e], fma2(fy[e], fy[e], sum));
+                        float lo, hi;
+                        unpack2(sum, lo, hi);
+                        all = lo + hi;
+                    }
+                    for (int off = n.group >> 1; off > 0; off >>= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
+                    inv = rsqrtf(fmaf(all, n.inv_dim, n.eps));
+                }
+                if (!mine) continue;
+                if (h < turning) {
+                    if (normed) {
+                        const float* w = s_weight[h < a.q_heads ? 0 : 1];
+                        const f2 inv2 = pack2(inv, inv);
+#pragma unroll
+                        for (int e = 0; e < kTwos; e += 2) {
+                            const float4 wx = *reinterpret_cast<const float4*>(w + x0 + 2 * e);
+                            const float4 wy = *reinterpret_cast<const float4*>(w + y0 + 2 * e);
+                            fx[e] = mul2(fx[e], mul2(inv2, pack2(wx.x, wx.y)));
+                            fx[e + 1] = mul2(fx[e + 1], mul2(inv2, pack2(wx.z, wx.w)));
+                            fy[e] = mul2(fy[e], mul2(inv2, pack2(wy.x, wy.y)));
+                            fy[e + 1] = mul2(fy[e + 1], mul2(inv2, pack2(wy.z, wy.w)));
+                        }
+                    }
+                    if (turns) {
+                        if constexpr (MODE == kApart) {
+#pragma unroll
+                            for (int e = 0; e < kTwos; ++e)
+                                append_apart(fx[e], fy[e], pack2(c[2 * e], c[2 * e + 1]), pack2(s[2 * e], s[2 * e + 1]));
+                        } else {
+                            append_neighbours<kTwos>(fx, c, s);
+                            if (both) append_neighbours<kTwos>(fy, c + kTwos, s + kTwos);
+                        }
+                    }
+                    append_close<T>(fx, x[j]);
+                    append_close<T>(fy, y[j]);
+                }
+                T* to = h < a.q_heads ? q_out + h * kv.dim
+                        : h < turning ? k_out + (h - a.q_heads) * next
+                                      : v_out + (h - turning) * next;
+                *reinterpret_cast<Vec*>(to + (h < turning ? x0 : 2 * u * kVec)) = x[j];
+                *reinterpret_cast<Vec*>(to + (h < turning ? y0 : 2 * u * kVec + kVec)) = y[j];
+            }
+        }
+    }
+}
+
+}  // namespace specv

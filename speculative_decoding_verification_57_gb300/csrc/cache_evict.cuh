@@ -1,0 +1,258 @@
+// cache_evict.cuh -- sequences of a paged cache brought back to a budget of
+// positions: per layer and kv head the first `first` and the last `recent`
+// positions stay, and of those between the ones that gathered the largest
+// mass (attention_mass.cuh), equal ones by the lowest position.
+//
+// With `line` = budget - recent, kept positions below the line stay where
+// they are; the i-th hole below it takes the i-th kept position above it; the
+// recent ones follow from the line on in their order.  Attention does not ask
+// for an order of the positions before a pass (their rotation is in the
+// keys), so that no more moves than that: a stable order would move nearly
+// every kept position of a head.
+//
+// A CTA, or where there are few heads some side by side, has a row of masses
+// (a layer, sequence and kv head).  CTAs of one row find the kept set each by
+// itself and move columns of their own of the keys or the values, so that they
+// need not meet; masses and lengths go to other memory than they come from.
+// The least kept mass is found by its bits, eight at a time, from the top;
+// moves are listed in position order by block-wide scans.  Moves run in
+// order, 16 bytes a thread and row, all loads of a step before its stores: a
+// step's stores go to places that no later step reads, as sources of kept
+// positions lie above the line and the recent ones, behind them, move down.
+#pragma once
+#include "kv_cache.cuh"
+#include "ptx.cuh"
+
+namespace specv {
+
+constexpr int kEvictThreads = 256;
+constexpr int kEvictMoves = 1024;  // listed at a time
+constexpr int kEvictAhead = 4;     // of a thread, in flight
+constexpr int kEvictItems = 4;     // positions of a thread in a scan
+
+struct EvictArgs {
+    KvView kv;
+    const float* mass;  // [layers, B, heads, width]
+    float* mass_out;
+    int32_t* lens_out;
+    int32_t* evicted;
+    int32_t* row_status;
+    int64_t layer_stride, width;
+    int layers, batch;
+    int budget, recent, first;
+    int split;          // CTAs of a row: 1, or some for the columns of the keys and as many for those of the values
+    int pieces;         // of 16 bytes a CTA moves of a row
+    FastDiv piece_div;  // by pieces
+    int vec_elems;
+};
+
+// Masses as whole numbers in the same order; zeros alike, what is no number above all others.
+__device__ __forceinline__ uint32_t evict_key(float x) {
+    if (x != x) return 0xffffffffu;
+    const uint32_t b = __float_as_uint(x + 0.0f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+struct EvictShared {
+    uint32_t hist[kEvictThreads / 32][256];
+    uint32_t warp_sum[2][kEvictThreads / 32];
+    uint32_t key, more;  // the digits found so far, and how many of the equal ones are kept
+    int src[kEvictMoves], dst[kEvictMoves];
+    int64_t from[kEvictMoves], to[kEvictMoves];
+};
+
+// Exclusive sums over the CTA of two counts below 2^16, packed; `total` the
+// CTA's.  Calls in turn use the two halves of warp_sum, so that one barrier
+// each is enough.
+__device__ __forceinline__ uint32_t evict_scan(EvictShared& sh, uint32_t v, int half, uint32_t& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t incl = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += o;
+    }
+    if (lane == 31) sh.warp_sum[half][warp] = incl;
+    __syncthreads();
+    uint32_t ahead = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kEvictThreads / 32; ++w) {
+        const uint32_t x = sh.warp_sum[half][w];
+        if (w < warp) ahead += x;
+        all += x;
+    }
+    total = all;
+    return ahead + incl - v;
+}
+
+// The key of the `many`-th largest of n masses (1 <= many <= n) and how many
+// of those equal to it are among them.
+__device__ inline void evict_select(EvictShared& sh, const float* mass, int n, uint32_t many) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint32_t key = 0;
+    for (int shift = 24; shift >= 0; shift -= 8) {
+        for (int i = lane; i < 256; i += 32) sh.hist[warp][i] = 0;
+        __syncwarp();
+        const uint32_t above = shift == 24 ? 0u : ~0u << (shift + 8);
+        for (int i = tid; i < n; i += kEvictThreads) {
+            const uint32_t k = evict_key(mass[i]);
+            if ((k & above) == key) atomicAdd(&sh.hist[warp][k >> shift & 255], 1u);
+        }
+        __syncthreads();
+        // the digit in which the counts from the top pass `many`: thread t has digit 255 - t
+        uint32_t c = 0;
+#pragma unroll
+        for (int w = 0; w < kEvictThreads / 32; ++w) c += sh.hist[w][255 - tid];
+        uint32_t incl = c;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += o;
+        }
+        if (lane == 31) sh.warp_sum[0][warp] = incl;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) incl += sh.warp_sum[0][w];
+        if (incl >= many && incl - c < many) {
+            sh.key = key | static_cast<uint32_t>(255 - tid) << shift;
+            sh.more = many - (incl - c);
+        }
+        __syncthreads();
+        key = sh.key;
+        many = sh.more;
+    }
+}
+
+__global__ void __launch_bounds__(kEvictThreads, 4) cache_evict_kernel(const EvictArgs e) {
+    __shared__ EvictShared sh;
+    const int tid = threadIdx.x;
+    const KvView& kv = e.kv;
+    const int part = blockIdx.x % e.split;
+    const int64_t row = blockIdx.x / e.split;  // (layer * batch + b) * heads + h
+    const int h = static_cast<int>(row % kv.heads), b = static_cast<int>(row / kv.heads % e.batch);
+    const int layer = static_cast<int>(row / kv.heads / e.batch);
+    const int len = kv.lens[b];
+    int status = len < 0 || !kv.fits(len) || len > e.width ? KV_LENGTH : 0;
+    const bool over = status == 0 && len > e.budget;
+    const int32_t* table = kv.tables + static_cast<int64_t>(b) * kv.max_blocks;
+    if (over) {
+        bool hole = false;
+        for (int i = kv.block.div(e.first) + tid, last = kv.block.div(len - 1); i <= last; i += kEvictThreads)
+            hole |= !kv.valid(table[i]);
+        if (__syncthreads_or(hole)) status |= KV_BLOCK;
+    }
+    if (tid == 0 && part == 0 && layer == 0 && h == 0) {
+        const bool cut = over && status == 0;
+        e.lens_out[b] = cut ? e.budget : len;
+        if (e.evicted) e.evicted[b] = cut ? len - e.budget : 0;
+        if (e.row_status) e.row_status[b] = status;
+    }
+    const float* mass = e.mass + row * e.width;
+    float* mass_out = e.mass_out + row * e.width;
+    if (status != 0 || !over) {
+        if (status == 0)
+            for (int i = tid + part * kEvictThreads; i < len; i += kEvictThreads * e.split) mass_out[i] = mass[i];
+        return;
+    }
+    const int line = e.budget - e.recent, many = line - e.first, tail = len - e.recent;
+    const int n = tail - e.first;  // positions to choose from: more than `many`
+    if (part == 0)  // (what lies in holes is written over below, behind barriers)
+        for (int i = tid; i < line; i += kEvictThreads) mass_out[i] = mass[i];
+    uint32_t key = 0xffffffffu, ties = 0;  // kept: above key, or one of the first `ties` equal to it
+    if (many > 0) {
+        evict_select(sh, mass + e.first, n, static_cast<uint32_t>(many));
+        key = sh.key;
+        ties = sh.more;
+    }
+    // the moves of rank [round, round + kEvictMoves): first those that fill holes, then the recent ones
+    unsigned char* pool = static_cast<unsigned char*>(e.split > 1 ? (part & 1 ? kv.v : kv.k) : kv.k);
+    const int parts = e.split > 1 ? 1 : 2;  // one CTA moves keys and then values
+    const int64_t elem = 16 / e.vec_elems;
+    const int64_t head_at = layer * e.layer_stride + static_cast<int64_t>(h) * kv.block_size() * kv.dim;
+    const int64_t column = static_cast<int64_t>(part >> 1) * e.pieces * 16;
+    int fills = INT32_MAX;
+    for (int round = 0;; round += kEvictMoves) {
+        // holes below the line and kept positions above it, by their ranks; both lists are as long
+        if (many > 0 && round < fills) {
+            uint32_t equal = 0, holes = 0, above = 0;
+            for (int i0 = 0; i0 < n; i0 += kEvictThreads * kEvictItems) {
+                const int i = i0 + tid * kEvictItems;
+                uint32_t k[kEvictItems], same = 0;
+#pragma unroll
+                for (int j = 0; j < kEvictItems; ++j) {
+                    k[j] = i + j < n ? evict_key(mass[e.first + i + j]) : 0;
+                    same += i + j < n && k[j] == key;
+                }
+                uint32_t all;
+                uint32_t rank = equal + evict_scan(sh, same, 0, all);
+                equal += all;
+                uint32_t take = 0, counts = 0;
+#pragma unroll
+                for (int j = 0; j < kEvictItems; ++j) {
+                    if (i + j >= n) continue;
+                    const bool kept = k[j] > key || (k[j] == key && rank++ < ties);
+                    if (i + j < many ? !kept : kept) {
+                        take |= 1u << j;
+                        counts += i + j < many ? 1u : 1u << 16;
+                    }
+                }
+                const uint32_t at = evict_scan(sh, counts, 1, all);
+                uint32_t hole_rank = holes + (at & 0xffff), above_rank = above + (at >> 16);
+#pragma unroll
+                for (int j = 0; j < kEvictItems; ++j) {
+                    if (!(take >> j & 1)) continue;
+                    const bool hole = i + j < many;
+                    const uint32_t x = (hole ? hole_rank++ : above_rank++) - static_cast<uint32_t>(round);
+                    if (x < kEvictMoves) (hole ? sh.dst : sh.src)[x] = e.first + i + j;
+                }
+                holes += all & 0xffff;
+                above += all >> 16;
+            }
+            fills = static_cast<int>(above);
+        } else if (many == 0) {
+            fills = 0;
+        }
+        const int total = fills + e.recent;
+        __syncthreads();
+        for (int x = tid; x < kEvictMoves && round + x < total; x += kEvictThreads) {
+            int src, dst;
+            if (round + x < fills) {
+                src = sh.src[x];
+                dst = sh.dst[x];
+            } else {
+                src = tail + round + x - fills;
+                dst = line + round + x - fills;
+            }
+            const int ls = kv.block.div(src), ld = kv.block.div(dst);
+            sh.from[x] = (kv.at(table[ls], 0, src - ls * kv.block_size()) + head_at) * elem + column;
+            sh.to[x] = (kv.at(table[ld], 0, dst - ld * kv.block_size()) + head_at) * elem + column;
+            if (part == 0) mass_out[dst] = mass[src];
+        }
+        __syncthreads();
+        const int here = total - round < kEvictMoves ? total - round : kEvictMoves;
+        for (int which = 0; which < parts; ++which) {
+            unsigned char* p = which ? static_cast<unsigned char*>(kv.v) : pool;
+            const int units = here * e.pieces;
+            for (int u0 = 0; u0 < units; u0 += kEvictThreads * kEvictAhead) {
+                uint4 x[kEvictAhead];
+                int64_t to[kEvictAhead];
+#pragma unroll
+                for (int j = 0; j < kEvictAhead; ++j) {
+                    const int u = u0 + j * kEvictThreads + tid;
+                    to[j] = -1;
+                    if (u >= units) continue;
+                    const int m = e.piece_div.div(u), c = (u - m * e.pieces) * 16;
+                    x[j] = *reinterpret_cast<const uint4*>(p + sh.from[m] + c);
+                    to[j] = sh.to[m] + c;
+                }
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < kEvictAhead; ++j)
+                    if (to[j] >= 0) *reinterpret_cast<uint4*>(p + to[j]) = x[j];
+            }
+        }
+        if (round + kEvictMoves >= total) break;
+        __syncthreads();
+    }
+}
+
+}  // namespace specv

@@ -2,18 +2,12 @@
 // (small-vocabulary warp kernel or split-vocabulary cluster kernel) and the
 // host-buffer convenience call.  The kernels live in verify_cluster.cuh and
 // verify_warp.cuh.
-#include <cuda_runtime.h>
-
-#include <atomic>
-#include <cstring>
 #include <cmath>
-#include <cstdint>
-#include <cstdio>
 #include <cstdlib>
 #include <cstring>
 #include <new>
 
-#include "../../include/specv.h"
+#include "handle.cuh"
 #include "verify_cluster.cuh"
 #include "verify_warp.cuh"
 #include "rollback.cuh"
@@ -22,52 +16,7 @@
 
 using namespace specv;
 
-struct specv_ctx {
-    int device = 0;
-    int sm_count = 0;
-    int max_batch = 0;
-    int max_k = 0;
-    int64_t vocab = 0;
-    std::atomic<int64_t> launches{0};
-    // most clusters of each size (1..16) that can be resident at once, per
-    // logits type (index 0: fp32, 1: bf16); 0 if that size cannot launch
-    int max_clusters[2][17] = {};
-    // device staging for specv_verify_sample_host
-    void* stage = nullptr;
-    size_t stage_bytes = 0;
-    // one-shot test hook: the next cluster-kernel launch withholds one
-    // pass-1 stage of CTA 0 and waits at most `test_polls` polls
-    int test_withhold = -1;
-    uint32_t test_polls = 0;
-};
-
-static thread_local char g_last_error[256] = "";
-
-static specv_status cuda_fail(cudaError_t e, const char* what) {
-    snprintf(g_last_error, sizeof g_last_error, "%s: %s", what, cudaGetErrorString(e));
-    return SPECV_ERR_CUDA;
-}
-
-#define SPECV_CUDA(call)                                         \
-    do {                                                         \
-        cudaError_t e_ = (call);                                 \
-        if (e_ != cudaSuccess) return cuda_fail(e_, #call);      \
-    } while (0)
-
 namespace {
-
-struct DeviceGuard {
-    int prev = -1;
-    bool ok = false;
-    explicit DeviceGuard(int dev) {
-        if (cudaGetDevice(&prev) == cudaSuccess) ok = (prev == dev) || cudaSetDevice(dev) == cudaSuccess;
-    }
-    ~DeviceGuard() {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-    }
-};
-
 
 struct Plan {
     bool warp = false;  // V <= kWarpKernelMaxV: one warp per row, or (row) one CTA per row

@@ -98,7 +98,8 @@ struct AttnCursor {
     int b, s, tile;  // sequence, segment of it (kv head * row_tiles + row tile), tile
     int tiles, len;  // of the sequence
 
-    __device__ __forceinline__ void next(const AttnArgs& a, int tile_keys) {
+    template <typename A>
+    __device__ __forceinline__ void next(const A& a, int tile_keys) {
         if (++tile < tiles) return;
         tile = 0;
         if (++s < a.kv.heads * a.row_tiles) return;
@@ -137,8 +138,8 @@ struct AttnRun {
 // whole CTA (THREADS threads, a multiple of 32).  COST: a segment's extra
 // units, in tiles, where a run has eight tiles or more.  Up to 32 sequences
 // every warp finds out by itself; with more, each thread has some of them.
-template <int THREADS, int COST>
-__device__ AttnRun attn_cut(const AttnArgs& a, AttnCut& sh, int tile_keys, int cta, int ctas, AttnCursor& cur) {
+template <int THREADS, int COST, typename A>
+__device__ AttnRun attn_cut(const A& a, AttnCut& sh, int tile_keys, int cta, int ctas, AttnCursor& cur) {
     constexpr int kEnds = COST > 0 ? 2 : 1;  // of the run, looked for among the sequences
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int segs = a.kv.heads * a.row_tiles;

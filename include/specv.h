@@ -375,6 +375,33 @@ specv_status specv_tree_attention(specv_handle h, const specv_kv_cache *cache, c
 int64_t specv_tree_attention_workspace(specv_handle h, specv_dtype dtype, int kv_heads, int head_dim, int q_heads,
                                        int batch, int rows);
 
+/* specv_tree_attention for a batch whose sequences share a prefix (a system
+ * prompt, a document): the prefix is read once for all of them.  Positions
+ * before prefix_len are those of prefix_table, for every sequence; the others
+ * are its own, by its block table (whose entries before prefix_len / block_size
+ * are not looked at: they may name the same blocks, as the other calls need them).
+ *   prefix_table  [prefix_blocks] int32
+ *   prefix_len    [1] int32, device memory: positions of the prefix, a multiple
+ *                 of block_size up to prefix_blocks * block_size; 0: none
+ *   seq_lens      of the cache: whole lengths, the prefix's positions among them.
+ *                 A sequence shorter than prefix_len + rows is refused
+ *                 (bit 2048; 0 is idle as ever); so are all where prefix_len is
+ *                 not as said (bit 2048) or an entry of prefix_table in use is
+ *                 outside the pool (bit 4096)
+ * Everything else, the roundings among it, as for specv_tree_attention;
+ * workspace of specv_prefix_attention_workspace(...) bytes.  batch * rows *
+ * q_heads * head_dim / 4 is below 2^31 - 128. */
+specv_status specv_prefix_attention(specv_handle h, const specv_kv_cache *cache, const int32_t *prefix_table,
+                                    int prefix_blocks, const int32_t *prefix_len, const void *q, int64_t q_stride,
+                                    int q_heads, const int32_t *parents, int batch, int rows, float scale, void *out,
+                                    float *lse, int32_t *row_status, void *workspace, int64_t workspace_bytes,
+                                    void *stream);
+
+/* Bytes of workspace that specv_prefix_attention needs for these sizes (it
+ * does not depend on lengths); 0 if the sizes are invalid. */
+int64_t specv_prefix_attention_workspace(specv_handle h, specv_dtype dtype, int kv_heads, int head_dim, int q_heads,
+                                         int batch, int rows);
+
 /* Move the kept path of a verified tree together in the cache, before
  * specv_rollback cuts the sequence off behind it: node path[i] (at position
  * seq_len - M + path[i]) is copied to position seq_len - M + i, for i <

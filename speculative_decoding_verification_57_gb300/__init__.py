@@ -27,6 +27,8 @@ __all__ = [
     "specv_tree_attention",
     "specv_tree_attention_workspace",
     "specv_cache_compact",
+    "specv_prefix_attention",
+    "specv_prefix_attention_workspace",
     "specv_cache_append_norm",
     "specv_attention_mass",
     "specv_cache_evict",
@@ -527,18 +529,10 @@ def specv_cache_append_norm(h: Handle, k_cache, v_cache, block_tables, seq_lens,
     return out
 
 
-def specv_tree_attention(h: Handle, q, k_cache, v_cache, block_tables, seq_lens, *, parents=None, scale=None,
-                         lse=False, out=None, workspace=None, stream=None):
-    """Attention of a pass's rows over the paged cache they were appended to:
-    q [B, rows, q_heads, head_dim], rows evenly spaced, rows <= max_k + 1;
-    the caches, block_tables and seq_lens as for specv_cache_append; parents
-    [B, rows - 1] int32 (None: chains); scale defaults to head_dim ** -0.5.
-    The pass's rows are the last ``rows`` positions of every sequence.  Weights
-    of a bf16 cache are rounded to bf16 for the product with the values.
-    Returns a dict: out [B, rows, q_heads, head_dim], row_status [B] and,
-    with ``lse``, lse [B, rows, q_heads] fp32; ``out`` may supply them.
-    ``workspace`` may supply a CUDA uint8 tensor of at least
-    specv_tree_attention_workspace bytes that no other call uses meanwhile."""
+def _attention_args(h, q, k_cache, v_cache, block_tables, seq_lens, parents, scale, lse, out, stream):
+    """What the two attentions have in common: the cache's descriptor, the
+    sizes that the workspace depends on, the arguments from q to the row
+    status, and the outputs."""
     c, _, _ = _kv_cache(h, k_cache, v_cache, block_tables, seq_lens)
     if q.dim() != 4:
         raise ValueError("q must have the shape [B, rows, q_heads, head_dim]")
@@ -559,19 +553,67 @@ def specv_tree_attention(h: Handle, q, k_cache, v_cache, block_tables, seq_lens,
         if "lse" not in out:
             out["lse"] = _empty(h, (B, rows, q_heads), _f32, stream)
         pl = _on(h, out["lse"], _f32, "lse", (B, rows, q_heads))
-    lib = _lib.load()
+    sizes = (c.dtype, c.kv_heads, c.head_dim, q_heads, B, rows)
+    return c, sizes, (pq, q_stride, q_heads, pp, B, rows, c.head_dim ** -0.5 if scale is None else scale, po, pl, ps), out
+
+
+def _workspace_of(h, workspace, need, key, sizes, stream):
+    """Pointer and bytes of a call's workspace; without one, new memory of
+    as many bytes as ``need`` says for the sizes, asked once."""
     if workspace is None:
-        sizes = (c.dtype, c.kv_heads, c.head_dim, q_heads, B, rows)
-        need = h._workspace.get(sizes)
-        if need is None:
-            need = h._workspace[sizes] = lib.specv_tree_attention_workspace(h.ptr, *sizes)
-        workspace = _empty(h, (need,), _torch().uint8, stream) if need else None
-    pw = None if workspace is None else _on(h, workspace, _torch().uint8, "workspace")
-    st = lib.specv_tree_attention(
-        h.ptr, c, pq, q_stride, q_heads, pp, B, rows, c.head_dim ** -0.5 if scale is None else scale, po, pl, ps, pw,
-        0 if workspace is None else workspace.numel(), _stream_of(h, stream))
-    _check(st, "specv_tree_attention")
+        n = h._workspace.get((key, sizes))
+        if n is None:
+            n = h._workspace[key, sizes] = need(h.ptr, *sizes)
+        workspace = _empty(h, (n,), _torch().uint8, stream) if n else None
+    if workspace is None:
+        return None, 0
+    return _on(h, workspace, _torch().uint8, "workspace"), workspace.numel()
+
+
+def specv_tree_attention(h: Handle, q, k_cache, v_cache, block_tables, seq_lens, *, parents=None, scale=None,
+                         lse=False, out=None, workspace=None, stream=None):
+    """Attention of a pass's rows over the paged cache they were appended to:
+    q [B, rows, q_heads, head_dim], rows evenly spaced, rows <= max_k + 1;
+    the caches, block_tables and seq_lens as for specv_cache_append; parents
+    [B, rows - 1] int32 (None: chains); scale defaults to head_dim ** -0.5.
+    The pass's rows are the last ``rows`` positions of every sequence.  Weights
+    of a bf16 cache are rounded to bf16 for the product with the values.
+    Returns a dict: out [B, rows, q_heads, head_dim], row_status [B] and,
+    with ``lse``, lse [B, rows, q_heads] fp32; ``out`` may supply them.
+    ``workspace`` may supply a CUDA uint8 tensor of at least
+    specv_tree_attention_workspace bytes that no other call uses meanwhile."""
+    c, sizes, args, out = _attention_args(h, q, k_cache, v_cache, block_tables, seq_lens, parents, scale, lse, out, stream)
+    lib = _lib.load()
+    work = _workspace_of(h, workspace, lib.specv_tree_attention_workspace, "tree", sizes, stream)
+    _check(lib.specv_tree_attention(h.ptr, c, *args, *work, _stream_of(h, stream)), "specv_tree_attention")
     return out
+
+
+def specv_prefix_attention(h: Handle, q, k_cache, v_cache, block_tables, seq_lens, prefix_table, prefix_len, *,
+                           parents=None, scale=None, lse=False, out=None, workspace=None, stream=None):
+    """specv_tree_attention for a batch whose sequences share a prefix, read
+    once for all of them: the first prefix_len positions ([1] int32 on the
+    device, a multiple of the block size) are those of prefix_table
+    [prefix_blocks] int32, the others each sequence's own, by block_tables
+    (whose entries for the prefix are not looked at); seq_lens counts both.
+    The rest, and the result, as for specv_tree_attention; ``workspace`` of at
+    least specv_prefix_attention_workspace bytes."""
+    c, sizes, args, out = _attention_args(h, q, k_cache, v_cache, block_tables, seq_lens, parents, scale, lse, out, stream)
+    pt = _on(h, prefix_table, _i32, "prefix_table")
+    if prefix_table.dim() != 1:
+        raise ValueError("prefix_table must have the shape [prefix_blocks]")
+    pn = _on(h, prefix_len, _i32, "prefix_len", (1,))
+    lib = _lib.load()
+    work = _workspace_of(h, workspace, lib.specv_prefix_attention_workspace, "prefix", sizes, stream)
+    _check(lib.specv_prefix_attention(h.ptr, c, pt, prefix_table.shape[0], pn, *args, *work, _stream_of(h, stream)),
+           "specv_prefix_attention")
+    return out
+
+
+def specv_prefix_attention_workspace(h: Handle, dtype, kv_heads, head_dim, q_heads, batch, rows) -> int:
+    """Bytes of workspace a specv_prefix_attention call of these sizes needs
+    (dtype SPECV_BF16 or SPECV_F32)."""
+    return int(_lib.load().specv_prefix_attention_workspace(h.ptr, dtype, kv_heads, head_dim, q_heads, batch, rows))
 
 
 def specv_tree_attention_workspace(h: Handle, dtype, kv_heads, head_dim, q_heads, batch, rows) -> int:

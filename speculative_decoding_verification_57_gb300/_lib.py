@@ -113,6 +113,11 @@ def load(build_if_missing=True):
     lib.specv_cache_append.restype = i32
     lib.specv_cache_append.argtypes = [vp, cache, vp, i64, i32, vp, i64, vp, i64, vp, i32, i32, vp, vp, i32, i32, vp,
                                        vp, vp]
+    lib.specv_prefix_attention.restype = i32
+    lib.specv_prefix_attention.argtypes = [vp, cache, vp, i32, vp, vp, i64, i32, vp, i32, i32, ctypes.c_float, vp, vp, vp,
+                                           vp, i64, vp]
+    lib.specv_prefix_attention_workspace.restype = i64
+    lib.specv_prefix_attention_workspace.argtypes = [vp, i32, i32, i32, i32, i32, i32]
     lib.specv_cache_append_norm.restype = i32
     lib.specv_cache_append_norm.argtypes = [vp, cache, vp, i64, i32, vp, i64, vp, i64, ctypes.POINTER(SpecvHeadNorm), vp,
                                             i32, i32, ctypes.POINTER(SpecvPositions), vp, vp, i32, i32, vp, vp, vp]

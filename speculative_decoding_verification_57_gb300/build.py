@@ -15,7 +15,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libspecv.so")
 SOURCES = sorted(glob.glob(os.path.join(PKG, "csrc", "*.cu")) + glob.glob(os.path.join(PKG, "csrc", "*.cuh")))
-UNITS = ("library.cu", "serving.cu")
+UNITS = ("library.cu", "prefix.cu", "serving.cu")
 HEADER = os.path.join(ROOT, "include", "specv.h")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 

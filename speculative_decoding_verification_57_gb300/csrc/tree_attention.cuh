@@ -39,6 +39,8 @@
 // (about 8 us) and by the join (4.5 us); fp32 by instructions (to split keys
 // and values) with 12 warps an SM.
 #pragma once
+#include <type_traits>
+
 #include "kv_cache.cuh"
 #include "ptx.cuh"
 
@@ -62,6 +64,15 @@ struct AttnArgs {
     uint32_t polls;  // most polls of a wait
 };
 
+// A part of an attention whose parts join later (prefix_attention.cuh): every
+// segment leaves its outputs, undivided, in the workspace.
+struct PartArgs : AttnArgs {
+    const int32_t* prefix;  // positions before it, whole blocks, are left to another part; NULL: this is that part, of one
+                            // sequence whose length is the prefix's and whose rows are all sequences', in their order
+    int prefix_cap;         // the most positions that the prefix's table holds
+    int own;                // rows of the pass among a sequence's positions: `rows`, or of the prefix none
+};
+
 // Factor of the scores in base 2.  A scale of zero still has to tell hidden
 // positions (an infinite score) from the others: the smallest number there is,
 // so that the largest scores differ by less than 2^-20 of a weight.
@@ -75,6 +86,27 @@ __device__ __forceinline__ int attn_len(const AttnArgs& a, int b) {
     const int len = a.kv.lens[b];
     return len == 0 || (len >= a.rows && a.kv.fits(len)) ? len : -1;
 }
+
+// The shared prefix's length; -1 if it is none of whole blocks that its table holds.
+__device__ __forceinline__ int attn_prefix(const KvView& kv, int len, int cap) {
+    return len >= 0 && len <= cap && len == static_cast<int>(kv.block.div(len)) * kv.block_size() ? len : -1;
+}
+// Of a part: the positions behind the prefix, or those of the prefix.
+__device__ __forceinline__ int attn_len(const PartArgs& a, int b) {
+    const int len = a.kv.lens[b];
+    if (!a.prefix) return attn_prefix(a.kv, len, a.prefix_cap);
+    if (len == 0) return 0;
+    const int skip = attn_prefix(a.kv, *a.prefix, a.prefix_cap);
+    return skip >= 0 && len - a.rows >= skip && a.kv.fits(len) ? len - skip : -1;
+}
+// The first entry of the tables that is looked at (of sequences that are not refused).
+__device__ __forceinline__ int attn_first_block(const AttnArgs&) { return 0; }
+__device__ __forceinline__ int attn_first_block(const PartArgs& a) {
+    return a.prefix ? static_cast<int>(a.kv.block.div(max(*a.prefix, 0))) : 0;
+}
+// Rows of the pass that are the last positions of a sequence.
+__device__ __forceinline__ int attn_own(const AttnArgs& a) { return a.rows; }
+__device__ __forceinline__ int attn_own(const PartArgs& a) { return a.own; }
 
 // An idle or refused sequence counts as a tile, whose CTA writes its zeros.
 __device__ __forceinline__ int attn_tiles(int len, int tile) { return len <= 0 ? 1 : (len + tile - 1) / tile; }
@@ -284,6 +316,50 @@ __host__ __device__ inline AttnWork attn_work(unsigned char* p, int ctas, int tm
     return w;
 }
 
+// ... and of a part: a note for every segment, and behind the partial results
+// those of segments that one CTA has whole.
+struct alignas(8) PartNote {
+    int first, last;  // the CTAs with the segment's first and last tiles
+};
+
+struct PartWork {
+    AttnNote* notes;  // [ctas]: whether a wait of the CTA ran out
+    PartNote* segs;   // [segs]
+    int* status;      // [ctas * 2 + segs]
+    float2* ml;
+    float4* acc;
+};
+
+__host__ __device__ inline int64_t part_pieces(int ctas, int64_t segs) { return 2ll * ctas + segs; }
+
+__host__ __device__ inline int64_t part_work_bytes(int ctas, int64_t segs, int tm, int dp) {
+    const int64_t pieces = part_pieces(ctas, segs);
+    return (ctas * static_cast<int64_t>(sizeof(AttnNote)) + pieces * tm * (sizeof(float2) + dp * 4ll) +
+            segs * static_cast<int64_t>(sizeof(PartNote)) + pieces * static_cast<int64_t>(sizeof(int)) + 255) / 256 * 256;
+}
+
+__host__ __device__ inline PartWork part_work(unsigned char* p, int ctas, int64_t segs, int tm, int dp) {
+    const int64_t pieces = part_pieces(ctas, segs);
+    PartWork w;
+    w.notes = reinterpret_cast<AttnNote*>(p);
+    w.ml = reinterpret_cast<float2*>(w.notes + ctas);
+    w.acc = reinterpret_cast<float4*>(w.ml + pieces * tm);
+    w.segs = reinterpret_cast<PartNote*>(w.acc + pieces * tm * (dp / 4));
+    w.status = reinterpret_cast<int*>(w.segs + segs);
+    return w;
+}
+
+// Where a CTA leaves the results of its segments, for either kind of call.
+__device__ __forceinline__ AttnWork attn_work_of(const AttnArgs& a, int ctas, int tm, int dp) {
+    return attn_work(a.workspace, ctas, tm, dp);
+}
+__device__ __forceinline__ PartWork attn_work_of(const PartArgs& a, int ctas, int tm, int dp) {
+    return part_work(a.workspace, ctas, static_cast<int64_t>(a.batch) * a.kv.heads * a.row_tiles, tm, dp);
+}
+__device__ __forceinline__ int64_t attn_seg(const AttnArgs& a, const AttnCursor& cur) {
+    return static_cast<int64_t>(cur.b) * a.kv.heads * a.row_tiles + cur.s;
+}
+
 // ------------------------------------------------------------------ matrix instructions
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -406,8 +482,9 @@ __device__ float attn_dot(uint32_t sq, int m, uint32_t sk, int n) {
 }
 
 // ------------------------------------------------------------------ the kernel
-template <typename S>
-__global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(const AttnArgs a) {
+template <typename S, typename A>
+__global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(const A a) {
+    constexpr bool kParts = std::is_same_v<A, PartArgs>;
     using T = typename S::Type;
     constexpr int DP = S::DP, RG = S::RG, KT = S::KT, KW = S::KW, TM = S::TM, kStages = S::kStages, kAhead = S::kAhead;
     constexpr int kVec = KvType<T>::kVec;
@@ -425,7 +502,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
     const int quad = lane >> 2, two = (lane & 3) * 2;
     const KvView& kv = a.kv;
     const int cta = blockIdx.x, ctas = gridDim.x;
-    const AttnWork work = attn_work(a.workspace, ctas, TM, DP);
+    const auto work = attn_work_of(a, ctas, TM, DP);
     const uint32_t base_s = smem_u32(smem);
     const int m_rows = a.rows * static_cast<int>(a.group.d);  // rows of a kv head
     const float c_scale = attn_scale(a.scale);
@@ -434,6 +511,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
     AttnCursor cur, ahead, ids;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // what the kernels before wrote
     const AttnRun run = attn_cut<S::kThreads, 0>(a, s_cut, KT, cta, ctas, cur);
+    const int first_block = attn_first_block(a);
     if (tid == 0) {
         s_wild[0] = s_wild[1] = 0;
         work.notes[cta].b = -1;
@@ -456,7 +534,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
             if (tid < KT && t < ids.len) {
                 const int lb = kv.block.div(t);
                 // (no read-only load: the kernel may have started before the one that wrote the table ended)
-                p.blk = kv.tables[static_cast<int64_t>(ids.b) * kv.max_blocks + lb];
+                p.blk = kv.tables[static_cast<int64_t>(ids.b) * kv.max_blocks + first_block + lb];
                 p.in = t - lb * kv.block_size();
                 p.h = ids.s / a.row_tiles;
             }
@@ -585,7 +663,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
 #pragma unroll
         for (int w = 0; w < (KT + 31) / 32; ++w)
             if (s_hole[i & 3][w]) status |= KV_BLOCK;
-        const int t0 = cur.tile * KT, base = cur.len - a.rows;
+        const int t0 = cur.tile * KT, base = cur.len - attn_own(a);
         const bool edge = t0 + KT > base;  // positions that not every row sees
         if (edge && cur.len > 0) {
             // values of the pass's rows that are not finite are taken out of
@@ -817,7 +895,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
                 __syncthreads();
             }
             const bool whole = first_tile == 0 && ends;
-            const int piece = 2 * cta + (first_tile == 0 ? 1 : 0);
+            const int64_t piece = kParts && whole ? 2ll * ctas + attn_seg(a, cur) : 2ll * cta + (first_tile == 0 ? 1 : 0);
             const uint32_t wild = s_wild[seg & 1];
             constexpr int kGroup = S::kThreads / TM;  // threads of a row
             const int row = tid / kGroup, lane_r = tid % kGroup;
@@ -858,7 +936,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
                         for (int j = 0; j < a.rows; ++j) {
                             if (!(seen >> j & 1)) continue;
                             const int t = base + j, lb = kv.block.div(t);
-                            const int blk = kv.tables[static_cast<int64_t>(cur.b) * kv.max_blocks + lb];
+                            const int blk = kv.tables[static_cast<int64_t>(cur.b) * kv.max_blocks + first_block + lb];
                             if (!kv.valid(blk)) continue;
                             const T* v = static_cast<const T*>(kv.v) + kv.at(blk, h, t - lb * kv.block_size()) + d;
                             for (int e = 0; e < 4; ++e) {
@@ -867,32 +945,39 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
                             }
                         }
                     }
-                    if (whole) {
+                    if (!kParts && whole) {
                         T* out = static_cast<T*>(a.out) + head * kv.dim + d;
                         attn_store4(out, zero ? 0.0f : x[0] * inv, zero ? 0.0f : x[1] * inv, zero ? 0.0f : x[2] * inv,
                                     zero ? 0.0f : x[3] * inv);
                     } else {
-                        work.acc[(static_cast<int64_t>(piece) * (DP / 4) + d / 4) * TM + row] =
+                        work.acc[(piece * (DP / 4) + d / 4) * TM + row] =
                             make_float4(x[0], x[1], x[2], x[3]);
                     }
                 }
                 if (lane_r == 0) {
-                    if (whole) {
+                    if (!kParts && whole) {
                         if (a.lse) a.lse[head] = zero ? -INFINITY : m * 0.693147181f + logf(l);
                     } else {
-                        work.ml[static_cast<int64_t>(piece) * TM + row] = make_float2(m, l);
+                        work.ml[piece * TM + row] = make_float2(m, l);
                     }
                 }
             }
             if (tid == 0) {
-                if (first_tile == 0 && cur.s == 0 && a.row_status) a.row_status[cur.b] = status;
-                if (!whole) {
+                if constexpr (kParts) {
                     work.status[piece] = status;
-                    if (first_tile == 0) {
-                        work.notes[cta].b = cur.b;
-                        work.notes[cta].s = cur.s;
-                        work.notes[cta].last =
-                            attn_owner(run.units, run.unit(i + cur.tiles - cur.tile - 1, seg), run.used);
+                    if (first_tile == 0)
+                        work.segs[attn_seg(a, cur)] =
+                            PartNote{cta, attn_owner(run.units, run.unit(i + cur.tiles - cur.tile - 1, seg), run.used)};
+                } else {
+                    if (first_tile == 0 && cur.s == 0 && a.row_status) a.row_status[cur.b] = status;
+                    if (!whole) {
+                        work.status[piece] = status;
+                        if (first_tile == 0) {
+                            work.notes[cta].b = cur.b;
+                            work.notes[cta].s = cur.s;
+                            work.notes[cta].last =
+                                attn_owner(run.units, run.unit(i + cur.tiles - cur.tile - 1, seg), run.used);
+                        }
                     }
                 }
             }

@@ -249,7 +249,8 @@ struct TcUses {
     int u = 0, seg = 0;
 
     __device__ __forceinline__ TcUses(const AttnCursor& c, int n_) : cur(c), n(n_), nt(tc_part(c, n_)) {}
-    __device__ __forceinline__ void next(const AttnArgs& a) {
+    template <typename A>
+    __device__ __forceinline__ void next(const A& a) {
         if (++u < 2 * nt) return;
         u = 0;
         ++seg;
@@ -298,13 +299,14 @@ __device__ __forceinline__ void tc_copy_queries(const AttnArgs& a, TcShared<S>& 
 // one of the tile's blocks; its block number is read a slot ahead.  A block
 // that is outside the pool or past the sequence's end is asked for at block
 // number `blocks`, which reads as zeros.
-template <typename S>
-__device__ void tc_box_role(const AttnArgs& a, const TcMaps& maps, TcShared<S>& sh, const AttnCursor& cur, int n,
+template <typename S, typename A>
+__device__ void tc_box_role(const A& a, const TcMaps& maps, TcShared<S>& sh, const AttnCursor& cur, int n,
                             int warp, int lane) {
     const KvView& kv = a.kv;
     const int part = lane / S::kPanels, panel = lane % S::kPanels;  // block of the tile, and columns
     const int rows = maps.rows;                                    // of a box
     const bool mine = part * rows < S::KT;
+    const int first_block = attn_first_block(a);
     TcUses<S> it(cur, n);
     // what this lane asks for: block number (0: nothing to ask), and where in it
     struct Box {
@@ -318,7 +320,7 @@ __device__ void tc_box_role(const AttnArgs& a, const TcMaps& maps, TcShared<S>& 
         const int t = tile * S::KT + part * rows;
         x.in = mine && t < it.cur.len;
         const int lb = kv.block.div(x.in ? t : 0);
-        x.blk = x.in ? kv.tables[static_cast<int64_t>(it.cur.b) * kv.max_blocks + lb] : 0;
+        x.blk = x.in ? kv.tables[static_cast<int64_t>(it.cur.b) * kv.max_blocks + first_block + lb] : 0;
         x.row = t - lb * kv.block_size();
         x.h = it.cur.s / a.row_tiles;
         x.seg = it.seg;
@@ -373,8 +375,8 @@ __device__ void tc_box_role(const AttnArgs& a, const TcMaps& maps, TcShared<S>& 
 
 // Queries where the keys and values are boxes: one warp, by boxes of its own
 // or, where groups of heads do not fill row tiles, by 16-byte copies.
-template <typename S>
-__device__ void tc_query_role(const AttnArgs& a, const TcMaps& maps, TcShared<S>& sh, AttnCursor cur, int n, int p) {
+template <typename S, typename A>
+__device__ void tc_query_role(const A& a, const TcMaps& maps, TcShared<S>& sh, AttnCursor cur, int n, int p) {
     const uint32_t bar = smem_u32(&sh.q_shown);
     int sent = -1;
     for (int j = 0, seg = 0; j < n; ++seg) {
@@ -410,8 +412,8 @@ __device__ void tc_query_role(const AttnArgs& a, const TcMaps& maps, TcShared<S>
 // 16-byte copies: four warps.  A warp copies 32 rows of every tile; lane l
 // finds the place of one of them in the pool (while the slot it goes to is
 // still in use) and hands it to the lanes that copy the row's pieces.
-template <typename S>
-__device__ void tc_copy_role(const AttnArgs& a, TcShared<S>& sh, const AttnCursor& cur, int n, int p) {
+template <typename S, typename A>
+__device__ void tc_copy_role(const A& a, TcShared<S>& sh, const AttnCursor& cur, int n, int p) {
     using T = typename S::Type;
     constexpr int kPieces = S::DP / 8;    // 16-byte pieces of a row
     constexpr int kStep = 128 / kPieces;  // rows a pass of the 128 threads
@@ -422,6 +424,7 @@ __device__ void tc_copy_role(const AttnArgs& a, TcShared<S>& sh, const AttnCurso
     const int mine = (lane / kOwn) * kStep + warp * kOwn + lane % kOwn;  // the row whose place this lane finds
     const bool col = c * 8 < kv.dim;
     const int withhold = blockIdx.x == 0 ? a.withhold : -1;
+    const int first_block = attn_first_block(a);
     TcUses<S> it(cur, n);
     for (int use = 0; use < 2 * n; ++use, it.next(a)) {
         if (it.u == 0) {
@@ -440,7 +443,7 @@ __device__ void tc_copy_role(const AttnArgs& a, TcShared<S>& sh, const AttnCurso
         const int t = tile * S::KT + mine;
         if (t < it.cur.len) {
             const int lb = kv.block.div(t);
-            const int blk = kv.tables[static_cast<int64_t>(it.cur.b) * kv.max_blocks + lb];
+            const int blk = kv.tables[static_cast<int64_t>(it.cur.b) * kv.max_blocks + first_block + lb];
             if (kv.valid(blk))
                 at = kv.at(blk, it.cur.s / a.row_tiles, t - lb * kv.block_size());
             else
@@ -468,8 +471,8 @@ __device__ void tc_copy_role(const AttnArgs& a, TcShared<S>& sh, const AttnCurso
 // What the copies wrote is shown to the tensor cores' proxy by a thread of its
 // own: the fence takes some 300 cycles, which would otherwise stand between
 // the products.
-template <typename S>
-__device__ void tc_show_role(const AttnArgs& a, TcShared<S>& sh, const AttnCursor& cur, int n) {
+template <typename S, typename A>
+__device__ void tc_show_role(const A& a, TcShared<S>& sh, const AttnCursor& cur, int n) {
     TcUses<S> it(cur, n);
     for (int use = 0; use < 2 * n; ++use, it.next(a)) {
         if (it.u == 0) {
@@ -493,8 +496,8 @@ __device__ void tc_show_role(const AttnArgs& a, TcShared<S>& sh, const AttnCurso
 // a segment's part belongs to stream i & 1 and
 // tile i >> 1 (WIDE) or i.  A stream's next scores follow its output product,
 // whose weights lie where they go: products of one thread run in order.
-template <typename S>
-__device__ void tc_mma_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor cur, int n, int x, uint32_t lead) {
+template <typename S, typename A>
+__device__ void tc_mma_role(const A& a, TcShared<S>& sh, AttnCursor cur, int n, int x, uint32_t lead) {
     const uint32_t tm = sh.tmem;
     const uint32_t ts = tm + x * 128, to = tm + 256 + x * S::DP;
     constexpr uint32_t kScores = tc_idesc(S::KT, false), kOutputs = tc_idesc(S::DP, true);
@@ -575,13 +578,15 @@ __device__ void tc_mma_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor cur, 
 }
 
 // ------------------------------------------------------------------ softmax
-template <typename S>
-__device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor cur, const AttnRun& run, int x, int row) {
+template <typename S, typename A>
+__device__ void tc_softmax_role(const A& a, TcShared<S>& sh, AttnCursor cur, const AttnRun& run, int x, int row) {
     const int n = run.n;
     using T = typename S::Type;
     const KvView& kv = a.kv;
+    constexpr bool kParts = std::is_same_v<A, PartArgs>;
     const int lane = row & 31, cta = blockIdx.x;
-    const AttnWork work = attn_work(a.workspace, gridDim.x, S::TM, S::DP);
+    const auto work = attn_work_of(a, gridDim.x, S::TM, S::DP);
+    const int first_block = attn_first_block(a), own = attn_own(a);
     const int m_rows = a.rows * static_cast<int>(a.group.d);
     const uint32_t lanes = static_cast<uint32_t>(row & ~31) << 16;
     const uint32_t ts = sh.tmem + x * 128 + lanes;
@@ -602,7 +607,7 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
         const int grow = rt * S::TM + (S::WIDE ? x * 128 : 0) + row;
         const bool warp_in = grow - lane < m_rows;  // the warp has rows
         const int r = a.group.div(grow), gq = grow - r * static_cast<int>(a.group.d);
-        const int base = cur.len - a.rows;
+        const int base = cur.len - own;
         // the next part's sequence is read while this one is worked on
         AttnCursor ahead = cur;
         ahead.tile += nt - 1;
@@ -611,7 +616,7 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
         next_parent = parent_of(ahead.b);
         uint32_t line = 0;
         bool tree_ok = true;
-        if ((first_tile + nt) * S::KT > base) {
+        if (own && (first_tile + nt) * S::KT > base) {
             int depth;
             tree_ok = warp_tree_of(parent, a.rows, lane, line, depth);
         }
@@ -766,7 +771,7 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
         }
         const bool ends = first_tile + nt == cur.tiles;
         const bool whole = first_tile == 0 && ends;
-        const int piece = 2 * cta + (first_tile == 0 ? 1 : 0);
+        const int64_t piece = kParts && whole ? 2ll * gridDim.x + attn_seg(a, cur) : 2ll * cta + (first_tile == 0 ? 1 : 0);
         int status = cur.len < 0 ? KV_LENGTH : cur.len == 0 ? 0 : tree_ok ? 0 : KV_PARENT;
         if (sh.hole[seg & 15]) status |= KV_BLOCK;
         if (tc_failed(&sh.fail)) status |= KV_TIMEOUT;
@@ -800,7 +805,7 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
                 if (grow < m_rows) {
                     for (uint32_t left = seen; left; left &= left - 1) {
                         const int pos = base + __ffs(left) - 1, lb = kv.block.div(pos);
-                        const int blk = kv.tables[static_cast<int64_t>(cur.b) * kv.max_blocks + lb];
+                        const int blk = kv.tables[static_cast<int64_t>(cur.b) * kv.max_blocks + first_block + lb];
                         if (!kv.valid(blk)) continue;
                         const T* v = static_cast<const T*>(kv.v) + kv.at(blk, h, pos - lb * kv.block_size()) + d0;
 #pragma unroll
@@ -809,7 +814,7 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
                             if (!finite(y)) o[e] += y;
                         }
                     }
-                    if (whole) {
+                    if (!kParts && whole) {
                         T* out = static_cast<T*>(a.out) + head * kv.dim + d0;
 #pragma unroll
                         for (int e = 0; e < 32; e += 8) {
@@ -821,7 +826,7 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
                                                                             kv_pack_bf16(y[4], y[5]), kv_pack_bf16(y[6], y[7]));
                         }
                     } else {
-                        float4* acc = work.acc + (static_cast<int64_t>(piece) * (S::DP / 4) + d0 / 4) * S::TM +
+                        float4* acc = work.acc + (piece * (S::DP / 4) + d0 / 4) * S::TM +
                                       (S::WIDE ? x * 128 : 0) + row;
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
@@ -830,20 +835,27 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
                 }
             }
             if (grow < m_rows && (S::WIDE || x == 0)) {
-                if (!whole)
-                    work.ml[static_cast<int64_t>(piece) * S::TM + (S::WIDE ? x * 128 : 0) + row] = make_float2(m_run, l_run);
+                if (kParts || !whole)
+                    work.ml[piece * S::TM + (S::WIDE ? x * 128 : 0) + row] = make_float2(m_run, l_run);
                 else if (a.lse)
                     a.lse[head] = zero ? -INFINITY : m_run * 0.693147181f + logf(l_run);
             }
         }
         if (x == 0 && row == 0) {
-            if (first_tile == 0 && cur.s == 0 && a.row_status) a.row_status[cur.b] = status;
-            if (!whole) {
+            if constexpr (kParts) {
                 work.status[piece] = status;
-                if (first_tile == 0) {
-                    work.notes[cta].b = cur.b;
-                    work.notes[cta].s = cur.s;
-                    work.notes[cta].last = attn_owner(run.units, run.unit(j0 + cur.tiles - 1, seg), run.used);
+                if (first_tile == 0)
+                    work.segs[attn_seg(a, cur)] =
+                        PartNote{cta, attn_owner(run.units, run.unit(j0 + cur.tiles - 1, seg), run.used)};
+            } else {
+                if (first_tile == 0 && cur.s == 0 && a.row_status) a.row_status[cur.b] = status;
+                if (!whole) {
+                    work.status[piece] = status;
+                    if (first_tile == 0) {
+                        work.notes[cta].b = cur.b;
+                        work.notes[cta].s = cur.s;
+                        work.notes[cta].last = attn_owner(run.units, run.unit(j0 + cur.tiles - 1, seg), run.used);
+                    }
                 }
             }
         }
@@ -860,8 +872,8 @@ __device__ void tc_softmax_role(const AttnArgs& a, TcShared<S>& sh, AttnCursor c
 }
 
 // ------------------------------------------------------------------ the kernel
-template <typename S>
-__global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
+template <typename S, typename A>
+__global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const A a, const __grid_constant__ TcMaps maps) {
     extern __shared__ __align__(1024) unsigned char tc_smem[];
     TcShared<S>& sh = *reinterpret_cast<TcShared<S>*>(tc_smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -874,7 +886,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const
     const AttnRun run = attn_cut<S::kThreads, S::kCost>(a, sh.cut, S::KT, blockIdx.x, gridDim.x, cur);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this grid's end
     if (tid == 0) {
-        AttnNote* note = attn_work(a.workspace, gridDim.x, S::TM, S::DP).notes + blockIdx.x;
+        AttnNote* note = attn_work_of(a, gridDim.x, S::TM, S::DP).notes + blockIdx.x;
         note->b = -1;
         note->failed = 0;
         note->b0 = cur.b;
@@ -941,7 +953,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const
             at.tile += nt - 1;
             at.next(a, S::KT);
         }
-        AttnNote* note = attn_work(a.workspace, gridDim.x, S::TM, S::DP).notes + blockIdx.x;
+        AttnNote* note = attn_work_of(a, gridDim.x, S::TM, S::DP).notes + blockIdx.x;
         note->b1 = at.b;
         note->failed = 1;
     }

@@ -110,7 +110,7 @@ def prefix_attention(q, kc, vc, tables, lens, prefix_table, prefix, parents, sca
             refused[b] |= ST_LENGTH
         if not P.tree(None if parents is None else parents[b], rows)[0]:
             refused[b] |= ST_PARENT
-        if not refused[b]:
+        if not refused[b] & ST_LENGTH:  # (a bad tree and a bad block are both told)
             own = full[b, n:-(-int(lens[b]) // bs)]
             if not (inside and np.all((own >= 0) & (own < blocks))):
                 refused[b] |= ST_BLOCK

@@ -43,6 +43,8 @@ __device__ __forceinline__ int attn_len(const MassArgs& a, int b) {
     return len > a.skip ? len - a.skip : 0;
 }
 
+__device__ __forceinline__ int attn_side(const MassArgs&) { return 1; }
+
 // DP: head_dim rounded up to 64, 128 or 256; NT tiles of eight queries at a
 // time; MT row groups of 16 positions a warp, four warps.
 template <typename T, int DP_, int NT_>
@@ -86,7 +88,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) attention_mass_kernel(c
 
     AttnCursor cur, ahead, ids;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // what the kernels before wrote
-    const AttnRun run = attn_cut<S::kThreads, 0>(a, s_cut, KT, blockIdx.x, gridDim.x, cur);
+    const AttnRun run = attn_cut<S::kThreads, 0>(a, s_cut, KT, kv.heads, blockIdx.x, gridDim.x, cur);
     const int n = run.n;
     if (n == 0) return;
     ids = ahead = cur;

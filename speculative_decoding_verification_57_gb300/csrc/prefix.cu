@@ -10,14 +10,18 @@ namespace {
 // The launches of a call: its kernels, and what each part needs of the workspace.
 struct PrefixPlan {
     const AttnPlan<PartArgs>*prefix, *own;
-    int prefix_ctas, own_ctas, prefix_tiles, own_tiles;
+    int prefix_ctas, own_ctas, prefix_tiles, own_tiles, side;
     int64_t prefix_bytes, own_bytes;
 };
 
 PrefixPlan prefix_plan(const specv_ctx* h, specv_dtype dt, int heads, int dim, int group, int batch, int rows) {
     PrefixPlan p;
     const int own = rows * group, all = batch * own;
-    p.prefix = &attn_plan<PartArgs>(dt, dim, all);
+    // Row tiles of 128 up to eight a kv head, side by side over the same positions, so that they read them from the L2 at
+    // about the same time; more rows take tiles of 256, which read the positions half as often
+    const int side = (all + 127) / 128;
+    p.prefix = &attn_plan<PartArgs>(dt, dim, side <= 8 && all > 128 ? 128 : all);
+    p.side = p.prefix->tc && side <= 8 ? side : 1;
     p.own = &attn_plan<PartArgs>(dt, dim, own);
     p.prefix_ctas = h->sm_count * p.prefix->ctas;
     p.own_ctas = h->sm_count * p.own->ctas;
@@ -35,13 +39,19 @@ bool prefix_sizes(const specv_ctx* h, int heads, int dim, int q_heads, int batch
     return static_cast<int64_t>(batch) * rows * q_heads * (dim / 4) <= INT32_MAX - kPrefixJoinThreads;
 }
 
-PartView part_view(unsigned char* w, const AttnPlan<PartArgs>& p, int ctas, int row_tiles, int64_t segs) {
+template <typename T>
+auto prefix_join(bool many) {
+    return many ? prefix_join_kernel<T, 4, 2> : prefix_join_kernel<T, 1, 8>;
+}
+
+PartView part_view(unsigned char* w, const AttnPlan<PartArgs>& p, int ctas, int row_tiles, int side, int64_t segs) {
     PartView v;
     v.workspace = w;
     v.segs = segs;
     v.ctas = ctas;
     v.tm = p.tm;
     v.row_tiles = row_tiles;
+    v.side = side;
     v.dp = p.dp;
     v.tile = FastDiv(static_cast<uint32_t>(p.tm));
     return v;
@@ -88,6 +98,7 @@ specv_status specv_prefix_attention(specv_handle h, const specv_kv_cache* cache,
     own.rows = own.own = rows;
     own.batch = batch;
     own.row_tiles = p.own_tiles;
+    own.side = 1;
     own.scale = scale;
     own.withhold = -1;
     own.polls = 1u << 30;
@@ -103,6 +114,7 @@ specv_status specv_prefix_attention(specv_handle h, const specv_kv_cache* cache,
     all.own = 0;
     all.batch = 1;
     all.row_tiles = p.prefix_tiles;
+    all.side = p.side;
     all.prefix = nullptr;
     if (p.prefix->tc && h->test_withhold >= 0) {  // the test hook arms one launch
         all.withhold = h->test_withhold;
@@ -110,18 +122,21 @@ specv_status specv_prefix_attention(specv_handle h, const specv_kv_cache* cache,
         h->test_withhold = -1;
     }
     PrefixJoinArgs j = {};
-    j.prefix = part_view(all.workspace, *p.prefix, p.prefix_ctas, p.prefix_tiles,
+    j.prefix = part_view(all.workspace, *p.prefix, p.prefix_ctas, p.prefix_tiles, all.side,
                          static_cast<int64_t>(cache->kv_heads) * p.prefix_tiles);
-    j.own = part_view(own.workspace, *p.own, p.own_ctas, p.own_tiles,
+    j.own = part_view(own.workspace, *p.own, p.own_ctas, p.own_tiles, 1,
                       static_cast<int64_t>(batch) * cache->kv_heads * p.own_tiles);
     j.lens = cache->seq_lens;
     j.out = out;
     j.lse = lse;
     j.row_status = row_status;
     j.rows_of_head = FastDiv(static_cast<uint32_t>(rows * group));
-    j.columns = FastDiv(static_cast<uint32_t>(cache->head_dim / 4));
+    // sixteen columns a thread where there are more threads than the SMs hold at once
+    const int64_t fours = static_cast<int64_t>(batch) * rows * q_heads * (cache->head_dim / 4);
+    const bool many = fours > static_cast<int64_t>(h->sm_count) * 1024;
+    j.columns = FastDiv(static_cast<uint32_t>(cache->head_dim / (many ? 16 : 4)));
     j.group = own.group;
-    j.all = static_cast<int64_t>(batch) * rows * q_heads * (cache->head_dim / 4);
+    j.all = many ? fours / 4 : fours;
     j.batch = batch;
     j.heads = cache->kv_heads;
     j.rows = rows;
@@ -135,8 +150,8 @@ specv_status specv_prefix_attention(specv_handle h, const specv_kv_cache* cache,
     if (e == cudaSuccess) e = p.own->launch(own, p.own_ctas, s);
     const unsigned grid = static_cast<unsigned>(j.blocks + (batch + kPrefixJoinThreads - 1) / kPrefixJoinThreads);
     if (e == cudaSuccess)
-        e = launch_early(cache->dtype == SPECV_BF16 ? prefix_join_kernel<__nv_bfloat16> : prefix_join_kernel<float>,
-                         dim3(grid), kPrefixJoinThreads, 0, s, j);
+        e = launch_early(cache->dtype == SPECV_BF16 ? prefix_join<__nv_bfloat16>(many) : prefix_join<float>(many), dim3(grid),
+                         kPrefixJoinThreads, 0, s, j);
     if (e != cudaSuccess) return cuda_fail(e, "prefix_attention launch");
     h->launches.fetch_add(3, std::memory_order_relaxed);
     return SPECV_OK;

@@ -19,6 +19,7 @@ struct PartView {
     unsigned char* workspace;
     int64_t segs;
     int ctas, tm, row_tiles, dp;
+    int side;     // from a CTA with a segment's piece to the next
     FastDiv tile;  // by tm
 };
 
@@ -29,91 +30,120 @@ struct PrefixJoinArgs {
     float* lse;
     int32_t* row_status;
     FastDiv rows_of_head;  // rows * group
-    FastDiv columns;       // groups of four columns of a head
+    FastDiv columns;       // a thread's columns of a head
     FastDiv group;
     int64_t all;  // threads: batch * kv heads * columns * rows * group
     int batch, heads, rows, q_heads, dim;
     int blocks;  // of the threads; behind them those that write the status
 };
 
-// The parts of a row joined so far.
+// The parts of a row joined so far, of COLS groups of four columns.
+template <int COLS>
 struct PrefixSum {
     float m = -INFINITY, l = 0.0f;
-    float4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+    float4 x[COLS];
     int status = 0;
 };
 
-// The pieces of segment `seg`, row `row` of its tile, columns 4 col ..
-__device__ __forceinline__ void prefix_join_part(const PartView& p, int64_t seg, int row, int col, PrefixSum& sum) {
+// The pieces of segment `seg`, row `row` of its tile, columns 4 col ..; PIECES of them in flight.
+template <int COLS, int PIECES>
+__device__ __forceinline__ void prefix_join_part(const PartView& p, const PartNote& note, int64_t seg, int row, int col,
+                                                 PrefixSum<COLS>& sum) {
     const PartWork work = part_work(p.workspace, p.ctas, p.segs, p.tm, p.dp);
-    const PartNote note = work.segs[seg];
-    constexpr int kPieces = 4;  // in flight
-    for (int c = note.first; c <= note.last; c += kPieces) {
-        float2 ml[kPieces];
-        float4 y[kPieces];
+    for (int c = note.first; c <= note.last; c += PIECES * p.side) {
+        float2 ml[PIECES];
+        float4 y[PIECES][COLS];
+        int status[PIECES];
 #pragma unroll
-        for (int u = 0; u < kPieces; ++u) {
+        for (int u = 0; u < PIECES; ++u) {
             ml[u] = make_float2(-INFINITY, 0.0f);
-            y[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (c + u > note.last) continue;
+            status[u] = 0;
+#pragma unroll
+            for (int k = 0; k < COLS; ++k) y[u][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const int at = c + u * p.side;
+            if (at > note.last) continue;
             // whole; or [1] of the CTA that starts the segment, then [0] of the next ones
-            const int64_t piece = note.first == note.last ? 2ll * p.ctas + seg : 2ll * (c + u) + (c + u == note.first);
-            sum.status |= work.status[piece];
+            const int64_t piece = note.first == note.last ? 2ll * p.ctas + seg : 2ll * at + (at == note.first);
+            status[u] = work.status[piece];
             ml[u] = work.ml[piece * p.tm + row];
-            y[u] = work.acc[(piece * (p.dp / 4) + col) * p.tm + row];
+#pragma unroll
+            for (int k = 0; k < COLS; ++k) y[u][k] = work.acc[(piece * (p.dp / 4) + col + k) * p.tm + row];
         }
         float m = sum.m;
 #pragma unroll
-        for (int u = 0; u < kPieces; ++u) m = fmaxf(m, ml[u].x);
+        for (int u = 0; u < PIECES; ++u) m = fmaxf(m, ml[u].x);
         const float m_use = m == -INFINITY ? 0.0f : m;
         const float before = ex2(sum.m - m_use);
         sum.m = m;
         sum.l *= before;
-        sum.x = make_float4(sum.x.x * before, sum.x.y * before, sum.x.z * before, sum.x.w * before);
 #pragma unroll
-        for (int u = 0; u < kPieces; ++u) {
-            if (c + u > note.last) break;
+        for (int k = 0; k < COLS; ++k)
+            sum.x[k] = make_float4(sum.x[k].x * before, sum.x[k].y * before, sum.x[k].z * before, sum.x[k].w * before);
+#pragma unroll
+        for (int u = 0; u < PIECES; ++u) {
+            if (c + u * p.side > note.last) break;
+            sum.status |= status[u];
             const float w = ex2(ml[u].x - m_use);
             sum.l = fmaf(ml[u].y, w, sum.l);
-            sum.x = make_float4(fmaf(y[u].x, w, sum.x.x), fmaf(y[u].y, w, sum.x.y), fmaf(y[u].z, w, sum.x.z),
-                                fmaf(y[u].w, w, sum.x.w));
+#pragma unroll
+            for (int k = 0; k < COLS; ++k)
+                sum.x[k] = make_float4(fmaf(y[u][k].x, w, sum.x[k].x), fmaf(y[u][k].y, w, sum.x[k].y),
+                                       fmaf(y[u][k].z, w, sum.x[k].z), fmaf(y[u][k].w, w, sum.x[k].w));
         }
     }
 }
 
-// Status bits of a segment's pieces.
-__device__ __forceinline__ int prefix_status(const PartView& p, int64_t seg) {
+__device__ __forceinline__ PartNote prefix_note(const PartView& p, int64_t seg) {
+    return part_work(p.workspace, p.ctas, p.segs, p.tm, p.dp).segs[seg];
+}
+
+// Status bits of a segment's pieces, of every `step`-th from the `start`-th on.
+__device__ __forceinline__ int prefix_status(const PartView& p, int64_t seg, int start, int step) {
     const PartWork work = part_work(p.workspace, p.ctas, p.segs, p.tm, p.dp);
     const PartNote note = work.segs[seg];
-    if (note.first == note.last) return work.status[2ll * p.ctas + seg];
     int status = 0;
-    for (int c = note.first; c <= note.last; ++c) status |= work.status[2ll * c + (c == note.first)];
+    for (int c = note.first + start * p.side; c <= note.last; c += step * p.side)
+        status |= work.status[note.first == note.last ? 2ll * p.ctas + seg : 2ll * c + (c == note.first)];
     return status;
 }
 
-// Four columns of a row a thread, rows of a kv head side by side.
-template <typename T>
-__global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(const PrefixJoinArgs a) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (blockIdx.x >= a.blocks) {  // a sequence's status: its first head's, that head's of the prefix, and waits that ran out
-        if (!a.row_status) return;
-        const int b = (blockIdx.x - a.blocks) * kPrefixJoinThreads + threadIdx.x;
-        const AttnNote* prefix = reinterpret_cast<const AttnNote*>(a.prefix.workspace);
-        const AttnNote* own = reinterpret_cast<const AttnNote*>(a.own.workspace);
-        bool late = false;
-        for (int c = threadIdx.x; c < a.prefix.ctas; c += kPrefixJoinThreads) late |= prefix[c].failed != 0;
-        late = __syncthreads_or(late) != 0;
-        if (b >= a.batch) return;
-        int status = 0;
-        if (a.lens[b] != 0) {
-            status = prefix_status(a.own, static_cast<int64_t>(b) * a.heads * a.own.row_tiles);
-            // (a sequence of a bad length is not looked at any further; the prefix's table is the same for every head)
-            if (!(status & KV_LENGTH)) status |= prefix_status(a.prefix, 0);
-            if (late) status |= KV_TIMEOUT;
+// A sequence's status: its first head's, that head's of the prefix, and waits
+// that ran out.  A thread a sequence; what is the same for all is looked at by the CTA.
+__device__ __forceinline__ void prefix_join_status(const PrefixJoinArgs& a, int b) {
+    const AttnNote* prefix = reinterpret_cast<const AttnNote*>(a.prefix.workspace);
+    const AttnNote* own = reinterpret_cast<const AttnNote*>(a.own.workspace);
+    int late = 0;  // 1: a wait of the prefix's, 2: of the own part's CTAs
+    for (int c = threadIdx.x; c < a.prefix.ctas; c += kPrefixJoinThreads) late |= prefix[c].failed != 0;
+    for (int c = threadIdx.x; c < a.own.ctas; c += kPrefixJoinThreads) late |= own[c].failed != 0 ? 2 : 0;
+    const int before = prefix_status(a.prefix, 0, threadIdx.x, kPrefixJoinThreads);
+    __shared__ int s_late, s_before;
+    if (threadIdx.x == 0) s_late = s_before = 0;
+    __syncthreads();
+    if (late) atomicOr(&s_late, late);
+    if (before) atomicOr(&s_before, before);
+    __syncthreads();
+    if (b >= a.batch) return;
+    int status = 0;
+    if (a.lens[b] != 0) {
+        status = prefix_status(a.own, static_cast<int64_t>(b) * a.heads * a.own.row_tiles, 0, 1);
+        if (!(status & KV_LENGTH)) status |= s_before;  // (a sequence of a bad length is not looked at any further)
+        if (s_late & 1) status |= KV_TIMEOUT;
+        if (s_late & 2)
             for (int c = 0; c < a.own.ctas; ++c)
                 if (own[c].failed && own[c].b0 <= b && b <= own[c].b1) status |= KV_TIMEOUT;
-        }
-        a.row_status[b] = status;
+    }
+    a.row_status[b] = status;
+}
+
+// COLS groups of four columns of a row a thread, rows of a kv head side by
+// side.  Bound by latency (length, notes, pieces, one behind the other): a
+// thread has many pieces in flight where there are few rows, each spread over
+// many CTAs, and many columns where there are many, in two or three pieces.
+template <typename T, int COLS, int PIECES>
+__global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(const PrefixJoinArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (blockIdx.x >= a.blocks) {
+        if (a.row_status) prefix_join_status(a, (blockIdx.x - a.blocks) * kPrefixJoinThreads + threadIdx.x);
         return;
     }
     const int64_t at = static_cast<int64_t>(blockIdx.x) * kPrefixJoinThreads + threadIdx.x;
@@ -121,24 +151,31 @@ __global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(const P
     // rows of a head fastest, then columns, heads, sequences (the quotients below 2^31: `all` is)
     const uint32_t i = static_cast<uint32_t>(at);
     const uint32_t x = a.rows_of_head.div(i), m = i - x * a.rows_of_head.d;
-    const uint32_t y = a.columns.div(x), col = x - y * a.columns.d;
+    const uint32_t y = a.columns.div(x), col = (x - y * a.columns.d) * COLS;
     const int b = static_cast<int>(y / static_cast<uint32_t>(a.heads)), h = static_cast<int>(y) - b * a.heads;
     const uint32_t r = a.group.div(m), g = m - r * a.group.d;
-    PrefixSum sum;
+    const uint32_t own_tile = a.own.tile.div(m);
+    const int64_t own_seg = (static_cast<int64_t>(b) * a.heads + h) * a.own.row_tiles + own_tile;
+    const uint32_t row = static_cast<uint32_t>(b) * a.rows_of_head.d + m, tile = a.prefix.tile.div(row);
+    const int64_t seg = static_cast<int64_t>(h) * a.prefix.row_tiles + tile;
+    const PartNote own_note = prefix_note(a.own, own_seg), note = prefix_note(a.prefix, seg);
+    PrefixSum<COLS> sum;
+#pragma unroll
+    for (int k = 0; k < COLS; ++k) sum.x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const bool idle = a.lens[b] == 0;
     if (!idle) {
-        const uint32_t mine = a.own.tile.div(m);
-        prefix_join_part(a.own, (static_cast<int64_t>(b) * a.heads + h) * a.own.row_tiles + mine, m - mine * a.own.tm, col,
-                         sum);
-        const uint32_t row = static_cast<uint32_t>(b) * a.rows_of_head.d + m, tile = a.prefix.tile.div(row);
-        prefix_join_part(a.prefix, static_cast<int64_t>(h) * a.prefix.row_tiles + tile, row - tile * a.prefix.tm, col, sum);
+        prefix_join_part<COLS, 2>(a.own, own_note, own_seg, m - own_tile * a.own.tm, col, sum);
+        prefix_join_part<COLS, PIECES>(a.prefix, note, seg, row - tile * a.prefix.tm, col, sum);
     }
     const bool zero = idle || sum.status != 0;
     const float inv = zero ? 0.0f : 1.0f / sum.l;
-    if (zero) sum.x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const int64_t head = (static_cast<int64_t>(b) * a.rows + r) * a.q_heads + static_cast<int64_t>(h) * a.group.d + g;
-    attn_store4(static_cast<T*>(a.out) + head * a.dim + col * 4, sum.x.x * inv, sum.x.y * inv, sum.x.z * inv,
-                sum.x.w * inv);
+#pragma unroll
+    for (int k = 0; k < COLS; ++k) {
+        if (zero) sum.x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        attn_store4(static_cast<T*>(a.out) + head * a.dim + (col + k) * 4, sum.x[k].x * inv, sum.x[k].y * inv,
+                    sum.x[k].z * inv, sum.x[k].w * inv);
+    }
     if (col == 0 && a.lse) a.lse[head] = zero ? -INFINITY : sum.m * 0.693147181f + logf(sum.l);
 }
 

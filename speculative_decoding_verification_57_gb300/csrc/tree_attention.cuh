@@ -71,6 +71,7 @@ struct PartArgs : AttnArgs {
                             // sequence whose length is the prefix's and whose rows are all sequences', in their order
     int prefix_cap;         // the most positions that the prefix's table holds
     int own;                // rows of the pass among a sequence's positions: `rows`, or of the prefix none
+    int side;               // row tiles of a kv head that as many CTAs side by side take over the same positions; 1: none
 };
 
 // Factor of the scores in base 2.  A scale of zero still has to tell hidden
@@ -104,9 +105,22 @@ __device__ __forceinline__ int attn_first_block(const AttnArgs&) { return 0; }
 __device__ __forceinline__ int attn_first_block(const PartArgs& a) {
     return a.prefix ? static_cast<int>(a.kv.block.div(max(*a.prefix, 0))) : 0;
 }
+// What the kernels before wrote is waited for at a kernel's start; by a part
+// behind another at its end.  The part before lets it start when all of its CTAs
+// are through with that wait, so that whatever was written before the call is
+// there; and a kernel behind this one finds both parts' results, as this one
+// ends after the part before.
+__device__ __forceinline__ bool attn_waits_late(const AttnArgs&) { return false; }
+__device__ __forceinline__ bool attn_waits_late(const PartArgs& a) { return a.prefix != nullptr; }
+__device__ __forceinline__ void attn_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Rows of the pass that are the last positions of a sequence.
 __device__ __forceinline__ int attn_own(const AttnArgs& a) { return a.rows; }
 __device__ __forceinline__ int attn_own(const PartArgs& a) { return a.own; }
+
+// CTAs side by side, each with a row tile of its own of the same positions.
+__device__ __forceinline__ int attn_side(const AttnArgs&) { return 1; }
+__device__ __forceinline__ int attn_side(const PartArgs& a) { return a.side; }
 
 // An idle or refused sequence counts as a tile, whose CTA writes its zeros.
 __device__ __forceinline__ int attn_tiles(int len, int tile) { return len <= 0 ? 1 : (len + tile - 1) / tile; }
@@ -132,9 +146,14 @@ struct AttnCursor {
 
     template <typename A>
     __device__ __forceinline__ void next(const A& a, int tile_keys) {
+        next(a, tile_keys, attn_side(a), a.kv.heads * a.row_tiles);
+    }
+    // ... on a line of `segs` segments a sequence, of which every `side`-th is on it
+    template <typename A>
+    __device__ __forceinline__ void next(const A& a, int tile_keys, int side, int segs) {
         if (++tile < tiles) return;
         tile = 0;
-        if (++s < a.kv.heads * a.row_tiles) return;
+        if ((s += side) < segs) return;
         s = 0;
         if (++b < a.batch) {
             len = attn_len(a, b);
@@ -166,15 +185,14 @@ struct AttnRun {
     }
 };
 
-// The run of CTA `cta` of `ctas` and the cursor at its first tile, by the
-// whole CTA (THREADS threads, a multiple of 32).  COST: a segment's extra
+// The run of CTA `cta` of `ctas` on a line of `segs` segments a sequence, and
+// the cursor at its first tile, by the whole CTA (THREADS threads, a multiple of 32).  COST: a segment's extra
 // units, in tiles, where a run has eight tiles or more.  Up to 32 sequences
 // every warp finds out by itself; with more, each thread has some of them.
 template <int THREADS, int COST, typename A>
-__device__ AttnRun attn_cut(const A& a, AttnCut& sh, int tile_keys, int cta, int ctas, AttnCursor& cur) {
+__device__ AttnRun attn_cut(const A& a, AttnCut& sh, int tile_keys, int segs, int cta, int ctas, AttnCursor& cur) {
     constexpr int kEnds = COST > 0 ? 2 : 1;  // of the run, looked for among the sequences
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int segs = a.kv.heads * a.row_tiles;
     const bool small = a.batch <= 32;
     // the total
     int64_t sum = 0, mine = 0, incl = 0;
@@ -277,7 +295,7 @@ __device__ AttnRun attn_cut(const A& a, AttnCut& sh, int tile_keys, int cta, int
         cur.tile = at < t ? at : t - 1;
         if (at >= t) {  // in the units behind a segment's last tile: on to the next segment
             run.first += t + run.extra - at;
-            cur.next(a, tile_keys);
+            cur.next(a, tile_keys, 1, segs);
         }
     }
     run.n = static_cast<int>(kEnds == 2 ? tiles[kEnds - 1] - tiles[0] : ends[1] - ends[0]);
@@ -509,8 +527,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
     const float hidden = c_scale < 0.0f ? INFINITY : -INFINITY;
 
     AttnCursor cur, ahead, ids;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // what the kernels before wrote
-    const AttnRun run = attn_cut<S::kThreads, 0>(a, s_cut, KT, cta, ctas, cur);
+    if (!attn_waits_late(a)) attn_wait();
+    const AttnRun run = attn_cut<S::kThreads, 0>(a, s_cut, KT, kv.heads * a.row_tiles, cta, ctas, cur);
     const int first_block = attn_first_block(a);
     if (tid == 0) {
         s_wild[0] = s_wild[1] = 0;
@@ -519,7 +537,10 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this grid's end
     const int n = run.n;
-    if (n == 0) return;
+    if (n == 0) {
+        if (attn_waits_late(a)) attn_wait();
+        return;
+    }
     ids = ahead = cur;
 
     // block number of this thread's position in tile `i` of the run, whose cursor `ids` is: into a register ...
@@ -985,6 +1006,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
         }
         cur.next(a, KT);
     }
+    if (attn_waits_late(a)) attn_wait();
 }
 
 // ------------------------------------------------------------------ the join

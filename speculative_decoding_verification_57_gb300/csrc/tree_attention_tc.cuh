@@ -60,32 +60,36 @@ __device__ __forceinline__ void tc_after_sync() { asm volatile("tcgen05.fence::a
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// The issuing warp runs as one and one lane of it (`lead` not 0) issues.
-// Arrives on `bar` when every product that lane issued so far is done.
-__device__ __forceinline__ void tc_commit(uint32_t bar, uint32_t lead) {
-    asm volatile(
-        "{\n .reg .pred q;\n setp.ne.u32 q, %1, 0;\n"
-        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
-        "r"(lead)
-        : "memory");
+// One lane of a converged warp, the same every time.  Products are issued in
+// branches on this: told by a lane's number instead, the compiler cannot see
+// that one thread runs them, and an instruction took 80 to 100 cycles to
+// issue, more than its 64 on the tensor cores (64 trees of 17 rows behind a
+// prefix of 8192 positions: 216 us for 204).
+__device__ __forceinline__ bool tc_elect() {
+    uint32_t x;
+    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(x));
+    return x != 0;
+}
+
+// Arrives on `bar` when every product that this thread issued so far is done.
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // d (+)= a b, a and b in shared memory
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add,
-                                          uint32_t lead) {
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
     asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(add), "r"(lead)
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add)
         : "memory");
 }
 // d (+)= a b, a in tensor memory
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add,
-                                          uint32_t lead) {
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
     asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(add), "r"(lead)
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add)
         : "memory");
 }
 
@@ -130,13 +134,14 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) 
 
 // Shared memory operands in 128-byte swizzled panels (64 columns of bf16; row
 // r at 128 r, eight rows an atom of 1024 bytes).
-// ... contraction along the columns: atoms 1024 bytes apart along the rows
-__device__ __forceinline__ uint64_t tc_desc_rows(uint32_t addr) {
-    return (2ull << 61) | (1ull << 46) | (64ull << 32) | (1ull << 16) | ((addr >> 4) & 0x3fff);
+// ... contraction along the columns: atoms `step` bytes apart along the rows
+__device__ __forceinline__ uint64_t tc_desc_rows(uint32_t addr, uint32_t step) {
+    return (2ull << 61) | (1ull << 46) | (static_cast<uint64_t>(step >> 4) << 32) | (1ull << 16) | ((addr >> 4) & 0x3fff);
 }
-// ... contraction along the rows: atoms 1024 bytes apart along it, panels of 128 rows apart along the columns
-__device__ __forceinline__ uint64_t tc_desc_cols(uint32_t addr) {
-    return (2ull << 61) | (1ull << 46) | (64ull << 32) | (1024ull << 16) | ((addr >> 4) & 0x3fff);
+// ... contraction along the rows: atoms `step` bytes apart along it, panels `panel` bytes apart along the columns
+__device__ __forceinline__ uint64_t tc_desc_cols(uint32_t addr, uint32_t step, uint32_t panel) {
+    return (2ull << 61) | (1ull << 46) | (static_cast<uint64_t>(step >> 4) << 32) |
+           (static_cast<uint64_t>(panel >> 4) << 16) | ((addr >> 4) & 0x3fff);
 }
 
 // bf16 x bf16 -> fp32, 128 rows, n columns; cols: the right operand's contraction runs along its rows
@@ -183,14 +188,34 @@ struct TcShape {
     }
 };
 
+// How the keys and values of a tile lie in their slot: eight rows of a panel
+// are 1024 bytes; `step` bytes on lie the next eight rows, `panel` bytes on the
+// next panel of the same rows.
+struct TcLayout {
+    uint32_t step, panel;
+
+    __device__ __forceinline__ uint32_t at(int row, int piece) const {  // byte offset of 16-byte piece `piece` of a row
+        return (piece >> 3) * panel + (row >> 3) * step + (row & 7) * 128 + (((piece & 7) ^ (row & 7)) << 4);
+    }
+};
+
 // Tensor maps of the two pools ([blocks, heads, block_size, head_dim], boxes
 // of `rows` rows of 64 columns), where boxes are used, and of the queries
 // ([batch, rows, heads, head_dim], boxes of a group of heads of q_rows rows,
 // 128 rows of a row tile) where groups fill row tiles (q_rows 0: they do not).
+// Rows of 128 values in pools whose blocks lie whole heads apart come with both
+// panels in one box ([blocks and heads, block_size / 8, 2, 8, 64]: `flat` heads
+// from a block to the next; else 0): half as many boxes, of which a warp takes
+// some 90 cycles each to issue.
 struct TcMaps {
     CUtensorMap k, v, q;
-    int rows, q_rows;
+    int rows, q_rows, flat;
 };
+
+template <typename S>
+__device__ __forceinline__ TcLayout tc_layout(const TcMaps& maps) {
+    return S::TMA && maps.flat ? TcLayout{2048, 1024} : TcLayout{1024, S::kPanel};
+}
 
 template <typename S>
 struct TcShared {
@@ -200,7 +225,7 @@ struct TcShared {
     AttnCut cut;
     // a slot's copies have landed, are visible to the tensor cores, are used up
     uint64_t full[S::kSlots], shown[S::kSlots], empty[S::kSlots];
-    uint64_t q_full, q_shown, q_empty, s_full[2], p_ready[2], o_done[2], turn[2], end[2];
+    uint64_t q_full, q_shown, q_empty, s_full[2], p_half[2], p_ready[2], o_done[2], turn[2], end[2];
     uint32_t wild[16];  // by segment: nodes with values that are not finite ...
     int hole[16];       // ... and whether a block is outside the pool
     uint32_t tmem;
@@ -238,6 +263,15 @@ __device__ __forceinline__ void tc_box(uint32_t dst, const CUtensorMap* map, int
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
         "[%6];" ::"r"(dst),
         "l"(map), "r"(col), "r"(row), "r"(h), "r"(blk), "r"(bar)
+        : "memory");
+}
+
+// Both panels of rows 8 `row8` .. of a head of a block.
+__device__ __forceinline__ void tc_box2(uint32_t dst, const CUtensorMap* map, int row8, int head, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(map), "r"(0), "r"(row8), "r"(head), "r"(bar)
         : "memory");
 }
 
@@ -303,7 +337,8 @@ template <typename S, typename A>
 __device__ void tc_box_role(const A& a, const TcMaps& maps, TcShared<S>& sh, const AttnCursor& cur, int n,
                             int warp, int lane) {
     const KvView& kv = a.kv;
-    const int part = lane / S::kPanels, panel = lane % S::kPanels;  // block of the tile, and columns
+    const int panels = maps.flat ? 1 : S::kPanels;
+    const int part = lane / panels, panel = lane % panels;         // block of the tile, and columns
     const int rows = maps.rows;                                    // of a box
     const bool mine = part * rows < S::KT;
     const int first_block = attn_first_block(a);
@@ -356,7 +391,10 @@ __device__ void tc_box_role(const A& a, const TcMaps& maps, TcShared<S>& sh, con
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(bar, S::kSlot);
         __syncwarp();
-        if (mine)
+        if (mine && maps.flat)
+            tc_box2(smem_u32(sh.slot[slot]) + part * rows * 256, x.values ? &maps.v : &maps.k, valid ? x.row >> 3 : 0,
+                    (valid ? x.blk : kv.blocks) * maps.flat + (valid ? x.h : 0), bar);
+        else if (mine)
             tc_box(smem_u32(sh.slot[slot]) + panel * S::kPanel + part * rows * 128, x.values ? &maps.v : &maps.k,
                    panel * 64, valid ? x.row : 0, x.h, valid ? x.blk : kv.blocks, bar);
     }
@@ -497,7 +535,7 @@ __device__ void tc_show_role(const A& a, TcShared<S>& sh, const AttnCursor& cur,
 // tile i >> 1 (WIDE) or i.  A stream's next scores follow its output product,
 // whose weights lie where they go: products of one thread run in order.
 template <typename S, typename A>
-__device__ void tc_mma_role(const A& a, TcShared<S>& sh, AttnCursor cur, int n, int x, uint32_t lead) {
+__device__ void tc_mma_role(const A& a, TcShared<S>& sh, const TcLayout& lay, AttnCursor cur, int n, int x) {
     const uint32_t tm = sh.tmem;
     const uint32_t ts = tm + x * 128, to = tm + 256 + x * S::DP;
     constexpr uint32_t kScores = tc_idesc(S::KT, false), kOutputs = tc_idesc(S::DP, true);
@@ -518,23 +556,25 @@ __device__ void tc_mma_role(const A& a, TcShared<S>& sh, AttnCursor cur, int n, 
     while (fine && j0 < n) {
         const int nt = tc_part(cur, n - j0);
         const int items = nt * S::kTiles;
-        const uint64_t qd = tc_desc_rows(smem_u32(sh.q) + (S::WIDE ? x * S::kSlot : 0));
+        const uint64_t qd = tc_desc_rows(smem_u32(sh.q) + (S::WIDE ? x * S::kSlot : 0), 1024);
         auto scores = [&](int slot) {
-            const uint64_t kd = tc_desc_rows(smem_u32(sh.slot[slot]));
+            const uint64_t kd = tc_desc_rows(smem_u32(sh.slot[slot]), lay.step);
 #pragma unroll
-            for (int kk = 0; kk < S::DP / 16; ++kk) {
-                const uint32_t off = ((kk >> 2) * S::kPanel + (kk & 3) * 32) >> 4;
-                tc_mma_ss(ts, qd + off, kd + off, kScores, kk > 0, lead);
-            }
+            for (int kk = 0; kk < S::DP / 16; ++kk)
+                tc_mma_ss(ts, qd + (((kk >> 2) * S::kPanel + (kk & 3) * 32) >> 4),
+                          kd + (((kk >> 2) * lay.panel + (kk & 3) * 32) >> 4), kScores, kk > 0);
         };
         wait(&sh.q_shown, seg & 1);  // (both warps are through with the part before)
         if (x < items) {
             const int slot = wait_slot(use0 + S::keys_at(S::WIDE ? 0 : x, nt));
             if (!fine) break;
             tc_after_sync();
-            scores(slot);
-            tc_commit(smem_u32(&sh.s_full[x]), lead);
-            tc_commit(smem_u32(&sh.empty[slot]), lead);
+            if (tc_elect()) {
+                scores(slot);
+                tc_commit(smem_u32(&sh.s_full[x]));
+                tc_commit(smem_u32(&sh.empty[slot]));
+            }
+            __syncwarp();
         }
         for (int i = x; i < items; i += 2) {
             const int t = S::WIDE ? i >> 1 : i;
@@ -545,27 +585,37 @@ __device__ void tc_mma_role(const A& a, TcShared<S>& sh, AttnCursor cur, int n, 
                 if (more) k_slot = wait_slot(use0 + S::keys_at(t + S::kLead, nt));
             };
             if (S::WIDE) wait_slots();
-            wait(&sh.p_ready[x], p_seen & 1);
-            ++p_seen;
             if (i > 0) {
                 wait(&sh.turn[x], turns & 1);
                 ++turns;
             }
             if (!S::WIDE) wait_slots();
-            if (!fine) break;
-            tc_after_sync();
-            const uint64_t vd = tc_desc_cols(smem_u32(sh.slot[v_slot]));
+            // weights of the tile's first half, and then of the second
+            const uint64_t vd = tc_desc_cols(smem_u32(sh.slot[v_slot]), lay.step, lay.panel);
 #pragma unroll
-            for (int kk = 0; kk < S::KT / 16; ++kk)
-                tc_mma_ts(to, ts + kk * 8, vd + kk * (2048 >> 4), kOutputs, i >= 2 || kk > 0, lead);
-            if (more) scores(k_slot);
-            if (lead && i + 1 < items) mbar_arrive(smem_u32(&sh.turn[x ^ 1]));
-            __syncwarp();
-            tc_commit(smem_u32(more ? &sh.s_full[x] : &sh.o_done[x]), lead);
-            tc_commit(smem_u32(&sh.empty[v_slot]), lead);
-            if (more) tc_commit(smem_u32(&sh.empty[k_slot]), lead);
+            for (int half = 0; half < 2; ++half) {
+                wait(half ? &sh.p_ready[x] : &sh.p_half[x], p_seen & 1);
+                if (!fine) break;
+                tc_after_sync();
+                if (tc_elect()) {
+#pragma unroll
+                    for (int kk = half * S::KT / 32; kk < (half + 1) * S::KT / 32; ++kk)
+                        tc_mma_ts(to, ts + kk * 8, vd + kk * (2 * lay.step >> 4), kOutputs, i >= 2 || kk > 0);
+                    if (half) {
+                        if (more) scores(k_slot);
+                        if (i + 1 < items) mbar_arrive(smem_u32(&sh.turn[x ^ 1]));
+                        tc_commit(smem_u32(more ? &sh.s_full[x] : &sh.o_done[x]));
+                        tc_commit(smem_u32(&sh.empty[v_slot]));
+                        if (more) tc_commit(smem_u32(&sh.empty[k_slot]));
+                    }
+                }
+                __syncwarp();
+            }
+            if (!fine) break;
+            ++p_seen;
         }
-        tc_commit(smem_u32(&sh.q_empty), lead);
+        if (tc_elect()) tc_commit(smem_u32(&sh.q_empty));
+        __syncwarp();
         j0 += nt;
         use0 += 2 * nt;
         cur.tile += nt - 1;
@@ -573,13 +623,15 @@ __device__ void tc_mma_role(const A& a, TcShared<S>& sh, AttnCursor cur, int n, 
         ++seg;
     }
     // nothing of this warp's is in flight when tensor memory is freed
-    tc_commit(smem_u32(&sh.end[x]), lead);
+    if (tc_elect()) tc_commit(smem_u32(&sh.end[x]));
+    __syncwarp();
     mbar_wait_bounded(smem_u32(&sh.end[x]), 0, 1u << 30);
 }
 
 // ------------------------------------------------------------------ softmax
 template <typename S, typename A>
-__device__ void tc_softmax_role(const A& a, TcShared<S>& sh, AttnCursor cur, const AttnRun& run, int x, int row) {
+__device__ void tc_softmax_role(const A& a, TcShared<S>& sh, const TcLayout& lay, AttnCursor cur, const AttnRun& run,
+                                int x, int row) {
     const int n = run.n;
     using T = typename S::Type;
     const KvView& kv = a.kv;
@@ -628,12 +680,19 @@ __device__ void tc_softmax_role(const A& a, TcShared<S>& sh, AttnCursor cur, con
             ++s_seen;
             if (!__all_sync(0xffffffffu, fine)) break;
             tc_after_sync();
+            const bool edge = t0 + S::KT > base;
+            auto half_ready = [&] {
+                tc_wait_st();
+                tc_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.p_half[x]));
+            };
             if (warp_in) {
                 uint32_t s[4][32];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tc_ld32(ts + c * 32, s[c]);
                 tc_wait_ld();
-                if (t0 + S::KT > base) {  // positions that not every row sees
+                if (edge) {  // positions that not every row sees
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         // bit e: position t0 + 32 c + e is before the pass's rows, or one that this row sees
@@ -650,15 +709,15 @@ __device__ void tc_softmax_role(const A& a, TcShared<S>& sh, AttnCursor cur, con
                 float top[4] = {hidden, hidden, hidden, hidden};
                 if (scale >= 0.0f) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
+                    for (int e = 0; e < 32; e += 2)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) top[c] = fmaxf(top[c], __uint_as_float(s[c][e]));
+                        for (int c = 0; c < 4; ++c) top[c] = max3(top[c], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
                     top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
+                    for (int e = 0; e < 32; e += 2)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) top[c] = fminf(top[c], __uint_as_float(s[c][e]));
+                        for (int c = 0; c < 4; ++c) top[c] = min3(top[c], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
                     top[0] = fminf(fminf(top[0], top[1]), fminf(top[2], top[3]));
                 }
                 top[0] *= scale;
@@ -700,13 +759,14 @@ __device__ void tc_softmax_role(const A& a, TcShared<S>& sh, AttnCursor cur, con
                         w[e] = kv_pack_bf16(w0, w1);
                     }
                     tc_st32(ts + half * 32, w);
+                    if (half == 0 && !edge) half_ready();
                 }
                 float l0, l1;
                 unpack2(add2(sum[0], sum[1]), l0, l1);
                 l_run += l0 + l1;
                 tc_wait_st();
             }
-            if (cur.len > 0 && t0 + S::KT > base) {
+            if (cur.len > 0 && edge) {
                 // values of the pass's rows that are not finite are taken out of the product, where a weight of zero
                 // would not hide them; they are added to the rows that see them at the segment's end
                 const int slot = (use0 + S::values_at(t, nt)) % S::kSlots;
@@ -721,8 +781,7 @@ __device__ void tc_softmax_role(const A& a, TcShared<S>& sh, AttnCursor cur, con
                 }
                 for (int y = lo_r * (S::DP / 8) + row; y < hi_r * (S::DP / 8); y += 128) {
                     const int vr = y / (S::DP / 8), vc = y % (S::DP / 8);
-                    KvVec<T>* vx = reinterpret_cast<KvVec<T>*>(sh.slot[slot] + (vc >> 3) * S::kPanel + vr * 128 +
-                                                               (((vc & 7) ^ (vr & 7)) << 4));
+                    KvVec<T>* vx = reinterpret_cast<KvVec<T>*>(sh.slot[slot] + lay.at(vr, vc));
                     if (vr >= end_r) {
                         *reinterpret_cast<uint4*>(vx) = make_uint4(0, 0, 0, 0);
                         continue;
@@ -745,6 +804,8 @@ __device__ void tc_softmax_role(const A& a, TcShared<S>& sh, AttnCursor cur, con
                 fence_proxy_async_smem();
                 __syncwarp();
             }
+            // (values that the products must not see are gone before the first of them)
+            if (!warp_in || edge) half_ready();
             tc_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.p_ready[x]));
@@ -846,7 +907,8 @@ __device__ void tc_softmax_role(const A& a, TcShared<S>& sh, AttnCursor cur, con
                 work.status[piece] = status;
                 if (first_tile == 0)
                     work.segs[attn_seg(a, cur)] =
-                        PartNote{cta, attn_owner(run.units, run.unit(j0 + cur.tiles - 1, seg), run.used)};
+                        PartNote{cta, attn_owner(run.units, run.unit(j0 + cur.tiles - 1, seg), run.used) * a.side +
+                                          cta % a.side};
             } else {
                 if (first_tile == 0 && cur.s == 0 && a.row_status) a.row_status[cur.b] = status;
                 if (!whole) {
@@ -882,8 +944,12 @@ __global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const
     }
     AttnCursor cur;
     cur.b = 0;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // what the kernels before wrote
-    const AttnRun run = attn_cut<S::kThreads, S::kCost>(a, sh.cut, S::KT, blockIdx.x, gridDim.x, cur);
+    if (!attn_waits_late(a)) attn_wait();
+    // row tiles side by side share the positions' cut
+    const int side = attn_side(a), line = blockIdx.x / side, beside = blockIdx.x - line * side;
+    const AttnRun run = attn_cut<S::kThreads, S::kCost>(a, sh.cut, S::KT, a.kv.heads * (side > 1 ? 1 : a.row_tiles), line,
+                                                        gridDim.x / side, cur);
+    if (side > 1) cur.s = cur.s * side + beside;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this grid's end
     if (tid == 0) {
         AttnNote* note = attn_work_of(a, gridDim.x, S::TM, S::DP).notes + blockIdx.x;
@@ -893,7 +959,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const
         sh.start = cur;
     }
     const int n = run.n;
-    if (n == 0) return;
+    if (n == 0) {
+        if (attn_waits_late(a)) attn_wait();
+        return;
+    }
     if (tid == 0) {
         for (int i = 0; i < S::kSlots; ++i) {
             mbar_init(smem_u32(&sh.full[i]), S::TMA ? 1 : 128);
@@ -905,6 +974,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const
         mbar_init(smem_u32(&sh.q_empty), 2);
         for (int x = 0; x < 2; ++x) {
             mbar_init(smem_u32(&sh.s_full[x]), 1);
+            mbar_init(smem_u32(&sh.p_half[x]), 4);
             mbar_init(smem_u32(&sh.p_ready[x]), 4);
             mbar_init(smem_u32(&sh.o_done[x]), 1);
             mbar_init(smem_u32(&sh.turn[x]), 1);
@@ -922,13 +992,14 @@ __global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
+    const TcLayout lay = tc_layout<S>(maps);
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kMany));
-        tc_softmax_role<S>(a, sh, cur, run, warp >> 2, tid & 127);
+        tc_softmax_role<S>(a, sh, lay, cur, run, warp >> 2, tid & 127);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kFew));
         if (warp == 12 || warp == 13) {
-            tc_mma_role<S>(a, sh, cur, n, warp - 12, lane == 0);
+            tc_mma_role<S>(a, sh, lay, cur, n, warp - 12);
         } else if constexpr (S::TMA) {
             if (warp < 8 + S::kBoxWarps)
                 tc_box_role<S>(a, maps, sh, cur, n, warp - 8, lane);
@@ -957,6 +1028,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const
         note->b1 = at.b;
         note->failed = 1;
     }
+    if (attn_waits_late(a)) attn_wait();
 }
 
 }  // namespace specv

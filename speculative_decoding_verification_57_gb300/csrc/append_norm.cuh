@@ -9,9 +9,11 @@
 // Layout, loads ahead of the length and the rest as in cache_append.cuh.  A
 // head belongs to a group of 1, 2, 4, .. 32 neighbouring lanes, the least that
 // hold its pieces, so that its sum of squares is added up by shuffles; lanes
-// behind the head's pieces (heads of 96: two of eight) are idle.  Weights
-// lie in shared memory in fp32, read as often as the data: in registers they
-// would cost resident CTAs.
+// behind the head's pieces (heads of 96: two of eight) are idle.  A thread has
+// the same two pieces of every head it works on: the products of their weights
+// with their sines and cosines stay in its registers, for queries and then
+// for keys, so that a norm costs a head eight multiply-adds, the shuffles and
+// eight products more than the turn.
 #pragma once
 #include "cache_append.cuh"
 
@@ -65,23 +67,28 @@ __device__ __forceinline__ void append_close(const f2 (&f)[KvType<T>::kVec / 2],
     }
 }
 
-// Neighbours f[e] turned by the angle of pair e.
+// Neighbours f[e] by (their weights times) the cosine, c[e], and the sine, s[e], of the pair.
 template <int N>
-__device__ __forceinline__ void append_neighbours(f2 (&f)[N], const float* c, const float* s) {
+__device__ __forceinline__ void append_neighbours(f2 (&f)[N], const f2 (&c)[N], const f2 (&s)[N]) {
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-        float x, y;
+        float x, y, c0, c1, s0, s1;
         unpack2(f[e], x, y);
-        f[e] = pack2(x * c[e] - y * s[e], x * s[e] + y * c[e]);
+        unpack2(c[e], c0, c1);
+        unpack2(s[e], s0, s1);
+        f[e] = pack2(x * c0 - y * s1, x * s0 + y * c1);
     }
 }
 
+// Threads of an SM: more registers each than a plain append's need.
+constexpr int kNormResident = 672;
+
 template <typename T, int MODE, int THREADS>
-__global__ void __launch_bounds__(THREADS, kAppendResident / THREADS)
+__global__ void __launch_bounds__(THREADS, kNormResident / THREADS)
 cache_append_norm_kernel(const __grid_constant__ AppendNormArgs n) {
     constexpr int kVec = KvType<T>::kVec, kTwos = kVec / 2;
     using Vec = KvVec<T>;
-    __shared__ __align__(16) float s_cos[128], s_sin[128], s_weight[2][256];
+    __shared__ __align__(16) float s_cos[128], s_sin[128];
     __shared__ float s_head[MODE == kValues ? THREADS / 32 : 1][MODE == kValues ? 256 : 1];
     const AppendArgs& a = n.a;
     const int rows = static_cast<int>(a.rows.d);
@@ -143,11 +150,6 @@ cache_append_norm_kernel(const __grid_constant__ AppendNormArgs n) {
                 s_cos[j] = cs.x;
                 s_sin[j] = cs.y;
             }
-            for (int d = tid; d < kv.dim; d += THREADS) {
-                const T *wq = static_cast<const T*>(n.q_weight), *wk = static_cast<const T*>(n.k_weight);
-                s_weight[0][d] = wq ? KvType<T>::load(wq[d]) + n.weight_add : 1.0f;
-                s_weight[1][d] = wk ? KvType<T>::load(wk[d]) + n.weight_add : 1.0f;
-            }
         }
         for (int i = kv.block.div(base) + tid, last = kv.block.div(len - 1); i <= last; i += THREADS)
             block_bad |= !kv.valid(table[i]);
@@ -180,7 +182,7 @@ cache_append_norm_kernel(const __grid_constant__ AppendNormArgs n) {
             for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
             __syncwarp();
             const float inv = normed ? rsqrtf(fmaf(sum, n.inv_dim, n.eps)) : 1.0f;
-            const float* w = s_weight[h < a.q_heads ? 0 : 1];
+            const T* w = static_cast<const T*>(h < a.q_heads ? n.q_weight : n.k_weight);
             T* to = h < a.q_heads ? q_out + h * kv.dim
                     : h < turning ? k_out + (h - a.q_heads) * next
                                   : v_out + (h - turning) * next;
@@ -189,8 +191,8 @@ cache_append_norm_kernel(const __grid_constant__ AppendNormArgs n) {
                 const int d0 = far ? j : 2 * j, d1 = far ? j + half : 2 * j + 1;
                 float e0 = head[d0], e1 = head[d1];
                 if (normed) {
-                    e0 *= inv * w[d0];
-                    e1 *= inv * w[d1];
+                    e0 *= inv * (KvType<T>::load(w[d0]) + n.weight_add);
+                    e1 *= inv * (KvType<T>::load(w[d1]) + n.weight_add);
                 }
                 if (turns) {
                     const float c = s_cos[j], s = s_sin[j], f = e0;
@@ -207,14 +209,51 @@ cache_append_norm_kernel(const __grid_constant__ AppendNormArgs n) {
         const int first = MODE == kApart ? x0 : x0 / 2;
         const bool turns = piece && (MODE == kApart ? apart : x0 < a.rot);
         const bool both = MODE == kApart || y0 < a.rot;  // (neighbours: whether the second piece turns too)
-        float c[kVec], s[kVec];
-        if (turns) {
+        // the pieces' weights, times cosines and sines where they turn: of x with cos and sin of its pairs, of y alike
+        f2 cx[kTwos], sx[kTwos], cy[kTwos], sy[kTwos];
+        auto coefficients = [&](const T* w) {
 #pragma unroll
-            for (int e = 0; e < kVec; e += 4) {
-                *reinterpret_cast<float4*>(c + e) = *reinterpret_cast<const float4*>(s_cos + first + e);
-                *reinterpret_cast<float4*>(s + e) = *reinterpret_cast<const float4*>(s_sin + first + e);
+            for (int e = 0; e < kTwos; ++e) cx[e] = cy[e] = pack2(1.0f, 1.0f);
+            if (w) {
+                const f2 add = pack2(n.weight_add, n.weight_add);
+                append_open<T>(*reinterpret_cast<const Vec*>(w + x0), cx);
+                append_open<T>(*reinterpret_cast<const Vec*>(w + y0), cy);
+#pragma unroll
+                for (int e = 0; e < kTwos; ++e) {
+                    cx[e] = add2(cx[e], add);
+                    cy[e] = add2(cy[e], add);
+                }
             }
-        }
+            if (!turns) return;
+            if constexpr (MODE == kApart) {
+#pragma unroll
+                for (int e = 0; e < kTwos; e += 2) {
+                    const float4 c = *reinterpret_cast<const float4*>(s_cos + first + 2 * e);
+                    const float4 s = *reinterpret_cast<const float4*>(s_sin + first + 2 * e);
+                    const f2 c2[2] = {pack2(c.x, c.y), pack2(c.z, c.w)}, s2[2] = {pack2(s.x, s.y), pack2(s.z, s.w)};
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        sx[e + k] = mul2(cx[e + k], s2[k]);
+                        cx[e + k] = mul2(cx[e + k], c2[k]);
+                        sy[e + k] = mul2(cy[e + k], s2[k]);
+                        cy[e + k] = mul2(cy[e + k], c2[k]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < kTwos; ++e) {
+                    const float c = s_cos[first + e], s = s_sin[first + e];
+                    sx[e] = mul2(cx[e], pack2(s, s));
+                    cx[e] = mul2(cx[e], pack2(c, c));
+                    if (both) {
+                        const float c1 = s_cos[first + kTwos + e], s1 = s_sin[first + kTwos + e];
+                        sy[e] = mul2(cy[e], pack2(s1, s1));
+                        cy[e] = mul2(cy[e], pack2(c1, c1));
+                    }
+                }
+            }
+        };
+        int kind = -1;  // whose they are: 0 queries', 1 keys'
         for (int h1 = 0; h1 < heads; h1 += kAppendHeads * hstep) {
             if (h1 > 0) load_all(h1);
 #pragma unroll
@@ -239,31 +278,37 @@ cache_append_norm_kernel(const __grid_constant__ AppendNormArgs n) {
                         all = lo + hi;
                     }
                     for (int off = n.group >> 1; off > 0; off >>= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
-                    inv = rsqrtf(fmaf(all, n.inv_dim, n.eps));
+                    if (normed) inv = rsqrtf(fmaf(all, n.inv_dim, n.eps));
                 }
                 if (!mine) continue;
                 if (h < turning) {
-                    if (normed) {
-                        const float* w = s_weight[h < a.q_heads ? 0 : 1];
-                        const f2 inv2 = pack2(inv, inv);
-#pragma unroll
-                        for (int e = 0; e < kTwos; e += 2) {
-                            const float4 wx = *reinterpret_cast<const float4*>(w + x0 + 2 * e);
-                            const float4 wy = *reinterpret_cast<const float4*>(w + y0 + 2 * e);
-                            fx[e] = mul2(fx[e], mul2(inv2, pack2(wx.x, wx.y)));
-                            fx[e + 1] = mul2(fx[e + 1], mul2(inv2, pack2(wx.z, wx.w)));
-                            fy[e] = mul2(fy[e], mul2(inv2, pack2(wy.x, wy.y)));
-                            fy[e + 1] = mul2(fy[e + 1], mul2(inv2, pack2(wy.z, wy.w)));
-                        }
+                    if (kind != (h < a.q_heads ? 0 : 1)) {
+                        kind = h < a.q_heads ? 0 : 1;
+                        coefficients(static_cast<const T*>(kind ? n.k_weight : n.q_weight));
                     }
-                    if (turns) {
+                    const f2 inv2 = pack2(inv, inv);
+                    if (!turns) {
+#pragma unroll
+                        for (int e = 0; e < kTwos; ++e) {
+                            fx[e] = mul2(fx[e], mul2(inv2, cx[e]));
+                            fy[e] = mul2(fy[e], mul2(inv2, cy[e]));
+                        }
+                    } else {
                         if constexpr (MODE == kApart) {
 #pragma unroll
-                            for (int e = 0; e < kTwos; ++e)
-                                append_apart(fx[e], fy[e], pack2(c[2 * e], c[2 * e + 1]), pack2(s[2 * e], s[2 * e + 1]));
+                            for (int e = 0; e < kTwos; ++e) {
+                                const f2 v = fx[e], w = fy[e];
+                                fx[e] = sub2(mul2(v, cx[e]), mul2(w, sy[e]));
+                                fy[e] = fma2(v, sx[e], mul2(w, cy[e]));
+                            }
                         } else {
-                            append_neighbours<kTwos>(fx, c, s);
-                            if (both) append_neighbours<kTwos>(fy, c + kTwos, s + kTwos);
+                            append_neighbours<kTwos>(fx, cx, sx);
+                            if (both) append_neighbours<kTwos>(fy, cy, sy);
+                        }
+#pragma unroll
+                        for (int e = 0; e < kTwos; ++e) {
+                            fx[e] = mul2(fx[e], inv2);
+                            fy[e] = MODE == kApart || both ? mul2(fy[e], inv2) : mul2(fy[e], mul2(inv2, cy[e]));
                         }
                     }
                     append_close<T>(fx, x[j]);

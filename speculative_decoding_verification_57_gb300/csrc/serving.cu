@@ -5,9 +5,10 @@
 #include <cmath>
 
 #include "append_norm.cuh"
-#include "attention_mass.cuh"
+#include "attention_mass_tc.cuh"
 #include "cache_evict.cuh"
 #include "cache_host.cuh"
+#include "tensor_maps.cuh"
 
 namespace {
 
@@ -36,17 +37,44 @@ cudaError_t launch_mass_of(const MassArgs& a, int sms, cudaStream_t stream) {
                         a);
 }
 
-// The fewest tiles of eight queries that hold a kv head's, or tens of them in turns.
+// Tens of tiles of eight queries, in turns, or the fewest that hold a kv head's.
 template <typename T, int DP>
 cudaError_t launch_mass(const MassArgs& a, int sms, cudaStream_t stream) {
-    const int m = a.rows * static_cast<int>(a.group.d);
-    if (m <= 8) return launch_mass_of<T, DP, 1>(a, sms, stream);
-    if (m <= 32) return launch_mass_of<T, DP, 4>(a, sms, stream);
+    if constexpr (sizeof(T) == 4 || DP > 128) {
+        const int m = a.rows * static_cast<int>(a.group.d);
+        if (m <= 8) return launch_mass_of<T, DP, 1>(a, sms, stream);
+        if (m <= 32) return launch_mass_of<T, DP, 4>(a, sms, stream);
+    }
     return launch_mass_of<T, DP, 10>(a, sms, stream);
 }
 
+template <typename S>
+cudaError_t launch_mass_tc_of(const MassArgs& a, const TcMaps& maps, int sms, cudaStream_t stream) {
+    constexpr int kBytes = sizeof(MassShared<S>);
+    static_assert(kBytes <= 227 * 1024, "a CTA's shared memory");
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(done, reinterpret_cast<const void*>(attention_mass_tc_kernel<S>), kBytes);
+    if (e != cudaSuccess) return e;
+    return launch_early(attention_mass_tc_kernel<S>, dim3(static_cast<unsigned>(sms)), S::kThreads, kBytes, stream, a, maps);
+}
+
+template <int DP>
+cudaError_t launch_mass_tc(const MassArgs& a, int sms, cudaStream_t stream) {
+    TcMaps maps = {};
+    if (make_pool_maps(a.kv, maps)) return launch_mass_tc_of<MassTc<DP, true>>(a, maps, sms, stream);
+    return launch_mass_tc_of<MassTc<DP, false>>(a, maps, sms, stream);
+}
+
+// bf16, head_dim up to 128 and up to 256 queries a kv head go to the tcgen05
+// kernel (64 single rows of 32/8 heads of 128 over 1000..2000 positions 40 us, on
+// the other 48; trees of 17 rows over 2048..4096 78 and 276).
 template <typename T>
 cudaError_t launch_mass(const MassArgs& a, int sms, cudaStream_t stream) {
+    if constexpr (sizeof(T) == 2) {
+        const bool few = a.rows * static_cast<int>(a.group.d) <= 256;
+        if (few && a.kv.dim <= 64) return launch_mass_tc<64>(a, sms, stream);
+        if (few && a.kv.dim <= 128) return launch_mass_tc<128>(a, sms, stream);
+    }
     if (a.kv.dim <= 64) return launch_mass<T, 64>(a, sms, stream);
     if (a.kv.dim <= 128) return launch_mass<T, 128>(a, sms, stream);
     return launch_mass<T, 256>(a, sms, stream);
@@ -94,6 +122,10 @@ specv_status specv_cache_append_norm(specv_handle h, const specv_kv_cache* cache
     } else if (positions) {
         n.offsets = positions->offsets;
     }
+    // nothing that the plain append does not do
+    if (!n.q_weight && !n.k_weight && !n.positions && !n.offsets)
+        return specv_cache_append(h, cache, q, q_stride, q_heads, k, k_stride, v, v_stride, inv_freq, rot_dim, interleaved,
+                                  parents, row_counts, batch, rows, q_out, row_status, stream);
     if (batch == 0) return SPECV_OK;
     if (!rows_ok(cache, k, k_stride) || !rows_ok(cache, v, v_stride)) return SPECV_ERR_INVALID_ARGUMENT;
     if (q && (!rows_ok(cache, q, q_stride) || !q_out || !aligned16(q_out) || q_heads < 1 || q_heads > 65536 ||

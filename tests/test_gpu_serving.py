@@ -83,14 +83,16 @@ def test_append_norm_matches_the_formula(sv, h, dtype, shape, which):  # noqa: F
     assert (np.abs(gq - q_out) <= S.append_norm_bound(q_out, q_mag, dim, half)).all(), np.max(np.abs(gq - q_out))
 
 
-def test_append_norm_without_more_is_append(sv, h):  # noqa: F811
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rot,inter", [(128, False), (64, True), (0, False), (22, False), (22, True)])
+def test_append_norm_without_more_is_append(sv, h, dtype, rot, inter):  # noqa: F811
     import torch
 
-    rng, lens, tables, pools, xs, inv, par = _append_case(5, torch.bfloat16, 3, 9, 8, 2, 128, 16, [9, 40, 100], "tree", 128)
+    rng, lens, tables, pools, xs, inv, par = _append_case(5, _dtype(dtype), 3, 9, 8, 2, 128, 16, [9, 40, 100], "tree", rot)
     (kc, _), (vc, _) = pools
     k2, v2 = kc.clone(), vc.clone()
     args = (_dev(tables), _dev(lens), xs[1][0], xs[2][0])
-    kw = dict(q=xs[0][0], inv_freq=_dev(inv), parents=_dev(par))
+    kw = dict(q=xs[0][0], inv_freq=None if inv is None else _dev(inv), interleaved=inter, parents=_dev(par))
     one = sv.specv_cache_append(h, kc, vc, *args, **kw)
     two = sv.specv_cache_append_norm(h, k2, v2, *args, **kw)
     assert torch.equal(one["q_out"], two["q_out"]) and torch.equal(kc, k2) and torch.equal(vc, v2)
@@ -169,6 +171,11 @@ MASSES = [
     (3, 31, 5, 5, 48, 3, [31, 95, 96], "tree", 1000),
     (70, 2, 4, 2, 64, 16, [2 + 5 * i for i in range(70)], "tree", 16),
     (2, 21, 4, 1, 64, 128, [21, 500], "tree", 130),  # a queries' tile more than at a time
+    (2, 32, 40, 1, 128, 16, [33, 260], "tree", 0),
+    (3, 7, 80, 2, 64, 8, [7, 100, 0], "star", 0),    # 280 queries
+    (1, 32, 5, 1, 112, 24, [900], "tree", 5),
+    (2, 25, 20, 4, 128, 40, [25, 700], "tree", 0),   # 125 queries, blocks that do not fill tiles
+    (40, 1, 12, 6, 128, 16, [1 + 90 * (i % 8) for i in range(40)], "chain", 0),
 ]
 
 

@@ -14,8 +14,10 @@
 // (a layer, sequence and kv head).  CTAs of one row find the kept set each by
 // itself and move columns of their own of the keys or the values, so that they
 // need not meet; masses and lengths go to other memory than they come from.
-// The least kept mass is found by its bits, eight at a time, from the top;
-// moves are listed in position order by block-wide scans.  Moves run in
+// The least kept mass is found by its bits, eight at a time, from the top, and
+// no further than it takes to tell the kept ones; moves are listed in position
+// order by ballots and a scan over the warps' counts.  A thread has the masses
+// of eight positions in registers, so that up to 2048 are read once.  Moves run in
 // order, 16 bytes a thread and row, all loads of a step before its stores: a
 // step's stores go to places that no later step reads, as sources of kept
 // positions lie above the line and the recent ones, behind them, move down.
@@ -28,7 +30,9 @@ namespace specv {
 constexpr int kEvictThreads = 256;
 constexpr int kEvictMoves = 1024;  // listed at a time
 constexpr int kEvictAhead = 4;     // of a thread, in flight
-constexpr int kEvictItems = 4;     // positions of a thread in a scan
+constexpr int kEvictItems = 8;    // masses of a thread, kEvictThreads positions apart
+constexpr int kEvictSpan = kEvictThreads * kEvictItems;
+constexpr int kEvictWarps = kEvictThreads / 32;
 
 struct EvictArgs {
     KvView kv;
@@ -54,71 +58,94 @@ __device__ __forceinline__ uint32_t evict_key(float x) {
 }
 
 struct EvictShared {
-    uint32_t hist[kEvictThreads / 32][256];
-    uint32_t warp_sum[2][kEvictThreads / 32];
-    uint32_t key, more;  // the digits found so far, and how many of the equal ones are kept
+    uint32_t hist[kEvictWarps][256];
+    uint32_t count[kEvictItems * kEvictWarps];  // of a span, by item and warp: in position order
+    uint32_t warp_sum[kEvictWarps];
+    uint32_t total;
+    uint32_t key, more, equal;  // the digits found so far, how many of those equal to them are kept, and how many there are
     int src[kEvictMoves], dst[kEvictMoves];
     int64_t from[kEvictMoves], to[kEvictMoves];
 };
 
-// Exclusive sums over the CTA of two counts below 2^16, packed; `total` the
-// CTA's.  Calls in turn use the two halves of warp_sum, so that one barrier
-// each is enough.
-__device__ __forceinline__ uint32_t evict_scan(EvictShared& sh, uint32_t v, int half, uint32_t& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Keys of the positions base + tid, base + tid + kEvictThreads, ..: those of n.
+__device__ __forceinline__ void evict_load(const float* mass, int n, int base, uint32_t (&k)[kEvictItems]) {
+#pragma unroll
+    for (int j = 0; j < kEvictItems; ++j) {
+        const int i = base + j * kEvictThreads + static_cast<int>(threadIdx.x);
+        k[j] = 0;
+        if (i < n) k[j] = evict_key(mass[i]);
+    }
+}
+
+// sh.count (a barrier before) as exclusive sums, and their total; packed counts below 2^16 too.
+__device__ __forceinline__ void evict_scan(EvictShared& sh) {
+    static_assert(kEvictItems * kEvictWarps <= kEvictThreads, "a count a thread");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t v = tid < kEvictItems * kEvictWarps ? sh.count[tid] : 0;
     uint32_t incl = v;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const uint32_t o = __shfl_up_sync(0xffffffffu, incl, off);
         if (lane >= off) incl += o;
     }
-    if (lane == 31) sh.warp_sum[half][warp] = incl;
+    if (lane == 31) sh.warp_sum[warp] = incl;
     __syncthreads();
-    uint32_t ahead = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kEvictThreads / 32; ++w) {
-        const uint32_t x = sh.warp_sum[half][w];
-        if (w < warp) ahead += x;
-        all += x;
-    }
-    total = all;
-    return ahead + incl - v;
+    for (int w = 0; w < warp; ++w) incl += sh.warp_sum[w];
+    if (tid < kEvictItems * kEvictWarps) sh.count[tid] = incl - v;
+    if (tid == kEvictThreads - 1) sh.total = incl;
+    __syncthreads();
 }
 
-// The key of the `many`-th largest of n masses (1 <= many <= n) and how many
-// of those equal to it are among them.
-__device__ inline void evict_select(EvictShared& sh, const float* mass, int n, uint32_t many) {
+// The `many`-th largest of n masses (1 <= many < n), as far as it takes:
+// kept are keys above sh.key, and sh.more of the sh.equal ones equal to it.
+// k: the first span's keys.
+__device__ inline void evict_select(EvictShared& sh, const float* mass, int n, uint32_t many, uint32_t (&k)[kEvictItems]) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t key = 0;
     for (int shift = 24; shift >= 0; shift -= 8) {
         for (int i = lane; i < 256; i += 32) sh.hist[warp][i] = 0;
         __syncwarp();
         const uint32_t above = shift == 24 ? 0u : ~0u << (shift + 8);
-        for (int i = tid; i < n; i += kEvictThreads) {
-            const uint32_t k = evict_key(mass[i]);
-            if ((k & above) == key) atomicAdd(&sh.hist[warp][k >> shift & 255], 1u);
+        for (int base = 0; base < n; base += kEvictSpan) {
+            if (n > kEvictSpan) evict_load(mass, n, base, k);
+#pragma unroll
+            for (int j = 0; j < kEvictItems; ++j) {
+                if (base + j * kEvictThreads >= n) break;
+                if (base + j * kEvictThreads + tid < n && (k[j] & above) == key)
+                    atomicAdd(&sh.hist[warp][k[j] >> shift & 255], 1u);
+            }
         }
         __syncthreads();
         // the digit in which the counts from the top pass `many`: thread t has digit 255 - t
         uint32_t c = 0;
 #pragma unroll
-        for (int w = 0; w < kEvictThreads / 32; ++w) c += sh.hist[w][255 - tid];
+        for (int w = 0; w < kEvictWarps; ++w) c += sh.hist[w][255 - tid];
         uint32_t incl = c;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const uint32_t o = __shfl_up_sync(0xffffffffu, incl, off);
             if (lane >= off) incl += o;
         }
-        if (lane == 31) sh.warp_sum[0][warp] = incl;
+        if (lane == 31) sh.warp_sum[warp] = incl;
         __syncthreads();
-        for (int w = 0; w < warp; ++w) incl += sh.warp_sum[0][w];
+        for (int w = 0; w < warp; ++w) incl += sh.warp_sum[w];
         if (incl >= many && incl - c < many) {
             sh.key = key | static_cast<uint32_t>(255 - tid) << shift;
             sh.more = many - (incl - c);
+            sh.equal = c;
         }
         __syncthreads();
         key = sh.key;
         many = sh.more;
+        if (many == sh.equal) {  // all with these digits are kept: those above the key before them
+            __syncthreads();
+            if (tid == 0) {
+                sh.key = key - 1;  // (not of 0, above which all are kept: `many` is below n)
+                sh.more = 0;
+            }
+            __syncthreads();
+            return;
+        }
     }
 }
 
@@ -157,62 +184,85 @@ __global__ void __launch_bounds__(kEvictThreads, 4) cache_evict_kernel(const Evi
     const int n = tail - e.first;  // positions to choose from: more than `many`
     if (part == 0)  // (what lies in holes is written over below, behind barriers)
         for (int i = tid; i < line; i += kEvictThreads) mass_out[i] = mass[i];
-    uint32_t key = 0xffffffffu, ties = 0;  // kept: above key, or one of the first `ties` equal to it
+    uint32_t key = 0, ties = 0, k[kEvictItems];  // kept: above key, or one of the first `ties` equal to it
     if (many > 0) {
-        evict_select(sh, mass + e.first, n, static_cast<uint32_t>(many));
+        evict_load(mass + e.first, n, 0, k);
+        evict_select(sh, mass + e.first, n, static_cast<uint32_t>(many), k);
         key = sh.key;
         ties = sh.more;
     }
     // the moves of rank [round, round + kEvictMoves): first those that fill holes, then the recent ones
-    unsigned char* pool = static_cast<unsigned char*>(e.split > 1 ? (part & 1 ? kv.v : kv.k) : kv.k);
+    const int lane = tid & 31, warp = tid >> 5;
     const int parts = e.split > 1 ? 1 : 2;  // one CTA moves keys and then values
+    unsigned char* pool = static_cast<unsigned char*>(e.split > 1 && (part & 1) ? kv.v : kv.k);
     const int64_t elem = 16 / e.vec_elems;
     const int64_t head_at = layer * e.layer_stride + static_cast<int64_t>(h) * kv.block_size() * kv.dim;
     const int64_t column = static_cast<int64_t>(part >> 1) * e.pieces * 16;
-    int fills = INT32_MAX;
+    int fills = many > 0 ? INT32_MAX : 0;
     for (int round = 0;; round += kEvictMoves) {
         // holes below the line and kept positions above it, by their ranks; both lists are as long
-        if (many > 0 && round < fills) {
+        if (round < fills) {
             uint32_t equal = 0, holes = 0, above = 0;
-            for (int i0 = 0; i0 < n; i0 += kEvictThreads * kEvictItems) {
-                const int i = i0 + tid * kEvictItems;
-                uint32_t k[kEvictItems], same = 0;
+            for (int base = 0; base < n; base += kEvictSpan) {
+                if (n > kEvictSpan) evict_load(mass + e.first, n, base, k);
+                uint32_t kept = 0, move = 0;  // of the thread's items
+                if (ties > 0) {  // equal ones by their order
 #pragma unroll
-                for (int j = 0; j < kEvictItems; ++j) {
-                    k[j] = i + j < n ? evict_key(mass[e.first + i + j]) : 0;
-                    same += i + j < n && k[j] == key;
-                }
-                uint32_t all;
-                uint32_t rank = equal + evict_scan(sh, same, 0, all);
-                equal += all;
-                uint32_t take = 0, counts = 0;
-#pragma unroll
-                for (int j = 0; j < kEvictItems; ++j) {
-                    if (i + j >= n) continue;
-                    const bool kept = k[j] > key || (k[j] == key && rank++ < ties);
-                    if (i + j < many ? !kept : kept) {
-                        take |= 1u << j;
-                        counts += i + j < many ? 1u : 1u << 16;
+                    for (int j = 0; j < kEvictItems; ++j) {
+                        if (lane == 0) sh.count[j * kEvictWarps + warp] = 0;
+                        if (base + j * kEvictThreads >= n) continue;
+                        const bool same = base + j * kEvictThreads + tid < n && k[j] == key;
+                        const uint32_t all = __ballot_sync(0xffffffffu, same);
+                        if (lane == 0) sh.count[j * kEvictWarps + warp] = __popc(all);
+                        if (same) kept |= 1u << j;
                     }
+                    __syncthreads();
+                    evict_scan(sh);
+#pragma unroll
+                    for (int j = 0; j < kEvictItems; ++j) {
+                        if (base + j * kEvictThreads >= n) break;
+                        const uint32_t all = __ballot_sync(0xffffffffu, kept >> j & 1);
+                        const uint32_t rank = equal + sh.count[j * kEvictWarps + warp] + __popc(all & ((1u << lane) - 1));
+                        if (rank >= ties) kept &= ~(1u << j);
+                    }
+                    equal += sh.total;
+                    __syncthreads();
                 }
-                const uint32_t at = evict_scan(sh, counts, 1, all);
-                uint32_t hole_rank = holes + (at & 0xffff), above_rank = above + (at >> 16);
 #pragma unroll
                 for (int j = 0; j < kEvictItems; ++j) {
-                    if (!(take >> j & 1)) continue;
-                    const bool hole = i + j < many;
-                    const uint32_t x = (hole ? hole_rank++ : above_rank++) - static_cast<uint32_t>(round);
-                    if (x < kEvictMoves) (hole ? sh.dst : sh.src)[x] = e.first + i + j;
+                    if (lane == 0) sh.count[j * kEvictWarps + warp] = 0;
+                    if (base + j * kEvictThreads >= n) continue;
+                    const int i = base + j * kEvictThreads + tid;
+                    if (k[j] > key) kept |= 1u << j;
+                    const bool stays = kept >> j & 1;
+                    const bool moves = i < n && (i < many ? !stays : stays);
+                    if (moves) move |= 1u << j;
+                    const uint32_t all = __ballot_sync(0xffffffffu, moves);
+                    const uint32_t low = __ballot_sync(0xffffffffu, moves && i < many);
+                    if (lane == 0) sh.count[j * kEvictWarps + warp] = __popc(low) | __popc(all & ~low) << 16;
                 }
-                holes += all & 0xffff;
-                above += all >> 16;
+                __syncthreads();
+                evict_scan(sh);
+#pragma unroll
+                for (int j = 0; j < kEvictItems; ++j) {
+                    if (base + j * kEvictThreads >= n) break;
+                    const int i = base + j * kEvictThreads + tid;
+                    const bool moves = move >> j & 1;
+                    const uint32_t all = __ballot_sync(0xffffffffu, moves), low = __ballot_sync(0xffffffffu, moves && i < many);
+                    const uint32_t at = sh.count[j * kEvictWarps + warp], before = (1u << lane) - 1;
+                    if (!moves) continue;
+                    const uint32_t x = (i < many ? holes + (at & 0xffff) + __popc(low & before)
+                                                 : above + (at >> 16) + __popc(all & ~low & before)) -
+                                       static_cast<uint32_t>(round);
+                    if (x < kEvictMoves) (i < many ? sh.dst : sh.src)[x] = e.first + i;
+                }
+                holes += sh.total & 0xffff;
+                above += sh.total >> 16;
+                __syncthreads();
             }
             fills = static_cast<int>(above);
-        } else if (many == 0) {
-            fills = 0;
         }
         const int total = fills + e.recent;
-        __syncthreads();
         for (int x = tid; x < kEvictMoves && round + x < total; x += kEvictThreads) {
             int src, dst;
             if (round + x < fills) {
@@ -229,9 +279,9 @@ __global__ void __launch_bounds__(kEvictThreads, 4) cache_evict_kernel(const Evi
         }
         __syncthreads();
         const int here = total - round < kEvictMoves ? total - round : kEvictMoves;
+        const int units = here * e.pieces;
         for (int which = 0; which < parts; ++which) {
             unsigned char* p = which ? static_cast<unsigned char*>(kv.v) : pool;
-            const int units = here * e.pieces;
             for (int u0 = 0; u0 < units; u0 += kEvictThreads * kEvictAhead) {
                 uint4 x[kEvictAhead];
                 int64_t to[kEvictAhead];

@@ -116,6 +116,18 @@ specv_status specv_prefix_attention(specv_handle h, const specv_kv_cache* cache,
     all.row_tiles = p.prefix_tiles;
     all.side = p.side;
     all.prefix = nullptr;
+    // the sequences' part before the prefix's where these can run side by side, else behind it
+    const bool beside = p.prefix->tc && p.own->tc;
+    all.late = beside;
+    own.late = !beside;
+    if (beside) {
+        own.lens = all.lens = cache->seq_lens;
+        own.prefix_len = all.prefix_len = prefix_len;
+        own.sequences = all.sequences = batch;
+        own.own_rows = all.own_rows = rows;
+        own.own_segs = all.own_segs = cache->kv_heads * p.own_tiles;
+        own.prefix_segs = all.prefix_segs = cache->kv_heads * ((batch * rows * group + 127) / 128);
+    }
     if (p.prefix->tc && h->test_withhold >= 0) {  // the test hook arms one launch
         all.withhold = h->test_withhold;
         all.polls = h->test_polls;
@@ -146,8 +158,8 @@ specv_status specv_prefix_attention(specv_handle h, const specv_kv_cache* cache,
     DeviceGuard g(h->device);
     if (!g.ok) return cuda_fail(cudaErrorInvalidDevice, "cudaSetDevice");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = p.prefix->launch(all, p.prefix_ctas, s);
-    if (e == cudaSuccess) e = p.own->launch(own, p.own_ctas, s);
+    cudaError_t e = beside ? p.own->launch(own, p.own_ctas, s) : p.prefix->launch(all, p.prefix_ctas, s);
+    if (e == cudaSuccess) e = beside ? p.prefix->launch(all, p.prefix_ctas, s) : p.own->launch(own, p.own_ctas, s);
     const unsigned grid = static_cast<unsigned>(j.blocks + (batch + kPrefixJoinThreads - 1) / kPrefixJoinThreads);
     if (e == cudaSuccess)
         e = launch_early(cache->dtype == SPECV_BF16 ? prefix_join<__nv_bfloat16>(many) : prefix_join<float>(many), dim3(grid),

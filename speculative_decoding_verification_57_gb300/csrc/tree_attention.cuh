@@ -72,6 +72,11 @@ struct PartArgs : AttnArgs {
     int prefix_cap;         // the most positions that the prefix's table holds
     int own;                // rows of the pass among a sequence's positions: `rows`, or of the prefix none
     int side;               // row tiles of a kv head that as many CTAs side by side take over the same positions; 1: none
+    bool late;              // the second of the two parts: waits at its end for what the kernels before wrote
+    // both parts at the same time (tcgen05 kernels): what each has to know of the other; `lens` NULL: one behind the other
+    const int32_t *lens, *prefix_len;  // of the sequences, and the prefix's
+    int sequences, own_rows, own_segs;  // sequences, rows of the pass, segments of a sequence
+    int prefix_segs;                    // segments of 128 rows of the prefix
 };
 
 // Factor of the scores in base 2.  A scale of zero still has to tell hidden
@@ -106,12 +111,12 @@ __device__ __forceinline__ int attn_first_block(const PartArgs& a) {
     return a.prefix ? static_cast<int>(a.kv.block.div(max(*a.prefix, 0))) : 0;
 }
 // What the kernels before wrote is waited for at a kernel's start; by a part
-// behind another at its end.  The part before lets it start when all of its CTAs
+// launched behind another at its end.  The part before lets it start when all of its CTAs
 // are through with that wait, so that whatever was written before the call is
 // there; and a kernel behind this one finds both parts' results, as this one
 // ends after the part before.
 __device__ __forceinline__ bool attn_waits_late(const AttnArgs&) { return false; }
-__device__ __forceinline__ bool attn_waits_late(const PartArgs& a) { return a.prefix != nullptr; }
+__device__ __forceinline__ bool attn_waits_late(const PartArgs& a) { return a.late; }
 __device__ __forceinline__ void attn_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Rows of the pass that are the last positions of a sequence.
@@ -164,7 +169,7 @@ struct AttnCursor {
 
 // Shared memory of attn_cut.
 struct AttnCut {
-    int64_t sum[32];
+    int64_t sum[32], share[32];
     int64_t tiles[2];  // of the sequences before that at the run's start, and end
     int b[2];
 };
@@ -178,11 +183,27 @@ struct AttnRun {
     int used;       // CTAs that have runs
     int n;          // tiles of the run
     int extra;      // units behind a segment's last tile
+    int early;      // CTAs of longer runs, which the first `early_units` units are cut into; the others have the rest
+    int64_t early_units;
 
     // unit of a tile `tiles` tiles and `segments` segments on from the first
     __device__ __forceinline__ int64_t unit(int tiles, int segments) const {
         return first + tiles + static_cast<int64_t>(extra) * segments;
     }
+    __device__ __forceinline__ int64_t bound(int c) const {
+        return c <= early ? attn_run(early_units, c, early)
+                          : early_units + attn_run(units - early_units, c - early, used - early);
+    }
+    __device__ __forceinline__ int owner(int64_t x) const {
+        return x < early_units ? attn_owner(early_units, x, early)
+                               : early + attn_owner(units - early_units, x - early_units, used - early);
+    }
+};
+
+// CTAs from `early` on start late, by the time of `less` units; 0: none does.
+struct AttnLate {
+    int early = 0;
+    int64_t less = 0;
 };
 
 // The run of CTA `cta` of `ctas` on a line of `segs` segments a sequence, and
@@ -190,7 +211,8 @@ struct AttnRun {
 // units, in tiles, where a run has eight tiles or more.  Up to 32 sequences
 // every warp finds out by itself; with more, each thread has some of them.
 template <int THREADS, int COST, typename A>
-__device__ AttnRun attn_cut(const A& a, AttnCut& sh, int tile_keys, int segs, int cta, int ctas, AttnCursor& cur) {
+__device__ AttnRun attn_cut(const A& a, AttnCut& sh, int tile_keys, int segs, int cta, int ctas, AttnCursor& cur,
+                            AttnLate late = {}) {
     constexpr int kEnds = COST > 0 ? 2 : 1;  // of the run, looked for among the sequences
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool small = a.batch <= 32;
@@ -225,8 +247,20 @@ __device__ AttnRun attn_cut(const A& a, AttnCut& sh, int tile_keys, int segs, in
     run.used = static_cast<int>(run.units < ctas ? run.units : ctas);
     run.first = 0;
     run.n = 0;
+    run.early = run.used;
+    run.early_units = run.units;
+    if (late.less > 0 && run.units >= 8ll * ctas) {
+        // runs of `more` units, and of `less` fewer
+        const int rest = ctas - late.early;
+        const int64_t more = (run.units + rest * late.less) / ctas;
+        run.early = late.early;
+        if (more > late.less)
+            run.early_units = run.units - rest * (more - late.less);
+        else
+            run.used = late.early;
+    }
     if (cta >= run.used) return run;
-    const int64_t ends[2] = {attn_run(run.units, cta, run.used), attn_run(run.units, cta + 1, run.used)};
+    const int64_t ends[2] = {run.bound(cta), run.bound(cta + 1)};
     // the sequences that hold the run's ends, and the tiles of those before them
     int at_b[kEnds], at_len[kEnds];
     int64_t at_before[kEnds];
@@ -988,7 +1022,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
                     work.status[piece] = status;
                     if (first_tile == 0)
                         work.segs[attn_seg(a, cur)] =
-                            PartNote{cta, attn_owner(run.units, run.unit(i + cur.tiles - cur.tile - 1, seg), run.used)};
+                            PartNote{cta, run.owner(run.unit(i + cur.tiles - cur.tile - 1, seg))};
                 } else {
                     if (first_tile == 0 && cur.s == 0 && a.row_status) a.row_status[cur.b] = status;
                     if (!whole) {
@@ -997,7 +1031,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) tree_attention_kernel(c
                             work.notes[cta].b = cur.b;
                             work.notes[cta].s = cur.s;
                             work.notes[cta].last =
-                                attn_owner(run.units, run.unit(i + cur.tiles - cur.tile - 1, seg), run.used);
+                                run.owner(run.unit(i + cur.tiles - cur.tile - 1, seg));
                         }
                     }
                 }

@@ -907,8 +907,7 @@ __device__ void tc_softmax_role(const A& a, TcShared<S>& sh, const TcLayout& lay
                 work.status[piece] = status;
                 if (first_tile == 0)
                     work.segs[attn_seg(a, cur)] =
-                        PartNote{cta, attn_owner(run.units, run.unit(j0 + cur.tiles - 1, seg), run.used) * a.side +
-                                          cta % a.side};
+                        PartNote{cta, run.owner(run.unit(j0 + cur.tiles - 1, seg)) * a.side + cta % a.side};
             } else {
                 if (first_tile == 0 && cur.s == 0 && a.row_status) a.row_status[cur.b] = status;
                 if (!whole) {
@@ -916,7 +915,7 @@ __device__ void tc_softmax_role(const A& a, TcShared<S>& sh, const TcLayout& lay
                     if (first_tile == 0) {
                         work.notes[cta].b = cur.b;
                         work.notes[cta].s = cur.s;
-                        work.notes[cta].last = attn_owner(run.units, run.unit(j0 + cur.tiles - 1, seg), run.used);
+                        work.notes[cta].last = run.owner(run.unit(j0 + cur.tiles - 1, seg));
                     }
                 }
             }
@@ -933,6 +932,54 @@ __device__ void tc_softmax_role(const A& a, TcShared<S>& sh, const TcLayout& lay
     }
 }
 
+// ------------------------------------------------------------------ two parts at a time
+// The tensor cores bound the prefix's part, the memory the other: they run
+// side by side where the prefix has as many tiles as the sequences or more.
+// The sequences' part comes first and takes half of the CTAs (which read nearly
+// as fast as all: 64 trees of 17 rows over 500..1000 positions of their own take
+// 48 us on 76 SMs, 53 on 152); the prefix's CTAs have the other SMs at once,
+// and those of the sequences when these are through, which their shorter runs
+// take into account.  A tile of a sequence counts as one of the prefix's, a
+// segment's end as two, a start as five (measured, at heads of 128).
+struct TcShare {
+    int ctas;
+    AttnLate late;
+};
+
+template <typename S>
+__device__ __forceinline__ TcShare tc_share(const AttnArgs&, AttnCut&) {
+    return TcShare{static_cast<int>(gridDim.x), {}};
+}
+template <typename S>
+__device__ TcShare tc_share(const PartArgs& a, AttnCut& sh) {
+    TcShare share{static_cast<int>(gridDim.x), {}};
+    const int prefix = a.lens ? attn_prefix(a.kv, *a.prefix_len, a.prefix_cap) : 0;
+    if (prefix <= 0) return share;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int64_t tiles = 0;  // of the sequences, of a segment each
+    for (int b = tid; b < a.sequences; b += S::kThreads) {
+        const int len = a.lens[b];
+        tiles += attn_tiles(len > prefix ? len - prefix : 0, S::KT);
+    }
+    for (int off = 16; off > 0; off >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, off);
+    if (lane == 0) sh.share[warp] = tiles;
+    __syncthreads();
+    tiles = 0;
+    for (int w = 0; w < S::kThreads / 32; ++w) tiles += sh.share[w];
+    const int64_t own = tiles * a.own_segs;
+    const int64_t all = static_cast<int64_t>(attn_tiles(prefix, S::KT)) * a.prefix_segs;
+    if (all < own) return share;
+    const int half = gridDim.x / 2;
+    if (!a.late) {
+        share.ctas = half;
+    } else {
+        share.late.early = (static_cast<int>(gridDim.x) - half) / a.side;
+        const int64_t time = 5 + (own + 2ll * a.sequences * a.own_segs) * 7 / (4 * half);
+        share.late.less = S::WIDE ? (time + 1) / 2 : time;
+    }
+    return share;
+}
+
 // ------------------------------------------------------------------ the kernel
 template <typename S, typename A>
 __global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const A a, const __grid_constant__ TcMaps maps) {
@@ -947,8 +994,9 @@ __global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const
     if (!attn_waits_late(a)) attn_wait();
     // row tiles side by side share the positions' cut
     const int side = attn_side(a), line = blockIdx.x / side, beside = blockIdx.x - line * side;
+    const TcShare share = tc_share<S>(a, sh.cut);
     const AttnRun run = attn_cut<S::kThreads, S::kCost>(a, sh.cut, S::KT, a.kv.heads * (side > 1 ? 1 : a.row_tiles), line,
-                                                        gridDim.x / side, cur);
+                                                        share.ctas / side, cur, share.late);
     if (side > 1) cur.s = cur.s * side + beside;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this grid's end
     if (tid == 0) {

@@ -68,10 +68,10 @@ cudaError_t launch_tc(const A& a, const TcMaps& maps, int ctas, cudaStream_t str
     return e != cudaSuccess ? e : launch_join<S>(a, ctas, stream);
 }
 
-template <int DP, bool WIDE, typename A>
+template <int DP, bool WIDE, typename A, int BOXES = 2>
 cudaError_t launch_attention_tc(const A& a, int ctas, cudaStream_t stream) {
     TcMaps maps = {};
-    if (make_maps(a, maps)) return launch_tc<TcShape<DP, WIDE, true>, A>(a, maps, ctas, stream);
+    if (make_maps(a, maps)) return launch_tc<TcShape<DP, WIDE, true, BOXES>, A>(a, maps, ctas, stream);
     return launch_tc<TcShape<DP, WIDE, false>, A>(a, maps, ctas, stream);
 }
 
@@ -126,6 +126,13 @@ const AttnPlan<A>& attn_plan(specv_dtype dt, int dim, int m) {
     if (dt == SPECV_F32) return f32[d][m <= 16 ? 0 : m <= 32 ? 1 : 2];
     if (d == 2) return big[m <= 16 ? 0 : 1];
     return m < kTcLeast ? few[d] : many[d][m <= 128 ? 0 : 1];
+}
+
+// The prefix's part in row tiles of 128 side by side (bf16, head_dim up to 128).
+inline const AttnPlan<PartArgs>& side_plan(int dim) {
+    static constexpr AttnPlan<PartArgs> plans[2] = {{64, 128, 1, true, launch_attention_tc<64, false, PartArgs, 3>},
+                                                    {128, 128, 1, true, launch_attention_tc<128, false, PartArgs, 3>}};
+    return plans[dim <= 64 ? 0 : 1];
 }
 
 }  // namespace

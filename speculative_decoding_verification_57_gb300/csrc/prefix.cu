@@ -20,8 +20,12 @@ PrefixPlan prefix_plan(const specv_ctx* h, specv_dtype dt, int heads, int dim, i
     // Row tiles of 128 up to eight a kv head, side by side over the same positions, so that they read them from the L2 at
     // about the same time; more rows take tiles of 256, which read the positions half as often
     const int side = (all + 127) / 128;
-    p.prefix = &attn_plan<PartArgs>(dt, dim, side <= 8 && all > 128 ? 128 : all);
-    p.side = p.prefix->tc && side <= 8 ? side : 1;
+    p.prefix = &attn_plan<PartArgs>(dt, dim, all);
+    p.side = 1;
+    if (p.prefix->tc && side > 1 && side <= 8) {
+        p.prefix = &side_plan(dim);
+        p.side = side;
+    }
     p.own = &attn_plan<PartArgs>(dt, dim, own);
     p.prefix_ctas = h->sm_count * p.prefix->ctas;
     p.own_ctas = h->sm_count * p.own->ctas;

@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(const P
     for (int k = 0; k < COLS; ++k) sum.x[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const bool idle = a.lens[b] == 0;
     if (!idle) {
-        prefix_join_part<COLS, 2>(a.own, own_note, own_seg, m - own_tile * a.own.tm, col, sum);
+        prefix_join_part<COLS, COLS == 1 ? 8 : 2>(a.own, own_note, own_seg, m - own_tile * a.own.tm, col, sum);
         prefix_join_part<COLS, PIECES>(a.prefix, note, seg, row - tile * a.prefix.tm, col, sum);
     }
     const bool zero = idle || sum.status != 0;

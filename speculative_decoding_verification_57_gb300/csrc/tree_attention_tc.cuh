@@ -151,7 +151,7 @@ __host__ __device__ constexpr uint32_t tc_idesc(int n, bool cols) {
 }
 
 // ------------------------------------------------------------------ shapes
-template <int DP_, bool WIDE_, bool TMA_>
+template <int DP_, bool WIDE_, bool TMA_, int BOXES = 2>
 struct TcShape {
     using Type = __nv_bfloat16;
     static constexpr int DP = DP_;
@@ -170,13 +170,19 @@ struct TcShape {
     // rate times its latency several times over.
     static constexpr int kLead = WIDE ? 1 : 2;
     static constexpr int kSlots = DP == 64 ? 10 : WIDE ? 5 : 6;
-    static constexpr int kBoxWarps = 3;
+    // Warps that bring boxes: two, or three for row tiles of 128 that the L2 serves at the tensor cores' pace (16 chains of
+    // 6 rows behind 65536 positions 104 us with three, 119 with two), at the price of registers (in 12 warps trees of 32
+    // rows with 64 heads take 104 us, in 16 107; chains of 6 rows over 2000 positions 78 and 82).
+    static constexpr int kBoxWarps = BOXES;
     // of a segment, besides its tiles, in tiles (64 trees of 17 rows over 4096 positions: 0 152 us, 2 149, 4 147; 64 chains
     // of 6 over 2000: 80.5, 77.2, 76.7; WIDE, 16 trees of 32 rows with 64 heads over 8192: 0 114, 2 109.4, 3 109.2, 4 109.5)
     static constexpr int kCost = WIDE ? 3 : 4;
-    static constexpr int kThreads = 16 * 32;
-    // registers of a softmax thread, and of the others: together the 128 a thread that the launch has
-    static constexpr int kMany = 184, kFew = 72;
+    // eight warps of softmax, two of products, and those for boxes, or four that copy and one that shows
+    static constexpr bool kTwelve = TMA && BOXES == 2;
+    static constexpr int kThreads = (kTwelve ? 12 : 16) * 32;
+    // registers of a softmax thread, and of the others: together those that the launch has
+    static constexpr int kMany = kTwelve ? 208 : 176, kFew = kTwelve ? 88 : 80;
+    static_assert(256 * kMany + (kThreads - 256) * kFew <= kThreads * (65536 / kThreads / 8 * 8), "registers of the launch");
     // place, in the order of use from its part's first slot on, of the values of tile t of nt
     static __device__ __forceinline__ int values_at(int t, int nt) {
         const int more = nt > kLead ? nt - kLead : 0;
@@ -411,40 +417,31 @@ __device__ void tc_box_role(const A& a, const TcMaps& maps, TcShared<S>& sh, con
     }
 }
 
-// Queries where the keys and values are boxes: one warp, by boxes of its own
-// or, where groups of heads do not fill row tiles, by 16-byte copies.
+// Queries of a segment where the keys and values are boxes, by the warp that
+// issues the first products with them: by boxes of their own or, where groups
+// of heads do not fill row tiles, by 16-byte copies.
 template <typename S, typename A>
-__device__ void tc_query_role(const A& a, const TcMaps& maps, TcShared<S>& sh, AttnCursor cur, int n, int p) {
+__device__ __forceinline__ void tc_queries(const A& a, const TcMaps& maps, TcShared<S>& sh, const AttnCursor& cur, int p) {
     const uint32_t bar = smem_u32(&sh.q_shown);
-    int sent = -1;
-    for (int j = 0, seg = 0; j < n; ++seg) {
-        const int nt = tc_part(cur, n - j);
-        const bool go_on = seg == 0 || tc_wait(smem_u32(&sh.q_empty), (seg - 1) & 1, &sh.fail, a.polls);
-        if (!__all_sync(0xffffffffu, go_on)) break;
-        if (maps.q_rows) {
-            // box p: panel p % kPanels of row tile p / kPanels; tiles behind the last row are left out
-            const int h = cur.s / a.row_tiles, rt = cur.s - h * a.row_tiles;
-            const int tile = p / S::kPanels, panel = p % S::kPanels;
-            const int r = (rt * S::kTiles + tile) * maps.q_rows;
-            const bool mine = tile < S::kTiles && r < a.rows;
-            const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, mine));
-            if (p == 0) mbar_arrive_expect_tx(bar, boxes * S::kPanel);
-            __syncwarp();
-            if (mine)
-                tc_box(smem_u32(sh.q) + tile * S::kSlot + panel * S::kPanel, &maps.q, panel * 64,
-                       h * static_cast<int>(a.group.d), r, cur.b, bar);
-        } else {
-            tc_copy_queries<S, 32>(a, sh, cur, p);
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            fence_proxy_async_smem();
-            mbar_arrive(bar);
-        }
-        j += nt;
-        cur.tile += nt - 1;
-        cur.next(a, S::KT);
-        sent = seg;
+    if (maps.q_rows) {
+        // box p: panel p % kPanels of row tile p / kPanels; tiles behind the last row are left out
+        const int h = cur.s / a.row_tiles, rt = cur.s - h * a.row_tiles;
+        const int tile = p / S::kPanels, panel = p % S::kPanels;
+        const int r = (rt * S::kTiles + tile) * maps.q_rows;
+        const bool mine = tile < S::kTiles && r < a.rows;
+        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, mine));
+        if (p == 0) mbar_arrive_expect_tx(bar, boxes * S::kPanel);
+        __syncwarp();
+        if (mine)
+            tc_box(smem_u32(sh.q) + tile * S::kSlot + panel * S::kPanel, &maps.q, panel * 64,
+                   h * static_cast<int>(a.group.d), r, cur.b, bar);
+    } else {
+        tc_copy_queries<S, 32>(a, sh, cur, p);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        mbar_arrive(bar);
     }
-    if (maps.q_rows && sent >= 0) mbar_wait_bounded(bar, sent & 1, 1u << 30);  // no box is in flight when the CTA ends
+    __syncwarp();
 }
 
 // 16-byte copies: four warps.  A warp copies 32 rows of every tile; lane l
@@ -535,12 +532,13 @@ __device__ void tc_show_role(const A& a, TcShared<S>& sh, const AttnCursor& cur,
 // tile i >> 1 (WIDE) or i.  A stream's next scores follow its output product,
 // whose weights lie where they go: products of one thread run in order.
 template <typename S, typename A>
-__device__ void tc_mma_role(const A& a, TcShared<S>& sh, const TcLayout& lay, AttnCursor cur, int n, int x) {
+__device__ void tc_mma_role(const A& a, const TcMaps& maps, TcShared<S>& sh, const TcLayout& lay, AttnCursor cur, int n,
+                            int x, int lane) {
     const uint32_t tm = sh.tmem;
     const uint32_t ts = tm + x * 128, to = tm + 256 + x * S::DP;
     constexpr uint32_t kScores = tc_idesc(S::KT, false), kOutputs = tc_idesc(S::DP, true);
     uint32_t p_seen = 0, turns = 0;
-    int j0 = 0, seg = 0, use0 = 0;
+    int j0 = 0, seg = 0, use0 = 0, sent = -1;
     bool fine = true;  // no wait ran out; the same in all lanes
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         fine = __all_sync(0xffffffffu, fine && tc_wait(smem_u32(bar), parity, &sh.fail, a.polls));
@@ -564,6 +562,12 @@ __device__ void tc_mma_role(const A& a, TcShared<S>& sh, const TcLayout& lay, At
                 tc_mma_ss(ts, qd + (((kk >> 2) * S::kPanel + (kk & 3) * 32) >> 4),
                           kd + (((kk >> 2) * lay.panel + (kk & 3) * 32) >> 4), kScores, kk > 0);
         };
+        if (S::TMA && x == 0) {
+            if (seg > 0) wait(&sh.q_empty, (seg - 1) & 1);
+            if (!fine) break;
+            tc_queries(a, maps, sh, cur, lane);
+            sent = seg;
+        }
         wait(&sh.q_shown, seg & 1);  // (both warps are through with the part before)
         if (x < items) {
             const int slot = wait_slot(use0 + S::keys_at(S::WIDE ? 0 : x, nt));
@@ -626,6 +630,7 @@ __device__ void tc_mma_role(const A& a, TcShared<S>& sh, const TcLayout& lay, At
     if (tc_elect()) tc_commit(smem_u32(&sh.end[x]));
     __syncwarp();
     mbar_wait_bounded(smem_u32(&sh.end[x]), 0, 1u << 30);
+    if (sent >= 0) mbar_wait_bounded(smem_u32(&sh.q_shown), sent & 1, 1u << 30);  // nor a box of queries
 }
 
 // ------------------------------------------------------------------ softmax
@@ -692,20 +697,44 @@ __device__ void tc_softmax_role(const A& a, TcShared<S>& sh, const TcLayout& lay
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tc_ld32(ts + c * 32, s[c]);
                 tc_wait_ld();
-                if (edge) {  // positions that not every row sees
+                // positions that not every row sees: of 32 columns
+                auto hide = [&](int c) {
+                    // bit e: position t0 + 32 c + e is before the pass's rows, or one that this row sees
+                    const int gap = base - (t0 + c * 32);
+                    const uint32_t open = gap >= 32 ? ~0u
+                                          : gap >= 0 ? (anc << gap) | ((1u << gap) - 1)
+                                          : gap > -32 ? anc >> -gap
+                                                      : 0u;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        // bit e: position t0 + 32 c + e is before the pass's rows, or one that this row sees
-                        const int gap = base - (t0 + c * 32);
-                        const uint32_t open = gap >= 32 ? ~0u
-                                              : gap >= 0 ? (anc << gap) | ((1u << gap) - 1)
-                                              : gap > -32 ? anc >> -gap
-                                                          : 0u;
+                    for (int e = 0; e < 32; ++e)
+                        if (!(open >> e & 1)) s[c][e] = __float_as_uint(hidden);
+                };
+                if (edge) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!(open >> e & 1)) s[c][e] = __float_as_uint(hidden);
-                    }
+                    for (int c = 0; c < 4; ++c) hide(c);
                 }
+                // weights of columns 64 half .., in bf16 for the product (relative 2^-8 each, random in sign); their sum is
+                // of the fp32 ones
+                uint32_t w[32];
+                const f2 sc = pack2(scale, scale);
+                auto weigh = [&](int half) {
+                    const float m_use = m_run == -INFINITY ? 0.0f : m_run;
+                    const f2 nm = pack2(-m_use, -m_use);
+                    f2 sum[2] = {pack2(0.0f, 0.0f), pack2(0.0f, 0.0f)};
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const uint32_t* p = &s[2 * half + (e >> 4)][2 * (e & 15)];
+                        float w0, w1;
+                        unpack2(fma2(pack2(__uint_as_float(p[0]), __uint_as_float(p[1])), sc, nm), w0, w1);
+                        w0 = ex2(w0);
+                        w1 = ex2(w1);
+                        sum[e & 1] = add2(sum[e & 1], pack2(w0, w1));
+                        w[e] = kv_pack_bf16(w0, w1);
+                    }
+                    float l0, l1;
+                    unpack2(add2(sum[0], sum[1]), l0, l1);
+                    return l0 + l1;
+                };
                 float top[4] = {hidden, hidden, hidden, hidden};
                 if (scale >= 0.0f) {
 #pragma unroll
@@ -741,29 +770,12 @@ __device__ void tc_softmax_role(const A& a, TcShared<S>& sh, const TcLayout& lay
                         }
                     }
                 }
-                const float m_use = m_run == -INFINITY ? 0.0f : m_run;
-                const f2 sc = pack2(scale, scale), nm = pack2(-m_use, -m_use);
-                f2 sum[2] = {pack2(0.0f, 0.0f), pack2(0.0f, 0.0f)};
-                // weights in bf16 for the product (relative 2^-8 each, random in sign); their sum is of the fp32 ones
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t w[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const uint32_t* p = &s[2 * half + (e >> 4)][2 * (e & 15)];
-                        float w0, w1;
-                        unpack2(fma2(pack2(__uint_as_float(p[0]), __uint_as_float(p[1])), sc, nm), w0, w1);
-                        w0 = ex2(w0);
-                        w1 = ex2(w1);
-                        sum[e & 1] = add2(sum[e & 1], pack2(w0, w1));
-                        w[e] = kv_pack_bf16(w0, w1);
-                    }
-                    tc_st32(ts + half * 32, w);
-                    if (half == 0 && !edge) half_ready();
-                }
-                float l0, l1;
-                unpack2(add2(sum[0], sum[1]), l0, l1);
-                l_run += l0 + l1;
+                const float l_half = weigh(0);
+                tc_st32(ts, w);
+                if (!edge) half_ready();
+                l_run += l_half;
+                l_run += weigh(1);
+                tc_st32(ts + 32, w);
                 tc_wait_st();
             }
             if (cur.len > 0 && edge) {
@@ -1036,7 +1048,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const
         sh.hole[tid] = 0;
     }
     __syncwarp();
-    if (warp == 12) tc_alloc(smem_u32(&sh.tmem), 512);
+    if (warp == 8) tc_alloc(smem_u32(&sh.tmem), 512);
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
@@ -1046,17 +1058,14 @@ __global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const
         tc_softmax_role<S>(a, sh, lay, cur, run, warp >> 2, tid & 127);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kFew));
-        if (warp == 12 || warp == 13) {
-            tc_mma_role<S>(a, sh, lay, cur, n, warp - 12);
+        if (warp < 10) {
+            tc_mma_role<S>(a, maps, sh, lay, cur, n, warp - 8, lane);
         } else if constexpr (S::TMA) {
-            if (warp < 8 + S::kBoxWarps)
-                tc_box_role<S>(a, maps, sh, cur, n, warp - 8, lane);
-            else if (warp < 12)
-                tc_query_role<S>(a, maps, sh, cur, n, lane);
+            if (warp < 10 + S::kBoxWarps) tc_box_role<S>(a, maps, sh, cur, n, warp - 10, lane);
         } else {
-            if (warp < 12)
-                tc_copy_role<S>(a, sh, cur, n, tid - 256);
-            else if (warp == 14 && lane == 0)
+            if (warp >= 12)
+                tc_copy_role<S>(a, sh, cur, n, tid - 384);
+            else if (warp == 10 && lane == 0)
                 tc_show_role<S>(a, sh, cur, n);
         }
     }
@@ -1064,7 +1073,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) tree_attention_tc_kernel(const
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
-    if (warp == 12) tc_dealloc(sh.tmem, 512);
+    if (warp == 8) tc_dealloc(sh.tmem, 512);
     // told when every role is done: a wait may run out after the threads that end a segment have looked at the flag
     if (tid == 0 && tc_failed(&sh.fail)) {
         AttnCursor at = sh.start;

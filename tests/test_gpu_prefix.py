@@ -277,3 +277,73 @@ def test_prefix_attention_is_refused_without_launching(sv, h):  # noqa: F811
     none = kc[:0]
     got = sv.specv_prefix_attention(h, q, none, none.clone(), tables[:, :0].contiguous(), torch.zeros_like(lens), t0[:0], n0 * 0)
     assert not got["out"].any() and not got["row_status"].any()
+
+
+def _exact_rows(c):
+    """Outputs, sums and the bounds' ingredients in 64 bits on the GPU, a sequence at a time."""
+    import torch
+
+    B, rows, hq, dim = c.q.shape
+    hkv, bs = c.kc_t.shape[1], c.bs
+    outs = [torch.zeros((B, rows, hq, dim), dtype=torch.float64, device="cuda") for _ in range(2)]
+    sums = [torch.zeros((B, rows, hq), dtype=torch.float64, device="cuda") for _ in range(2)]
+    for b, n in enumerate(c.lens.tolist()):
+        t = torch.arange(n, device="cuda")
+        full = c.tables[b].copy()
+        full[:c.prefix // bs] = c.table0
+        blk = _dev(full).long()[t // bs]
+        K, V = (x[blk, :, t % bs].double() for x in (c.kc_t, c.vc_t))
+        _, _, seen = P.tree(None if c.parents is None else c.parents[b], rows)
+        shut = torch.zeros((rows, n), dtype=torch.bool)
+        for r in range(rows):
+            shut[r, [n - rows + j for j in range(rows) if j not in seen[r]]] = True
+        q = c.q_t[b].double().reshape(rows, hkv, -1, dim)
+        s = (torch.einsum("rhgd,nhd->hgrn", q, K) * c.scale).masked_fill(shut.cuda(), -math.inf)
+        p = torch.softmax(s, -1)
+        for o, v in zip(outs, (V, V.abs())):
+            o[b] = torch.einsum("hgrn,nhd->rhgd", p, v).reshape(rows, hq, dim)
+        sums[0][b] = torch.logsumexp(s, -1).permute(2, 0, 1).reshape(rows, hq)
+        mag = torch.einsum("rhgd,nhd->hgrn", q.abs(), K.abs()).amax(-1) * c.scale
+        sums[1][b] = mag.permute(2, 0, 1).reshape(rows, hq)
+    return [x.cpu().numpy() for x in (outs[0], sums[0], outs[1], sums[1])]
+
+
+@pytest.mark.parametrize("B,hq,hkv,dim,bs,prefix,lens", [
+    (16, 8, 2, 64, 16, 20480, [17 + 29 * i for i in range(16)]),    # row tiles of 256, the sequences beside them
+    (5, 8, 2, 128, 16, 25600, [17, 600, 30, 256, 900]),             # three row tiles side by side
+    (6, 24, 4, 112, 40, 20000, [40, 17, 500, 90, 1000, 120]),       # five, blocks that do not fill tiles
+    (3, 16, 2, 128, 128, 384, [2000, 1500, 3000]),                  # more of their own than shared
+])
+def test_prefix_attention_with_both_parts_at_a_time(sv, h, B, hq, hkv, dim, bs, prefix, lens):  # noqa: F811
+    c = Shared(B + prefix, "bf16", B, 17, hq, hkv, dim, bs, prefix, lens)
+    got = c.call(sv, h)
+    out, lse, avg, mag = _exact_rows(c)
+    assert not got["row_status"].any()
+    t_out, t_lse = P.attention_bounds(out, lse, avg, mag, int(c.lens.max()), dim, True)
+    assert (np.abs(_np(got["out"]) - out) <= t_out).all()
+    assert (np.abs(_np(got["lse"]) - lse) <= t_lse).all()
+    again = c.call(sv, h)
+    assert (got["out"] == again["out"]).all() and (got["lse"] == again["lse"]).all()
+
+
+def test_prefix_attention_past_32_bit_offsets(sv, h):  # noqa: F811
+    """A pool of more than 2^32 bytes and elements: blocks far in it, for the prefix and the sequences."""
+    import torch
+
+    bs, hkv, dim, rows = 16, 8, 128, 17
+    blocks = 2 ** 32 // (bs * hkv * dim) // 2 + 600
+    kc = torch.zeros((blocks, hkv, bs, dim), dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    c = Shared(77, "bf16", 3, rows, 32, hkv, dim, bs, 640, [rows, 100, 300])
+    n = c.kc_t.shape[0]
+    kc[-n:], vc[-n:] = c.kc_t, c.vc_t
+    shift = blocks - n
+    tables, table0 = _dev(c.tables + np.where(c.tables >= 0, shift, 0).astype(np.int32)), _dev(c.table0 + shift)
+    for r in (rows, 1):
+        q = c.q_t[:, :r].contiguous()
+        lens = _dev(c.lens)
+        par = _dev(c.parents) if r > 1 else None
+        a = sv.specv_prefix_attention(h, q, kc, vc, tables, lens, table0, c.args()[6], parents=par, lse=True)
+        b = sv.specv_prefix_attention(h, q, c.kc_t, c.vc_t, _dev(c.tables), lens, _dev(c.table0), c.args()[6], parents=par,
+                                      lse=True)
+        assert torch.equal(a["out"], b["out"]) and torch.equal(a["lse"], b["lse"])

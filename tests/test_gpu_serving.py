@@ -454,3 +454,224 @@ def test_serving_calls_of_empty_batches_and_pools(sv, h):  # noqa: F811
         assert got["mass"].shape == (B, 2, 0) and not got["row_status"].any()
         got = sv.specv_cache_evict(h, kc, kc.clone(), tables, lens, got["mass"], 5)
         assert not got["row_status"].any() and not got["seq_lens"].any()
+
+
+# ---------------------------------------------------------------------------- together
+def test_serving_calls_in_one_captured_graph(sv):  # noqa: F811
+    """Append with norms, attention over a shared prefix, the weight gathered and the eviction in one graph, replayed with
+    other lengths, tables and values; each replay gives what the calls one by one give."""
+    import torch
+
+    B, rows, hq, hkv, dim, bs, width, prefix = 3, 9, 8, 2, 64, 16, 20, 32
+    hv = sv.specv_create(0, max_batch=B, max_k=31, vocab=100)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    rng = np.random.default_rng(8)
+    inv = _dev((10000.0 ** (-np.arange(dim // 2) * 2 / dim)).astype(np.float32))
+    w = _rounded(rng, (dim,), torch.bfloat16)[0]
+    kc, vc = (torch.zeros((70, hkv, bs, dim), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    fused = torch.zeros((B, rows, hq + 2 * hkv, dim), dtype=torch.bfloat16, device="cuda")
+    tables, lens, off, par = torch.zeros((B, width), **i32), torch.zeros(B, **i32), torch.zeros(B, **i32), torch.zeros((B, rows - 1), **i32)
+    table0, len0 = torch.zeros(2, **i32), torch.full((1,), prefix, **i32)
+    mass = torch.zeros((B, hkv, width * bs), device="cuda")
+
+    def calls():
+        q, k, v = fused[:, :, :hq], fused[:, :, hq:hq + hkv], fused[:, :, hq + hkv:]
+        app = sv.specv_cache_append_norm(hv, kc, vc, tables, lens, k, v, q=q, q_norm=w, k_norm=w, inv_freq=inv, offsets=off,
+                                         parents=par)
+        att = sv.specv_prefix_attention(hv, app["q_out"], kc, vc, tables, lens, table0, len0, parents=par, lse=True)
+        got = sv.specv_attention_mass(hv, app["q_out"], kc, vc, tables, lens, att["lse"], mass=mass, first=prefix, parents=par)
+        ev = sv.specv_cache_evict(hv, kc, vc, tables, lens, got["mass"], 96, recent=20, first=prefix)
+        return app["q_out"], att["out"], att["lse"], got["mass"], ev["mass"], ev["seq_lens"], ev["evicted"], ev["row_status"]
+
+    def fill(seed):
+        r = np.random.default_rng(seed)
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        for t in (kc, vc, fused):
+            t.copy_(torch.randn(t.shape, generator=g, device="cuda"))
+        mass.copy_(torch.rand(mass.shape, generator=g, device="cuda"))
+        order = r.permutation(70)
+        full = np.array([np.concatenate((order[:2], order[2 + 20 * b:20 + 20 * b])) for b in range(B)], np.int32)
+        tables.copy_(_dev(full))
+        table0.copy_(_dev(order[:2].astype(np.int32)))
+        lens.copy_(_dev(np.array([prefix + rows, 288 if seed % 2 else 0, int(r.integers(100, 280))], np.int32)))
+        off.copy_(_dev(r.integers(0, 999, B).astype(np.int32)))
+        par.copy_(_dev(np.array([[r.integers(-1, i) for i in range(rows - 1)] for _ in range(B)], np.int32)))
+
+    fill(0)
+    calls()
+    torch.cuda.synchronize()
+    graphs, outs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], []
+    for g in graphs:
+        with torch.cuda.graph(g):
+            outs.append(calls())
+    for seed in (1, 2, 3):
+        fill(seed)
+        want = [x.clone() for x in (*calls(), kc, vc)]
+        for g, out in zip(graphs, outs):
+            fill(seed)
+            g.replay()
+            torch.cuda.synchronize()
+            for x, y in zip((*out, kc, vc), want):
+                assert torch.equal(x, y)
+    sv.specv_destroy(hv)
+
+
+def test_serving_calls_on_two_streams(sv, h):  # noqa: F811
+    """Calls in flight together on two streams keep apart."""
+    import torch
+
+    cs = [_mass_case(40 + i, d, (4, r, 8, 2, 64, 16, [500, 40, 0, 900], "tree", 0)) for i, (d, r) in enumerate((("bf16", 9), ("f32", 3)))]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    pools = [[(c.kc_t.clone(), c.vc_t.clone()) for _ in range(4)] for c in cs]
+    args = [(_dev(c.tables), _dev(c.lens), _dev(c.lse), _dev(c.parents), _dev(c.rng.random((4, 2, 960)).astype(np.float32)))
+            for c in cs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for k in range(4):
+        for i, (c, s) in enumerate(zip(cs, streams)):
+            t, n, l, p, m = args[i]
+            a = sv.specv_attention_mass(h, c.q_t, *pools[i][k], t, n, l, mass=m, parents=p, stream=s)
+            e = sv.specv_cache_evict(h, *pools[i][k], t, n, a["mass"], 100, recent=30, first=4, stream=s)
+            got[i].append((a["mass"], e["mass"], e["seq_lens"], *pools[i][k]))
+    torch.cuda.synchronize()
+    for i, c in enumerate(cs):
+        t, n, l, p, m = args[i]
+        kc, vc = c.kc_t.clone(), c.vc_t.clone()
+        a = sv.specv_attention_mass(h, c.q_t, kc, vc, t, n, l, mass=m, parents=p)
+        e = sv.specv_cache_evict(h, kc, vc, t, n, a["mass"], 100, recent=30, first=4)
+        for one in got[i]:
+            for x, y in zip(one, (a["mass"], e["mass"], e["seq_lens"], kc, vc)):
+                assert torch.equal(torch.nan_to_num(x.double()), torch.nan_to_num(y.double()))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_mass_of_a_long_cache_past_32_bit_offsets(sv, h, dtype):  # noqa: F811
+    """Blocks far in a pool of more than 2^32 bytes, a long context, with the last position's mass at the end of a wide row."""
+    import torch
+
+    rng = np.random.default_rng(4)
+    bs, hkv, dim, n, rows = 16, 4, 128, 40000, 3
+    dt = _dtype(dtype)
+    blocks = 2 ** 32 // (bs * hkv * dim * dt.itemsize) + 2600
+    kc = torch.zeros((blocks, hkv, bs, dim), dtype=dt, device="cuda")
+    used = -(-n // bs)
+    tables = np.full((1, used), -1, np.int32)
+    tables[0] = blocks - 1 - rng.permutation(used)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    kc[blocks - used:] = torch.randn((used, hkv, bs, dim), generator=g, device="cuda").to(dt)
+    q = (torch.randn((1, rows, 8, dim), generator=g, device="cuda") * 2).to(dt)
+    lens = _dev(np.array([n], np.int32))
+    att = sv.specv_tree_attention(h, q, kc, kc, _dev(tables), lens, lse=True)
+    got = sv.specv_attention_mass(h, q, kc, kc, _dev(tables), lens, att["lse"])["mass"]
+    t = torch.arange(n, device="cuda")
+    K = kc[_dev(tables).long()[0][t // bs], :, t % bs].double()
+    s = torch.einsum("rhgd,nhd->hgrn", q[0].double().reshape(rows, hkv, 2, dim), K) * dim ** -0.5
+    late = t[None] > n - rows + torch.arange(rows, device="cuda")[:, None]
+    s.masked_fill_(late, -math.inf)
+    want = torch.exp(s - att["lse"][0].double().reshape(rows, hkv, 2).permute(1, 2, 0)[..., None]).sum((1, 2))
+    # each weight is off by 2^-23 of (dim + 16) times the magnitudes (below 60), its arguments' and the exponential's rounding
+    assert ((got[0, :, :n].double() - want).abs() <= want * (144 * 60 + 200) * 2.0 ** -23 + 1e-30).all()
+
+
+def test_a_bounded_cache_of_all_of_them(sv):  # noqa: F811
+    """Rounds of append with norms, attention over a shared prefix, verification's kept chain, the gathered weight, and
+    eviction with the blocks given back, against a dense history in 64 bits: each head holds what it should hold."""
+    import torch
+
+    B, M, hq, hkv, dim, bs, prefix, budget, recent = 3, 5, 4, 2, 64, 4, 16, 40, 12
+    rng = np.random.default_rng(21)
+    hv = sv.specv_create(0, max_batch=B, max_k=M, vocab=60)
+    inv = (10000.0 ** (-np.arange(dim // 2) * 2 / dim)).astype(np.float32)
+    w_t, w = _rounded(rng, (dim,), torch.float32)
+    blocks = 200
+    kc = torch.zeros((blocks, hkv, bs, dim), device="cuda")
+    vc = torch.zeros_like(kc)
+    free = [int(x) for x in rng.permutation(blocks)]
+    n0 = prefix // bs
+    table0 = [free.pop() for _ in range(n0)]
+    tables = np.full((B, 40), -1, np.int32)
+    tables[:, :n0] = table0
+    nb, lens, off = [n0] * B, np.full(B, prefix, np.int32), np.zeros(B, np.int32)
+    free_list, free_count = torch.zeros(blocks, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    # the prefix, appended once
+    (k_t, k), (v_t, v) = [_rounded(rng, (1, prefix, hkv, dim), torch.float32) for _ in range(2)]
+    sv.specv_cache_append_norm(hv, kc, vc, _dev(tables[:1]), _dev(lens[:1]), k_t, v_t, k_norm=w_t, inv_freq=_dev(inv))
+    turned = lambda x, p, wt: S.turn(S.norm(x, wt, 1e-6, 0.0), p * inv.astype(np.float64), False)  # noqa: E731
+    # by sequence and head: keys, values, positions as tokens, masses, in cache order
+    hist = [[[(turned(k[0, t], t, w)[h_], v[0, t, h_], t, 0.0) for t in range(prefix)] for h_ in range(hkv)] for _ in range(B)]
+    mass = torch.zeros((B, hkv, 160), device="cuda")
+    spare = torch.zeros_like(mass)
+    for step in range(12):
+        for b in range(B):
+            lens[b] += M + 1
+            while nb[b] * bs < lens[b]:
+                tables[b, nb[b]] = free.pop()
+                nb[b] += 1
+        (q_t, q), (k_t, k), (v_t, v) = [_rounded(rng, (B, M + 1, n, dim), torch.float32) for n in (hq, hkv, hkv)]
+        t_t, l_t = _dev(tables), _dev(lens)
+        app = sv.specv_cache_append_norm(hv, kc, vc, t_t, l_t, k_t, v_t, q=q_t, q_norm=w_t, k_norm=w_t, inv_freq=_dev(inv),
+                                         offsets=_dev(off))
+        att = sv.specv_prefix_attention(hv, app["q_out"], kc, vc, t_t, l_t, _dev(np.array(table0, np.int32)),
+                                        _dev(np.array([prefix], np.int32)), lse=True)
+        accepted = rng.integers(0, M + 1, B).astype(np.int32)
+        lse = att["lse"].clone()
+        for b in range(B):
+            lse[b, 1 + accepted[b]:] = math.inf  # rejected drafts gather nothing
+        sv.specv_attention_mass(hv, app["q_out"], kc, vc, t_t, l_t, lse, mass=mass, first=prefix, out={"mass": mass})
+        for b in range(B):
+            base = len(hist[b][0])
+            for h_ in range(hkv):
+                for r in range(M + 1):
+                    hist[b][h_].append((turned(k[b, r], base + off[b] + r, w)[h_], v[b, r, h_], base + int(off[b]) + r, 0.0))
+            gained = np.zeros((hkv, base + M + 1))
+            for r in range(M + 1):
+                qq = turned(q[b, r], base + off[b] + r, w)
+                for hh in range(hq):
+                    seen = hist[b][hh // 2][:base + r + 1]
+                    s = np.array([x[0] for x in seen]) @ qq[hh] * dim ** -0.5
+                    e = np.exp(s - s.max())
+                    o = e @ np.array([x[1] for x in seen]) / e.sum()
+                    # as in the verify round of the other cache calls: fp32 throughout
+                    assert np.max(np.abs(_np(att["out"][b, r, hh]) - o)) < 2e-3 * max(np.abs(x[1]).max() for x in seen)
+                    if r <= accepted[b]:
+                        gained[hh // 2, :base + r + 1] += e / e.sum()
+            for h_ in range(hkv):
+                hist[b][h_] = [(x[0], x[1], x[2], x[3] + (gained[h_, t] if t >= prefix else 0.0)) for t, x in enumerate(hist[b][h_])]
+                got = _np(mass[b, h_, :len(hist[b][h_])])
+                assert np.max(np.abs(got - [x[3] for x in hist[b][h_]])[prefix:]) < 1e-3
+        # the rejected drafts leave, with their blocks
+        nb_t, acc_t = _dev(np.array(nb, np.int32)), _dev(accepted)
+        free_count.zero_()
+        sv.specv_rollback(hv, acc_t, M, l_t, t_t, nb_t, bs, free_list, free_count)
+        free.extend(free_list[:int(free_count)].tolist())
+        ev = sv.specv_cache_evict(hv, kc, vc, t_t, l_t, mass, budget, recent=recent, first=prefix, out={"mass": spare})
+        mass, spare = spare, mass
+        off += ev["evicted"].cpu().numpy()
+        free_count.zero_()
+        new = ev["seq_lens"]
+        sv.specv_rollback(hv, torch.full((B,), M, dtype=torch.int32, device="cuda"), M, new, t_t, nb_t, bs, free_list, free_count)
+        free.extend(free_list[:int(free_count)].tolist())
+        tables, nb, lens = t_t.cpu().numpy().copy(), nb_t.tolist(), new.cpu().numpy().copy()
+        assert all(n == -(-int(x) // bs) for n, x in zip(nb, lens)) and max(lens) <= budget
+        for b in range(B):
+            for h_ in range(hkv):
+                rows_ = hist[b][h_][:len(hist[b][h_]) - (M - int(accepted[b]))]
+                if len(rows_) > budget:
+                    line = budget - recent
+                    got = _np(spare[b, h_, :len(rows_)])  # ties in 64 bits could fall either way: the kernel's own masses decide
+                    mid = range(prefix, len(rows_) - recent)
+                    kept = set(sorted(mid, key=lambda t: (-got[t], t))[:line - prefix])
+                    holes = [t for t in range(prefix, line) if t not in kept]
+                    above = [t for t in range(line, len(rows_) - recent) if t in kept]
+                    place = list(range(line)) + list(range(len(rows_) - recent, len(rows_)))
+                    for t, x in zip(holes, above):
+                        place[t] = x
+                    rows_ = [rows_[t] for t in place]
+                hist[b][h_] = rows_
+                assert len(rows_) == lens[b]
+                t = np.arange(lens[b])
+                ids = tables[b][t // bs]
+                assert np.max(np.abs(_np(kc)[ids, h_, t % bs] - [x[0] for x in rows_])) < 2.0 ** -18
+                np.testing.assert_array_equal(_np(vc)[ids, h_, t % bs], [x[1] for x in rows_])
+    assert (off > 0).all()
+    sv.specv_destroy(hv)

@@ -419,8 +419,9 @@ specv_status specv_cache_compact(specv_handle h, const specv_kv_cache *cache, in
 /* Norms of the heads of an append (each weight nullable: those heads are
  * then not normed): a head x of queries or keys becomes x * rsqrt(mean(x^2) +
  * eps) * (weight + weight_add) before its pairs turn.  Weights [head_dim] of
- * the cache's type, device memory; weight_add 1 for models that keep weights as
- * their difference from one, else 0.  eps >= 0 and weight_add finite. */
+ * the cache's type, device memory, 16-byte aligned; weight_add 1 for models that
+ * keep weights as their difference from one, else 0.  eps >= 0 and weight_add
+ * finite. */
 typedef struct {
     const void *q_weight, *k_weight;
     float eps, weight_add;
@@ -467,7 +468,8 @@ specv_status specv_cache_append_norm(specv_handle h, const specv_kv_cache *cache
  *               takes no part (set it so for rows of rejected drafts)
  *   mass        [B, kv_heads, width] fp32 (nullable: zeros).  The pass's own
  *               positions start from 0: what it holds there is not read
- *   mass_out    [B, kv_heads, width] fp32 out; mass itself, or other memory.
+ *   mass_out    [B, kv_heads, width] fp32 out; mass itself, or memory apart
+ *               from it.
  *               Written for positions first .. length - 1
  *   first       positions before it are left alone (a shared prefix)
  *   row_status  [B] out (nullable): 0, or bits 512, 2048 (also a length above
@@ -492,8 +494,8 @@ specv_status specv_attention_mass(specv_handle h, const specv_kv_cache *cache, c
  *   mass        [layers, B, kv_heads, width] fp32 as specv_attention_mass
  *               gathers it
  *   mass_out    [layers, B, kv_heads, width] out: the masses of the positions
- *               that remain, at their places; not mass's memory.  Behind the new
- *               length it is left alone
+ *               that remain, at their places; memory apart from mass's.  Behind
+ *               the new length it is left alone
  *   budget      1 or more, at least first + recent
  *   lens_out    [B] out: the new lengths; not cache->seq_lens' memory
  *   evicted     [B] out (nullable): old minus new length

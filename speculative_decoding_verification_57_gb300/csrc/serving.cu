@@ -103,7 +103,8 @@ specv_status specv_cache_append_norm(specv_handle h, const specv_kv_cache* cache
     if (rot_dim < 0 || rot_dim > cache->head_dim || rot_dim % 2 || (rot_dim > 0 && !inv_freq))
         return SPECV_ERR_INVALID_ARGUMENT;
     if (norm) {
-        if (!std::isfinite(norm->eps) || norm->eps < 0.0f || !std::isfinite(norm->weight_add))
+        if (!std::isfinite(norm->eps) || norm->eps < 0.0f || !std::isfinite(norm->weight_add) ||
+            !aligned16(norm->q_weight) || !aligned16(norm->k_weight))
             return SPECV_ERR_INVALID_ARGUMENT;
         n.q_weight = norm->q_weight;
         n.k_weight = norm->k_weight;
@@ -174,6 +175,8 @@ specv_status specv_attention_mass(specv_handle h, const specv_kv_cache* cache, c
         return SPECV_ERR_INVALID_ARGUMENT;
     if (batch == 0) return SPECV_OK;
     if (!rows_ok(cache, q, q_stride) || !lse || (width > 0 && !mass_out)) return SPECV_ERR_INVALID_ARGUMENT;
+    if (mass && mass != mass_out && overlap(mass, mass_out, static_cast<int64_t>(batch) * cache->kv_heads * width * 4))
+        return SPECV_ERR_INVALID_ARGUMENT;
     a.q = q;
     a.q_stride = q_stride;
     a.parents = rows > 1 ? parents : nullptr;

@@ -103,7 +103,7 @@ __device__ __forceinline__ int attn_len(const PartArgs& a, int b) {
     if (!a.prefix) return attn_prefix(a.kv, len, a.prefix_cap);
     if (len == 0) return 0;
     const int skip = attn_prefix(a.kv, *a.prefix, a.prefix_cap);
-    return skip >= 0 && len - a.rows >= skip && a.kv.fits(len) ? len - skip : -1;
+    return skip >= 0 && len >= a.rows && len - a.rows >= skip && a.kv.fits(len) ? len - skip : -1;
 }
 // The first entry of the tables that is looked at (of sequences that are not refused).
 __device__ __forceinline__ int attn_first_block(const AttnArgs&) { return 0; }

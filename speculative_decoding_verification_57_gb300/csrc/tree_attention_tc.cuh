@@ -970,7 +970,7 @@ __device__ TcShare tc_share(const PartArgs& a, AttnCut& sh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int64_t tiles = 0;  // of the sequences, of a segment each
     for (int b = tid; b < a.sequences; b += S::kThreads) {
-        const int len = a.lens[b];
+        const int len = min(a.lens[b], INT32_MAX - 512);
         tiles += attn_tiles(len > prefix ? len - prefix : 0, S::KT);
     }
     for (int off = 16; off > 0; off >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, off);

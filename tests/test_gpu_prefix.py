@@ -71,7 +71,7 @@ class Shared:
         np.testing.assert_array_equal(np.isnan(g), np.isnan(out))
         np.testing.assert_array_equal(g[np.isinf(out)], out[np.isinf(out)])
         fin = np.isfinite(lse)
-        t_out, t_lse = P.attention_bounds(out, np.where(fin, lse, 0), avg, mag, int(max(self.lens.max(), 1)),
+        t_out, t_lse = P.attention_bounds(out, np.where(fin, lse, 0), avg, mag, int(self.lens[status == 0].max(initial=1)),
                                           self.q.shape[-1], str(self.dtype).endswith("bfloat16"))
         same = np.isfinite(out)
         bad = same & ~(np.abs(g - np.where(same, out, 0)) <= t_out)
@@ -131,6 +131,11 @@ def test_prefix_attention_refuses_sequences(sv, h, dtype, B, rows):  # noqa: F81
         c.parents[4, 3] = 3
     c.check(c.call(sv, h))
     assert c.ref[1][2].tolist() == [0, 0, 2048, 4096, 512 if rows > 1 else 0, 2048]
+    for low in (-2 ** 31, -2 ** 31 + 5, 2 ** 31 - 1):  # nothing is taken off a length that has too little
+        lens, c.ref = c.lens.copy(), None
+        c.lens[5], c.lens[0] = low, low
+        c.check(c.call(sv, h))
+        c.lens, c.ref = lens, None
     # a hole in the prefix, and lengths of the prefix that are none
     table0 = c.table0.copy()
     c.table0[9], c.ref = -1, None

@@ -411,6 +411,7 @@ def test_serving_calls_are_refused_without_launching(sv, h):  # noqa: F811
 
     for kw in (dict(q_norm=w, eps=-1.0), dict(k_norm=w, eps=math.nan), dict(k_norm=w, weight_add=math.inf),
                dict(k_norm=w[:32]), dict(k_norm=w.double()), dict(k_norm=w.cpu()),
+               dict(q_norm=torch.ones(65, device="cuda")[1:]), dict(k_norm=torch.ones(66, device="cuda")[2:]),
                dict(positions=pos, inv_freq=inv), dict(positions=pos, inv_freq=inv, pair_axis=[0] * 31),
                dict(positions=pos, inv_freq=inv, pair_axis=[0] * 31 + [3]), dict(pair_axis=[0] * 32, inv_freq=inv),
                dict(positions=pos, pair_axis=[0] * 32, inv_freq=inv, offsets=off),
@@ -426,6 +427,8 @@ def test_serving_calls_are_refused_without_launching(sv, h):  # noqa: F811
     refused(m, q, kc, vc, tables, lens, lse, scale=math.inf)
     refused(m, q, kc, vc, tables, lens, lse[:1])
     refused(m, q, kc, vc, tables, lens, lse, mass=mass[:, :1])
+    long = torch.zeros((3, 2, 32), device="cuda")
+    refused(m, q, kc, vc, tables, lens, lse, mass=long[:2], out={"mass": long[1:]})
     refused(m, q, kc, vc, tables, lens, lse, mass=mass, out={"mass": torch.zeros((2, 2, 31), device="cuda")})
     refused(m, torch.zeros((2, 33, 4, 64), device="cuda"), kc, vc, tables, lens, torch.zeros((2, 33, 4), device="cuda"))
     e = sv.specv_cache_evict

@@ -14,6 +14,17 @@
 // with their sines and cosines stay in its registers, for queries and then
 // for keys, so that a norm costs a head eight multiply-adds, the shuffles and
 // eight products more than the turn.
+//
+// Measured (GB300, graph replays over sets of inputs beyond the L2; 32/8 heads of
+// 128 in bf16): one token for 8 sequences 3.6 us (2.5 without norms), 64 trees of 17
+// rows 10.7 us (8.0), 4 ragged prompts of up to 2048 tokens with images on three
+// axes 41.7 us, 53% of 6803 GB/s (four sets of inputs, which the L2 partly holds:
+// 37.5; with one axis 35.4, without norms 32.6, the plain append 27.8).  Bound by
+// instructions and the chain of loads together: 2.05 of 4 instructions a cycle with
+// 21 warps an SM.  No one part of it weighs: angles, shuffles, weights, stores and
+// the look at the blocks are 1 to 4 us each; 64 or 32 threads a token, one, two or
+// four heads a thread in flight and 480 to 960 threads an SM are all within 40.4 to
+// 52 us, 672 threads of 96 among the best for prompts and trees.
 #pragma once
 #include "cache_append.cuh"
 
@@ -80,7 +91,7 @@ __device__ __forceinline__ void append_neighbours(f2 (&f)[N], const f2 (&c)[N], 
     }
 }
 
-// Threads of an SM: more registers each than a plain append's need.
+// Threads of an SM: more registers each than a plain append's need (576: trees 14.0 us, prompts 45.2; 960: 12.4 and 43.9).
 constexpr int kNormResident = 672;
 
 template <typename T, int MODE, int THREADS>

@@ -10,8 +10,9 @@
 // the queries eight columns each, so that a thread adds up the columns of its
 // positions by itself and three shuffles finish a position.
 //
-// Bound by reading the keys (half of a cache) up to some 70 queries a kv head,
-// above by the matrix instructions.
+// For fp32, heads above 128 and more than 256 queries a kv head; the rest is in
+// attention_mass_tc.cuh.  fp32 is bound by the instructions that split keys and
+// queries into tf32 parts, bf16 by the scores' way through registers.
 #pragma once
 #include "tree_attention.cuh"
 

@@ -97,15 +97,15 @@ constexpr AttnPlan<A> plan_of_tc() {
 // time than its positions cost the memory; up to 16 the other's pipeline is
 // shorter.  Single rows, 32/8 heads of 128, this kernel | the tcgen05 one, us:
 //   sequences   500 positions   2000          20,000        131,072
-//   1           9.0 | 11.2      14.5 | 14.3   28.9 | 27.6   99 | 92
-//   4           10.4 | 12.6     16.7 | 19.4   54.0 | 52.4   285 | 264
-//   64          32.5 | 44.8     75.1 | 76.0   618 | 577
-// (4 rows, 16 a kv head, within 3% of these); 16 heads of 64, 128 single rows
-// over 1000 positions 89 | 150, 16 rows for 64 over 2000 82 | 108, for 4 over
-// 20,000 56 | 60.  So long contexts of heads of 128 would be 3 to 8% faster
+//   1           9.2 | 10.6      15.1 | 14.1   29.8 | 27.4   101 | 93
+//   4           10.5 | 12.5     16.9 | 18.4   53.4 | 50.7   283 | 261
+//   64          33.1 | 40.6     79.5 | 75.4   605 | 562
+// 16 heads of 64, 128 single rows over 1000 positions 92 | 139, 16 rows for 64
+// over 2000 87 | 104, for 4 over 20,000 56 | 61.  So long contexts of heads of 128
+// would be 5 to 8% faster
 // there; but lengths are device memory, and the rule does not look at them.  Of
-// 20 rows a kv head, 64 sequences over 300 positions take 42.3 us on this
-// kernel (with a row tile of 32) and 36.6 there, 1 over 2000 13.7 and 14.6.  In
+// 20 rows a kv head, 64 sequences over 300 positions took 42.3 us on this
+// kernel (with a row tile of 32) and take 33.4 there, 1 over 2000 13.7 and 14.3.  In
 // each, the narrowest row tile that holds the rows, or the widest: a tile's
 // keys and values are read once for all of its rows.
 constexpr int kTcLeast = 17;

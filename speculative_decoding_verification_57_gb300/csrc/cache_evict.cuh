@@ -21,6 +21,13 @@
 // order, 16 bytes a thread and row, all loads of a step before its stores: a
 // step's stores go to places that no later step reads, as sources of kept
 // positions lie above the line and the recent ones, behind them, move down.
+//
+// Measured (GB300, graph replays over sets of inputs beyond the L2; 8 heads of 128
+// in bf16, budget 1024, 256 recent, up to twice as long before): 8 layers of 32
+// sequences 158 us, 92% of 6803 GB/s; one layer of 8 sequences 14.9 us, a chain
+// of length and blocks (2.8 us), the least mass (2.8), lists (2.9) and moves (6).
+// Four pieces a thread in flight (two: 176 us, eight: 221, which spills), four CTAs
+// an SM (five or six: 201 and 195), eight masses a thread (16, which spill: 212).
 #pragma once
 #include "kv_cache.cuh"
 #include "ptx.cuh"

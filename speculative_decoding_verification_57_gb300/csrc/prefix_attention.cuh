@@ -6,7 +6,20 @@
 // part with one sequence whose rows are those of the whole batch, the own
 // positions one with a sequence each: two launches of the kernels of tree
 // attention, which leave every segment's results undivided in the workspace,
-// and one that joins them.
+// and one that joins them.  The second launch does not wait for the first, only
+// at its end; where both are tcgen05 kernels they share the SMs
+// (tree_attention_tc.cuh).
+//
+// Measured (GB300, graph replays over sets of inputs beyond the L2; 32/8 heads of
+// 128 in bf16; of 1896 TFLOP/s and 6803 GB/s measured):
+//   64 single rows behind 4096 positions, 250..500 of their own   58.6 us, 29%
+//   64 trees of 17 rows behind 8192, 500..1000                    173 us, 49%
+//   16 chains of 6 rows behind 65536, 250..500                    110 us, 50%
+//   fp32, 8 chains of 5, 12 heads of 64, behind 1024, 150..300    32 us, 8%
+// (the second by tree attention over all of its positions reads 2.3 GB).  The prefix
+// of the trees alone takes 108 us, 70% of the tensor cores' rate, where the
+// streams' turns bound it; their own positions alone 50; the join, some 12, and the
+// short calls by latency.
 #pragma once
 #include "tree_attention.cuh"
 

@@ -2,9 +2,9 @@
 // head_dim up to 128.  Mathematics, work line and joining as in
 // tree_attention.cuh; a tile is 128 positions, a row tile 128 rows.
 //
-// One CTA an SM, 16 warps: two streams of four softmax warps, four warps that
-// copy, two that issue the products, and two that help or only make up their
-// warpgroup, so that registers can be moved to the softmax warps.  A stream
+// One CTA an SM, 12 or 16 warps: two streams of four softmax warps, two warps
+// that issue the products, and those that bring keys and values: two or three
+// for boxes, four that copy.  Registers move to the softmax warps.  A stream
 // has the scores of one row tile and tile of positions (128 x 128 fp32) and
 // its outputs (128 x DP fp32) in tensor memory; a softmax thread owns a row,
 // so that maxima and sums need no exchange.  While one stream's weights are
@@ -19,26 +19,29 @@
 // columns.
 //
 // Blocks whose rows fill tiles evenly (a multiple of eight that divides 128,
-// or a multiple of 128) come as tensor boxes, a box a block and panel; others
-// by 16-byte copies.  Boxes land where the tensor cores see them at once and
-// cost the softmax warps' schedulers next to nothing (with the issuing warps'
-// turns, they took the trees and the wide trees of the list below from 178 and
-// 149 us to 156 and 129).
+// or a multiple of 128) come as tensor boxes, a box a block (of heads of 128) or
+// a block and panel; others by 16-byte copies.  Boxes land where the tensor cores
+// see them at once and cost the softmax warps' schedulers next to nothing (with
+// the issuing warps' turns, they took the trees and the wide trees of the list
+// below from 178 and 149 us to 156 and 129).
 //
 // Measured (GB300, 2070 MHz, graph replays over sets of inputs of more than
-// twice the L2; bytes and operations counted once; of 6691 GB/s and 1926 TFLOP/s measured):
-//   64 chains of 6 rows, 32/8 heads of 128, 1000..2000 positions    77 us  78%
-//   64 trees of 17 rows, same heads, 2048..4096                    147 us  84%
-//   one tree of 17 rows, same heads, 131072                         94 us  85%
-//   16 trees of 32 rows, 64/8 heads, 4096..8192 (WIDE)             108 us  59%,
-//     972 TFLOP/s, 50%
+// twice the L2; bytes and operations counted once; of 6803 GB/s and 1896 TFLOP/s measured):
+//   64 chains of 6 rows, 32/8 heads of 128, 1000..2000 positions    77 us  76%
+//   64 trees of 17 rows, same heads, 2048..4096                    144 us  85%
+//   one tree of 17 rows, same heads, 131072                         94 us  84%
+//   16 trees of 32 rows, 64/8 heads, 4096..8192 (WIDE)             103 us  61%,
+//     1015 TFLOP/s, 54%
 // With one row tile the memory bounds it, short of it by each run's start
-// (5 us), its segments' ends and the join (5 to 10 us).  WIDE, a tile takes a
-// stream 3500 cycles: 1300 for its products (16 instructions of 64 cycles and
-// their issue), 1900 for its weights, the rest to tell one of the other; two
-// streams hide half of that.  The compiler counts 128 registers a thread for all
-// roles (what the launch has, not what the softmax warps get) and spills 300 to
-// 560 bytes of them a thread.
+// (5 us), its segments' ends and the join (5 to 10 us).  WIDE, two streams take
+// 3050 cycles for a tile each, 2048 of them for their 32 products: a stream has
+// its scores, 1050 cycles on the first half of its weights are ready, 550 later
+// the second, 1400 on from the first half its next scores.  Halving the
+// products' columns gains 3%, the maxima left out 3%, a second of the parts no
+// more: the hand-overs bound it, four of some 150 cycles.  Not built, as they
+// gained nothing here: maxima formed beside the first half's weights (spills: 199 us
+// for 175 with the trees behind a prefix), one issuing warp for both streams (203),
+// waits that poll without rest (268).
 #pragma once
 #include <cuda.h>
 
@@ -527,7 +530,9 @@ __device__ void tc_show_role(const A& a, TcShared<S>& sh, const AttnCursor& cur,
 // the two take turns, an output product and the next scores at a time, because
 // streams that share the tensor cores fall into step and then form their
 // weights at the same time, while these idle (16 trees of 32 rows over 8192
-// positions: one warp for both 134 us, two 153, two in turns 129).  Item i of
+// positions: one warp for both 134 us, two 153, two in turns 129; since products
+// are issued at the tensor cores' pace, 64 trees of 17 rows behind a shared
+// prefix: one warp 203 us, two in turns 175).  Item i of
 // a segment's part belongs to stream i & 1 and
 // tile i >> 1 (WIDE) or i.  A stream's next scores follow its output product,
 // whose weights lie where they go: products of one thread run in order.

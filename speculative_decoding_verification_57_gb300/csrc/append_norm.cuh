@@ -18,7 +18,7 @@
 // Measured (GB300, graph replays over sets of inputs beyond the L2; 32/8 heads of
 // 128 in bf16): one token for 8 sequences 3.6 us (2.5 without norms), 64 trees of 17
 // rows 10.7 us (8.0), 4 ragged prompts of up to 2048 tokens with images on three
-// axes 41.7 us, 53% of 6803 GB/s (four sets of inputs, which the L2 partly holds:
+// axes 40.4 us, 55% of 6803 GB/s (four sets of inputs, which the L2 partly holds:
 // 37.5; with one axis 35.4, without norms 32.6, the plain append 27.8).  Bound by
 // instructions and the chain of loads together: 2.05 of 4 instructions a cycle with
 // 21 warps an SM.  No one part of it weighs: angles, shuffles, weights, stores and
@@ -37,7 +37,7 @@ struct AppendNormArgs {
     const int32_t* offsets;           // [B]; NULL: 0
     float eps, weight_add, inv_dim;
     int axes;
-    int group;  // lanes of a head
+    int group_log;  // lanes of a head, their base-2 logarithm
     uint8_t axis[128];  // of each pair
 };
 
@@ -107,8 +107,8 @@ cache_append_norm_kernel(const __grid_constant__ AppendNormArgs n) {
     const int tid = threadIdx.x, lane = tid & 31;
     const KvView& kv = a.kv;
     const int turning = a.q_heads + kv.heads, heads = turning + kv.heads;
-    const int per = static_cast<int>(a.units.d), hstep = THREADS / n.group;
-    const int h0 = tid / n.group, u = tid - h0 * n.group;
+    const int per = static_cast<int>(a.units.d), hstep = THREADS >> n.group_log;
+    const int h0 = tid >> n.group_log, u = tid - (h0 << n.group_log);
     const bool piece = u < per;  // the lane has pieces of its head
     const int half = a.rot / 2;
     // the unit's pieces of a head that turns, and of a value's
@@ -162,8 +162,10 @@ cache_append_norm_kernel(const __grid_constant__ AppendNormArgs n) {
                 s_sin[j] = cs.y;
             }
         }
-        for (int i = kv.block.div(base) + tid, last = kv.block.div(len - 1); i <= last; i += THREADS)
-            block_bad |= !kv.valid(table[i]);
+        const int first_block = kv.block.div(base), many = kv.block.div(len - 1) - first_block + 1;
+#pragma unroll 2
+        for (int i = tid; i < many; i += THREADS)
+            block_bad |= static_cast<uint32_t>(table[first_block + i]) >= static_cast<uint32_t>(kv.blocks);
         if (__syncthreads_or(parent_bad || block_bad))
             status = (__syncthreads_or(parent_bad) ? KV_PARENT : 0) | (__syncthreads_or(block_bad) ? KV_BLOCK : 0);
     }
@@ -288,7 +290,9 @@ cache_append_norm_kernel(const __grid_constant__ AppendNormArgs n) {
                         unpack2(sum, lo, hi);
                         all = lo + hi;
                     }
-                    for (int off = n.group >> 1; off > 0; off >>= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
+#pragma unroll
+                    for (int step = 4; step >= 0; --step)
+                        if (step < n.group_log) all += __shfl_xor_sync(0xffffffffu, all, 1 << step);
                     if (normed) inv = rsqrtf(fmaf(all, n.inv_dim, n.eps));
                 }
                 if (!mine) continue;

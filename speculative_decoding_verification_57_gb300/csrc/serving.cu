@@ -150,8 +150,7 @@ specv_status specv_cache_append_norm(specv_handle h, const specv_kv_cache* cache
     const int vec = cache->dtype == SPECV_BF16 ? 8 : 4;
     const int units = cache->head_dim / vec / 2;
     a.units = FastDiv(static_cast<uint32_t>(units));
-    n.group = 1;
-    while (n.group < units) n.group *= 2;
+    while ((1 << n.group_log) < units) ++n.group_log;
     n.inv_dim = 1.0f / static_cast<float>(cache->head_dim);
     DeviceGuard g(h->device);
     if (!g.ok) return cuda_fail(cudaErrorInvalidDevice, "cudaSetDevice");

@@ -473,7 +473,8 @@ specv_status specv_cache_append_norm(specv_handle h, const specv_kv_cache *cache
  *               Written for positions first .. length - 1
  *   first       positions before it are left alone (a shared prefix)
  *   row_status  [B] out (nullable): 0, or bits 512, 2048 (also a length above
- *               width), 4096.  Of a refused sequence nothing is written
+ *               width), 4096, 64.  Of a refused sequence nothing is written;
+ *               with bit 64 what mass_out holds of it is not determined
  * Sums are fp32 in a fixed order: results repeat.  The values of the cache are
  * not read. */
 specv_status specv_attention_mass(specv_handle h, const specv_kv_cache *cache, const void *q, int64_t q_stride,
@@ -515,7 +516,8 @@ int specv_plan_cluster(specv_handle h, specv_dtype logits_dtype, int batch, int 
 
 /* Test hook, off unless called: arms the next launch of the split-vocabulary
  * kernel (V > 2048) or of the tcgen05 tree-attention kernel (bf16, head_dim up
- * to 128, more than 16 rows a kv head) on this handle so that CTA 0 of the
+ * to 128, more than 16 rows a kv head; of a shared prefix, more than 16 of the
+ * batch: its own launch) on this handle so that CTA 0 of the
  * grid never issues the bulk copy of its pass-1 stage use (the copies of its
  * slot use) number `stage_use` (counted from 0
  * in issue order) nor signals it, and every wait of that launch gives up

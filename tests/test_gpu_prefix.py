@@ -352,3 +352,21 @@ def test_prefix_attention_past_32_bit_offsets(sv, h):  # noqa: F811
         b = sv.specv_prefix_attention(h, q, c.kc_t, c.vc_t, _dev(c.tables), lens, _dev(c.table0), c.args()[6], parents=par,
                                       lse=True)
         assert torch.equal(a["out"], b["out"]) and torch.equal(a["lse"], b["lse"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,rows,hq,hkv,dim,bs,prefix,lens", [
+    (500, 1, 1, 1, 16, 3, 9, [1 + i % 7 for i in range(500)]),      # many sequences
+    (8, 32, 256, 1, 64, 64, 128, [32 + 9 * i for i in range(8)]),   # 65,536 rows of one kv head
+    (2, 3, 64, 64, 32, 8, 64, [3, 40]),                             # many kv heads
+    (3, 17, 8, 2, 128, 1024, 1024, [17, 1024, 2000]),               # blocks longer than tiles
+    (2, 32, 1, 1, 256, 16, 4096, [32, 33]),
+])
+def test_prefix_attention_at_the_ends_of_the_sizes(sv, h, dtype, B, rows, hq, hkv, dim, bs, prefix, lens):  # noqa: F811
+    c = Shared(B + rows, dtype, B, rows, hq, hkv, dim, bs, prefix, lens)
+    got = c.call(sv, h)
+    out, lse, avg, mag = _exact_rows(c)
+    assert not got["row_status"].any()
+    t_out, t_lse = P.attention_bounds(out, lse, avg, mag, int(c.lens.max()), dim, dtype == "bf16")
+    assert (np.abs(_np(got["out"]) - out) <= t_out).all()
+    assert (np.abs(_np(got["lse"]) - lse) <= t_lse).all()

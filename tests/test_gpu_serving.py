@@ -176,6 +176,9 @@ MASSES = [
     (1, 32, 5, 1, 112, 24, [900], "tree", 5),
     (2, 25, 20, 4, 128, 40, [25, 700], "tree", 0),   # 125 queries, blocks that do not fill tiles
     (40, 1, 12, 6, 128, 16, [1 + 90 * (i % 8) for i in range(40)], "chain", 0),
+    (500, 1, 2, 1, 16, 2, [1 + i % 9 for i in range(500)], "chain", 1),
+    (2, 2, 64, 64, 32, 8, [40, 300], "chain", 0),    # many kv heads
+    (2, 5, 8, 2, 64, 1024, [1500, 2048], "tree", 1024),
 ]
 
 
@@ -302,6 +305,8 @@ EVICTS = [
     (1, 2, 1, 96, 16, [6000], 3000, 10, 0),
     (80, 1, 8, 64, 16, [20 + i for i in range(80)], 50, 20, 2),
     (3, 40, 8, 32, 8, [30, 29, 64], 29, 5, 1),
+    (1, 1, 2, 16, 256, [30000], 17000, 3000, 100),    # many spans of masses, many lists of moves
+    (500, 1, 1, 16, 2, [3 + i % 11 for i in range(500)], 6, 2, 1),
 ]
 
 

@@ -465,22 +465,30 @@ specv_status specv_cache_append_norm(specv_handle h, const specv_kv_cache *cache
  *   q, q_stride, q_heads, parents, rows, scale  as for specv_tree_attention
  *   lse         [B, rows, q_heads] fp32, as specv_tree_attention (or
  *               specv_prefix_attention) left it.  A row whose lse is infinite
- *               takes no part (set it so for rows of rejected drafts)
+ *               takes no part
+ *   path, num_accepted  [B, rows - 1], [B] (nullable) as a verify call gives
+ *               them (path NULL: chains): rows of rejected drafts take no part,
+ *               and a kept node's mass goes where specv_cache_compact moves its
+ *               keys, behind this call; those behind the path are not written.
+ *               Without num_accepted all rows stay
  *   mass        [B, kv_heads, width] fp32 (nullable: zeros).  The pass's own
  *               positions start from 0: what it holds there is not read
  *   mass_out    [B, kv_heads, width] fp32 out; mass itself, or memory apart
  *               from it.
  *               Written for positions first .. length - 1
- *   first       positions before it are left alone (a shared prefix)
+ *   first       positions before it are left alone (a shared prefix).  Of a
+ *               sequence that ends within the whole blocks before it only the
+ *               length is looked at
  *   row_status  [B] out (nullable): 0, or bits 512, 2048 (also a length above
- *               width), 4096, 64.  Of a refused sequence nothing is written;
- *               with bit 64 what mass_out holds of it is not determined
+ *               width), 4096, 128 and 8192 (as for specv_cache_compact), 64.  Of
+ *               a refused sequence nothing is written; with bit 64 what mass_out holds of it is not determined
  * Sums are fp32 in a fixed order: results repeat.  The values of the cache are
  * not read. */
 specv_status specv_attention_mass(specv_handle h, const specv_kv_cache *cache, const void *q, int64_t q_stride,
                                   int q_heads, const int32_t *parents, int batch, int rows, float scale,
-                                  const float *lse, const float *mass, float *mass_out, int64_t width, int first,
-                                  int32_t *row_status, void *stream);
+                                  const float *lse, const int32_t *path, const int32_t *num_accepted,
+                                  const float *mass, float *mass_out, int64_t width, int first, int32_t *row_status,
+                                  void *stream);
 
 /* Eviction: sequences longer than `budget` are brought back to it, in keys and
  * values of `layers` layers at once (as specv_cache_compact counts them).  Of

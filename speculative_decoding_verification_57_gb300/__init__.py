@@ -644,14 +644,17 @@ def specv_cache_compact(h: Handle, k_cache, v_cache, block_tables, seq_lens, pat
 
 
 def specv_attention_mass(h: Handle, q, k_cache, v_cache, block_tables, seq_lens, lse, *, mass=None, first=0,
-                         parents=None, scale=None, out=None, stream=None):
+                         parents=None, path=None, num_accepted=None, scale=None, out=None, stream=None):
     """The attention weight that the cache's positions gather from a pass:
     mass[b, h, t] plus the sum of exp(scale * q . k_t - lse) over the pass's
     rows that see position t and the query heads of kv head h.  q, the cache,
     parents and scale as for specv_tree_attention, lse [B, rows, q_heads] fp32
     as it left it (rows of an infinite lse take no part); mass [B, kv_heads,
     width] fp32 (None: zeros; the pass's own positions start from zero);
-    positions before ``first`` are left alone.  Returns a dict: mass [B,
+    positions before ``first`` are left alone.  path [B, rows - 1] (None:
+    chains) and num_accepted [B] int32 as a verify call gives them: rejected
+    drafts take no part, and kept nodes' masses go where specv_cache_compact,
+    behind this call, moves their keys.  Returns a dict: mass [B,
     kv_heads, width] and row_status [B]; ``out`` may supply them (mass itself
     among them).  Without it mass is new, zero where nothing is written, and
     as wide as ``mass`` or the table."""
@@ -664,6 +667,10 @@ def specv_attention_mass(h: Handle, q, k_cache, v_cache, block_tables, seq_lens,
     pq, q_stride = _token_rows(h, q, "q", k_cache, (B, rows, q_heads, c.head_dim))
     pp = None if parents is None else _on(h, parents, _i32, "parents", (B, rows - 1))
     pl = _on(h, lse, _f32, "lse", (B, rows, q_heads))
+    if path is not None and num_accepted is None:
+        raise ValueError("path needs num_accepted")
+    pt = None if path is None else _on(h, path, _i32, "path", (B, rows - 1))
+    pa = None if num_accepted is None else _on(h, num_accepted, _i32, "num_accepted", (B,))
     out = {} if out is None else out
     if "mass" not in out:
         width = c.max_blocks * c.block_size if mass is None else mass.shape[-1]
@@ -675,8 +682,8 @@ def specv_attention_mass(h: Handle, q, k_cache, v_cache, block_tables, seq_lens,
         out["row_status"] = _empty(h, (B,), _i32, stream)
     ps = _on(h, out["row_status"], _i32, "row_status", (B,))
     st = _lib.load().specv_attention_mass(
-        h.ptr, c, pq, q_stride, q_heads, pp, B, rows, c.head_dim ** -0.5 if scale is None else scale, pl, pm, po, width,
-        int(first), ps, _stream_of(h, stream))
+        h.ptr, c, pq, q_stride, q_heads, pp, B, rows, c.head_dim ** -0.5 if scale is None else scale, pl, pt, pa, pm, po,
+        width, int(first), ps, _stream_of(h, stream))
     _check(st, "specv_attention_mass")
     return out
 

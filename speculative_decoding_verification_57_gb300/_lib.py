@@ -122,8 +122,8 @@ def load(build_if_missing=True):
     lib.specv_cache_append_norm.argtypes = [vp, cache, vp, i64, i32, vp, i64, vp, i64, ctypes.POINTER(SpecvHeadNorm), vp,
                                             i32, i32, ctypes.POINTER(SpecvPositions), vp, vp, i32, i32, vp, vp, vp]
     lib.specv_attention_mass.restype = i32
-    lib.specv_attention_mass.argtypes = [vp, cache, vp, i64, i32, vp, i32, i32, ctypes.c_float, vp, vp, vp, i64, i32, vp,
-                                         vp]
+    lib.specv_attention_mass.argtypes = [vp, cache, vp, i64, i32, vp, i32, i32, ctypes.c_float, vp, vp, vp, vp, vp, i64,
+                                         i32, vp, vp]
     lib.specv_cache_evict.restype = i32
     lib.specv_cache_evict.argtypes = [vp, cache, i32, i64, vp, vp, i64, i32, i32, i32, i32, vp, vp, vp, vp]
     lib.specv_tree_attention.restype = i32

@@ -26,6 +26,7 @@ struct MassArgs {
     const float* lse;   // [B, rows, q_heads]
     const float* mass;  // [B, heads, width]; NULL: zeros
     float* out;         // [B, heads, width]
+    const int32_t *path, *num_accepted;  // of a verified pass (NULL: all rows stay)
     int32_t* row_status;
     int64_t width;
     FastDiv group;
@@ -45,6 +46,27 @@ __device__ __forceinline__ int attn_len(const MassArgs& a, int b) {
 }
 
 __device__ __forceinline__ int attn_side(const MassArgs&) { return 1; }
+
+// What stays of sequence b's pass, by one converged warp; lane r holds row r.
+// Returns the rows that stay (bit r: row 0, and a kept node's), and as `to` the
+// row's place among the pass's positions behind them, -1 if it goes; `status`
+// gets the bits of a count or a path that are none.
+__device__ __forceinline__ uint32_t mass_kept(const MassArgs& a, int b, int lane, int& to, int& status) {
+    to = lane < a.rows ? lane : -1;
+    if (!a.num_accepted) return ~0u;
+    const int nodes = a.rows - 1, n = a.num_accepted[b];
+    if (n < 0 || n > nodes) status |= KV_ACCEPTED;
+    const bool mine = lane < nodes && lane < n;
+    const int node = mine ? a.path ? a.path[static_cast<int64_t>(b) * nodes + lane] : lane : -1;
+    const int before = __shfl_up_sync(0xffffffffu, node, 1);
+    if (!__all_sync(0xffffffffu, !mine || (node >= 0 && node < nodes && (lane == 0 || node > before)))) status |= KV_PATH;
+    uint32_t kept = 1 | (mine && node >= 0 && node < nodes ? 2u << node : 0u);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) kept |= __shfl_xor_sync(0xffffffffu, kept, off);
+    // (a path is increasing: a kept row's place is the number of kept rows above it)
+    to = kept >> lane & 1 ? __popc(kept & ((1u << lane) - 1)) : -1;
+    return kept;
+}
 
 // DP: head_dim rounded up to 64, 128 or 256; NT tiles of eight queries at a
 // time; MT row groups of 16 positions a warp, four warps.
@@ -78,6 +100,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) attention_mass_kernel(c
     __shared__ int64_t s_row[2][KT];
     __shared__ __align__(16) float s_lse[NQ];
     __shared__ uint32_t s_anc[NQ];
+    __shared__ int s_to[32];  // places of the pass's rows behind the kept ones
     __shared__ AttnCut s_cut;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int quad = lane >> 2, two = (lane & 3) * 2;
@@ -147,7 +170,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) attention_mass_kernel(c
         }
     };
     // ... their sums (an infinite one: the row takes no part) and ancestors, by the whole CTA
-    auto note_queries = [&](int b, int h, int m0, uint32_t line) {
+    auto note_queries = [&](int b, int h, int m0, uint32_t line, uint32_t kept) {
         for (int m = tid; m < (NQ + 31) / 32 * 32; m += S::kThreads) {  // (whole warps: they shuffle)
             const int row = m0 + m;
             const bool real = row < m_rows;
@@ -155,7 +178,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) attention_mass_kernel(c
             const uint32_t anc = __shfl_sync(0xffffffffu, line, r);
             if (m >= NQ) continue;
             float l = INFINITY;
-            if (real) l = a.lse[(static_cast<int64_t>(b) * a.rows + r) * a.q_heads + static_cast<int64_t>(h) * group + g];
+            if (real && (kept >> r & 1))
+                l = a.lse[(static_cast<int64_t>(b) * a.rows + r) * a.q_heads + static_cast<int64_t>(h) * group + g];
             s_lse[m] = fabsf(l) == INFINITY ? INFINITY : l * 1.44269504f;
             s_anc[m] = real ? anc : 0;
         }
@@ -172,7 +196,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) attention_mass_kernel(c
     }
     Place place = places[kAhead];
 
-    uint32_t line = 0;  // ancestors of row `lane`
+    uint32_t line = 0, kept = ~0u;  // ancestors of row `lane`; the rows that take part
     bool refused = false;
     for (int i = 0; i < n; ++i) {
         post_row(i + kAhead, place);
@@ -181,20 +205,23 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) attention_mass_kernel(c
         if (starts) {  // a segment: its sequence's checks, alike in every CTA that has some of it
             int status = cur.len < 0 ? KV_LENGTH : 0;
             bool hole = false;
+            int to = lane;
             if (cur.len > 0) {
                 int depth;
                 if (!warp_tree(a.parents ? a.parents + static_cast<int64_t>(cur.b) * (a.rows - 1) : nullptr, a.rows, lane,
                                line, depth))
                     status |= KV_PARENT;
+                kept = mass_kept(a, cur.b, lane, to, status);
                 const int32_t* table = kv.tables + static_cast<int64_t>(cur.b) * kv.max_blocks + skip_blocks;
                 for (int x = tid, last = kv.block.div(cur.len - 1); x <= last; x += S::kThreads) hole |= !kv.valid(table[x]);
             }
             if (__syncthreads_or(hole)) status |= KV_BLOCK;
+            if (warp == 0) s_to[lane] = to;  // (the last tile has read its own, before this barrier)
             refused = status != 0;
             if (tid == 0 && cur.tile == 0 && cur.s == 0 && a.row_status) a.row_status[cur.b] = status;
             if (cur.len > 0 && !refused) {
                 copy_queries(cur.b, cur.s, 0);
-                note_queries(cur.b, cur.s, 0, line);
+                note_queries(cur.b, cur.s, 0, line, kept);
             }
             cp_commit();
             cp_wait<0>();
@@ -224,7 +251,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) attention_mass_kernel(c
                     // more queries than are kept: the next ones, for this tile
                     __syncthreads();
                     copy_queries(cur.b, cur.s, m0);
-                    note_queries(cur.b, cur.s, m0, line);
+                    note_queries(cur.b, cur.s, m0, line, kept);
                     cp_commit();
                     cp_wait<0>();
                     __syncthreads();
@@ -324,7 +351,11 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas) attention_mass_kernel(c
                     sum[g][e] += __shfl_xor_sync(0xffffffffu, sum[g][e], 1);
                     sum[g][e] += __shfl_xor_sync(0xffffffffu, sum[g][e], 2);
                     const int pos = pos0 + g * 16 + 8 * e;
-                    if ((lane & 3) == 0 && pos >= a.first && pos < len) a.out[line0 + pos] = before[g][e] + sum[g][e];
+                    // (a kept node moves to its place, maybe to one before `first`, which stays as it was)
+                    const int to = pos >= base && pos < len ? s_to[pos - base] : 0;
+                    const int at = pos >= base ? base + to : pos;
+                    if ((lane & 3) == 0 && at >= a.first && pos < len && to >= 0)
+                        a.out[line0 + at] = before[g][e] + sum[g][e];
                 }
         }
         cur.next(a, KT);

@@ -52,6 +52,7 @@ struct MassShared {
     AttnCut cut;
     uint64_t full[S::kSlots], empty[S::kSlots], q_full[2], q_empty[2], s_full[2], s_empty[2], end;
     int status[2];  // of a set's sequence
+    int to[2][32];  // places of its pass's rows behind the kept ones
     uint32_t tmem;
     int fail;
 };
@@ -98,11 +99,14 @@ __device__ void mass_query_role(const MassArgs& a, MassShared<S>& sh, MassRun ru
         int depth;
         const bool ok = warp_tree(a.parents ? a.parents + static_cast<int64_t>(cur.b) * (a.rows - 1) : nullptr, a.rows, lane,
                                   line, depth);
+        int to, path_status = 0;
+        const uint32_t kept = mass_kept(a, cur.b, lane, to, path_status);
+        sh.to[set][lane] = to;
         for (int m0 = 0; m0 < m_rows; m0 += 32) {
             const int m = m0 + lane, r = a.group.div(m < m_rows ? m : 0), g = m - r * group;
             const uint32_t anc = __shfl_sync(0xffffffffu, line, r);
             float l = INFINITY;
-            if (m < m_rows)
+            if (m < m_rows && (kept >> r & 1))
                 l = a.lse[(static_cast<int64_t>(cur.b) * a.rows + r) * a.q_heads + static_cast<int64_t>(cur.s) * group + g];
             const uint32_t part = __ballot_sync(0xffffffffu, fabsf(l) != INFINITY);
             if (lane == 0) sh.part[(set * q_rows + m0) >> 5] = part;
@@ -123,7 +127,9 @@ __device__ void mass_query_role(const MassArgs& a, MassShared<S>& sh, MassRun ru
             checked = cur.b;
         }
         if (lane == 0) {
-            const int status = cur.len < 0 ? KV_LENGTH : cur.len == 0 ? 0 : (ok ? 0 : KV_PARENT) | (holes ? KV_BLOCK : 0);
+            const int status = cur.len < 0    ? KV_LENGTH
+                               : cur.len == 0 ? 0
+                                              : (ok ? 0 : KV_PARENT) | (holes ? KV_BLOCK : 0) | path_status;
             sh.status[set] = status;
             if (cur.tile == 0 && cur.s == 0 && a.row_status) a.row_status[cur.b] = status;
         }
@@ -343,7 +349,9 @@ __device__ void mass_weight_role(const MassArgs& a, MassShared<S>& sh, MassRun r
             }
             float lo, hi;
             unpack2(sum, lo, hi);
-            if (writes) a.out[line0 + pos] = before + (lo + hi);
+            // (a kept node moves to its place, maybe to one before `first`, which stays as it was)
+            const int to = node >= 0 && node < 32 ? sh.to[set][node] : 0, at = node >= 0 ? base + to : pos;
+            if (writes && to >= 0 && at >= a.first) a.out[line0 + at] = before + (lo + hi);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.q_empty[set]));

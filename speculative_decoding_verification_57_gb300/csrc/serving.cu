@@ -165,8 +165,9 @@ specv_status specv_cache_append_norm(specv_handle h, const specv_kv_cache* cache
 
 specv_status specv_attention_mass(specv_handle h, const specv_kv_cache* cache, const void* q, int64_t q_stride,
                                   int q_heads, const int32_t* parents, int batch, int rows, float scale,
-                                  const float* lse, const float* mass, float* mass_out, int64_t width, int first,
-                                  int32_t* row_status, void* stream) {
+                                  const float* lse, const int32_t* path, const int32_t* num_accepted,
+                                  const float* mass, float* mass_out, int64_t width, int first, int32_t* row_status,
+                                  void* stream) {
     MassArgs a = {};
     if (!make_view(h, cache, batch, a.kv)) return SPECV_ERR_INVALID_ARGUMENT;
     if (rows < 1 || rows - 1 > h->max_k || q_heads < 1 || q_heads > 65536 || q_heads % cache->kv_heads ||
@@ -180,6 +181,8 @@ specv_status specv_attention_mass(specv_handle h, const specv_kv_cache* cache, c
     a.q_stride = q_stride;
     a.parents = rows > 1 ? parents : nullptr;
     a.lse = lse;
+    a.path = num_accepted ? path : nullptr;
+    a.num_accepted = num_accepted;
     a.mass = mass;
     a.out = mass_out;
     a.row_status = row_status;

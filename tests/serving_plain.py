@@ -119,7 +119,19 @@ def prefix_attention(q, kc, vc, tables, lens, prefix_table, prefix, parents, sca
     return out, lse, status | refused, avg, mag
 
 
-def mass(q, kc, tables, lens, lse, parents, scale, before, first, width):
+def kept_of(path, accepted, rows):
+    """(ok bits, rows that stay, their places) of one sequence's pass."""
+    if accepted is None:
+        return 0, list(range(rows)), list(range(rows))
+    n = int(accepted)
+    nodes = list(range(max(min(n, rows - 1), 0))) if path is None else [int(x) for x in path[:max(min(n, rows - 1), 0)]]
+    bad = 0 if 0 <= n <= rows - 1 else P.ST_ACCEPTED
+    if any(x < 0 or x >= rows - 1 for x in nodes) or any(y <= x for x, y in zip(nodes, nodes[1:])):
+        bad |= P.ST_PATH
+    return bad, [0] + [1 + x for x in nodes], list(range(len(nodes) + 1))
+
+
+def mass(q, kc, tables, lens, lse, parents, scale, before, first, width, path=None, accepted=None):
     """Returns (gained [B, heads, width], status, written, bound): the new
     masses where written, and how far a kernel's may be off.
 
@@ -146,7 +158,8 @@ def mass(q, kc, tables, lens, lse, parents, scale, before, first, width):
             continue
         ok, _, seen = P.tree(None if parents is None else parents[b], rows)
         ids, inside = P.blocks_of(tables[b], skip, n, bs, kc.shape[0])
-        status[b] = (0 if ok else ST_PARENT) | (0 if inside else ST_BLOCK)
+        bad, kept, places = kept_of(None if path is None else path[b], None if accepted is None else accepted[b], rows)
+        status[b] = (0 if ok else ST_PARENT) | (0 if inside else ST_BLOCK) | bad
         if status[b]:
             continue
         K = kc[ids, :, np.arange(skip, n) % bs]  # [n - skip, heads, dim]
@@ -154,7 +167,7 @@ def mass(q, kc, tables, lens, lse, parents, scale, before, first, width):
             see = np.array([t < n - rows or t - (n - rows) in seen[r] for t in range(skip, n)])
             for h in range(hq):
                 l = float(lse[b, r, h])
-                if np.isinf(l):
+                if np.isinf(l) or r not in kept:
                     continue
                 kk = K[see, h // group]
                 with np.errstate(all="ignore"):
@@ -170,6 +183,13 @@ def mass(q, kc, tables, lens, lse, parents, scale, before, first, width):
             out[b, :, :n - rows] += before[b, :, :n - rows]
             tol[b, :, :n - rows] += np.abs(out[b, :, :n - rows]) * 2.0 ** -23
         written[b, :, first:n] = True
+        if accepted is not None:  # kept nodes to their places, the others nowhere
+            base = n - rows
+            for x in (out, tol):
+                x[b, :, base:base + len(kept)] = x[b, :, [base + r for r in kept]].T
+            written[b, :, base:n] = False
+            for r, to in zip(kept, places):
+                written[b, :, base + to] = base + to >= first
     return out, status, written, 1.01 * tol
 
 

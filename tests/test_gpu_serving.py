@@ -274,6 +274,37 @@ def test_mass_of_hidden_and_infinite_keys(sv, h, dtype, rows, hq):  # noqa: F811
         assert x == math.inf or torch.isnan(got[0, 0, t])
 
 
+@pytest.mark.parametrize("dtype,rows,hq,first",
+                         [("bf16", 17, 8, 0), ("bf16", 6, 8, 197), ("f32", 9, 4, 194), ("bf16", 32, 24, 0), ("f32", 32, 8, 0)])
+def test_mass_of_a_verified_pass(sv, h, dtype, rows, hq, first):  # noqa: F811
+    """Rejected rows give nothing, kept nodes' masses go along the path; a path or count that is none is refused."""
+    import torch
+
+    B, lens = 6, [rows, 150, 0, 200, 130, 131]  # (`first` of 197 and 194: inside the pass of the fourth)
+    c = _mass_case(rows, dtype, (B, rows, hq, 2, 64, 16, lens, "star", first))
+    M = rows - 1
+    acc = np.array([0, M, 1, M // 2, M + 1, 2], np.int32)
+    path = np.full((B, M), -1, np.int32)
+    for b in range(B):
+        path[b, :min(acc[b], M)] = np.sort(c.rng.permutation(M)[:min(acc[b], M)])
+    path[5, :2] = path[5, 1::-1]  # not increasing
+    width = c.tables.shape[1] * 16
+    for p in (path, None):
+        before = c.rng.random((B, 2, width)).astype(np.float32)
+        out = torch.full((B, 2, width), -7.0, device="cuda")
+        got = sv.specv_attention_mass(h, c.q_t, c.kc_t, c.vc_t, _dev(c.tables), _dev(c.lens), _dev(c.lse), mass=_dev(before),
+                                      first=first, parents=_dev(c.parents), path=None if p is None else _dev(p),
+                                      num_accepted=_dev(acc), out={"mass": out})
+        torch.cuda.synchronize()
+        ref, status, written, tol = S.mass(c.q, _np(c.kc_t), c.tables, c.lens, c.lse, c.parents, c.scale, before, first, width,
+                                           p, acc)
+        assert got["row_status"].tolist() == status.tolist()
+        # (of a sequence within the whole blocks before `first` only the length is looked at)
+        assert status.tolist()[4:] == ([0, 0] if first >= lens[5] else [128, 0 if p is None else 8192])
+        g = _np(out)
+        assert (g[~written] == -7.0).all() and (np.abs(g - ref) <= tol)[written].all()
+
+
 def test_mass_refuses_sequences(sv, h):  # noqa: F811
     import torch
 
@@ -429,6 +460,9 @@ def test_serving_calls_are_refused_without_launching(sv, h):  # noqa: F811
     m = sv.specv_attention_mass
     refused(m, q[:, :, :3], kc, vc, tables, lens, lse[:, :, :3].contiguous())
     refused(m, q, kc, vc, tables, lens, lse, first=-1)
+    refused(m, q, kc, vc, tables, lens, lse, path=par)
+    refused(m, q, kc, vc, tables, lens, lse, path=par[:, :1], num_accepted=off)
+    refused(m, q, kc, vc, tables, lens, lse, num_accepted=off[:1])
     refused(m, q, kc, vc, tables, lens, lse, scale=math.inf)
     refused(m, q, kc, vc, tables, lens, lse[:1])
     refused(m, q, kc, vc, tables, lens, lse, mass=mass[:, :1])
@@ -622,10 +656,8 @@ def test_a_bounded_cache_of_all_of_them(sv):  # noqa: F811
         att = sv.specv_prefix_attention(hv, app["q_out"], kc, vc, t_t, l_t, _dev(np.array(table0, np.int32)),
                                         _dev(np.array([prefix], np.int32)), lse=True)
         accepted = rng.integers(0, M + 1, B).astype(np.int32)
-        lse = att["lse"].clone()
-        for b in range(B):
-            lse[b, 1 + accepted[b]:] = math.inf  # rejected drafts gather nothing
-        sv.specv_attention_mass(hv, app["q_out"], kc, vc, t_t, l_t, lse, mass=mass, first=prefix, out={"mass": mass})
+        sv.specv_attention_mass(hv, app["q_out"], kc, vc, t_t, l_t, att["lse"], mass=mass, first=prefix,
+                                num_accepted=_dev(accepted), out={"mass": mass})  # rejected drafts gather nothing
         for b in range(B):
             base = len(hist[b][0])
             for h_ in range(hkv):
@@ -645,8 +677,9 @@ def test_a_bounded_cache_of_all_of_them(sv):  # noqa: F811
                         gained[hh // 2, :base + r + 1] += e / e.sum()
             for h_ in range(hkv):
                 hist[b][h_] = [(x[0], x[1], x[2], x[3] + (gained[h_, t] if t >= prefix else 0.0)) for t, x in enumerate(hist[b][h_])]
-                got = _np(mass[b, h_, :len(hist[b][h_])])
-                assert np.max(np.abs(got - [x[3] for x in hist[b][h_]])[prefix:]) < 1e-3
+                stay = len(hist[b][h_]) - (M - int(accepted[b]))
+                got = _np(mass[b, h_, :stay])
+                assert np.max(np.abs(got - [x[3] for x in hist[b][h_][:stay]])[prefix:]) < 1e-3
         # the rejected drafts leave, with their blocks
         nb_t, acc_t = _dev(np.array(nb, np.int32)), _dev(accepted)
         free_count.zero_()

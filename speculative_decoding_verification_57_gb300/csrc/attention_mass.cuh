@@ -85,7 +85,7 @@ struct MassShape {
     static constexpr int kStages = kTile > 48 * 1024 ? 2 : 3;
     static constexpr int kAhead = kStages - 1;
     static constexpr int kSmem = kStages * kTile + kQ;
-    static constexpr int kFit = 227 * 1024 / (kSmem + 3072);
+    static constexpr int kFit = 227 * 1024 / (kSmem + 3 * 1024);
     // resident CTAs: by shared memory and by registers (scores, and some 70 others)
     static constexpr int kMost = 65536 / ((MT * NT * (kBf16 ? 4 : 8) + 70) * kThreads);
     static constexpr int kCtas = kFit > kMost ? kMost : kFit;

@@ -1,6 +1,6 @@
 """Plain float64 restatements of the calls for current models and long-running
 batches on the paged KV cache, one sequence, row and head at a time: the
-checker of the CUDA kernels.  The cache and the trees are those of
+reference of the CUDA kernels.  The cache and the trees are those of
 cache_plain.py."""
 import numpy as np
 

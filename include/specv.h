@@ -523,11 +523,12 @@ specv_status specv_cache_evict(specv_handle h, const specv_kv_cache *cache, int 
 int specv_plan_cluster(specv_handle h, specv_dtype logits_dtype, int batch, int k, int64_t V);
 
 /* Test hook, off unless called: arms the next launch of the split-vocabulary
- * kernel (V > 2048) or of the tcgen05 tree-attention kernel (bf16, head_dim up
+ * kernel (V > 2048), of the tcgen05 tree-attention kernel (bf16, head_dim up
  * to 128, more than 16 rows a kv head; of a shared prefix, more than 16 of the
- * batch: its own launch) on this handle so that CTA 0 of the
+ * batch: its own launch) or of the tcgen05 kernel of specv_attention_mass (bf16,
+ * head_dim up to 128, up to 256 rows a kv head) on this handle so that CTA 0 of the
  * grid never issues the bulk copy of its pass-1 stage use (the copies of its
- * slot use) number `stage_use` (counted from 0
+ * slot use, or tile) number `stage_use` (counted from 0
  * in issue order) nor signals it, and every wait of that launch gives up
  * after `polls` polls.  The waits that run out end the row's work: it
  * reports row_status bit 64 (num_accepted 0, out_tokens -1) and the call

@@ -35,6 +35,8 @@ struct MassArgs {
     int first;      // positions before it are left alone
     int skip;       // whole blocks before it, which are not read
     float scale;
+    int withhold;    // test hook: copy of CTA 0 that never happens; -1: none
+    uint32_t polls;  // most polls of a wait
 };
 
 // Positions of sequence b from `skip` on; 0: nothing to do; -1: refused by its length.

@@ -70,20 +70,26 @@ struct MassRun {
     }
 };
 
-// Queries, sums and ancestors of each segment, by one warp.
+// Queries, sums and ancestors of each segment, by one warp; and the statuses of the sequences that start in the run, of all
+// of them, also behind a wait that ran out (which is told for them here and, as for the others, at the kernel's end).
 template <typename S>
-__device__ void mass_query_role(const MassArgs& a, MassShared<S>& sh, MassRun run, int sets, uint32_t polls, int lane) {
+__device__ void mass_query_role(const MassArgs& a, MassShared<S>& sh, MassRun run, int sets, int lane) {
     const KvView& kv = a.kv;
     const int group = static_cast<int>(a.group.d), m_rows = a.rows * group, q_rows = S::kRows / sets;
     const int first_block = a.skip / kv.block_size();
     constexpr int kPieces = S::DP / 8;
     int checked = -1;
-    bool holes = false;
+    bool holes = false, fine = true;  // no wait ran out; the same in all lanes
     for (int seg = 0; run.left > 0; ++seg) {
         const int set = sets == 2 ? seg & 1 : 0, turn = sets == 2 ? seg >> 1 : seg;
-        const bool go = turn == 0 || tc_wait(smem_u32(&sh.q_empty[set]), (turn - 1) & 1, &sh.fail, polls);
-        if (!__all_sync(0xffffffffu, go)) return;
+        const bool go = fine && (turn == 0 || tc_wait(smem_u32(&sh.q_empty[set]), (turn - 1) & 1, &sh.fail, a.polls));
+        fine = __all_sync(0xffffffffu, go);
         const AttnCursor& cur = run.cur;
+        if (!fine) {
+            if (lane == 0 && cur.tile == 0 && cur.s == 0 && a.row_status) a.row_status[cur.b] = KV_TIMEOUT;
+            run.skip(a, run.part());
+            continue;
+        }
         const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
         const uint32_t dst = smem_u32(sh.q) + set * q_rows * S::DP * 2;
         const int c = lane % kPieces;
@@ -142,12 +148,13 @@ __device__ void mass_query_role(const MassArgs& a, MassShared<S>& sh, MassRun ru
 
 // Boxes: a tile a warp in turn, as tc_box_role brings them.
 template <typename S>
-__device__ void mass_box_role(const MassArgs& a, const TcMaps& maps, MassShared<S>& sh, MassRun run, uint32_t polls,
-                              int warp, int lane) {
+__device__ void mass_box_role(const MassArgs& a, const TcMaps& maps, MassShared<S>& sh, MassRun run, int warp,
+                              int lane) {
     const KvView& kv = a.kv;
     const int panels = maps.flat ? 1 : S::kPanels, part = lane / panels, panel = lane % panels, rows = maps.rows;
     const bool mine = part * rows < S::KT;
     const int first_block = a.skip / kv.block_size(), n = run.left;
+    const int withhold = blockIdx.x == 0 ? a.withhold : -1;
     int last = -1;
     for (int j = 0; j < n; ++j, run.cur.next(a, S::KT)) {
         if (j % S::kBoxWarps != warp) continue;
@@ -159,8 +166,8 @@ __device__ void mass_box_role(const MassArgs& a, const TcMaps& maps, MassShared<
         const bool valid = kv.valid(blk);
         const int row = valid ? t - lb * kv.block_size() : 0;
         const int slot = j % S::kSlots;
-        const bool go = j < S::kSlots || tc_wait(smem_u32(&sh.empty[slot]), (j / S::kSlots - 1) & 1, &sh.fail, polls);
-        if (!__all_sync(0xffffffffu, go)) break;
+        const bool go = j < S::kSlots || tc_wait(smem_u32(&sh.empty[slot]), (j / S::kSlots - 1) & 1, &sh.fail, a.polls);
+        if (!__all_sync(0xffffffffu, go) || j == withhold) break;
         const uint32_t bar = smem_u32(&sh.full[slot]);
         if (lane == 0) mbar_arrive_expect_tx(bar, S::kSlot);
         __syncwarp();
@@ -184,13 +191,14 @@ __device__ void mass_box_role(const MassArgs& a, const TcMaps& maps, MassShared<
 
 // 16-byte copies by four warps; a tile is told when those of two tiles on are under way.
 template <typename S>
-__device__ void mass_copy_role(const MassArgs& a, MassShared<S>& sh, MassRun run, uint32_t polls, int p) {
+__device__ void mass_copy_role(const MassArgs& a, MassShared<S>& sh, MassRun run, int p) {
     constexpr int kPieces = S::DP / 8, kStep = 128 / kPieces, kOwn = 32 / kPieces, kBehind = 2;
     const KvView& kv = a.kv;
     const int lane = p & 31, warp = p >> 5, c = p % kPieces, r0 = p / kPieces;
     const int mine = (lane / kOwn) * kStep + warp * kOwn + lane % kOwn;  // the row whose place this lane finds
     const bool col = c * 8 < kv.dim;
     const int first_block = a.skip / kv.block_size(), n = run.left;
+    const int withhold = blockIdx.x == 0 ? a.withhold : -1;
     auto tell = [&](int j) {
         fence_proxy_async_smem();
         mbar_arrive(smem_u32(&sh.full[j % S::kSlots]));
@@ -206,8 +214,8 @@ __device__ void mass_copy_role(const MassArgs& a, MassShared<S>& sh, MassRun run
             if (kv.valid(blk)) at = kv.at(blk, cur.s, t - lb * kv.block_size());
         }
         const int slot = j % S::kSlots;
-        const bool go = j < S::kSlots || tc_wait(smem_u32(&sh.empty[slot]), (j / S::kSlots - 1) & 1, &sh.fail, polls);
-        if (!__all_sync(0xffffffffu, go)) break;
+        const bool go = j < S::kSlots || tc_wait(smem_u32(&sh.empty[slot]), (j / S::kSlots - 1) & 1, &sh.fail, a.polls);
+        if (!__all_sync(0xffffffffu, go) || j == withhold) break;
         const uint32_t dst = smem_u32(sh.slot[slot]);
 #pragma unroll
         for (int i = 0; i < S::KT / kStep; ++i) {
@@ -229,14 +237,13 @@ __device__ void mass_copy_role(const MassArgs& a, MassShared<S>& sh, MassRun run
 
 // Products: 128 positions by the queries, one warp.
 template <typename S>
-__device__ void mass_mma_role(const MassArgs& a, MassShared<S>& sh, const TcLayout& lay, MassRun run, int sets,
-                              uint32_t polls) {
+__device__ void mass_mma_role(const MassArgs& a, MassShared<S>& sh, const TcLayout& lay, MassRun run, int sets) {
     const int m_rows = a.rows * static_cast<int>(a.group.d), q_rows = S::kRows / sets;
     const uint32_t idesc = tc_idesc((m_rows + 15) / 16 * 16, false);
     const uint32_t tm = __shfl_sync(0xffffffffu, sh.tmem, 0);
     bool fine = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        fine = __all_sync(0xffffffffu, fine && tc_wait(smem_u32(bar), parity, &sh.fail, polls));
+        fine = __all_sync(0xffffffffu, fine && tc_wait(smem_u32(bar), parity, &sh.fail, a.polls));
     };
     int j = 0;
     for (int seg = 0; fine && run.left > 0; ++seg) {
@@ -298,7 +305,7 @@ __device__ __forceinline__ f2 mass_weights(const uint32_t (&s)[32], const float*
 
 // Weights, of every second tile: four warps, a thread a position.
 template <typename S>
-__device__ void mass_weight_role(const MassArgs& a, MassShared<S>& sh, MassRun run, int sets, uint32_t polls, int x, int row) {
+__device__ void mass_weight_role(const MassArgs& a, MassShared<S>& sh, MassRun run, int sets, int x, int row) {
     const KvView& kv = a.kv;
     const int lane = row & 31, m_rows = a.rows * static_cast<int>(a.group.d), q_rows = S::kRows / sets;
     const uint32_t ts = sh.tmem + x * 256 + (static_cast<uint32_t>(row & ~31) << 16);
@@ -308,7 +315,7 @@ __device__ void mass_weight_role(const MassArgs& a, MassShared<S>& sh, MassRun r
     for (int seg = 0; run.left > 0; ++seg) {
         const int set = sets == 2 ? seg & 1 : 0, turn = sets == 2 ? seg >> 1 : seg, nt = run.part();
         const AttnCursor cur = run.cur;
-        fine = fine && tc_wait(smem_u32(&sh.q_full[set]), turn & 1, &sh.fail, polls);
+        fine = fine && tc_wait(smem_u32(&sh.q_full[set]), turn & 1, &sh.fail, a.polls);
         fine = __all_sync(0xffffffffu, fine);
         const int status = sh.status[set];
         const float* lse = sh.lse + set * q_rows;
@@ -320,7 +327,7 @@ __device__ void mass_weight_role(const MassArgs& a, MassShared<S>& sh, MassRun r
             const int t0 = (cur.tile + t) * S::KT + a.skip, pos = t0 + row;
             const bool writes = cur.len > 0 && status == 0 && pos >= a.first && pos < len;
             const float before = writes && a.mass && pos < base ? a.mass[line0 + pos] : 0.0f;
-            fine = __all_sync(0xffffffffu, tc_wait(smem_u32(&sh.s_full[x]), (j >> 1) & 1, &sh.fail, polls));
+            fine = __all_sync(0xffffffffu, tc_wait(smem_u32(&sh.s_full[x]), (j >> 1) & 1, &sh.fail, a.polls));
             if (!fine) continue;
             tc_after_sync();
             const bool edge = t0 + S::KT > base;
@@ -375,7 +382,6 @@ attention_mass_tc_kernel(const MassArgs a, const __grid_constant__ TcMaps maps) 
     run.left = cut.n;
     if (cut.n == 0) return;
     const int sets = a.rows * static_cast<int>(a.group.d) <= S::kRows / 2 ? 2 : 1;
-    constexpr uint32_t polls = 1u << 30;
     if (tid == 0) {
         for (int i = 0; i < S::kSlots; ++i) {
             mbar_init(smem_u32(&sh.full[i]), S::TMA ? 1 : 128);
@@ -398,15 +404,15 @@ attention_mass_tc_kernel(const MassArgs a, const __grid_constant__ TcMaps maps) 
     tc_after_sync();
     const int b0 = run.cur.b;
     if (warp < 8)
-        mass_weight_role<S>(a, sh, run, sets, polls, warp >> 2, tid & 127);
+        mass_weight_role<S>(a, sh, run, sets, warp >> 2, tid & 127);
     else if (warp == 8)
-        mass_mma_role<S>(a, sh, tc_layout<S>(maps), run, sets, polls);
+        mass_mma_role<S>(a, sh, tc_layout<S>(maps), run, sets);
     else if (warp == 9)
-        mass_query_role<S>(a, sh, run, sets, polls, lane);
+        mass_query_role<S>(a, sh, run, sets, lane);
     else if constexpr (S::TMA) {
-        if (warp < 10 + S::kBoxWarps) mass_box_role<S>(a, maps, sh, run, polls, warp - 10, lane);
+        if (warp < 10 + S::kBoxWarps) mass_box_role<S>(a, maps, sh, run, warp - 10, lane);
     } else {
-        mass_copy_role<S>(a, sh, run, polls, tid - 320);
+        mass_copy_role<S>(a, sh, run, tid - 320);
     }
     __syncwarp();
     tc_before_sync();

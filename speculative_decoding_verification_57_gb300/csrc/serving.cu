@@ -68,13 +68,16 @@ cudaError_t launch_mass_tc(const MassArgs& a, int sms, cudaStream_t stream) {
 // bf16, head_dim up to 128 and up to 256 queries a kv head go to the tcgen05
 // kernel (64 single rows of 32/8 heads of 128 over 1000..2000 positions 40 us, on
 // the other 48; trees of 17 rows over 2048..4096 78 and 276).
+bool mass_tc(specv_dtype dt, const MassArgs& a) {
+    return dt == SPECV_BF16 && a.kv.dim <= 128 && a.rows * static_cast<int>(a.group.d) <= 256;
+}
+
+cudaError_t launch_mass_tc(const MassArgs& a, int sms, cudaStream_t stream) {
+    return a.kv.dim <= 64 ? launch_mass_tc<64>(a, sms, stream) : launch_mass_tc<128>(a, sms, stream);
+}
+
 template <typename T>
 cudaError_t launch_mass(const MassArgs& a, int sms, cudaStream_t stream) {
-    if constexpr (sizeof(T) == 2) {
-        const bool few = a.rows * static_cast<int>(a.group.d) <= 256;
-        if (few && a.kv.dim <= 64) return launch_mass_tc<64>(a, sms, stream);
-        if (few && a.kv.dim <= 128) return launch_mass_tc<128>(a, sms, stream);
-    }
     if (a.kv.dim <= 64) return launch_mass<T, 64>(a, sms, stream);
     if (a.kv.dim <= 128) return launch_mass<T, 128>(a, sms, stream);
     return launch_mass<T, 256>(a, sms, stream);
@@ -195,11 +198,20 @@ specv_status specv_attention_mass(specv_handle h, const specv_kv_cache* cache, c
     a.first = first;
     a.skip = first / cache->block_size * cache->block_size;
     a.scale = scale;
+    a.withhold = -1;
+    a.polls = 1u << 30;
+    const bool tc = mass_tc(cache->dtype, a);
+    if (tc && h->test_withhold >= 0) {  // the test hook arms one launch
+        a.withhold = h->test_withhold;
+        a.polls = h->test_polls;
+        h->test_withhold = -1;
+    }
     DeviceGuard g(h->device);
     if (!g.ok) return cuda_fail(cudaErrorInvalidDevice, "cudaSetDevice");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = cache->dtype == SPECV_BF16 ? launch_mass<__nv_bfloat16>(a, h->sm_count, s)
-                                                     : launch_mass<float>(a, h->sm_count, s);
+    const cudaError_t e = tc                           ? launch_mass_tc(a, h->sm_count, s)
+                          : cache->dtype == SPECV_BF16 ? launch_mass<__nv_bfloat16>(a, h->sm_count, s)
+                                                       : launch_mass<float>(a, h->sm_count, s);
     if (e != cudaSuccess) return cuda_fail(e, "attention_mass launch");
     h->launches.fetch_add(1, std::memory_order_relaxed);
     return SPECV_OK;

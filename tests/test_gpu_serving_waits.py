@@ -1,0 +1,48 @@
+"""The bounded waits of the gathered weight's tcgen05 kernel: a copy that never
+arrives is told for every sequence that its CTA's run touches, and for no
+other, whatever the status held before."""
+import numpy as np
+import pytest
+
+from test_gpu_cache import Case, _dev, sv  # noqa: F401  (sv is a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("bs", [16, 5])  # boxes, and 16-byte copies
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("rows,hq", [(3, 8), (32, 16)])  # two sets of queries, and one
+def test_a_missing_copy_of_the_gathered_weight_is_told(sv, bs, dim, rows, hq):  # noqa: F811
+    """400 sequences of a tile for each of two kv heads: the run of CTA 0 holds some of
+    them from their start, and most of these come behind the wait that runs out."""
+    import torch
+
+    handle = sv.specv_create(0, max_batch=512, max_k=31, vocab=1000)
+    B = 400
+    c = Case(rows + dim + bs, "bf16", B, rows, hq, 2, dim, bs, [40 + i % 80 for i in range(B)], "tree", poison=False)
+    lse = c.call(sv, handle)["lse"]
+    args = (c.q_t, c.kc_t, c.vc_t, _dev(c.tables), _dev(c.lens), lse)
+
+    def call():
+        out = {"mass": torch.full((B, 2, c.tables.shape[1] * bs), -7.0, device="cuda"),
+               "row_status": torch.full((B,), -1, dtype=torch.int32, device="cuda")}
+        got = sv.specv_attention_mass(handle, *args, parents=_dev(c.parents), out=out)
+        torch.cuda.synchronize()
+        return got["mass"], got["row_status"].cpu().numpy()
+
+    want, status = call()
+    assert not status.any()
+    for use in (0, 1, 2, 4):
+        sv.specv_test_withhold_stage(handle, use, 2000)
+        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        start.record()
+        mass, status = call()
+        end.record()
+        end.synchronize()
+        n = int(np.count_nonzero(status))  # one run: the first sequences
+        assert 3 <= n < 20 and (status[:n] == sv.ST_TIMEOUT).all() and not status[n:].any(), (use, status[:20])
+        assert torch.equal(mass[n:], want[n:]), use
+        assert start.elapsed_time(end) < 150, use  # no role waits for what is over (2000 polls take less than 10 ms)
+        mass, status = call()
+        assert not status.any() and torch.equal(mass, want), use
+    sv.specv_destroy(handle)

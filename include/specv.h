@@ -525,7 +525,8 @@ int specv_plan_cluster(specv_handle h, specv_dtype logits_dtype, int batch, int 
 /* Test hook, off unless called: arms the next launch of the split-vocabulary
  * kernel (V > 2048), of the tcgen05 tree-attention kernel (bf16, head_dim up
  * to 128, more than 16 rows a kv head; of a shared prefix, more than 16 of the
- * batch: its own launch) or of the tcgen05 kernel of specv_attention_mass (bf16,
+ * batch: its own launch, or by numbers from 2^20 on, which then stand for 0 on,
+ * the sequences') or of the tcgen05 kernel of specv_attention_mass (bf16,
  * head_dim up to 128, up to 256 rows a kv head) on this handle so that CTA 0 of the
  * grid never issues the bulk copy of its pass-1 stage use (the copies of its
  * slot use, or tile) number `stage_use` (counted from 0

@@ -727,8 +727,8 @@ def specv_plan_cluster(h: Handle, logits_dtype, B, k, V) -> int:
 
 
 def specv_test_withhold_stage(h: Handle, stage_use: int, polls: int) -> None:
-    """Test hook: the next split-vocabulary (or tcgen05 tree-attention) launch
-    on ``h`` never fills stage use ``stage_use`` of CTA 0 and its waits give up after
+    """Test hook: the next split-vocabulary launch (or that of a tcgen05 kernel of
+    the cache calls) on ``h`` never fills stage use ``stage_use`` of CTA 0 and its waits give up after
     ``polls`` polls (see include/specv.h)."""
     _check(_lib.load().specv_test_withhold_stage(h.ptr, int(stage_use), int(polls)), "specv_test_withhold_stage")
 

@@ -7,6 +7,8 @@
 
 namespace {
 
+constexpr int kOwnUses = 1 << 20;  // of the test hook: uses of the sequences' launch are counted from here
+
 // The launches of a call: its kernels, and what each part needs of the workspace.
 struct PrefixPlan {
     const AttnPlan<PartArgs>*prefix, *own;
@@ -132,9 +134,11 @@ specv_status specv_prefix_attention(specv_handle h, const specv_kv_cache* cache,
         own.own_segs = all.own_segs = cache->kv_heads * p.own_tiles;
         own.prefix_segs = all.prefix_segs = cache->kv_heads * ((batch * rows * group + 127) / 128);
     }
-    if (p.prefix->tc && h->test_withhold >= 0) {  // the test hook arms one launch
-        all.withhold = h->test_withhold;
-        all.polls = h->test_polls;
+    // the test hook arms one launch: the prefix's, or by numbers from kOwnUses on the sequences'
+    PartArgs& armed = h->test_withhold < kOwnUses ? all : own;
+    if ((&armed == &all ? p.prefix : p.own)->tc && h->test_withhold >= 0) {
+        armed.withhold = h->test_withhold % kOwnUses;
+        armed.polls = h->test_polls;
         h->test_withhold = -1;
     }
     PrefixJoinArgs j = {};

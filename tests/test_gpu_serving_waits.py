@@ -1,10 +1,12 @@
-"""The bounded waits of the gathered weight's tcgen05 kernel: a copy that never
-arrives is told for every sequence that its CTA's run touches, and for no
-other, whatever the status held before."""
+"""The bounded waits of the tcgen05 kernels of gathered weight and of the
+sequences' part behind a shared prefix: a copy that never arrives is told for
+every sequence that its CTA's run touches, and for no other, whatever the
+status held before."""
 import numpy as np
 import pytest
 
 from test_gpu_cache import Case, _dev, sv  # noqa: F401  (sv is a fixture)
+from test_gpu_prefix import Shared
 
 pytestmark = pytest.mark.gpu
 
@@ -45,4 +47,44 @@ def test_a_missing_copy_of_the_gathered_weight_is_told(sv, bs, dim, rows, hq):  
         assert start.elapsed_time(end) < 150, use  # no role waits for what is over (2000 polls take less than 10 ms)
         mass, status = call()
         assert not status.any() and torch.equal(mass, want), use
+    sv.specv_destroy(handle)
+
+
+@pytest.mark.parametrize("bs", [16, 5])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("rows,hq,prefix", [(17, 8, 160), (17, 8, 12000), (32, 16, 160)])
+def test_a_missing_copy_of_the_sequences_part_is_told(sv, bs, dim, rows, hq, prefix):  # noqa: F811
+    """Sequences of two to four tiles for each of two kv heads behind a short prefix, and
+    beside a long one (two tiles a sequence and head, more of the prefix): those that CTA 0's run of the
+    sequences' launch touches are told, the others are the same bits."""
+    import torch
+
+    handle = sv.specv_create(0, max_batch=512, max_k=31, vocab=1000)
+    B = 40 if prefix > 1000 else 120
+    prefix = prefix // bs * bs
+    c = Shared(rows + dim + bs, "bf16", B, rows, hq, 2, dim, bs, prefix, [150 + 7 * (i % 40) for i in range(B)])
+
+    def call():
+        out = {"row_status": torch.full((B,), -1, dtype=torch.int32, device="cuda")}
+        got = c.call(sv, handle, out=out)
+        return got, got["row_status"].cpu().numpy()
+
+    want, status = call()
+    assert not status.any()
+    for use in (0, 1, 2, 3):
+        sv.specv_test_withhold_stage(handle, 2 ** 20 + use, 2000)
+        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        start.record()
+        got, status = call()
+        end.record()
+        end.synchronize()
+        n = int(np.count_nonzero(status))  # one run: the first sequences
+        assert 1 <= n < B // 2 and (status[:n] == sv.ST_TIMEOUT).all() and not status[n:].any(), (use, status)
+        for key in ("out", "lse"):
+            assert torch.equal(got[key][n:], want[key][n:]), use
+        assert start.elapsed_time(end) < 150, use
+        again, status = call()
+        assert not status.any(), use
+        for key in ("out", "lse"):
+            assert torch.equal(again[key], want[key]), use
     sv.specv_destroy(handle)

@@ -448,9 +448,10 @@ typedef struct {
 /* specv_cache_append for models that norm the heads of queries and keys
  * and for positions on several axes: in addition `norm` and `positions`,
  * both nullable (and then exactly that call).  Norms, turns and products are fp32
- * with one rounding at the end; the mean of squares is fp32 too: a head
- * with values beyond 2^63 has an infinite one and comes out as zeros.
- * Everything else as there. */
+ * with one rounding at the end; a head whose squares would leave fp32's range,
+ * or vanish in it, is scaled by a power of two first, so that heads of any
+ * finite values come out as the formula has them (one of zeros with eps 0 is
+ * no number).  Everything else as there. */
 specv_status specv_cache_append_norm(specv_handle h, const specv_kv_cache *cache, const void *q, int64_t q_stride,
                                      int q_heads, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                                      const specv_head_norm *norm, const float *inv_freq, int rot_dim, int interleaved,

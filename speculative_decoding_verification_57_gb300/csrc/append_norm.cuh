@@ -51,6 +51,16 @@ __device__ __forceinline__ float2 append_turn_at(double pos, float f) {
     return make_float2(c, s);
 }
 
+// Whether a mean of squares (and eps) lost nothing to fp32's range: squares below 2^-126 lose bits, of which this has 35
+// to spare, and a sum beyond the type is infinite.  Where not, the head is scaled by a power of two first.
+__device__ __forceinline__ bool append_mean_fits(float mean) { return mean >= 0x1p-90f && mean < INFINITY; }
+
+// The power of two that brings `top`, a head's largest magnitude or the root of eps, to 1..2 (ends of the type: near them).
+__device__ __forceinline__ float append_scale(float top) {
+    const uint32_t e = min(max(__float_as_uint(top) >> 23, 1u), 253u);
+    return __uint_as_float((254 - e) << 23);
+}
+
 // 16 bytes as floats, two at a time, and back.
 template <typename T>
 __device__ __forceinline__ void append_open(const KvVec<T>& x, f2 (&f)[KvType<T>::kVec / 2]) {
@@ -194,7 +204,22 @@ cache_append_norm_kernel(const __grid_constant__ AppendNormArgs n) {
             }
             for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
             __syncwarp();
-            const float inv = normed ? rsqrtf(fmaf(sum, n.inv_dim, n.eps)) : 1.0f;
+            float mean = fmaf(sum, n.inv_dim, n.eps);
+            if (normed && !append_mean_fits(mean)) {  // (the whole warp: it has the head)
+                float top = sqrtf(n.eps);
+                for (int d = lane; d < kv.dim; d += 32) top = fmaxf(top, fabsf(head[d]));
+                for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                const float s = append_scale(top);
+                sum = 0.0f;
+                for (int d = lane; d < kv.dim; d += 32) {
+                    head[d] *= s;
+                    sum = fmaf(head[d], head[d], sum);
+                }
+                for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                __syncwarp();
+                mean = fmaf(sum, n.inv_dim, n.eps * s * s);
+            }
+            const float inv = normed ? rsqrtf(mean) : 1.0f;
             const T* w = static_cast<const T*>(h < a.q_heads ? n.q_weight : n.k_weight);
             T* to = h < a.q_heads ? q_out + h * kv.dim
                     : h < turning ? k_out + (h - a.q_heads) * next
@@ -266,74 +291,117 @@ cache_append_norm_kernel(const __grid_constant__ AppendNormArgs n) {
                 }
             }
         };
+        // the warp's first head: those from `turning` on are values (told by a vote a head instead, trees took 10.7 us for
+        // 10.3, image prompts 40.3 for 39.2)
+        const int warp0 = __shfl_sync(0xffffffffu, h0, 0);
+        const bool norms = n.q_weight || n.k_weight;
         int kind = -1;  // whose they are: 0 queries', 1 keys'
+        auto has_norm = [&](int h) { return piece && (h < a.q_heads ? n.q_weight != nullptr : h < turning && n.k_weight); };
+        auto squares = [&](const f2 (&fx)[kTwos], const f2 (&fy)[kTwos]) {
+            f2 sum = pack2(0.0f, 0.0f);
+#pragma unroll
+            for (int e = 0; e < kTwos; ++e) sum = fma2(fx[e], fx[e], fma2(fy[e], fy[e], sum));
+            float lo, hi;
+            unpack2(sum, lo, hi);
+            return lo + hi;
+        };
+        // mean of a head's squares and eps, by its lanes
+        auto mean_of = [&](bool normed, const f2 (&fx)[kTwos], const f2 (&fy)[kTwos], float eps) {
+            float all = normed ? squares(fx, fy) : 0.0f;
+#pragma unroll
+            for (int step = 4; step >= 0; --step)
+                if (step < n.group_log) all += __shfl_xor_sync(0xffffffffu, all, 1 << step);
+            return fmaf(all, n.inv_dim, eps);
+        };
+        // a query's or key's pieces, normed and turned
+        auto turn = [&](int h, f2 (&fx)[kTwos], f2 (&fy)[kTwos], float inv, Vec& xo, Vec& yo) {
+            if (kind != (h < a.q_heads ? 0 : 1)) {
+                kind = h < a.q_heads ? 0 : 1;
+                coefficients(static_cast<const T*>(kind ? n.k_weight : n.q_weight));
+            }
+            const f2 inv2 = pack2(inv, inv);
+            if (!turns) {
+#pragma unroll
+                for (int e = 0; e < kTwos; ++e) {
+                    fx[e] = mul2(fx[e], mul2(inv2, cx[e]));
+                    fy[e] = mul2(fy[e], mul2(inv2, cy[e]));
+                }
+            } else {
+                if constexpr (MODE == kApart) {
+#pragma unroll
+                    for (int e = 0; e < kTwos; ++e) {
+                        const f2 v = fx[e], w = fy[e];
+                        fx[e] = sub2(mul2(v, cx[e]), mul2(w, sy[e]));
+                        fy[e] = fma2(v, sx[e], mul2(w, cy[e]));
+                    }
+                } else {
+                    append_neighbours<kTwos>(fx, cx, sx);
+                    if (both) append_neighbours<kTwos>(fy, cy, sy);
+                }
+#pragma unroll
+                for (int e = 0; e < kTwos; ++e) {
+                    fx[e] = mul2(fx[e], inv2);
+                    fy[e] = MODE == kApart || both ? mul2(fy[e], inv2) : mul2(fy[e], mul2(inv2, cy[e]));
+                }
+            }
+            append_close<T>(fx, xo);
+            append_close<T>(fy, yo);
+        };
+        auto store = [&](int h, const Vec& xo, const Vec& yo) {
+            T* to = h < a.q_heads ? q_out + h * kv.dim
+                    : h < turning ? k_out + (h - a.q_heads) * next
+                                  : v_out + (h - turning) * next;
+            *reinterpret_cast<Vec*>(to + (h < turning ? x0 : 2 * u * kVec)) = xo;
+            *reinterpret_cast<Vec*>(to + (h < turning ? y0 : 2 * u * kVec + kVec)) = yo;
+        };
         for (int h1 = 0; h1 < heads; h1 += kAppendHeads * hstep) {
             if (h1 > 0) load_all(h1);
 #pragma unroll
             for (int j = 0; j < kAppendHeads; ++j) {
                 const int h = h1 + h0 + j * hstep;
-                const bool mine = piece && h < heads;
-                const bool normed = mine && (h < a.q_heads ? n.q_weight != nullptr : h < turning && n.k_weight);
+                const bool mine = piece && h < heads, normed = has_norm(h);
                 f2 fx[kTwos], fy[kTwos];
                 float inv = 1.0f;
                 if (mine && h < turning) {
                     append_open<T>(x[j], fx);
                     append_open<T>(y[j], fy);
                 }
-                if (__any_sync(0xffffffffu, normed)) {
-                    float all = 0.0f;
-                    if (normed) {
-                        f2 sum = pack2(0.0f, 0.0f);
-#pragma unroll
-                        for (int e = 0; e < kTwos; ++e) sum = fma2(fx[e], fx[e], fma2(fy[e], fy[e], sum));
-                        float lo, hi;
-                        unpack2(sum, lo, hi);
-                        all = lo + hi;
-                    }
-#pragma unroll
-                    for (int step = 4; step >= 0; --step)
-                        if (step < n.group_log) all += __shfl_xor_sync(0xffffffffu, all, 1 << step);
-                    if (normed) inv = rsqrtf(fmaf(all, n.inv_dim, n.eps));
-                }
-                if (!mine) continue;
-                if (h < turning) {
-                    if (kind != (h < a.q_heads ? 0 : 1)) {
-                        kind = h < a.q_heads ? 0 : 1;
-                        coefficients(static_cast<const T*>(kind ? n.k_weight : n.q_weight));
-                    }
-                    const f2 inv2 = pack2(inv, inv);
-                    if (!turns) {
-#pragma unroll
-                        for (int e = 0; e < kTwos; ++e) {
-                            fx[e] = mul2(fx[e], mul2(inv2, cx[e]));
-                            fy[e] = mul2(fy[e], mul2(inv2, cy[e]));
-                        }
-                    } else {
-                        if constexpr (MODE == kApart) {
+                if (norms && h1 + warp0 + j * hstep < turning) {
+                    float mean = mean_of(normed, fx, fy, n.eps);
+                    const bool far = normed && !append_mean_fits(mean);
+                    if (__any_sync(0xffffffffu, far)) {  // once more, scaled
+                        float top = sqrtf(n.eps);
+                        if (normed) {
 #pragma unroll
                             for (int e = 0; e < kTwos; ++e) {
-                                const f2 v = fx[e], w = fy[e];
-                                fx[e] = sub2(mul2(v, cx[e]), mul2(w, sy[e]));
-                                fy[e] = fma2(v, sx[e], mul2(w, cy[e]));
+                                float p0, p1, r0, r1;
+                                unpack2(fx[e], p0, p1);
+                                unpack2(fy[e], r0, r1);
+                                top = fmaxf(fmaxf(fmaxf(top, fabsf(p0)), fmaxf(fabsf(p1), fabsf(r0))), fabsf(r1));
                             }
-                        } else {
-                            append_neighbours<kTwos>(fx, cx, sx);
-                            if (both) append_neighbours<kTwos>(fy, cy, sy);
                         }
+#pragma unroll 1
+                        for (int step = 0; step < n.group_log; ++step)
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1 << step));
+                        const float s = far ? append_scale(top) : 1.0f;
+                        float all = 0.0f;
+                        if (normed) {
 #pragma unroll
-                        for (int e = 0; e < kTwos; ++e) {
-                            fx[e] = mul2(fx[e], inv2);
-                            fy[e] = MODE == kApart || both ? mul2(fy[e], inv2) : mul2(fy[e], mul2(inv2, cy[e]));
+                            for (int e = 0; e < kTwos; ++e) {
+                                fx[e] = mul2(fx[e], pack2(s, s));
+                                fy[e] = mul2(fy[e], pack2(s, s));
+                            }
+                            all = squares(fx, fy);
                         }
+#pragma unroll 1
+                        for (int step = 0; step < n.group_log; ++step) all += __shfl_xor_sync(0xffffffffu, all, 1 << step);
+                        mean = fmaf(all, n.inv_dim, n.eps * s * s);
                     }
-                    append_close<T>(fx, x[j]);
-                    append_close<T>(fy, y[j]);
+                    if (normed) inv = rsqrtf(mean);
                 }
-                T* to = h < a.q_heads ? q_out + h * kv.dim
-                        : h < turning ? k_out + (h - a.q_heads) * next
-                                      : v_out + (h - turning) * next;
-                *reinterpret_cast<Vec*>(to + (h < turning ? x0 : 2 * u * kVec)) = x[j];
-                *reinterpret_cast<Vec*>(to + (h < turning ? y0 : 2 * u * kVec + kVec)) = y[j];
+                if (!mine) continue;
+                if (h < turning) turn(h, fx, fy, inv, x[j], y[j]);
+                store(h, x[j], y[j]);
             }
         }
     }

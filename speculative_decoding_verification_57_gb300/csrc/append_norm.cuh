@@ -102,6 +102,8 @@ __device__ __forceinline__ void append_neighbours(f2 (&f)[N], const f2 (&c)[N], 
 }
 
 // Threads of an SM: more registers each than a plain append's need (576: trees 14.0 us, prompts 45.2; 960: 12.4 and 43.9).
+// Tokens get the many threads of kAppendFew as long as the SMs hold all of them at once, three an SM (trees of 8 rows,
+// 32/8 heads of 128 in bf16: 456 tokens 6.95 us; 464 in two turns 10.2, with the threads of kAppendMany 8.4; 760 11.6 and 9.5).
 constexpr int kNormResident = 672;
 
 template <typename T, int MODE, int THREADS>

@@ -158,7 +158,7 @@ specv_status specv_cache_append_norm(specv_handle h, const specv_kv_cache* cache
     DeviceGuard g(h->device);
     if (!g.ok) return cuda_fail(cudaErrorInvalidDevice, "cudaSetDevice");
     const unsigned grid = static_cast<unsigned>(batch) * static_cast<unsigned>(rows);
-    const bool many = grid > static_cast<unsigned>(h->sm_count) * (kAppendResident / kAppendFew);
+    const bool many = grid > static_cast<unsigned>(h->sm_count) * (kNormResident / kAppendFew);
     // pieces of 16 bytes turn whole, apart or within, where rot_dim fills them
     const int mode = rot_dim % (interleaved ? vec : 2 * vec) ? kValues : interleaved && rot_dim ? kNeighbours : kApart;
     const NormKernel kernel = norm_kernel(cache->dtype, mode, many);

@@ -279,7 +279,9 @@ specv_status specv_rollback(specv_handle h, const int32_t *num_accepted, int bat
  * A sequence is refused, with its row_status saying why, if its length is
  * negative, below the rows of the pass (0 aside), above max_blocks *
  * block_size or above 2^31 - 513 (bit 2048), or if an entry of its table that the call needs is
- * outside [0, blocks) (bit 4096). */
+ * outside [0, blocks) (bit 4096).
+ * What a call writes is memory apart from what it reads, where its
+ * description does not say otherwise. */
 typedef struct {
     specv_dtype dtype;
     int kv_heads, head_dim, block_size, max_blocks;
@@ -507,7 +509,8 @@ specv_status specv_attention_mass(specv_handle h, const specv_kv_cache *cache, c
  *               that remain, at their places; memory apart from mass's.  Behind
  *               the new length it is left alone
  *   budget      1 or more, at least first + recent
- *   lens_out    [B] out: the new lengths; not cache->seq_lens' memory
+ *   lens_out    [B] out: the new lengths.  It, evicted and row_status are memory
+ *               apart from cache->seq_lens' and cache->block_tables'
  *   evicted     [B] out (nullable): old minus new length
  *   row_status  [B] out (nullable): 0, or bits 2048 (also a length above
  *               width), 4096 (an entry from position `first` on outside the

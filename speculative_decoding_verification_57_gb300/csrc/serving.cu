@@ -83,9 +83,10 @@ cudaError_t launch_mass(const MassArgs& a, int sms, cudaStream_t stream) {
     return launch_mass<T, 256>(a, sms, stream);
 }
 
-bool overlap(const void* p, const void* q, int64_t bytes) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q), n = static_cast<uintptr_t>(bytes);
-    return a < b + n && b < a + n;
+// Whether `m` bytes at p and `n` bytes at q have any in common.
+bool overlap(const void* p, int64_t m, const void* q, int64_t n) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a < b + static_cast<uintptr_t>(n) && b < a + static_cast<uintptr_t>(m);
 }
 
 }  // namespace
@@ -178,8 +179,8 @@ specv_status specv_attention_mass(specv_handle h, const specv_kv_cache* cache, c
         return SPECV_ERR_INVALID_ARGUMENT;
     if (batch == 0) return SPECV_OK;
     if (!rows_ok(cache, q, q_stride) || !lse || (width > 0 && !mass_out)) return SPECV_ERR_INVALID_ARGUMENT;
-    if (mass && mass != mass_out && overlap(mass, mass_out, static_cast<int64_t>(batch) * cache->kv_heads * width * 4))
-        return SPECV_ERR_INVALID_ARGUMENT;
+    const int64_t mass_bytes = static_cast<int64_t>(batch) * cache->kv_heads * width * 4;
+    if (mass && mass != mass_out && overlap(mass, mass_bytes, mass_out, mass_bytes)) return SPECV_ERR_INVALID_ARGUMENT;
     a.q = q;
     a.q_stride = q_stride;
     a.parents = rows > 1 ? parents : nullptr;
@@ -232,8 +233,15 @@ specv_status specv_cache_evict(specv_handle h, const specv_kv_cache* cache, int 
         return SPECV_ERR_INVALID_ARGUMENT;
     if (batch == 0) return SPECV_OK;
     const int64_t rows = static_cast<int64_t>(layers) * batch * cache->kv_heads;
-    if (!lens_out || lens_out == cache->seq_lens || rows > INT32_MAX / 16) return SPECV_ERR_INVALID_ARGUMENT;
-    if (width > 0 && (!mass || !mass_out || overlap(mass, mass_out, rows * width * 4))) return SPECV_ERR_INVALID_ARGUMENT;
+    if (!lens_out || rows > INT32_MAX / 16) return SPECV_ERR_INVALID_ARGUMENT;
+    // (every CTA of a sequence reads its length and its blocks, while one writes what the call tells of it)
+    const int64_t entries = static_cast<int64_t>(batch) * cache->max_blocks;
+    for (const int32_t* out : {lens_out, evicted, row_status})
+        if (out && (overlap(out, batch * 4ll, cache->seq_lens, batch * 4ll) ||
+                    overlap(out, batch * 4ll, cache->block_tables, entries * 4)))
+            return SPECV_ERR_INVALID_ARGUMENT;
+    if (width > 0 && (!mass || !mass_out || overlap(mass, rows * width * 4, mass_out, rows * width * 4)))
+        return SPECV_ERR_INVALID_ARGUMENT;
     e.mass = mass;
     e.mass_out = mass_out;
     e.lens_out = lens_out;

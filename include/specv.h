@@ -513,7 +513,7 @@ specv_status specv_attention_mass(specv_handle h, const specv_kv_cache *cache, c
  *               apart from cache->seq_lens' and cache->block_tables'
  *   evicted     [B] out (nullable): old minus new length
  *   row_status  [B] out (nullable): 0, or bits 2048 (also a length above
- *               width), 4096 (an entry from position `first` on outside the
+ *               width or 2^31 - 4096), 4096 (an entry from position `first` on outside the
  *               pool).  Of a refused sequence nothing moves, and its length stays
  * Sequences must not share blocks from position `first` on.  Blocks that are
  * no longer in use stay in the tables: specv_rollback with these lengths and

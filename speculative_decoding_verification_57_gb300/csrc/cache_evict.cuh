@@ -40,6 +40,7 @@ constexpr int kEvictAhead = 4;     // of a thread, in flight
 constexpr int kEvictItems = 8;    // masses of a thread, kEvictThreads positions apart
 constexpr int kEvictSpan = kEvictThreads * kEvictItems;
 constexpr int kEvictWarps = kEvictThreads / 32;
+constexpr int kEvictMost = INT32_MAX - 4095;  // positions of a sequence: a span behind them is still an int
 
 struct EvictArgs {
     KvView kv;
@@ -63,6 +64,8 @@ __device__ __forceinline__ uint32_t evict_key(float x) {
     const uint32_t b = __float_as_uint(x + 0.0f);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
+
+static_assert(kEvictSpan <= 4095 && kEvictMoves <= 4095 && 8 * kEvictThreads <= 4095, "counters of positions stay ints");
 
 struct EvictShared {
     uint32_t hist[kEvictWarps][256];
@@ -165,7 +168,7 @@ __global__ void __launch_bounds__(kEvictThreads, 4) cache_evict_kernel(const Evi
     const int h = static_cast<int>(row % kv.heads), b = static_cast<int>(row / kv.heads % e.batch);
     const int layer = static_cast<int>(row / kv.heads / e.batch);
     const int len = kv.lens[b];
-    int status = len < 0 || !kv.fits(len) || len > e.width ? KV_LENGTH : 0;
+    int status = len < 0 || !kv.fits(len) || len > kEvictMost || len > e.width ? KV_LENGTH : 0;
     const bool over = status == 0 && len > e.budget;
     const int32_t* table = kv.tables + static_cast<int64_t>(b) * kv.max_blocks;
     if (over) {

@@ -50,7 +50,7 @@ struct EvictArgs {
     int32_t* evicted;
     int32_t* row_status;
     int64_t layer_stride, width;
-    int layers, batch;
+    int batch;
     int budget, recent, first;
     int split;          // CTAs of a row: 1, or some for the columns of the keys and as many for those of the values
     int pieces;         // of 16 bytes a CTA moves of a row

@@ -130,7 +130,6 @@ specv_status specv_prefix_attention(specv_handle h, const specv_kv_cache* cache,
         own.lens = all.lens = cache->seq_lens;
         own.prefix_len = all.prefix_len = prefix_len;
         own.sequences = all.sequences = batch;
-        own.own_rows = all.own_rows = rows;
         own.own_segs = all.own_segs = cache->kv_heads * p.own_tiles;
         own.prefix_segs = all.prefix_segs = cache->kv_heads * ((batch * rows * group + 127) / 128);
     }

@@ -249,7 +249,6 @@ specv_status specv_cache_evict(specv_handle h, const specv_kv_cache* cache, int 
     e.row_status = row_status;
     e.layer_stride = layer_stride;
     e.width = width;
-    e.layers = layers;
     e.batch = batch;
     e.budget = budget;
     e.recent = recent;

@@ -75,7 +75,7 @@ struct PartArgs : AttnArgs {
     bool late;              // the second of the two parts: waits at its end for what the kernels before wrote
     // both parts at the same time (tcgen05 kernels): what each has to know of the other; `lens` NULL: one behind the other
     const int32_t *lens, *prefix_len;  // of the sequences, and the prefix's
-    int sequences, own_rows, own_segs;  // sequences, rows of the pass, segments of a sequence
+    int sequences, own_segs;            // sequences, and segments of a sequence
     int prefix_segs;                    // segments of 128 rows of the prefix
 };
 

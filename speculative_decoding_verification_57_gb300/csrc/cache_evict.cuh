@@ -17,14 +17,20 @@
 // The least kept mass is found by its bits, eight at a time, from the top, and
 // no further than it takes to tell the kept ones; moves are listed in position
 // order by ballots and a scan over the warps' counts.  A thread has the masses
-// of eight positions in registers, so that up to 2048 are read once.  Moves run in
-// order, 16 bytes a thread and row, all loads of a step before its stores: a
-// step's stores go to places that no later step reads, as sources of kept
-// positions lie above the line and the recent ones, behind them, move down.
+// of eight positions in registers.  Moves run in order, 16 bytes a thread and
+// row, all loads of a step before its stores: a step's stores go to places that
+// no later step reads, as sources of kept positions lie above the line and the
+// recent ones, behind them, move down.
+//
+// A list has 1024 moves; the next one is found where it ended.  Every list used to be
+// found among all positions, so that 131072 of them took 7.0 ms to 32768 (8 heads of
+// 128 of 8 sequences, one layer) and take 1.9, most of it the first look, of 64 spans,
+// at each row.  Masses of up to 2048 positions are read once for the choice, longer
+// rows' once for each digit and list, and both again where they are moved.
 //
 // Measured (GB300, graph replays over sets of inputs beyond the L2; 8 heads of 128
 // in bf16, budget 1024, 256 recent, up to twice as long before): 8 layers of 32
-// sequences 158 us, 92% of 6803 GB/s; one layer of 8 sequences 14.9 us, a chain
+// sequences 158 us, 92% of 6803 GB/s; one layer of 8 sequences 14.7 us, a chain
 // of length and blocks (2.8 us), the least mass (2.8), lists (2.9) and moves (6).
 // Four pieces a thread in flight (two: 176 us, eight: 221, which spills), four CTAs
 // an SM (five or six: 201 and 195), eight masses a thread (16, which spill: 212).
@@ -67,12 +73,19 @@ __device__ __forceinline__ uint32_t evict_key(float x) {
 
 static_assert(kEvictSpan <= 4095 && kEvictMoves <= 4095 && 8 * kEvictThreads <= 4095, "counters of positions stay ints");
 
+// The positions from `base` on: how many equal to the key, holes and kept ones above the line lie before.
+struct EvictCount {
+    int base;
+    uint32_t equal, holes, above;
+};
+
 struct EvictShared {
     uint32_t hist[kEvictWarps][256];
     uint32_t count[kEvictItems * kEvictWarps];  // of a span, by item and warp: in position order
     uint32_t warp_sum[kEvictWarps];
     uint32_t total;
     uint32_t key, more, equal;  // the digits found so far, how many of those equal to them are kept, and how many there are
+    EvictCount hole_at, above_at;  // where the lists of the next moves start
     int src[kEvictMoves], dst[kEvictMoves];
     int64_t from[kEvictMoves], to[kEvictMoves];
 };
@@ -210,10 +223,19 @@ __global__ void __launch_bounds__(kEvictThreads, 4) cache_evict_kernel(const Evi
     const int64_t column = static_cast<int64_t>(part >> 1) * e.pieces * 16;
     int fills = many > 0 ? INT32_MAX : 0;
     for (int round = 0;; round += kEvictMoves) {
-        // holes below the line and kept positions above it, by their ranks; both lists are as long
-        if (round < fills) {
-            uint32_t equal = 0, holes = 0, above = 0;
-            for (int base = 0; base < n; base += kEvictSpan) {
+        // holes below the line and kept positions above it, by their ranks; both lists are as long.  The first time all
+        // positions are looked at; then the holes from where the last list of them ended, and the others from there
+        const int stop = round + kEvictMoves;
+        for (int above_line = 0; round < fills && above_line < (round ? 2 : 1); ++above_line) {
+            EvictCount at = {};
+            if (round) at = above_line ? sh.above_at : sh.hole_at;
+            const int end = round && !above_line ? many : n;
+            while (at.base < end && (round == 0 || (above_line ? at.above : at.holes) < static_cast<uint32_t>(stop))) {
+                const int base = at.base;
+                if (tid == 0 && n > kEvictSpan) {  // (read behind the barriers below; a span has one list's moves at most)
+                    if (at.holes <= static_cast<uint32_t>(stop) && !above_line) sh.hole_at = at;
+                    if (at.above <= static_cast<uint32_t>(stop) && (above_line || round == 0)) sh.above_at = at;
+                }
                 if (n > kEvictSpan) evict_load(mass + e.first, n, base, k);
                 uint32_t kept = 0, move = 0;  // of the thread's items
                 if (ties > 0) {  // equal ones by their order
@@ -232,10 +254,10 @@ __global__ void __launch_bounds__(kEvictThreads, 4) cache_evict_kernel(const Evi
                     for (int j = 0; j < kEvictItems; ++j) {
                         if (base + j * kEvictThreads >= n) break;
                         const uint32_t all = __ballot_sync(0xffffffffu, kept >> j & 1);
-                        const uint32_t rank = equal + sh.count[j * kEvictWarps + warp] + __popc(all & ((1u << lane) - 1));
+                        const uint32_t rank = at.equal + sh.count[j * kEvictWarps + warp] + __popc(all & ((1u << lane) - 1));
                         if (rank >= ties) kept &= ~(1u << j);
                     }
-                    equal += sh.total;
+                    at.equal += sh.total;
                     __syncthreads();
                 }
 #pragma unroll
@@ -259,18 +281,19 @@ __global__ void __launch_bounds__(kEvictThreads, 4) cache_evict_kernel(const Evi
                     const int i = base + j * kEvictThreads + tid;
                     const bool moves = move >> j & 1;
                     const uint32_t all = __ballot_sync(0xffffffffu, moves), low = __ballot_sync(0xffffffffu, moves && i < many);
-                    const uint32_t at = sh.count[j * kEvictWarps + warp], before = (1u << lane) - 1;
+                    const uint32_t count = sh.count[j * kEvictWarps + warp], before = (1u << lane) - 1;
                     if (!moves) continue;
-                    const uint32_t x = (i < many ? holes + (at & 0xffff) + __popc(low & before)
-                                                 : above + (at >> 16) + __popc(all & ~low & before)) -
+                    const uint32_t x = (i < many ? at.holes + (count & 0xffff) + __popc(low & before)
+                                                 : at.above + (count >> 16) + __popc(all & ~low & before)) -
                                        static_cast<uint32_t>(round);
                     if (x < kEvictMoves) (i < many ? sh.dst : sh.src)[x] = e.first + i;
                 }
-                holes += sh.total & 0xffff;
-                above += sh.total >> 16;
+                at.holes += sh.total & 0xffff;
+                at.above += sh.total >> 16;
+                at.base += kEvictSpan;
                 __syncthreads();
             }
-            fills = static_cast<int>(above);
+            if (round == 0) fills = static_cast<int>(at.above);
         }
         const int total = fills + e.recent;
         for (int x = tid; x < kEvictMoves && round + x < total; x += kEvictThreads) {

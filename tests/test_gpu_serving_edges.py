@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 import serving_plain as S
-from test_gpu_cache import BF16_HALF, F32_HALF, _dtype, _np, h, sv  # noqa: F401
+from test_gpu_cache import BF16_HALF, F32_HALF, _dev, _dtype, _np, _rounded, _tables, h, sv  # noqa: F401
 from test_gpu_serving import _norm_call
 
 pytestmark = pytest.mark.gpu
@@ -33,3 +33,39 @@ def test_append_norm_where_threads_change(sv, h, dtype, a_sm, past, trees):  # n
     np.testing.assert_array_equal(_np(vc_t), ref_v)
     assert (np.abs(_np(kc_t) - ref_k) <= S.append_norm_bound(ref_k, k_mag, 64, half)).all()
     assert (np.abs(_np(got["q_out"]) - q_out) <= S.append_norm_bound(q_out, q_mag, 64, half)).all()
+
+
+@pytest.mark.parametrize("masses", ["spread", "ties", "late", "early"])
+@pytest.mark.parametrize("n,budget,recent,first", [(70000, 30000, 100, 4), (131072, 20480, 3000, 0), (40000, 39000, 1, 64),
+                                                   (5000, 2300, 200, 7)])
+def test_eviction_with_many_lists_of_moves(sv, h, n, budget, recent, first, masses):  # noqa: F811
+    """Lists of 1024 moves, each found where the last one ended: holes and kept positions spread, all of
+    them together at the ends, and ties that a list's end cuts."""
+    import torch
+
+    rng = np.random.default_rng(n)
+    lens = np.array([n, n - 300], np.int32)
+    tables, blocks = _tables(rng, lens, 64)
+    pools = [_rounded(rng, (1, blocks, 2, 64, 16), torch.bfloat16) for _ in range(2)]
+    m = rng.exponential(size=(1, 2, 2, n)).astype(np.float32)
+    if masses == "ties":
+        m = np.floor(m * 3)
+    if masses == "late":
+        m = np.sort(m, -1)
+    if masses == "early":
+        m = -np.sort(-m, -1)
+        m[0, 0, 0, ::5] = 0
+    ref = [p[1].copy() for p in pools]
+    places, new, status = S.evict(*ref, tables, lens, m, budget, recent, first)
+    got = sv.specv_cache_evict(h, pools[0][0][0], pools[1][0][0], _dev(tables), _dev(lens), _dev(m[0]), budget, recent=recent,
+                               first=first)
+    torch.cuda.synchronize()
+    assert got["row_status"].tolist() == [0, 0] and got["seq_lens"].tolist() == new.tolist()
+    for p, r in zip(pools, ref):
+        np.testing.assert_array_equal(_np(p[0]), r)
+    g = got["mass"].cpu().numpy()
+    for b in range(2):
+        for hh in range(2):
+            place = places[0][b][hh]
+            np.testing.assert_array_equal(g[b, hh, :len(place) if place is not None else lens[b]],
+                                          m[0, b, hh, place] if place is not None else m[0, b, hh, :lens[b]])

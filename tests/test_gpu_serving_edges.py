@@ -3,9 +3,11 @@ another number of threads, takes over."""
 import numpy as np
 import pytest
 
+import cache_plain as P
 import serving_plain as S
 from test_gpu_cache import BF16_HALF, F32_HALF, _dev, _dtype, _np, _rounded, _tables, h, sv  # noqa: F401
-from test_gpu_serving import _norm_call
+from test_gpu_prefix import Shared, _exact_rows
+from test_gpu_serving import _mass_case, _mass_check, _norm_call
 
 pytestmark = pytest.mark.gpu
 
@@ -69,3 +71,35 @@ def test_eviction_with_many_lists_of_moves(sv, h, n, budget, recent, first, mass
             place = places[0][b][hh]
             np.testing.assert_array_equal(g[b, hh, :len(place) if place is not None else lens[b]],
                                           m[0, b, hh, place] if place is not None else m[0, b, hh, :lens[b]])
+
+
+@pytest.mark.parametrize("dim", [64, 128, 112])
+@pytest.mark.parametrize("B,rows,hq", [
+    (16, 1, 1), (17, 1, 1),    # a kv head's rows of the batch on mma.sync, and on tcgen05
+    (32, 4, 1), (43, 3, 1),    # one row tile, and two side by side
+    (32, 32, 1), (41, 25, 1),  # eight row tiles side by side, and tiles of 256
+])
+def test_prefix_attention_where_kernels_change(sv, h, B, rows, hq, dim):  # noqa: F811
+    c = Shared(B + rows + dim, "bf16", B, rows, hq, 1, dim, 16, 4096, [rows + (37 * i) % 200 for i in range(B)])
+    got = c.call(sv, h)
+    out, lse, avg, mag = _exact_rows(c)
+    assert not got["row_status"].any()
+    t_out, t_lse = P.attention_bounds(out, lse, avg, mag, int(c.lens.max()), dim, True)
+    assert (np.abs(_np(got["out"]) - out) <= t_out).all()
+    assert (np.abs(_np(got["lse"]) - lse) <= t_lse).all()
+    again = c.call(sv, h)
+    assert (got["out"] == again["out"]).all() and (got["lse"] == again["lse"]).all()
+
+
+@pytest.mark.parametrize("dtype,dim", [("bf16", 64), ("bf16", 128), ("bf16", 144), ("f32", 64)])
+@pytest.mark.parametrize("rows,group", [(8, 1), (9, 1), (32, 1), (11, 3), (16, 5), (27, 3), (32, 4), (3, 43), (32, 8), (1, 257)])
+def test_mass_where_kernels_change(sv, h, dtype, dim, rows, group):  # noqa: F811
+    """Queries of a kv head on both sides of a tile of eight, of four and ten tiles, of two sets of
+    queries and of tcgen05's one."""
+    import torch
+
+    c = _mass_case(rows + group, dtype, (2, rows, 2 * group, 2, dim, 16, [rows + 150, rows], "tree", 5))
+    got = sv.specv_attention_mass(h, c.q_t, c.kc_t, c.vc_t, _dev(c.tables), _dev(c.lens), _dev(c.lse), first=5,
+                                  parents=None if c.parents is None else _dev(c.parents))
+    torch.cuda.synchronize()
+    _mass_check(c, got, None, 5, c.lse, 0.0)

@@ -20,7 +20,9 @@ PrefixPlan prefix_plan(const specv_ctx* h, specv_dtype dt, int heads, int dim, i
     PrefixPlan p;
     const int own = rows * group, all = batch * own;
     // Row tiles of 128 up to eight a kv head, side by side over the same positions, so that they read them from the L2 at
-    // about the same time; more rows take tiles of 256, which read the positions half as often
+    // about the same time; more rows take tiles of 256, which read the positions half as often (32/8 heads of 128 behind 65536
+    // positions, side by side and in tiles of 256: 384 rows 109 and 132 us, 896 207 and 229, 1024 224 and 230, 1152 254 and
+    // 267, 1280 263 and 252, 2048 419 and 399; behind 8192, 1024 rows 67 and 69, 1280 65 and 66, 2048 94 and 90)
     const int side = (all + 127) / 128;
     p.prefix = &attn_plan<PartArgs>(dt, dim, all);
     p.side = 1;
@@ -29,6 +31,9 @@ PrefixPlan prefix_plan(const specv_ctx* h, specv_dtype dt, int heads, int dim, i
         p.side = side;
     }
     p.own = &attn_plan<PartArgs>(dt, dim, own);
+    // ... and beside them the sequences' part goes the same way (16 chains of 6 rows behind 65536 positions 105 us; on twelve
+    // warps 110, behind 16384 52 and 57; beside tiles of 256 twelve are as good: 64 chains behind 16384 128 and 126)
+    if (p.side > 1 && p.own->tc && own <= 128) p.own = &side_plan(dim);
     p.prefix_ctas = h->sm_count * p.prefix->ctas;
     p.own_ctas = h->sm_count * p.own->ctas;
     p.prefix_tiles = (all + p.prefix->tm - 1) / p.prefix->tm;

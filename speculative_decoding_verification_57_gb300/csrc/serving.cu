@@ -37,7 +37,10 @@ cudaError_t launch_mass_of(const MassArgs& a, int sms, cudaStream_t stream) {
                         a);
 }
 
-// Tens of tiles of eight queries, in turns, or the fewest that hold a kv head's.
+// Ten tiles of eight queries at a time, in turns, or the fewest of one, four and ten that hold a kv head's: what a tile costs is
+// formed for all of them.  In one, four and ten tiles, us: fp32, 32 sequences over 1000..2000 positions, 32/8 heads of 128,
+// 8 queries a kv head 63, 146, 273, 32 queries 160 in four and 302 in ten, 68 queries 403 and 301; bf16, 64 sequences, 16/4
+// heads of 256, 8 queries 48, 78, 97, 32 queries 83 and 102, 68 queries 202 and 119 (bytes alone: 28.6).
 template <typename T, int DP>
 cudaError_t launch_mass(const MassArgs& a, int sms, cudaStream_t stream) {
     if constexpr (sizeof(T) == 4 || DP > 128) {

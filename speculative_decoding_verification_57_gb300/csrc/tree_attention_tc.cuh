@@ -956,8 +956,10 @@ __device__ void tc_softmax_role(const A& a, TcShared<S>& sh, const TcLayout& lay
 // as fast as all: 64 trees of 17 rows over 500..1000 positions of their own take
 // 48 us on 76 SMs, 53 on 152); the prefix's CTAs have the other SMs at once,
 // and those of the sequences when these are through, which their shorter runs
-// take into account.  A tile of a sequence counts as one of the prefix's, a
-// segment's end as two, a start as five (measured, at heads of 128).
+// take into account.  A tile of a sequence counts as 7/4 of the prefix's on all
+// SMs, a segment's end as two tiles, a start as five (64 trees of 17 rows, 500..1000
+// of their own behind 8192 positions, at heads of 64: 145 us; 1 instead of 7/4 154,
+// 11/4 164; 1000..2000 behind 16384 252, 250 and 284).
 struct TcShare {
     int ctas;
     AttnLate late;

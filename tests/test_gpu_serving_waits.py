@@ -52,15 +52,14 @@ def test_a_missing_copy_of_the_gathered_weight_is_told(sv, bs, dim, rows, hq):  
 
 @pytest.mark.parametrize("bs", [16, 5])
 @pytest.mark.parametrize("dim", [64, 128])
-@pytest.mark.parametrize("rows,hq,prefix", [(17, 8, 160), (17, 8, 12000), (32, 16, 160)])
-def test_a_missing_copy_of_the_sequences_part_is_told(sv, bs, dim, rows, hq, prefix):  # noqa: F811
-    """Sequences of two to four tiles for each of two kv heads behind a short prefix, and
-    beside a long one (two tiles a sequence and head, more of the prefix): those that CTA 0's run of the
-    sequences' launch touches are told, the others are the same bits."""
+@pytest.mark.parametrize("rows,hq,prefix,B", [(17, 8, 160, 120), (17, 8, 12000, 40), (32, 16, 160, 120), (17, 8, 30000, 14)])
+def test_a_missing_copy_of_the_sequences_part_is_told(sv, bs, dim, rows, hq, prefix, B):  # noqa: F811
+    """Sequences of two to four tiles for each of two kv heads behind a short prefix,
+    beside a long one (two tiles a sequence and head, more of the prefix), and so few that they go the way of
+    row tiles side by side: those that CTA 0's run of the sequences' launch touches are told, the others are the same bits."""
     import torch
 
     handle = sv.specv_create(0, max_batch=512, max_k=31, vocab=1000)
-    B = 40 if prefix > 1000 else 120
     prefix = prefix // bs * bs
     c = Shared(rows + dim + bs, "bf16", B, rows, hq, 2, dim, bs, prefix, [150 + 7 * (i % 40) for i in range(B)])
 
@@ -71,7 +70,7 @@ def test_a_missing_copy_of_the_sequences_part_is_told(sv, bs, dim, rows, hq, pre
 
     want, status = call()
     assert not status.any()
-    for use in (0, 1, 2, 3):
+    for use in (0, 1, 2, 3) if B > 14 else (0, 1):  # (two tiles a run, or one)
         sv.specv_test_withhold_stage(handle, 2 ** 20 + use, 2000)
         start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
         start.record()

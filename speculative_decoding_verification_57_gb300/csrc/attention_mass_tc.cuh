@@ -53,6 +53,7 @@ struct MassShared {
     uint64_t full[S::kSlots], empty[S::kSlots], q_full[2], q_empty[2], s_full[2], s_empty[2], end;
     int status[2];  // of a set's sequence
     int to[2][32];  // places of its pass's rows behind the kept ones
+    int issued[S::kSlots];  // the last tile whose box was asked for
     uint32_t tmem;
     int fail;
 };
@@ -146,7 +147,8 @@ __device__ void mass_query_role(const MassArgs& a, MassShared<S>& sh, MassRun ru
     }
 }
 
-// Boxes: a tile a warp in turn, as tc_box_role brings them.
+// Boxes: a tile a warp in turn, as tc_box_role brings them.  None is in flight when the CTA ends: the products waited for
+// every tile, or a wait ran out, and then mass_boxes_land does.
 template <typename S>
 __device__ void mass_box_role(const MassArgs& a, const TcMaps& maps, MassShared<S>& sh, MassRun run, int warp,
                               int lane) {
@@ -155,7 +157,6 @@ __device__ void mass_box_role(const MassArgs& a, const TcMaps& maps, MassShared<
     const bool mine = part * rows < S::KT;
     const int first_block = a.skip / kv.block_size(), n = run.left;
     const int withhold = blockIdx.x == 0 ? a.withhold : -1;
-    int last = -1;
     for (int j = 0; j < n; ++j, run.cur.next(a, S::KT)) {
         if (j % S::kBoxWarps != warp) continue;
         const AttnCursor& cur = run.cur;
@@ -169,7 +170,10 @@ __device__ void mass_box_role(const MassArgs& a, const TcMaps& maps, MassShared<
         const bool go = j < S::kSlots || tc_wait(smem_u32(&sh.empty[slot]), (j / S::kSlots - 1) & 1, &sh.fail, a.polls);
         if (!__all_sync(0xffffffffu, go) || j == withhold) break;
         const uint32_t bar = smem_u32(&sh.full[slot]);
-        if (lane == 0) mbar_arrive_expect_tx(bar, S::kSlot);
+        if (lane == 0) {
+            sh.issued[slot] = j;
+            mbar_arrive_expect_tx(bar, S::kSlot);
+        }
         __syncwarp();
         if (mine && maps.flat)
             tc_box2(smem_u32(sh.slot[slot]) + part * rows * 256, &maps.k, row >> 3,
@@ -177,16 +181,17 @@ __device__ void mass_box_role(const MassArgs& a, const TcMaps& maps, MassShared<
         else if (mine)
             tc_box(smem_u32(sh.slot[slot]) + panel * S::kPanel + part * rows * 128, &maps.k, panel * 64, row, cur.s,
                    valid ? blk : kv.blocks, bar);
-        last = j;
     }
-    // no box of this warp's is in flight when the CTA ends: each has landed, or its slot was used up since
-    const unsigned long long since = gtimer();
-    for (int j = last; j >= 0 && j > last - S::kSlots; j -= S::kBoxWarps) {
-        const uint32_t bar = smem_u32(&sh.full[j % S::kSlots]), used = smem_u32(&sh.empty[j % S::kSlots]);
-        const uint32_t phase = (j / S::kSlots) & 1;
-        while (!mbar_test_wait(used, phase) && !mbar_wait_bounded(bar, phase, 256) && gtimer() - since < kWaitNs) {
-        }
-    }
+}
+
+// Behind a wait that ran out, when every role is done: the last box of each slot has landed (what filled the slot before it was
+// used up).  Only then do the phases stand still: a warp that looked back at its own boxes while another filled a slot again, and
+// the products used that up, took the parities of both barriers for those of a box in flight and stood for its 200 ms, once in
+// some 50,000 calls.
+template <typename S>
+__device__ __forceinline__ void mass_boxes_land(MassShared<S>& sh, int tid) {
+    if (tid < S::kSlots && sh.issued[tid] >= 0)
+        mbar_wait_bounded(smem_u32(&sh.full[tid]), (sh.issued[tid] / S::kSlots) & 1, 1u << 30);
 }
 
 // 16-byte copies by four warps; a tile is told when those of two tiles on are under way.
@@ -386,6 +391,7 @@ attention_mass_tc_kernel(const MassArgs a, const __grid_constant__ TcMaps maps) 
         for (int i = 0; i < S::kSlots; ++i) {
             mbar_init(smem_u32(&sh.full[i]), S::TMA ? 1 : 128);
             mbar_init(smem_u32(&sh.empty[i]), 1);
+            sh.issued[i] = -1;
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(smem_u32(&sh.q_full[x]), 32);
@@ -419,6 +425,10 @@ attention_mass_tc_kernel(const MassArgs a, const __grid_constant__ TcMaps maps) 
     __syncthreads();
     tc_after_sync();
     if (warp == 8) tc_dealloc(sh.tmem, 512);
+    if (S::TMA && tc_failed(&sh.fail)) {
+        mass_boxes_land(sh, tid);
+        __syncthreads();
+    }
     // a wait that ran out, after all others are long done, is told for every sequence that the run touches
     if (tid == 0 && tc_failed(&sh.fail) && a.row_status) {
         for (int left = run.left; left > 0;) {

@@ -87,3 +87,33 @@ def test_a_missing_copy_of_the_sequences_part_is_told(sv, bs, dim, rows, hq, pre
         for key in ("out", "lse"):
             assert torch.equal(again[key], want[key]), use
     sv.specv_destroy(handle)
+
+
+@pytest.mark.parametrize("dim,rows", [(128, 17), (128, 1), (64, 17)])
+def test_no_call_of_the_gathered_weight_stands_still(sv, dim, rows):  # noqa: F811
+    """Many calls over several sets of inputs: none takes the time of a wait that runs out (200 ms; a hundred calls take
+    some 10), and all of them give the same bits."""
+    import torch
+
+    handle = sv.specv_create(0, max_batch=64, max_k=31, vocab=1000)
+    sets = []
+    for i in range(3):
+        c = Case(i, "bf16", 64, rows, 32, 8, dim, 16, [1500 + (977 * (i + j)) % 1500 for j in range(64)], "tree", poison=False)
+        q, kc, vc, tables, lens, par = c.q_t, c.kc_t, c.vc_t, _dev(c.tables), _dev(c.lens), _dev(c.parents)
+        lse = sv.specv_tree_attention(handle, q, kc, vc, tables, lens, parents=par, lse=True)["lse"]
+        out = {"mass": torch.zeros((64, 8, c.tables.shape[1] * 16), device="cuda"),
+               "row_status": torch.zeros(64, dtype=torch.int32, device="cuda")}
+        sets.append(((handle, q, kc, vc, tables, lens, lse), dict(parents=par, out=out)))
+    first = [sv.specv_attention_mass(*a, **kw)["mass"].clone() for a, kw in sets]
+    events = [torch.cuda.Event(enable_timing=True) for _ in range(151)]
+    events[0].record()
+    for e in events[1:]:
+        for i in range(100):
+            a, kw = sets[i % 3]
+            sv.specv_attention_mass(*a, **kw)
+        e.record()
+    torch.cuda.synchronize()
+    assert max(x.elapsed_time(y) for x, y in zip(events, events[1:])) < 100
+    for want, (_, kw) in zip(first, sets):
+        assert torch.equal(kw["out"]["mass"], want) and not kw["out"]["row_status"].any()
+    sv.specv_destroy(handle)

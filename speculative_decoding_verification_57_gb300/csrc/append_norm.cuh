@@ -4,7 +4,8 @@
 // turn by position * inv_freq as there, the position being that of the pair's
 // axis (positions[b, r, axis]) or, with one axis, base + depth(r) + offset[b].
 // Everything between the loads and the one rounding at the end is fp32 (the
-// angle float64).
+// angle float64); a head whose squares leave that type's range, or vanish in it,
+// is summed once more, scaled by a power of two.
 //
 // Layout, loads ahead of the length and the rest as in cache_append.cuh.  A
 // head belongs to a group of 1, 2, 4, .. 32 neighbouring lanes, the least that
@@ -16,15 +17,14 @@
 // eight products more than the turn.
 //
 // Measured (GB300, graph replays over sets of inputs beyond the L2; 32/8 heads of
-// 128 in bf16): one token for 8 sequences 3.6 us (2.5 without norms), 64 trees of 17
-// rows 10.7 us (8.0), 4 ragged prompts of up to 2048 tokens with images on three
-// axes 40.4 us, 55% of 6803 GB/s (four sets of inputs, which the L2 partly holds:
-// 37.5; with one axis 35.4, without norms 32.6, the plain append 27.8).  Bound by
-// instructions and the chain of loads together: 2.05 of 4 instructions a cycle with
-// 21 warps an SM.  No one part of it weighs: angles, shuffles, weights, stores and
-// the look at the blocks are 1 to 4 us each; 64 or 32 threads a token, one, two or
-// four heads a thread in flight and 480 to 960 threads an SM are all within 40.4 to
-// 52 us, 672 threads of 96 among the best for prompts and trees.
+// 128 in bf16): one token for 8 sequences 3.7 us (2.5 without norms), 64 trees of 17
+// rows 10.3 us (8.0), 4 ragged prompts of up to 2048 tokens with images on three
+// axes 39.7 us, 56% of 6803 GB/s (with one axis 37.5, without norms 35.4, with neither
+// 34.4, the plain append 29.9); fp32 57.4 us, 77%.  Bound by instructions and the chain
+// of loads together: 1.98 of 4 instructions a cycle with 21 warps an SM.  No one part
+// of it weighs: angles, shuffles, weights, stores and the look at the blocks are 1 to
+// 4 us each.  Part of the chain stands without need, left for another time: positions,
+// angles and weights depend on neither length nor block, and are asked for behind both.
 #pragma once
 #include "cache_append.cuh"
 
@@ -101,7 +101,8 @@ __device__ __forceinline__ void append_neighbours(f2 (&f)[N], const f2 (&c)[N], 
     }
 }
 
-// Threads of an SM: more registers each than a plain append's need (576: trees 14.0 us, prompts 45.2; 960: 12.4 and 43.9).
+// Threads of an SM: more registers each than a plain append's need (576: trees 14.0 us, prompts 45.0; 768: 10.9 and 42.8;
+// 960: 11.8 and 41.8).
 // Tokens get the many threads of kAppendFew as long as the SMs hold all of them at once, three an SM (trees of 8 rows,
 // 32/8 heads of 128 in bf16: 456 tokens 6.95 us; 464 in two turns 10.2, with the threads of kAppendMany 8.4; 760 11.6 and 9.5).
 constexpr int kNormResident = 672;

@@ -16,8 +16,8 @@
 // selection, where there are any.
 //
 // Measured (GB300, graph replays over sets of inputs beyond the L2; 32/8 heads of
-// 128): single rows of 64 sequences over 1000..2000 positions 40.0 us, 75% of 6803
-// GB/s, trees of 17 rows over 2048..4096 77.8 us, 79% (on mma.sync, whose scores
+// 128): single rows of 64 sequences over 1000..2000 positions 40.2 us, 75% of 6803
+// GB/s, trees of 17 rows over 2048..4096 77.5 us, 79% (on mma.sync, whose scores
 // have positions and queries in the same thread, 48 and 276).  Bound by memory:
 // without loads 29 and 66 us, with an eighth of the weights 40 and 76.  Blocks are
 // checked a segment ahead by the warp that brings the queries: by the weights' warps

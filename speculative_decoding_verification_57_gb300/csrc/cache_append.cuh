@@ -16,7 +16,8 @@
 // the chain of loads).  Prompts issue an instruction in two of three cycles:
 // rotation in packed pairs and angles that stay in registers took them from
 // 51 us to 31, CTAs of half the threads (a token that waits holds less of the
-// SM) to 28.6, leaving padding unread to 26.1.  One prompt of 32,768
+// SM) to 28.6, leaving padding unread to 26.1 (in later sessions, with the same code,
+// 29.9; trees 8.0).  One prompt of 32,768
 // tokens takes 120 us, all of the copy rate; in blocks of 1 it takes 285,
 // because every token looks at all blocks that its sequence writes to.
 //

@@ -12,10 +12,14 @@
 //
 // Measured (GB300, graph replays over sets of inputs beyond the L2; 32/8 heads of
 // 128 in bf16; of 1896 TFLOP/s and 6803 GB/s measured):
-//   64 single rows behind 4096 positions, 250..500 of their own   58.6 us, 29%
-//   64 trees of 17 rows behind 8192, 500..1000                    173 us, 49%
-//   16 chains of 6 rows behind 65536, 250..500                    110 us, 50%
+//   64 single rows behind 4096 positions, 250..500 of their own   58.8 us, 29%
+//   64 trees of 17 rows behind 8192, 500..1000                    171 us, 49%
+//   16 chains of 6 rows behind 65536, 250..500                    104 us, 53%
 //   fp32, 8 chains of 5, 12 heads of 64, behind 1024, 150..300    32 us, 8%
+//   (heads of 64: trees 145 us, chains 92)
+// On mma.sync, whose row tiles each read the prefix again: heads of 256 (16/4) single
+// rows 84 us (bytes 17), trees 1170 (products 84), chains 710 (55); fp32, 16 trees of 17
+// rows, 16/4 heads of 128, behind 4096 416 us (bytes 10.5).
 // (the second by tree attention over all of its positions reads 2.3 GB).  The prefix
 // of the trees alone takes 108 us, 70% of the tensor cores' rate, where the
 // streams' turns bound it; their own positions alone 50; the join, some 12, and the
